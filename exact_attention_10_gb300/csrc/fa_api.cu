@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "fa_bwd_launch.h"
+#include "fa_host.h"
 #include "fa_launch.cuh"
 
 namespace {
@@ -42,16 +43,14 @@ EncodeTiledFn encode_tiled()
     return fn;
 }
 
-constexpr int kMaxDevices = fa_launch::kMaxDevices;
-
-struct DeviceInfo {
-    bool probed = false;
-    bool supported = false;
-    int sms = 0;
-};
+static_assert(fa_host::kMaxDevices == fa_launch::kMaxDevices, "one device limit");
 
 std::mutex g_mu;
-DeviceInfo g_devices[kMaxDevices];
+fa_host::DeviceInfo g_devices[fa_host::kMaxDevices];
+
+}  // namespace
+
+namespace fa_host {
 
 // Probe the current device once: compute capability 10.3 is required because
 // the kernels are built for sm_103a only.
@@ -94,6 +93,56 @@ bool is_device_pointer(const void *p, int dev)
         return true;
     return a.type == cudaMemoryTypeDevice && a.device == dev;
 }
+
+fa_status check_args(const Arg *args, int n, int *dev, const DeviceInfo **info)
+{
+    for (int i = 0; i < n; ++i)
+        if (!args[i].p)
+            return FA_ERR_INVALID_VALUE;
+    for (int i = 0; i < n; ++i)
+        if (reinterpret_cast<uintptr_t>(args[i].p) & (args[i].align - 1u))
+            return FA_ERR_MISALIGNED;
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j)
+            if (i != j && args[i].out && ranges_overlap(args[i].p, args[i].bytes, args[j].p, args[j].bytes))
+                return FA_ERR_INVALID_VALUE;
+    *dev = -1;
+    if (cudaGetDevice(dev) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_UNSUPPORTED_DEVICE;
+    }
+    *info = device_info(*dev);
+    if (!*info || !(*info)->supported)
+        return FA_ERR_UNSUPPORTED_DEVICE;
+    for (int i = 0; i < n; ++i)
+        if (!is_device_pointer(args[i].p, *dev))
+            return FA_ERR_INVALID_VALUE;
+    return FA_OK;
+}
+
+fa_status allow_smem(const void *kern, int smem, int dev, bool *set)
+{
+    if (dev < 0 || dev >= kMaxDevices)
+        return FA_ERR_UNSUPPORTED_DEVICE;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_CUDA;
+        }
+        set[dev] = true;
+    }
+    return FA_OK;
+}
+
+}  // namespace fa_host
+
+namespace {
+
+using fa_host::device_info;
+using fa_host::DeviceInfo;
+using fa_host::is_device_pointer;
+using fa_host::ranges_overlap;
 
 // Rank-3 map over [B*H, N, D] (innermost first): per-head row bounds, so a
 // box that runs past N is zero-filled instead of reading the next head.

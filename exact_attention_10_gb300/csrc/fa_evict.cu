@@ -1,0 +1,353 @@
+// fa_evict.cu -- eviction from the 4-bit cache by accumulated attention
+// weight: which tokens stay (a selection per sequence and key head), and the
+// copy of their rows into another cache.
+//
+// Of the n = lens[b] tokens of a sequence, the first `sinks` and the last
+// `recent` stay, and of those between them the k = keep - sinks - recent with
+// the largest accumulated weight (equal weights: the lowest position first),
+// all in order of position; n <= keep keeps everything.
+//
+// Selection without sorting: weights become 32-bit keys that order as the
+// weights do, and the k-th largest key is found digit by digit (11 + 11 + 10
+// bits, a histogram of the candidates per digit); one more pass ranks what is
+// above it, and the first of those equal to it, by position.  A cluster of
+// CTAs shares a row, each holding its slice of the keys in shared memory and
+// adding the others' histograms through distributed shared memory, so the
+// weights are read from memory once and a few long rows still occupy many
+// SMs.
+#include "fa.h"
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fa_host.h"
+
+namespace {
+
+namespace cg = cooperative_groups;
+using fa_host::Arg;
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;         // the portable cluster size
+constexpr int kMaxHeld = 40960;        // keys held in shared memory per CTA (160 KB); longer slices are read again
+constexpr int kMinSlice = 2048;        // keys per CTA below which a row is not split further
+
+struct EvictParams {
+    const float *acc;
+    const int *lens;
+    const uint8_t *kc, *vc;
+    const uint32_t *kp, *vp;
+    float *acc2;
+    int *lens2, *index;
+    uint8_t *kc2, *vc2;
+    uint32_t *kp2, *vp2;
+    int Hkv, C, C2, keep, sinks, recent, held;
+    long long BH;
+};
+
+// A key that orders as the weight does: larger weight, larger key; -0 equals
+// 0, NaN is below every number.
+__device__ __forceinline__ uint32_t key_of(float x)
+{
+    if (x != x)
+        return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);   // -0 -> 0
+    return (u >> 31) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ int clamped(int n, int C)
+{
+    return n < 0 ? 0 : (n > C ? C : n);
+}
+
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    extern __shared__ uint32_t keys[];   // [held]
+    __shared__ __align__(16) int hist[kBins];
+    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_count[2], s_found[2];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const long long bh = blockIdx.x / CS;
+    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
+    const int n = clamped(p.lens[bh / p.Hkv], p.C);
+    const float *acc = p.acc + bh * p.C;
+    int *index = p.index + bh * p.keep;
+    if (rank == 0 && t == 0 && bh % p.Hkv == 0)
+        p.lens2[bh / p.Hkv] = n < p.keep ? n : p.keep;
+    if (n <= p.keep) {   // (the whole cluster leaves)
+        for (int j = rank * kSelThreads + t; j < p.keep; j += CS * kSelThreads)
+            index[j] = j < n ? j : -1;
+        return;
+    }
+    // What always stays.
+    for (int j = rank * kSelThreads + t; j < p.sinks; j += CS * kSelThreads)
+        index[j] = j;
+    for (int j = rank * kSelThreads + t; j < p.recent; j += CS * kSelThreads)
+        index[p.keep - p.recent + j] = n - p.recent + j;
+    const int k = p.keep - p.sinks - p.recent;
+    if (k == 0)
+        return;
+    const int M = n - p.recent - p.sinks;             // candidates, more than k
+    const int slice = (M + CS - 1) / CS;
+    const int lo = p.sinks + (int)min((long long)rank * slice, (long long)M), cnt = min(slice, p.sinks + M - lo);
+    const bool held = slice <= p.held;
+    if (held) {
+#pragma unroll 4
+        for (int i = t; i < cnt; i += kSelThreads)
+            keys[i] = key_of(acc[lo + i]);
+    }
+    auto key_at = [&](int i) { return held ? keys[i] : key_of(acc[lo + i]); };
+
+    uint32_t prefix = 0;   // the digits found so far
+    int left = k;          // candidates still to take among the keys that share them
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+        for (int i = t; i < kBins; i += kSelThreads)
+            hist[i] = 0;
+        __syncthreads();   // (and the keys are written)
+        for (int i = t; i < cnt; i += kSelThreads) {
+            const uint32_t key = key_at(i);
+            if (pass == 0 || (key >> (shift + bits)) == prefix)
+                atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
+        }
+        cluster.sync();
+        // Counts of the bins from the top, four to a thread, over all slices.
+        constexpr int kPer = kBins / kSelThreads;
+        const int top = kBins - 1 - t * kPer;   // this thread's highest bin
+        int c[kPer] = {}, sum = 0;
+        for (int r = 0; r < CS; ++r) {
+            const int *h = cluster.map_shared_rank(hist, r);
+            const int4 v = *reinterpret_cast<const int4 *>(h + top - (kPer - 1));
+            c[0] += v.w;
+            c[1] += v.z;
+            c[2] += v.y;
+            c[3] += v.x;
+        }
+        static_assert(kPer == 4, "one 16-byte load per histogram");
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            sum += c[i];
+        int inc = sum;
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m)
+                inc += v;
+        }
+        if (lane == 31)
+            s_gt[warp] = inc;
+        __syncthreads();
+        int before = inc - sum;
+        for (int w = 0; w < warp; ++w)
+            before += s_gt[w];
+        if (before < left && before + sum >= left) {   // exactly one thread: the counts add up to at least `left`
+            int i = 0;
+            while (before + c[i] < left)
+                before += c[i++];
+            s_found[0] = top - i;
+            s_found[1] = left - before;
+        }
+        __syncthreads();
+        prefix = (prefix << bits) | (uint32_t)s_found[0];
+        left = s_found[1];
+        cluster.sync();   // every histogram has been read
+    }
+    // prefix is the k-th largest key; `left` of the keys equal to it are taken.
+
+    // Rank by position: each warp counts its own consecutive part of the slice,
+    // then the slices and the warps before it give its first rank.
+    const int per = ((cnt + kSelWarps - 1) / kSelWarps + 31) & ~31;
+    const int w0 = min(warp * per, cnt), w1 = min(w0 + per, cnt);
+    int gt = 0, eq = 0;
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint32_t key = key_at(i);
+        gt += key > prefix;
+        eq += key == prefix;
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) {
+        s_gt[warp] = gt;
+        s_eq[warp] = eq;
+    }
+    __syncthreads();
+    if (t == 0) {
+        int a = 0, b = 0;
+        for (int w = 0; w < kSelWarps; ++w) {
+            a += s_gt[w];
+            b += s_eq[w];
+        }
+        s_count[0] = a;
+        s_count[1] = b;
+    }
+    cluster.sync();
+    int n_gt = 0, n_eq = 0;   // taken for certain, and equal, before this warp's part
+    for (int r = 0; r < rank; ++r) {
+        const int *o = cluster.map_shared_rank(s_count, r);
+        n_gt += o[0];
+        n_eq += o[1];
+    }
+    for (int w = 0; w < warp; ++w) {
+        n_gt += s_gt[w];
+        n_eq += s_eq[w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t key = i < w1 ? key_at(i) : 0u;
+        const bool g = i < w1 && key > prefix, e = i < w1 && key == prefix;
+        const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+        const int my_eq = n_eq + __popc(be & below);
+        if (g || (e && my_eq < left))
+            index[p.sinks + n_gt + __popc(bg & below) + min(my_eq, left)] = lo + i;
+        n_gt += __popc(bg);
+        n_eq += __popc(be);
+    }
+    cluster.sync();   // no CTA leaves while another may still read its counts
+}
+
+// Rows of the kept tokens into the other cache, 16 bytes a thread, and their
+// weights (0 behind the last one).  Rows behind the last one are left as they
+// are.
+template <int D>
+__global__ void __launch_bounds__(256) gather_kernel(const EvictParams p)
+{
+    constexpr int kHalf = D / 32;        // 16-byte chunks of codes per row, K or V
+    constexpr int kTpr = 2 * kHalf;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection's index
+    const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long row = g / kTpr;      // of [B Hkv C2]
+    if (row >= p.BH * p.C2)
+        return;
+    const int part = (int)(g % kTpr);
+    const long long bh = row / p.C2;
+    const int d = (int)(row - bh * p.C2);
+    const int src = d < p.keep ? p.index[bh * p.keep + d] : -1;
+    if (src < 0) {
+        if (part == 0)
+            p.acc2[row] = 0.f;
+        return;
+    }
+    const long long from = bh * p.C + src;
+    const bool v = part >= kHalf;
+    const int j = v ? part - kHalf : part;
+    const uint8_t *c = (v ? p.vc : p.kc) + from * (D / 2) + j * 16;
+    uint8_t *c2 = (v ? p.vc2 : p.kc2) + row * (D / 2) + j * 16;
+    *reinterpret_cast<uint4 *>(c2) = __ldg(reinterpret_cast<const uint4 *>(c));
+    if (j == 0)
+        (v ? p.vp2 : p.kp2)[row] = __ldg((v ? p.vp : p.kp) + from);
+    if (part == 1)
+        p.acc2[row] = p.acc[from];
+}
+
+// CTAs per row: more while every one of them still gets kMinSlice keys and
+// the rows do not fill the SMs twice over by themselves.
+int cluster_size(long long BH, int C, int sms)
+{
+    int cs = 1;
+    while (cs < kMaxCluster && BH * cs * 2 <= 2ll * sms && C / (cs * 2) >= kMinSlice)
+        cs *= 2;
+    return cs;
+}
+
+fa_status launch_evict(const EvictParams &q, int D, int sms, cudaStream_t s, int dev)
+{
+    static bool set[fa_host::kMaxDevices] = {};
+    const fa_status st = fa_host::allow_smem(reinterpret_cast<const void *>(&select_kernel), kMaxHeld * 4, dev, set);
+    if (st != FA_OK)
+        return st;
+    EvictParams p = q;
+    const int cs = cluster_size(p.BH, p.C, sms);
+    const long long slice = ((long long)p.C + cs - 1) / cs;
+    p.held = slice <= kMaxHeld ? (int)slice : 0;   // keys that fit are held; otherwise none are
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.BH * cs));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (size_t)p.held * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, select_kernel, p) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    const long long threads = p.BH * p.C2 * (D / 16);
+    cudaLaunchConfig_t cg2{};
+    cg2.gridDim = dim3((unsigned)((threads + 255) / 256));
+    cg2.blockDim = dim3(256);
+    cg2.stream = s;
+    cudaLaunchAttribute dep[1];
+    dep[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    dep[0].val.programmaticStreamSerializationAllowed = 1;
+    cg2.attrs = dep;
+    cg2.numAttrs = 1;
+    const cudaError_t e = D == 64 ? cudaLaunchKernelEx(&cg2, gather_kernel<64>, p) : cudaLaunchKernelEx(&cg2, gather_kernel<128>, p);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+}  // namespace
+
+extern "C" fa_status fa_cache_evict(const void *Kc, const void *Kp, const void *Vc, const void *Vp, const float *acc,
+                                    const int *lens, void *Kc2, void *Kp2, void *Vc2, void *Vp2, float *acc2,
+                                    int *lens2, int *index, int B, int Hkv, int C, int C2, int D, int keep, int sinks,
+                                    int recent, fa_stream_t stream)
+{
+    if (D != 64 && D != 128)
+        return FA_ERR_INVALID_VALUE;
+    if (B < 1 || Hkv < 1 || C < 1 || C2 < 1 || keep < 1 || keep > C2 || sinks < 0 || recent < 0)
+        return FA_ERR_INVALID_VALUE;
+    if ((long long)sinks + recent > keep)
+        return FA_ERR_INVALID_VALUE;
+    const long long BH = (long long)B * Hkv;
+    // (kMaxCluster CTAs per row at most, in one grid dimension)
+    if (BH >= (1ll << 31) / kMaxCluster || BH * C >= (1ll << 31) || BH * C2 >= (1ll << 31))
+        return FA_ERR_INVALID_VALUE;
+    const size_t from = (size_t)BH * C, to = (size_t)BH * C2;
+    const Arg args[13] = {{Kc, from * D / 2, false, 16}, {Kp, from * 4, false, 4}, {Vc, from * D / 2, false, 16},
+                          {Vp, from * 4, false, 4}, {acc, from * 4, false, 4}, {lens, (size_t)B * 4, false, 4},
+                          {Kc2, to * D / 2, true, 16}, {Kp2, to * 4, true, 4}, {Vc2, to * D / 2, true, 16},
+                          {Vp2, to * 4, true, 4}, {acc2, to * 4, true, 4}, {lens2, (size_t)B * 4, true, 4},
+                          {index, (size_t)BH * keep * 4, true, 4}};
+    int dev;
+    const fa_host::DeviceInfo *di;
+    const fa_status st = fa_host::check_args(args, 13, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    EvictParams p{};
+    p.acc = acc;
+    p.lens = lens;
+    p.kc = static_cast<const uint8_t *>(Kc);
+    p.kp = static_cast<const uint32_t *>(Kp);
+    p.vc = static_cast<const uint8_t *>(Vc);
+    p.vp = static_cast<const uint32_t *>(Vp);
+    p.acc2 = acc2;
+    p.lens2 = lens2;
+    p.index = index;
+    p.kc2 = static_cast<uint8_t *>(Kc2);
+    p.kp2 = static_cast<uint32_t *>(Kp2);
+    p.vc2 = static_cast<uint8_t *>(Vc2);
+    p.vp2 = static_cast<uint32_t *>(Vp2);
+    p.Hkv = Hkv;
+    p.C = C;
+    p.C2 = C2;
+    p.keep = keep;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.BH = BH;
+    return launch_evict(p, D, di->sms, reinterpret_cast<cudaStream_t>(stream), dev);
+}

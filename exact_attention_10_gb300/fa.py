@@ -8,6 +8,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+from functools import lru_cache
+from typing import NamedTuple
 
 from .build import LIB_PATH
 
@@ -15,8 +17,9 @@ FA_BF16, FA_FP16 = 0, 1
 FA_BWD_DETERMINISTIC = 1
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_VALUE", 2: "FA_ERR_MISALIGNED", 3: "FA_ERR_UNSUPPORTED_DEVICE",
           4: "FA_ERR_CUDA", 5: "FA_ERR_DEVICE_TIMEOUT", 6: "FA_ERR_NO_ALLOC_LIMIT"}
-EXPORTS = ("fa_bwd", "fa_bwd_band", "fa_bwd_ex", "fa_fwd", "fa_fwd_band", "fa_fwd_ex", "fa_fwd_noalloc", "fa_fwd_qkv", "fa_sync_status",
-           "fa_status_string")
+EXPORTS = ("fa_bwd", "fa_bwd_band", "fa_bwd_ex", "fa_cache_append", "fa_cache_evict", "fa_cache_fwd", "fa_cache_read",
+           "fa_cache_weights", "fa_cache_workspace", "fa_fwd", "fa_fwd_band", "fa_fwd_ex", "fa_fwd_noalloc",
+           "fa_fwd_qkv", "fa_sync_status", "fa_status_string")
 SCHEDULES = {"auto": 0, "whole_tiles": 1, "balanced": 2}
 
 _lib = None
@@ -55,6 +58,18 @@ def load(path: str = LIB_PATH):
     lib.fa_bwd_band.restype = c_int
     lib.fa_bwd_ex.argtypes = [vp] * 9 + [c_int] * 7 + [ctypes.c_float, c_int, ctypes.c_uint, vp]
     lib.fa_bwd_ex.restype = c_int
+    lib.fa_cache_append.argtypes = [vp] * 8 + [c_int] * 6 + [vp]
+    lib.fa_cache_append.restype = c_int
+    lib.fa_cache_read.argtypes = [vp] * 8 + [c_int] * 6 + [vp]
+    lib.fa_cache_read.restype = c_int
+    lib.fa_cache_workspace.argtypes = [c_int] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_cache_workspace.restype = c_int
+    lib.fa_cache_fwd.argtypes = [vp] * 8 + [c_int] * 8 + [ctypes.c_float, c_int, vp, ctypes.c_size_t, vp]
+    lib.fa_cache_fwd.restype = c_int
+    lib.fa_cache_weights.argtypes = [vp] * 6 + [c_int] * 9 + [ctypes.c_float, c_int, vp]
+    lib.fa_cache_weights.restype = c_int
+    lib.fa_cache_evict.argtypes = [vp] * 13 + [c_int] * 8 + [vp]
+    lib.fa_cache_evict.restype = c_int
     lib.fa_sync_status.argtypes = [vp]
     lib.fa_sync_status.restype = c_int
     lib.fa_status_string.argtypes = [c_int]
@@ -186,3 +201,227 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     if rc != 0:
         raise FAError(rc, "fa_bwd")
     return dq, dk, dv
+
+
+# ---- the 4-bit key/value cache
+
+class PackedCache(NamedTuple):
+    """K and V of [B, Hkv, C, D] held in 4 bits: codes [B, Hkv, C, D/2] uint8
+    and (scale, minimum) [B, Hkv, C, 2] in the model's type (the format is in
+    include/fa.h)."""
+
+    k_codes: "torch.Tensor"
+    k_params: "torch.Tensor"
+    v_codes: "torch.Tensor"
+    v_params: "torch.Tensor"
+
+
+def cache_empty(B: int, Hkv: int, C: int, D: int, dtype=None, device="cuda") -> PackedCache:
+    """A cache of capacity C for B sequences and Hkv key heads (all codes and
+    params zero); ``dtype`` bfloat16 (default) or float16."""
+    import torch
+    if D not in (64, 128):
+        raise ValueError("D must be 64 or 128")
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"a cache is of bfloat16 or float16, got {dtype}")
+    return PackedCache(*(torch.zeros((B, Hkv, C, n), dtype=t, device=device)
+                         for n, t in ((D // 2, torch.uint8), (2, dtype)) * 2))
+
+
+def _cache_sizes(cache: PackedCache):
+    """(B, Hkv, C, D, dtype code) of a cache whose parts fit together."""
+    import torch
+    kc, kp, vc, vp = cache
+    if kc.dim() != 4 or kc.shape != vc.shape or kp.shape != vp.shape or kp.shape != (*kc.shape[:3], 2):
+        raise ValueError("a cache is codes [B, Hkv, C, D/2] and params [B, Hkv, C, 2] for K and for V")
+    if kc.dtype != torch.uint8 or vc.dtype != torch.uint8 or kp.dtype != vp.dtype:
+        raise TypeError("cache codes are uint8, the params of K and V of one type")
+    if not (kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous() and vp.is_contiguous()):
+        raise ValueError("the cache must be contiguous")
+    B, Hkv, C, half = kc.shape
+    return B, Hkv, C, 2 * half, _dtype_code(kp)
+
+
+def _ints(t, B: int, name: str):
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.shape != (B,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{B}]")
+    return t.data_ptr()
+
+
+def _stream_of(stream, t) -> int:
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(t.device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _left_of(window, sinks) -> int:
+    """window_left of ``window`` = (left, 0) or None (no window)."""
+    if sinks < 0:
+        raise ValueError("sinks must not be negative")
+    if window is None:
+        return -1
+    if window[1] != 0:
+        raise ValueError("this attention is causal: window must be (left, 0)")
+    return max(-1, min(int(window[0]), 0x7FFFFFFF))
+
+
+def cache_append(cache: PackedCache, k, v, start, count=None, stream=None) -> None:
+    """Pack tokens k, v [B, Hkv, N, D] into the cache at positions start[b] + i
+    (``start`` int32 [B]); with ``count`` (int32 [B]) only the first count[b]
+    of a sequence.  Tokens whose place lies outside the cache are not written.
+    Raises FAError on any non-OK status.  Asynchronous on ``stream``
+    (default: the current torch stream)."""
+    B, Hkv, C, D, code = _cache_sizes(cache)
+    if k.dim() != 4 or k.shape != v.shape or k.shape[:2] != (B, Hkv) or k.shape[3] != D:
+        raise ValueError(f"k, v must be [{B}, {Hkv}, N, {D}]")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("k, v must be contiguous")
+    if k.dtype != cache.k_params.dtype or v.dtype != k.dtype:
+        raise TypeError("k, v must be of the cache's type")
+    rc = load().fa_cache_append(*(x.data_ptr() for x in cache), k.data_ptr(), v.data_ptr(), _ints(start, B, "start"),
+                                None if count is None else _ints(count, B, "count"), B, Hkv, k.shape[2], C, D, code,
+                                _stream_of(stream, k))
+    if rc != 0:
+        raise FAError(rc, "fa_cache_append")
+
+
+def cache_read(cache: PackedCache, start, n: int, count=None, stream=None):
+    """The values (k, v) [B, Hkv, n, D] that cache tokens start[b] + i stand
+    for; rows from count[b] on, or outside the cache, are zeros."""
+    import torch
+    B, Hkv, C, D, code = _cache_sizes(cache)
+    k = torch.empty((B, Hkv, n, D), dtype=cache.k_params.dtype, device=cache.k_codes.device)
+    v = torch.empty_like(k)
+    rc = load().fa_cache_read(*(x.data_ptr() for x in cache), k.data_ptr(), v.data_ptr(), _ints(start, B, "start"),
+                              None if count is None else _ints(count, B, "count"), B, Hkv, n, C, D, code,
+                              _stream_of(stream, k))
+    if rc != 0:
+        raise FAError(rc, "fa_cache_read")
+    return k, v
+
+
+@lru_cache(maxsize=None)
+def _cache_workspace(device: int, H: int, Hkv: int, Nq: int, D: int) -> int:
+    n = ctypes.c_size_t()
+    rc = load().fa_cache_workspace(H, Hkv, Nq, D, ctypes.byref(n))
+    if rc != 0:
+        raise FAError(rc, "fa_cache_workspace")
+    return n.value
+
+
+def _cache_queries(q, cache):
+    B, Hkv, C, D, code = _cache_sizes(cache)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or q.shape[1] % Hkv != 0:
+        raise ValueError(f"q must be [{B}, a multiple of {Hkv}, Nq, {D}]")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    if q.dtype != cache.k_params.dtype:
+        raise TypeError("q must be of the cache's type")
+    return B, q.shape[1], Hkv, q.shape[2], C, D, code
+
+
+def cache_forward(q, cache: PackedCache, lens, window: tuple[int, int] | None = None, sinks: int = 0,
+                  scale: float | None = None, out=None, lse=None, stream=None):
+    """Attention of each sequence's last Nq tokens, q [B, H, Nq, D], against
+    the cache's first lens[b] tokens (theirs among them; ``lens`` int32 [B]);
+    H / Hkv query heads share a key head.  Returns (O [B, H, Nq, D], LSE
+    [B, H, Nq]).  ``window = (left, 0)`` limits query position p to tokens
+    from p - left on, but for the first ``sinks`` tokens, which stay visible.
+
+    Raises FAError on any non-OK status.  Asynchronous on ``stream``
+    (default: the current torch stream); the workspace comes from torch, on
+    the current torch stream, and a given ``stream`` must be ordered with it.
+    """
+    import torch
+    B, H, Hkv, Nq, C, D, code = _cache_queries(q, cache)
+    left = _left_of(window, sinks)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, H, Nq]")
+    nbytes = _cache_workspace(q.device.index, H, Hkv, Nq, D)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    st = _stream_of(stream, q)
+    rc = load().fa_cache_fwd(q.data_ptr(), *(x.data_ptr() for x in cache), _ints(lens, B, "lens"), out.data_ptr(),
+                             lse.data_ptr(), B, H, Hkv, Nq, C, D, left, sinks,
+                             float(D ** -0.5 if scale is None else scale), code, ws.data_ptr(), nbytes, st)
+    if rc != 0:
+        raise FAError(rc, "fa_cache_fwd")
+    if stream is not None:
+        _keep_until_done(ws, stream)
+    return out, lse
+
+
+def _keep_until_done(t, stream) -> None:
+    """Let torch reuse ``t``'s memory only after the work queued on ``stream``."""
+    import torch
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    t.record_stream(stream)
+
+
+def cache_weights(q, cache: PackedCache, lse, lens, window: tuple[int, int] | None = None, sinks: int = 0,
+                  scale: float | None = None, acc=None, stream=None):
+    """What each cached token weighs in ``cache_forward`` of the same arguments
+    (``lse`` as it returned it): [B, Hkv, C] float32, the sum over a key
+    head's query rows of exp(scale q.k - lse).  With ``acc`` ([B, Hkv, C]
+    float32) the weights are added to it in place, and it is returned."""
+    import torch
+    B, H, Hkv, Nq, C, D, code = _cache_queries(q, cache)
+    left = _left_of(window, sinks)
+    if lse.shape != (B, H, Nq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous [B, H, Nq]")
+    if lse.dtype != torch.float32 or (acc is not None and acc.dtype != torch.float32):
+        raise TypeError("lse and acc must be float32")
+    out = torch.empty((B, Hkv, C), dtype=torch.float32, device=q.device) if acc is None else acc
+    if out.shape != (B, Hkv, C) or not out.is_contiguous():
+        raise ValueError("acc must be contiguous [B, Hkv, C]")
+    rc = load().fa_cache_weights(q.data_ptr(), cache.k_codes.data_ptr(), cache.k_params.data_ptr(), lse.data_ptr(),
+                                 _ints(lens, B, "lens"), out.data_ptr(), int(acc is not None), B, H, Hkv, Nq, C, D,
+                                 left, sinks, float(D ** -0.5 if scale is None else scale), code,
+                                 _stream_of(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_cache_weights")
+    return out
+
+
+def cache_evict(cache: PackedCache, acc, lens, keep: int, sinks: int = 0, recent: int = 0,
+                out: PackedCache | None = None, stream=None):
+    """Bring every sequence down to at most ``keep`` tokens per key head: the
+    first ``sinks``, the last ``recent`` and the heaviest by ``acc`` [B, Hkv,
+    C] float32 between them (ties: the lowest position first), in order.
+
+    Returns (cache, acc, lens, index): another cache (``out``, of any capacity
+    from ``keep`` on, or a new one of capacity ``keep``), the kept tokens'
+    weights [B, Hkv, capacity] (0 behind them), the new lengths [B] and the
+    kept positions [B, Hkv, keep] (-1 behind them)."""
+    import torch
+    B, Hkv, C, D, code = _cache_sizes(cache)
+    if acc.shape != (B, Hkv, C) or not acc.is_contiguous():
+        raise ValueError("acc must be contiguous [B, Hkv, C]")
+    if acc.dtype != torch.float32:
+        raise TypeError("acc must be float32")
+    if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep:
+        raise ValueError("keep must be at least 1 and hold the sinks and the recent tokens")
+    dev = cache.k_codes.device
+    if out is None:   # (its rows behind the last kept token are not written)
+        out = PackedCache(*(torch.empty((B, Hkv, keep, x.shape[3]), dtype=x.dtype, device=dev) for x in cache))
+    B2, Hkv2, C2, D2, code2 = _cache_sizes(out)
+    if (B2, Hkv2, D2, code2) != (B, Hkv, D, code) or C2 < keep:
+        raise ValueError("out must be a cache like the first one, of capacity keep at least")
+    acc2 = torch.empty((B, Hkv, C2), dtype=torch.float32, device=dev)
+    lens2 = torch.empty((B,), dtype=torch.int32, device=dev)
+    index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
+    rc = load().fa_cache_evict(*(x.data_ptr() for x in cache), acc.data_ptr(), _ints(lens, B, "lens"),
+                               *(x.data_ptr() for x in out), acc2.data_ptr(), lens2.data_ptr(), index.data_ptr(), B,
+                               Hkv, C, C2, D, keep, sinks, recent, _stream_of(stream, acc))
+    if rc != 0:
+        raise FAError(rc, "fa_cache_evict")
+    return out, acc2, lens2, index

@@ -47,6 +47,8 @@
 #define FA_API
 #endif
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -284,6 +286,118 @@ FA_API fa_status fa_bwd_ex(const void *Q, const void *K, const void *V, const vo
                            const float *LSE, void *dQ, void *dK, void *dV, int B, int H, int Nq, int Nkv, int D,
                            int window_left, int window_right, float scale, fa_dtype dtype, unsigned int flags,
                            fa_stream_t stream);
+
+/*
+ * ---- A key/value cache held in 4 bits ----
+ *
+ * A cache holds, for K and for V, one packed row per token and key head:
+ *   codes   [B, Hkv, C, D/2] bytes: D codes of 4 bits, the even channel in
+ *           the low half of its byte;
+ *   params  [B, Hkv, C, 2] of `dtype`: scale, minimum.
+ * C is the capacity.  A row x of D values of type t = `dtype` is held as
+ *   min = min_d x_d,  scale = t((max_d x_d - min) / 15),
+ *   code_d = clamp(round_half_even((x_d - min) / scale), 0, 15), 0 if scale = 0
+ * and stands for min + code_d * scale: D/2 + 4 bytes for 2 D, the values off
+ * by at most half a scale, plus 15 roundings of the scale to t at the row's
+ * upper end.  A row that holds an infinity or NaN stands for NaN throughout.
+ * Kc and Vc are the codes, Kp and Vp the params.
+ *
+ * lens [B] (int32, device memory) gives each sequence's tokens in the cache;
+ * values outside [0, C] are clamped to it.  It is read on the device, so a
+ * captured graph follows its changes; rows behind a sequence's last token are
+ * neither read nor written unless said otherwise.
+ *
+ * Arguments of all cache calls: device pointers to contiguous tensors;
+ * B, Hkv, C >= 1 with B*Hkv*C < 2^31; D = 64 or 128; codes, Q, K, V, O and
+ * workspaces 16-byte aligned, everything else to its element (params 4).
+ * Outputs overlap no other argument.  Errors as for fa_fwd, nothing enqueued
+ * on any of them.  The calls allocate nothing and keep nothing between calls:
+ * a workspace is the caller's, so calls that may overlap (other streams,
+ * other captured graphs) take different ones.
+ */
+
+/*
+ * fa_cache_append -- pack N new tokens per sequence into the cache.
+ *
+ * K, V  : [B, Hkv, N, D] of `dtype`; token i of sequence b becomes cache
+ *         token start[b] + i.
+ * start : [B] int32, device memory.
+ * count : [B] int32, device memory, or NULL: token i of sequence b counts
+ *         only if i < count[b] (a padded batch).  Tokens that do not count,
+ *         or whose place lies outside [0, C), are not written.
+ */
+FA_API fa_status fa_cache_append(void *Kc, void *Kp, void *Vc, void *Vp, const void *K, const void *V,
+                                 const int *start, const int *count, int B, int Hkv, int N, int C, int D,
+                                 fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * fa_cache_read -- the values that cache tokens start[b] .. start[b] + N - 1
+ * stand for, rounded once to `dtype`, into K and V [B, Hkv, N, D].  Rows that
+ * do not count (i >= count[b]) or lie outside [0, C) become zeros.
+ */
+FA_API fa_status fa_cache_read(const void *Kc, const void *Kp, const void *Vc, const void *Vp, void *K, void *V,
+                               const int *start, const int *count, int B, int Hkv, int N, int C, int D,
+                               fa_dtype dtype, fa_stream_t stream);
+
+/* fa_cache_workspace -- bytes of workspace that fa_cache_fwd needs on the
+ * current device for these sizes (any B and C). */
+FA_API fa_status fa_cache_workspace(int H, int Hkv, int Nq, int D, size_t *bytes);
+
+/*
+ * fa_cache_fwd -- attention of each sequence's last Nq tokens against the
+ * cache: decoding (Nq = 1), speculative decoding, or the end of a prompt.
+ *
+ * Q, O : [B, H, Nq, D] of `dtype`; H a multiple of Hkv, query heads h Hkv/H
+ *        sharing key head floor(h / (H / Hkv)).  LSE : [B, H, Nq] float32.
+ * Query i of sequence b sits at position p = lens[b] - Nq + i (its own key is
+ * in the cache) and sees the tokens j <= p with j >= p - window_left
+ * (window_left < 0: no bound) or j < sinks.  A query that sees no token
+ * (p < 0) gets O = 0 and LSE = -inf.
+ * workspace : fa_cache_workspace bytes; its contents need no set-up.
+ *
+ * K and V enter as their integer codes, exact in 16 bits, with scale and
+ * minimum applied outside the products in fp32; the softmax weights times V's
+ * scale are split into two 16-bit parts, so nothing but the final result is
+ * rounded to 16 bits.
+ */
+FA_API fa_status fa_cache_fwd(const void *Q, const void *Kc, const void *Kp, const void *Vc, const void *Vp,
+                              const int *lens, void *O, float *LSE, int B, int H, int Hkv, int Nq, int C, int D,
+                              int window_left, int sinks, float scale, fa_dtype dtype, void *workspace,
+                              size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_cache_weights -- what each cached token weighs in that attention, from
+ * the LSE that fa_cache_fwd returned for the same arguments:
+ *   w[b, h, j] = sum over the H/Hkv query heads of key head h and their Nq
+ *                queries that see token j of exp(scale * q . k_j - LSE).
+ * accumulate = 0: acc [B, Hkv, C] = w, every entry written (0 for tokens
+ * that no query sees and behind lens[b]).  accumulate = 1: acc += w at the
+ * tokens before lens[b]; the others are left as they are.  The sums have a
+ * fixed order: the same bits on every call.
+ */
+FA_API fa_status fa_cache_weights(const void *Q, const void *Kc, const void *Kp, const float *LSE, const int *lens,
+                                  float *acc, int accumulate, int B, int H, int Hkv, int Nq, int C, int D,
+                                  int window_left, int sinks, float scale, fa_dtype dtype, fa_stream_t stream);
+
+/*
+ * fa_cache_evict -- bring every sequence down to at most `keep` tokens, in
+ * another cache of capacity C2 >= keep: per key head the first `sinks`, the
+ * last `recent` (sinks + recent <= keep) and, of those between them, the ones
+ * with the largest acc [B, Hkv, C] (equal weights: the lowest position first;
+ * -0 equals 0; NaN is below every number), in order of position.  A sequence
+ * of at most `keep` tokens keeps them all.
+ *
+ * Kc2, Kp2, Vc2, Vp2 : the other cache; rows behind the last kept token are
+ *                      left as they are.
+ * acc2  : [B, Hkv, C2] float32: the kept tokens' weights, then zeros.
+ * lens2 : [B] int32: min(lens[b], keep).
+ * index : [B, Hkv, keep] int32: the kept tokens' positions in the first
+ *         cache, then -1.
+ */
+FA_API fa_status fa_cache_evict(const void *Kc, const void *Kp, const void *Vc, const void *Vp, const float *acc,
+                                const int *lens, void *Kc2, void *Kp2, void *Vc2, void *Vp2, float *acc2,
+                                int *lens2, int *index, int B, int Hkv, int C, int C2, int D, int keep, int sinks,
+                                int recent, fa_stream_t stream);
 
 /*
  * fa_sync_status -- synchronise `stream`, then return and clear the device
