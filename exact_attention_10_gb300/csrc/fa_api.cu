@@ -402,6 +402,112 @@ fa_status fwd_impl(const void *Q, const void *K, const void *V, void *O, float *
 
 }  // namespace
 
+namespace {
+
+// What the sink calls check of their sizes; window_left normalised (a window
+// that cannot bind becomes none).
+bool sink_sizes_ok(int B, int H, int Hkv, int Nq, int Nkv, int D, int window_left, int sinks, int *wl)
+{
+    if (D != 64 && D != 128)
+        return false;
+    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nkv < 1 || sinks < 0)
+        return false;
+    const long long BH = (long long)B * H;
+    if (BH >= (1ll << 31) || BH * Nq >= (1ll << 31) || (long long)B * Hkv * Nkv >= (1ll << 31))
+        return false;
+    int wr = 0;
+    *wl = window_left;
+    fa::sched_band_normalize(Nq, Nkv, *wl, wr);
+    return true;
+}
+
+// The current device, if it is one this library runs on.
+fa_status current_device(int *dev, const DeviceInfo **di)
+{
+    *dev = -1;
+    if (cudaGetDevice(dev) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_UNSUPPORTED_DEVICE;
+    }
+    *di = device_info(*dev);
+    return (*di && (*di)->supported) ? FA_OK : FA_ERR_UNSUPPORTED_DEVICE;
+}
+
+}  // namespace
+
+extern "C" fa_status fa_fwd_sink_workspace(int B, int H, int Hkv, int Nq, int Nkv, int D, int window_left, int sinks,
+                                           fa_schedule schedule, size_t *bytes)
+{
+    int wl;
+    if (!bytes || !sink_sizes_ok(B, H, Hkv, Nq, Nkv, D, window_left, sinks, &wl))
+        return FA_ERR_INVALID_VALUE;
+    if (schedule != FA_SCHEDULE_AUTO && schedule != FA_SCHEDULE_WHOLE_TILES && schedule != FA_SCHEDULE_BALANCED)
+        return FA_ERR_INVALID_VALUE;
+    int dev;
+    const DeviceInfo *di;
+    const fa_status st = current_device(&dev, &di);
+    if (st != FA_OK)
+        return st;
+    *bytes = (size_t)fa::sched_workspace_bytes(
+        fa::sched_plan_sink(Nq, Nkv, B * H, H / Hkv, di->sms, (int)schedule, wl, sinks), D);
+    return FA_OK;
+}
+
+extern "C" fa_status fa_fwd_sink(const void *Q, const void *K, const void *V, void *O, float *LSE, int B, int H,
+                                 int Hkv, int Nq, int Nkv, int D, int window_left, int sinks, float scale,
+                                 fa_dtype dtype, fa_schedule schedule, void *workspace, size_t workspace_bytes,
+                                 fa_stream_t stream)
+{
+    int wl;
+    if (dtype != FA_BF16 && dtype != FA_FP16)
+        return FA_ERR_INVALID_VALUE;
+    if (schedule != FA_SCHEDULE_AUTO && schedule != FA_SCHEDULE_WHOLE_TILES && schedule != FA_SCHEDULE_BALANCED)
+        return FA_ERR_INVALID_VALUE;
+    if (!sink_sizes_ok(B, H, Hkv, Nq, Nkv, D, window_left, sinks, &wl))
+        return FA_ERR_INVALID_VALUE;
+    if (!std::isfinite(scale) || !(scale > 0.f))
+        return FA_ERR_INVALID_VALUE;
+    const size_t qrows = (size_t)B * H * Nq, krows = (size_t)B * Hkv * Nkv;
+    const fa_host::Arg args[6] = {{Q, qrows * D * 2, false, 16}, {K, krows * D * 2, false, 16},
+                                  {V, krows * D * 2, false, 16}, {O, qrows * D * 2, true, 16},
+                                  {LSE, qrows * 4, true, 16},    {workspace, workspace_bytes, true, 16}};
+    int dev;
+    const DeviceInfo *di;
+    const fa_status st = fa_host::check_args(args, workspace ? 6 : 5, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    fa::SinkParams p{};
+    p.sch = fa::sched_plan_sink(Nq, Nkv, B * H, H / Hkv, di->sms, (int)schedule, wl, sinks);
+    const size_t need = (size_t)fa::sched_workspace_bytes(p.sch, D);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return FA_ERR_INVALID_VALUE;
+    const bool bf16 = dtype == FA_BF16;
+    alignas(64) CUtensorMap tq, tk, tv;
+    if (!encode_map(&tq, Q, B * H, Nq, D, bf16) || !encode_map(&tk, K, B * Hkv, Nkv, D, bf16) ||
+        !encode_map(&tv, V, B * Hkv, Nkv, D, bf16))
+        return FA_ERR_CUDA;
+    p.O = O;
+    p.LSE = LSE;
+    p.N = Nq;
+    p.Nkv = Nkv;
+    p.off = Nkv - Nq;
+    p.qk_scale = scale * 1.4426950408889634f;   // scale * log2(e)
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (p.sch.split) {   // the caller's workspace; its counters start at zero
+        size_t o_bytes, ml_bytes, cnt_bytes;
+        fa_launch::workspace_bytes(p.sch, D, &o_bytes, &ml_bytes, &cnt_bytes);
+        char *ws = static_cast<char *>(workspace);
+        p.part_o = reinterpret_cast<float *>(ws);
+        p.part_ml = reinterpret_cast<float2 *>(ws + o_bytes);
+        p.counters = reinterpret_cast<int *>(ws + o_bytes + ml_bytes);
+        if (cudaMemsetAsync(p.counters, 0, cnt_bytes, s) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_CUDA;
+        }
+    }
+    return fa_launch::launch_sink(D, bf16, p.sch.split != 0, tq, tk, tv, p, p.sch.G, s, dev);
+}
+
 extern "C" fa_status fa_fwd_ex(const void *Q, const void *K, const void *V, void *O, float *LSE, int B, int H,
                                int N, int D, int causal, float scale, fa_dtype dtype, fa_schedule schedule,
                                fa_stream_t stream)
@@ -578,6 +684,126 @@ extern "C" fa_status fa_bwd_ex(const void *Q, const void *K, const void *V, cons
                     stream);
 }
 
+namespace {
+
+// Workspace of fa_bwd_sink: -delta and -lg, the fused pass's dQ accumulator,
+// the sink tiles' parts (all offsets multiples of 512 bytes).
+struct BwdSinkSpace {
+    size_t rows;    // B * H * Npad
+    bool fused;
+    int nc;
+    size_t floats;  // in all
+    size_t part;    // first float of the parts
+};
+
+BwdSinkSpace bwd_sink_space(int B, int H, int Hkv, int N, int Nkv, int D, int wl, int sinks, unsigned int flags, int sms)
+{
+    BwdSinkSpace w;
+    const size_t npad = ((size_t)N + 127) / 128 * 128;
+    w.rows = (size_t)B * H * npad;
+    w.fused = D == 64 && !(flags & FA_BWD_DETERMINISTIC);
+    w.nc = fa_launch::sink_parts_for(B * H, B * Hkv, N, Nkv, wl, sinks, sms);
+    w.part = (2 + (w.fused ? (size_t)D : 0)) * w.rows;
+    w.floats = w.part;
+    if (w.nc > 1)
+        w.floats += (size_t)B * Hkv * (((size_t)sinks + 127) / 128) * w.nc * 2 * 128 * D;
+    return w;
+}
+
+// Sinks that matter: none without a window, at most all keys.
+int sinks_of(int wl, int sinks, int Nkv)
+{
+    return wl >= fa::kSchedUnbounded ? 0 : (sinks < Nkv ? sinks : Nkv);
+}
+
+bool bwd_sink_sizes_ok(int B, int H, int Nq)
+{
+    return (long long)B * H * (((long long)Nq + 127) / 128 * 128) < (1ll << 31);
+}
+
+}  // namespace
+
+extern "C" fa_status fa_bwd_sink_workspace(int B, int H, int Hkv, int Nq, int Nkv, int D, int window_left, int sinks,
+                                           unsigned int flags, size_t *bytes)
+{
+    int wl;
+    if (!bytes || (flags & ~FA_BWD_DETERMINISTIC) || !sink_sizes_ok(B, H, Hkv, Nq, Nkv, D, window_left, sinks, &wl) ||
+        !bwd_sink_sizes_ok(B, H, Nq))
+        return FA_ERR_INVALID_VALUE;
+    int dev;
+    const DeviceInfo *di;
+    const fa_status st = current_device(&dev, &di);
+    if (st != FA_OK)
+        return st;
+    *bytes = bwd_sink_space(B, H, Hkv, Nq, Nkv, D, wl, sinks_of(wl, sinks, Nkv), flags, di->sms).floats * sizeof(float);
+    return FA_OK;
+}
+
+extern "C" fa_status fa_bwd_sink(const void *Q, const void *K, const void *V, const void *O, const void *dO,
+                                 const float *LSE, void *dQ, void *dK, void *dV, int B, int H, int Hkv, int Nq, int Nkv,
+                                 int D, int window_left, int sinks, float scale, fa_dtype dtype, unsigned int flags,
+                                 void *workspace, size_t workspace_bytes, fa_stream_t stream)
+{
+    int wl;
+    if ((flags & ~FA_BWD_DETERMINISTIC) || (dtype != FA_BF16 && dtype != FA_FP16))
+        return FA_ERR_INVALID_VALUE;
+    if (!sink_sizes_ok(B, H, Hkv, Nq, Nkv, D, window_left, sinks, &wl) || !bwd_sink_sizes_ok(B, H, Nq))
+        return FA_ERR_INVALID_VALUE;
+    if (!std::isfinite(scale) || !(scale > 0.f))
+        return FA_ERR_INVALID_VALUE;
+    const size_t qbytes = (size_t)B * H * Nq * D * 2, kbytes = (size_t)B * Hkv * Nkv * D * 2;
+    const fa_host::Arg args[10] = {{Q, qbytes, false, 16}, {K, kbytes, false, 16}, {V, kbytes, false, 16},
+                                   {O, qbytes, false, 16}, {dO, qbytes, false, 16}, {LSE, (size_t)B * H * Nq * 4, false, 16},
+                                   {dQ, qbytes, true, 16}, {dK, kbytes, true, 16}, {dV, kbytes, true, 16},
+                                   {workspace, workspace_bytes, true, 16}};
+    int dev;
+    const DeviceInfo *di;
+    const fa_status st = fa_host::check_args(args, 10, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    const int ns = sinks_of(wl, sinks, Nkv);
+    const BwdSinkSpace sp = bwd_sink_space(B, H, Hkv, Nq, Nkv, D, wl, ns, flags, di->sms);
+    if (workspace_bytes < sp.floats * sizeof(float))
+        return FA_ERR_INVALID_VALUE;
+    const bool bf16 = dtype == FA_BF16;
+    fa_launch::BwdLaunch a{};
+    if (!encode_map(&a.tq, Q, B * H, Nq, D, bf16) || !encode_map(&a.tk, K, B * Hkv, Nkv, D, bf16) ||
+        !encode_map(&a.tv, V, B * Hkv, Nkv, D, bf16) || !encode_map(&a.tdo, dO, B * H, Nq, D, bf16))
+        return FA_ERR_CUDA;
+    float *ws = static_cast<float *>(workspace);
+    a.fused = sp.fused;
+    if (sp.fused) {
+        a.dqa = ws + 2 * sp.rows;
+        if (!encode_map_f32(&a.tdqa, a.dqa, (long long)sp.rows, D))
+            return FA_ERR_CUDA;
+    }
+    a.O = O;
+    a.dO = dO;
+    a.LSE = LSE;
+    a.dQ = dQ;
+    a.dK = dK;
+    a.dV = dV;
+    a.lg = ws;
+    a.dl = ws + sp.rows;
+    a.BH = B * H;
+    a.N = Nq;
+    a.Nkv = Nkv;
+    a.Npad = (Nq + 127) / 128 * 128;
+    a.D = D;
+    a.sms = di->sms;
+    a.bf16 = bf16;
+    a.causal = true;
+    a.wl = wl;
+    a.wr = 0;
+    a.scale = scale;
+    a.BHkv = B * Hkv;
+    a.group = H / Hkv;
+    a.sinks = ns;
+    a.nc = sp.nc;
+    a.part = ws + sp.part;
+    return fa_launch::launch_bwd_sink(a, reinterpret_cast<cudaStream_t>(stream), dev);
+}
+
 extern "C" fa_status fa_sync_status(fa_stream_t stream)
 {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
@@ -585,11 +811,12 @@ extern "C" fa_status fa_sync_status(fa_stream_t stream)
         return FA_ERR_CUDA;
     }
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned int w_whole = 0, w_split = 0, w_band = 0, w_bwd = 0;
+    unsigned int w_whole = 0, w_split = 0, w_band = 0, w_bwd = 0, w_sink = 0, w_bsink = 0;
     if (!fa_launch::take_status_word_whole(s, &w_whole) || !fa_launch::take_status_word_split(s, &w_split) ||
-        !fa_launch::take_status_word_band(s, &w_band) || !fa_launch::take_status_word_bwd(s, &w_bwd))
+        !fa_launch::take_status_word_band(s, &w_band) || !fa_launch::take_status_word_bwd(s, &w_bwd) ||
+        !fa_launch::take_status_word_sink(s, &w_sink) || !fa_launch::take_status_word_bwd_sink(s, &w_bsink))
         return FA_ERR_CUDA;
-    if ((w_whole | w_split | w_band | w_bwd) != 0) {
+    if ((w_whole | w_split | w_band | w_bwd | w_sink | w_bsink) != 0) {
         // an aborted launch may have left split-tile counters non-zero
         int dev = -1;
         cudaGetDevice(&dev);

@@ -119,6 +119,23 @@ struct Params {
     float scale;
 };
 
+// The same for a causal window with sinks (the first `sinks` keys stay
+// visible) and query heads that share key heads: BH counts query heads, T is
+// the pass's sink items and tiles.
+struct SinkParams : Params {
+    int sinks;      // at most Nkv; 0 where the window has no bound
+    int ss;         // key tiles that hold sinks
+    int group;      // query heads per key head
+    int BHkv;       // B * key heads
+    int nc;         // KV: parts that a sink tile's query tiles are cut into
+    float *part;    // KV, nc > 1: the parts' dK and dV, [BHkv * ss * nc][2][128][D] fp32, not yet scaled
+};
+
+template <class P>
+constexpr bool kSinkPass = false;
+template <>
+constexpr bool kSinkPass<SinkParams> = true;
+
 // FQ: the fused pass (KV, D = 64 only): dQ products beside dK and dV.
 template <int D, bool KV, bool FQ = false>
 struct BCfg {
@@ -270,6 +287,95 @@ __device__ __forceinline__ void bwd_decode(const Params &p, bool causal, int t, 
     }
 }
 
+// A work tile: its resident head and tile, and for each of its n steps the
+// streamed head and tile.
+struct Work {
+    int rh, rt, s0, n;
+    __device__ int head(int) const { return rh; }
+    __device__ int tile(int j) const { return s0 + j; }
+    __device__ int slot() const { return -1; }
+};
+
+template <bool KV>
+__device__ __forceinline__ Work bwd_work(const Params &p, bool causal, int t)
+{
+    Work w;
+    bwd_decode<KV>(p, causal, t, w.rh, w.rt, w.s0, w.n);
+    return w;
+}
+
+// With sinks and shared key heads.  dQ pass: a query tile sees the sink tiles
+// [0, ssz), then its window's from ks on, of its head's key head.  dK/dV pass:
+// a key tile streams the query tiles that see it -- its window's, or for a
+// sink tile all from the first on -- of each of the group's query heads in
+// turn.  A sink tile sees so many that its steps are cut into up to nc parts
+// of their own (`slot`: where a part's fp32 sums go, -1: a whole tile), which
+// come first; sink_reduce_kernel adds them in order.
+template <bool KV>
+struct SinkWork {
+    int rh, rt, n;
+    int base, per, s0, group;   // KV: step j is entry base + j of `per` query tiles from s0 on for each of the group's heads
+    int ssz, ks;                // dQ pass
+    int part;
+    __device__ int head(int j) const { return KV ? rh * group + (base + j) / per : rh / group; }
+    __device__ int tile(int j) const { return KV ? s0 + (base + j) % per : (j < ssz ? j : j - ssz + ks); }
+    __device__ int slot() const { return KV ? part : -1; }
+};
+
+// Parts of sink tile kt (at most nc, each at least one step) and its steps.
+__device__ __forceinline__ int sink_parts(const SinkParams &p, int kt, int &s0, int &steps)
+{
+    int n;
+    bwd_band_range<true>(p, kt, s0, n);
+    steps = p.group * (p.nqt - s0);
+    return p.nc < steps ? p.nc : steps;
+}
+
+template <bool KV>
+__device__ __forceinline__ SinkWork<KV> bwd_work(const SinkParams &p, bool, int t)
+{
+    SinkWork<KV> w;
+    w.group = p.group;
+    w.part = -1;
+    w.base = w.ssz = w.ks = 0;
+    if (!KV) {   // later (longer, without a window) query tiles first, heads interleaved
+        const int g = t / p.BH;
+        w.rh = t - g * p.BH;
+        w.rt = p.nqt - 1 - g;
+        int s0, n;
+        bwd_band_range<false>(p, w.rt, s0, n);
+        w.ssz = p.ss < s0 + n ? p.ss : s0 + n;
+        w.ks = s0 < w.ssz ? w.ssz : s0;
+        w.n = w.ssz + (s0 + n - w.ks);
+        w.s0 = 0;
+        w.per = 1;
+        return w;
+    }
+    const int sink_items = p.BHkv * p.ss * p.nc;
+    if (t < sink_items) {
+        w.rh = t % p.BHkv;
+        const int i = t / p.BHkv, c = i % p.nc;
+        w.rt = i / p.nc;
+        int steps;
+        const int parts = sink_parts(p, w.rt, w.s0, steps);
+        w.per = p.nqt - w.s0;
+        w.n = 0;
+        if (c < parts) {
+            w.base = (int)((long long)steps * c / parts);
+            w.n = (int)((long long)steps * (c + 1) / parts) - w.base;
+        }
+        if (p.nc > 1)
+            w.part = (w.rh * p.ss + w.rt) * p.nc + c;
+        return w;
+    }
+    const int i = t - sink_items, g = i / p.BHkv;
+    w.rh = i - g * p.BHkv;
+    w.rt = p.ss + g;
+    bwd_band_range<true>(p, w.rt, w.s0, w.per);
+    w.n = w.per * p.group;
+    return w;
+}
+
 // The band mask of one step, in terms of d = key - query: with (kt, qt) the
 // step's key and query tiles, d = 128 (kt - qt) + x where x = lane - column
 // (KV) or column - lane (dQ pass), and key j is visible from query i iff
@@ -315,6 +421,33 @@ __device__ __forceinline__ StepMask bwd_step_mask(const Params &p, bool causal, 
         m.e_hi = (int)max(-1024ll, min(1024ll, (long long)p.off + p.wr - base));
     m.whole = m.e_lo <= -(kTile - 1) && m.e_hi >= kTile - 1;
     return m;
+}
+
+// With sinks: a tile of sinks alone has no lower bound; in a tile that holds
+// the last of them, key row `row` (KV) has none if it is one, and columns
+// below sink_columns (dQ pass) are seen as far as the upper bound goes.
+__device__ __forceinline__ StepMask bwd_step_mask(const SinkParams &p, bool, int kt, int qt)
+{
+    StepMask m = bwd_step_mask(static_cast<const Params &>(p), true, kt, qt);
+    if ((kt + 1) * kTile <= p.sinks) {
+        m.e_lo = -1024;
+        m.whole = m.e_hi >= kTile - 1;
+    }
+    return m;
+}
+
+__device__ __forceinline__ void sink_row(const Params &, StepMask &, int, int) {}
+__device__ __forceinline__ void sink_row(const SinkParams &p, StepMask &m, int kt, int row)
+{
+    if (kt * kTile + row < p.sinks)
+        m.e_lo = -1024;
+}
+
+__device__ __forceinline__ int sink_columns(const Params &, const StepMask &, int, int, int) { return 0; }
+__device__ __forceinline__ int sink_columns(const SinkParams &p, const StepMask &m, int kt, int row, int limit)
+{
+    const int n = p.sinks - kt * kTile;   // (at most Nkv)
+    return min(min(n, limit), row + m.e_hi + 1);
 }
 
 // Work tiles of CTA c on a grid of G: serpentine rounds (c-th tile of even
@@ -413,9 +546,9 @@ __device__ __forceinline__ bool warp_wait_all(uint32_t b0, uint32_t p0, bool u0,
 
 // ------------------------------------------------------------------ producer
 
-template <int D, bool KV, bool FQ>
+template <int D, bool KV, bool FQ, class P>
 __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const CUtensorMap *tmS0,
-                         const CUtensorMap *tmS1, const Params &p, bool causal, uint32_t sRes, uint32_t sStage,
+                         const CUtensorMap *tmS1, const P &p, bool causal, uint32_t sRes, uint32_t sStage,
                          BBars<D, KV, FQ> b, Ctl c)
 {
     using C = BCfg<D, KV, FQ>;
@@ -425,21 +558,23 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
         if (t >= p.T)
             break;
-        int bh, rt, s0, n;
-        bwd_decode<KV>(p, causal, t, bh, rt, s0, n);
+        const auto wk = bwd_work<KV>(p, causal, t);
+        const int n = wk.n;
+        if (kSinkPass<P> && n == 0)
+            continue;
         if (tiles > 0 && !warp_wait(b.res_empty(), (uint32_t)(tiles - 1) & 1u, c, kSiteBwdResEmpty))
             break;
         if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(b.res_full(), 2 * C::kTileBytes);
             for (int x = 0; x < C::kBoxes; ++x) {
-                ptx::tma_load_3d(sRes + x * C::kBoxBytes, tmR0, b.res_full(), x * 64, rt * kTile, bh);
-                ptx::tma_load_3d(sRes + C::kTileBytes + x * C::kBoxBytes, tmR1, b.res_full(), x * 64, rt * kTile, bh);
+                ptx::tma_load_3d(sRes + x * C::kBoxBytes, tmR0, b.res_full(), x * 64, wk.rt * kTile, wk.rh);
+                ptx::tma_load_3d(sRes + C::kTileBytes + x * C::kBoxBytes, tmR1, b.res_full(), x * 64, wk.rt * kTile, wk.rh);
             }
         }
         __syncwarp();
         ++tiles;
         for (int j = 0; j < n; ++j, ++step) {
-            const int row = (s0 + j) * kTile;
+            const int row = wk.tile(j) * kTile, bh = wk.head(j);
             if (C::kSplitRing) {   // K into ring 0, V into ring 1, each on its own barriers
                 const int k0 = step % C::kRing0, k1 = step % C::kRing1;
                 if (!warp_wait(b.empty(k0), ((uint32_t)(step / C::kRing0) & 1u) ^ 1u, c, kSiteBwdSlotEmpty) ||
@@ -506,8 +641,8 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
 // overwrite follows the read it displaces.  S and dP complete separate
 // barriers (sd_full, dp_full), so the compute warps start on S_{g+1} while
 // dK_g and dP_{g+1} still run.
-template <int D, bool BF16, bool KV>
-__device__ void bwd_mma(const Params &p, bool causal, uint32_t sRes, uint32_t sStage, uint32_t tmem,
+template <int D, bool BF16, bool KV, class P>
+__device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage, uint32_t tmem,
                         BBars<D, KV> b, Ctl c)
 {
     static_assert(KV, "the serialized pass is the dK/dV pass");
@@ -546,8 +681,10 @@ __device__ void bwd_mma(const Params &p, bool causal, uint32_t sRes, uint32_t sS
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
         if (t >= p.T)
             break;
-        int bh, rt, s0, n;
-        bwd_decode<KV>(p, causal, t, bh, rt, s0, n);
+        const auto wk = bwd_work<KV>(p, causal, t);
+        const int n = wk.n;
+        if (kSinkPass<P> && n == 0)
+            continue;
         if (!warp_wait(b.res_full(), (uint32_t)tiles & 1u, c, kSiteBwdResFull))
             break;
         ptx::tc_fence_after_sync();
@@ -631,13 +768,33 @@ __device__ __forceinline__ void store_row32(void *dst, const uint32_t (&v)[32], 
         ptx::st_global_v4(d4 + q, pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
 }
 
+// A sink part's fp32 sums: row `row` of dK (h = 1) or dV (h = 0) in `slot`.
+template <int D>
+__device__ __forceinline__ float *part_row(const Params &, int, int, int)
+{
+    return nullptr;
+}
+
+template <int D>
+__device__ __forceinline__ float *part_row(const SinkParams &p, int slot, int h, int row)
+{
+    return p.part + (((size_t)slot * 2 + h) * kTile + row) * D;
+}
+
+__device__ __forceinline__ void store_part32(float *dst, const uint32_t (&v)[32])
+{
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        ptx::st_global_v4(dst + 4 * q, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+}
+
 // The serialized pass's compute warps: per step, S (sd_full): P^T = exp2(S^T
 // s log2 e - lg) over this warpgroup's 64 columns of S; then dP (dp_full):
 // dS^T = P^T (dP^T - delta) over its 64 columns of dP.  Each is written as
 // 32 columns of 16-bit pairs at the start of the columns it came from, once
 // this thread has loaded them.
-template <int D, bool BF16, bool CAUSAL, bool KV>
-__device__ void bwd_compute(const Params &p, uint32_t tmem, uint32_t sStage, BBars<D, KV> b, Ctl c)
+template <int D, bool BF16, bool CAUSAL, bool KV, class P>
+__device__ void bwd_compute(const P &p, uint32_t tmem, uint32_t sStage, BBars<D, KV> b, Ctl c)
 {
     static_assert(KV, "the serialized pass is the dK/dV pass");
     using C = BCfg<D, KV>;
@@ -652,11 +809,13 @@ __device__ void bwd_compute(const Params &p, uint32_t tmem, uint32_t sStage, BBa
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
         if (t >= p.T)
             break;
-        int bh, rt, s0, n;
-        bwd_decode<KV>(p, CAUSAL, t, bh, rt, s0, n);
+        const auto wk = bwd_work<KV>(p, CAUSAL, t);
+        const int bh = wk.rh, rt = wk.rt, n = wk.n;
+        if (kSinkPass<P> && n == 0)
+            continue;
         for (int j = 0; j < n; ++j, ++step) {
             const int st = step % C::kStages;
-            const int si = s0 + j;   // streamed (query) tile index
+            const int si = wk.tile(j);   // streamed (query) tile index
             if (!warp_wait(b.sd_full(), (uint32_t)step & 1u, c, kSiteBwdSdFull))
                 return;
             ptx::tc_fence_after_sync();
@@ -664,8 +823,9 @@ __device__ void bwd_compute(const Params &p, uint32_t tmem, uint32_t sStage, BBa
             // Masks: the band's edges (the causal diagonal); padding queries
             // and queries without keys have lg = +inf (stored as -lg = -inf),
             // so their P is already 0.
-            const StepMask sm = bwd_step_mask(p, CAUSAL, rt, si);
+            StepMask sm = bwd_step_mask(p, CAUSAL, rt, si);
             const bool masked = !sm.whole;   // warp-uniform
+            sink_row(p, sm, rt, lane_row);
             uint32_t pv[64];   // S, then P (fp32)
             ptx::tmem_ld64(tS, pv);
             ptx::tmem_wait_ld();
@@ -748,7 +908,9 @@ __device__ void bwd_compute(const Params &p, uint32_t tmem, uint32_t sStage, BBa
                 uint32_t v[32];
                 ptx::tmem_ld32(tA + 32 * cc, v);
                 ptx::tmem_wait_ld();
-                if (grow < p.Nkv)
+                if (kSinkPass<P> && wk.slot() >= 0)
+                    store_part32(part_row<D>(p, wk.slot(), h, lane_row) + 32 * cc, v);
+                else if (grow < p.Nkv)
                     store_row32<BF16>(dst + cc * 64, v, mul);
             }
         } else {
@@ -795,8 +957,8 @@ constexpr bool kPipeline = (D == 64) || (!KV && D == 128);
 // The fused pass (FQ) takes dS^T from shared memory for dK += dS^T Q (warp
 // 10 reads the same tile as dS for the dQ products, bwd_mma_dq), and its
 // pd_free, res_empty and drain barriers also count warp 10's commits.
-template <int D, bool BF16, bool KV, bool FQ>
-__device__ void bwd_mma_pipe(const Params &p, bool causal, uint32_t sRes, uint32_t sStage, uint32_t sDs, uint32_t tmem,
+template <int D, bool BF16, bool KV, bool FQ, class P>
+__device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sStage, uint32_t sDs, uint32_t tmem,
                              BBars<D, KV, FQ> b, Ctl c)
 {
     using C = BCfg<D, KV, FQ>;
@@ -847,8 +1009,10 @@ __device__ void bwd_mma_pipe(const Params &p, bool causal, uint32_t sRes, uint32
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
         if (t >= p.T)
             break;
-        int bh, rt, s0, n;
-        bwd_decode<KV>(p, causal, t, bh, rt, s0, n);
+        const auto wk = bwd_work<KV>(p, causal, t);
+        const int n = wk.n;
+        if (kSinkPass<P> && n == 0)
+            continue;
         if (!warp_wait(b.res_full(), (uint32_t)tiles & 1u, c, kSiteBwdResFull))
             break;
         ptx::tc_fence_after_sync();
@@ -916,8 +1080,8 @@ __device__ void bwd_mma_pipe(const Params &p, bool causal, uint32_t sRes, uint32
 }
 
 // FQ: dS^T goes to the shared-memory tile at sDs instead of TMEM.
-template <int D, bool BF16, bool CAUSAL, bool KV, bool FQ>
-__device__ void bwd_compute_pipe(const Params &p, uint32_t tmem, uint32_t sStage, uint32_t sDs, BBars<D, KV, FQ> b,
+template <int D, bool BF16, bool CAUSAL, bool KV, bool FQ, class P>
+__device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uint32_t sDs, BBars<D, KV, FQ> b,
                                  Ctl c)
 {
     using C = BCfg<D, KV, FQ>;
@@ -932,8 +1096,10 @@ __device__ void bwd_compute_pipe(const Params &p, uint32_t tmem, uint32_t sStage
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
         if (t >= p.T)
             break;
-        int bh, rt, s0, n;
-        bwd_decode<KV>(p, CAUSAL, t, bh, rt, s0, n);
+        const auto wk = bwd_work<KV>(p, CAUSAL, t);
+        const int bh = wk.rh, rt = wk.rt, n = wk.n;
+        if (kSinkPass<P> && n == 0)
+            continue;
         uint64_t nlg = 0, ndl = 0;   // dQ pass: this thread's query row's -lg and -delta
         if (!KV) {
             const size_t off = (size_t)bh * p.Npad + (size_t)rt * kTile + row;
@@ -941,7 +1107,7 @@ __device__ void bwd_compute_pipe(const Params &p, uint32_t tmem, uint32_t sStage
             ndl = ptx::f2_pack(p.dl[off], p.dl[off]);
         }
         for (int j = 0; j < n; ++j, ++g) {
-            const int si = s0 + j;   // streamed tile
+            const int si = wk.tile(j);   // streamed tile
             if (!warp_wait(b.sd_full(), (uint32_t)g & 1u, c, kSiteBwdSdFull))
                 return;
             ptx::tc_fence_after_sync();
@@ -957,8 +1123,10 @@ __device__ void bwd_compute_pipe(const Params &p, uint32_t tmem, uint32_t sStage
             // (padding queries and queries without keys have lg = +inf, stored as -inf).
             const uint32_t vec = sStage + (g % C::kStages) * C::kStageBytes + 2 * C::kTileBytes;
             const int limit = KV ? kTile : p.Nkv - si * kTile;   // dQ pass: columns >= limit past Nkv
-            const StepMask sm = bwd_step_mask(p, CAUSAL, KV ? rt : si, KV ? si : rt);
+            StepMask sm = bwd_step_mask(p, CAUSAL, KV ? rt : si, KV ? si : rt);
             const bool masked = !sm.whole || limit < 64 * h + 64;
+            if (KV)
+                sink_row(p, sm, rt, row);
             const LaneMask lm = bwd_lane_mask<KV>(sm, row, limit);
             // Scaled scores x = S * s log2(e) - lg in place; masked steps then set
             // hidden scores to -inf (exp2 gives 0) in a separate pass, so the
@@ -983,9 +1151,10 @@ __device__ void bwd_compute_pipe(const Params &p, uint32_t tmem, uint32_t sStage
             }
             if (masked) {
                 const uint32_t ninf = __float_as_uint(-INFINITY);
+                const int sink = KV ? 0 : sink_columns(p, sm, si, row, limit);
 #pragma unroll
                 for (int i = 0; i < 64; ++i)
-                    sv[i] = ((uint32_t)(lm.a + 64 * h + i) < lm.width) ? sv[i] : ninf;
+                    sv[i] = ((uint32_t)(lm.a + 64 * h + i) < lm.width || (kSinkPass<P> && !KV && 64 * h + i < sink)) ? sv[i] : ninf;
             }
 #pragma unroll
             for (int i = 0; i < 64; i += 4) {
@@ -1053,7 +1222,9 @@ __device__ void bwd_compute_pipe(const Params &p, uint32_t tmem, uint32_t sStage
                 uint32_t v[32];
                 ptx::tmem_ld32(tA + 32 * cc, v);
                 ptx::tmem_wait_ld();
-                if (grow < p.Nkv)
+                if (kSinkPass<P> && wk.slot() >= 0)
+                    store_part32(part_row<D>(p, wk.slot(), h, row) + 32 * cc, v);
+                else if (grow < p.Nkv)
                     store_row32<BF16>(dst + cc * 64, v, mul);
             }
         } else {
@@ -1084,8 +1255,8 @@ __device__ void bwd_compute_pipe(const Params &p, uint32_t tmem, uint32_t sStage
 // as in dV += P^T dO.  Its commits: dq_full (the product is final), pd_free
 // (the dS^T tile was read; that barrier also counts warp 9's commit of dV and
 // dK), res_empty after a tile's last step (K was read), and drain.
-template <int D, bool BF16, bool CAUSAL>
-__device__ void bwd_mma_dq(const Params &p, uint32_t sRes, uint32_t sDs, uint32_t tmem, BBars<D, true, true> b, Ctl c)
+template <int D, bool BF16, bool CAUSAL, class P>
+__device__ void bwd_mma_dq(const P &p, uint32_t sRes, uint32_t sDs, uint32_t tmem, BBars<D, true, true> b, Ctl c)
 {
     using C = BCfg<D, true, true>;
     // instr_desc_f16 with bit 15 (A MN-major) set as well: A and B MN-major
@@ -1098,8 +1269,10 @@ __device__ void bwd_mma_dq(const Params &p, uint32_t sRes, uint32_t sDs, uint32_
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
         if (t >= p.T)
             break;
-        int bh, rt, s0, n;
-        bwd_decode<true>(p, CAUSAL, t, bh, rt, s0, n);
+        const auto wk = bwd_work<true>(p, CAUSAL, t);
+        const int n = wk.n;
+        if (kSinkPass<P> && n == 0)
+            continue;
         if (!warp_wait(b.res_full(), (uint32_t)tiles & 1u, c, kSiteBwdResFull))
             break;
         for (int j = 0; j < n; ++j, ++g) {
@@ -1153,8 +1326,8 @@ __device__ __forceinline__ bool dq_all(bool ok)
 // product (dq_free), then one thread adds the tile into the accumulator rows
 // of the step's query tile with two tensor reductions (fp32 add in L2).  The
 // staging is rewritten only after the previous reductions have read it.
-template <int D, bool CAUSAL>
-__device__ void bwd_dq_out(const CUtensorMap *tmDQ, const Params &p, uint32_t tmem, uint32_t sDq,
+template <int D, bool CAUSAL, class P>
+__device__ void bwd_dq_out(const CUtensorMap *tmDQ, const P &p, uint32_t tmem, uint32_t sDq,
                            BBars<D, true, true> b, Ctl c)
 {
     using C = BCfg<D, true, true>;
@@ -1170,8 +1343,10 @@ __device__ void bwd_dq_out(const CUtensorMap *tmDQ, const Params &p, uint32_t tm
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
         if (t >= p.T)
             break;
-        int bh, rt, s0, n;
-        bwd_decode<true>(p, CAUSAL, t, bh, rt, s0, n);
+        const auto wk = bwd_work<true>(p, CAUSAL, t);
+        const int n = wk.n;
+        if (kSinkPass<P> && n == 0)
+            continue;
         for (int j = 0; j < n; ++j, ++g) {
             if (!dq_all(wait_bounded(b.dq_full(), (uint32_t)g & 1u, c, kSiteBwdDqFull))) {
                 ok = false;
@@ -1204,7 +1379,7 @@ __device__ void bwd_dq_out(const CUtensorMap *tmDQ, const Params &p, uint32_t tm
             ptx::fence_proxy_async_smem();   // the staging, visible to the reductions
             dq_sync();
             if (leader) {
-                const int y = bh * p.Npad + (s0 + j) * kTile;
+                const int y = wk.head(j) * p.Npad + wk.tile(j) * kTile;
                 fq::tma_reduce_add_2d(tmDQ, sDq, 0, y);
                 fq::tma_reduce_add_2d(tmDQ, sDq + C::kDqBoxBytes, 32, y);
                 fq::bulk_commit_group();
@@ -1221,11 +1396,11 @@ __device__ void bwd_dq_out(const CUtensorMap *tmDQ, const Params &p, uint32_t tm
 // KV = true:  tmR0 = K, tmR1 = V (resident), tmS0 = Q, tmS1 = dO (streamed)
 // KV = false: tmR0 = Q, tmR1 = dO (resident), tmS0 = K, tmS1 = V (streamed)
 // FQ (fused, KV at D = 64): tmDQ = the fp32 dQ accumulator [B*H*Npad, D] (32 x 128 boxes); otherwise unused.
-template <int D, bool BF16, bool CAUSAL, bool KV, bool FQ = false>
+template <int D, bool BF16, bool CAUSAL, bool KV, bool FQ = false, class P = Params>
 __global__ void __launch_bounds__(FQ ? kThreadsFused : kThreads, 1)
     fa_bwd_sm103(const __grid_constant__ CUtensorMap tmR0, const __grid_constant__ CUtensorMap tmR1,
                  const __grid_constant__ CUtensorMap tmS0, const __grid_constant__ CUtensorMap tmS1,
-                 const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ Params p)
+                 const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ P p)
 {
     using C = BCfg<D, KV, FQ>;
     extern __shared__ uint8_t smem_raw[];
@@ -1386,6 +1561,51 @@ __global__ void __launch_bounds__(256)
         lg[row] = l;
         dl[row] = (i < N) ? -acc : 0.f;
     }
+}
+
+// Sink tiles cut into parts: dK = scale * sum of the parts' dK, dV the sum of
+// their dV, in the input type, the parts added in order (8 values a thread).
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) sink_reduce_kernel(const __grid_constant__ SinkParams p)
+{
+    fq::grid_wait();   // launched right behind the pass: its parts are complete
+    const long long e = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 8;
+    const long long total = (long long)p.BHkv * p.ss * 2 * kTile * D;
+    if (e >= total)
+        return;
+    const int col = (int)(e % D);
+    long long i = e / D;
+    const int row = (int)(i % kTile);
+    i /= kTile;
+    const int h = (int)(i % 2);   // 0: dV, 1: dK
+    i /= 2;                       // key head and sink tile
+    const int kt = (int)(i % p.ss);
+    const long long bh = i / p.ss;
+    const int grow = kt * kTile + row;
+    if (grow >= p.Nkv)
+        return;
+    int s0, steps;
+    const int parts = sink_parts(p, kt, s0, steps);
+    float a[8] = {};
+    for (int c = 0; c < parts; ++c) {
+        const float4 *src = reinterpret_cast<const float4 *>(part_row<D>(p, (int)(i * p.nc) + c, h, row) + col);
+        const float4 x = src[0], y = src[1];
+        a[0] += x.x;
+        a[1] += x.y;
+        a[2] += x.z;
+        a[3] += x.w;
+        a[4] += y.x;
+        a[5] += y.y;
+        a[6] += y.z;
+        a[7] += y.w;
+    }
+    const float mul = h ? p.scale : 1.f;
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = BF16 ? ptx::pack_bf16x2(a[2 * k] * mul, a[2 * k + 1] * mul) : ptx::pack_f16x2(a[2 * k] * mul, a[2 * k + 1] * mul);
+    uint16_t *dst = static_cast<uint16_t *>(h ? p.dA : p.dB) + ((size_t)bh * p.Nkv + grow) * D + col;
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The fused pass's dQ: dQ = scale * the fp32 accumulator, in the input type,

@@ -22,11 +22,23 @@ struct BwdLaunch {
     bool bf16, causal;               // causal: masked by the band below
     int wl, wr;                      // band: query i sees keys [i + Nkv - N - wl, i + Nkv - N + wr] (kSchedUnbounded: none)
     float scale;
+    int BHkv, group, sinks;          // sink calls: key heads (K, V, dK, dV are [BHkv, Nkv, D]), query heads per key head
+    int nc;                          // sink calls: parts of a sink tile in the dK/dV pass (sink_parts_for)
+    float *part;                     // sink calls, nc > 1: workspace, the parts' fp32 dK and dV
 };
+
+// Parts that each sink tile's query tiles are cut into in the dK/dV pass, for
+// BH query and BHkv key heads: 1 where a CTA's share of the pass is at least
+// twice a sink tile's steps anyway.
+int sink_parts_for(int BH, int BHkv, int N, int Nkv, int wl, int sinks, int sms);
 
 // Enqueue the pre-pass, then the dQ pass and the dK/dV pass, or (fused) the
 // one pass and the conversion of the dQ accumulator, on `s`.
 fa_status launch_bwd(const BwdLaunch &a, cudaStream_t s, int dev);
 bool take_status_word_bwd(cudaStream_t s, unsigned int *word);
+
+// The same for a causal window with sinks and shared key heads (fa_bwd_sink.cu).
+fa_status launch_bwd_sink(const BwdLaunch &a, cudaStream_t s, int dev);
+bool take_status_word_bwd_sink(cudaStream_t s, unsigned int *word);
 
 }  // namespace fa_launch

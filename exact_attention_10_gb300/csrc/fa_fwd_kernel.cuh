@@ -128,6 +128,11 @@ constexpr int kThreads = 512;
 constexpr int kMaskNone = 0;
 constexpr int kMaskCausal = 1;
 constexpr int kMaskBand = 2;
+// A causal window with sinks: the steps of the first keys, which every query
+// behind them sees, then the band's; query heads may share key heads.
+constexpr int kMaskSink = 3;
+template <int MASK>
+constexpr bool kBanded = MASK == kMaskBand || MASK == kMaskSink;   // a left bound
 constexpr int kEpilogueWarpgroup = 2;
 constexpr int kLoadWarp = 12;
 constexpr int kMmaWarp = 13;          // MMA issuer(s): warp 13 (and 14 at D = 64)
@@ -236,30 +241,59 @@ struct Cfg {
     __host__ __device__ static constexpr uint32_t col_p_one_tile() { return col_s(1); }
 };
 
-struct FwdParams {
+template <class S>
+struct FwdParamsT {
     void *O;
     float *LSE;
     int N;               // query rows per head
     int Nkv;             // keys per head
     int off;             // causal: query i sees keys j <= i + off (Nkv - N, bottom-right alignment)
     float qk_scale;      // scale * log2(e)
-    Schedule sch;        // work decomposition (fa_schedule.h)
+    S sch;               // work decomposition (fa_schedule.h)
     float *part_o;       // balanced schedule: partial O, [2 * grid slots][256 rows][D] fp32
     float2 *part_ml;     // balanced schedule: partial (m, l) per row, [2 * grid slots][256]
     int *counters;       // balanced schedule: finished parts per (tile, Q tile), zero between launches
 };
+using FwdParams = FwdParamsT<Schedule>;
+using SinkParams = FwdParamsT<SinkSchedule>;
+template <int MASK>
+using ParamsOf = std::conditional_t<MASK == kMaskSink, SinkParams, FwdParams>;
+
+// First key of step j of CTA tile ct, and the key head of query head bh.
+template <int MASK, class S>
+__device__ __forceinline__ auto step_keys(const S &s, int ct)
+{
+    if constexpr (MASK == kMaskSink) {
+        return sched_tile_keys(s, ct);
+    } else {
+        struct Run {
+            int ks;
+            __device__ int first_key(int j) const { return (ks + j) * kBN; }
+        };
+        return Run{(MASK == kMaskBand) ? sched_kv_start(s, ct) : 0};
+    }
+}
+
+template <int MASK, class S>
+__device__ __forceinline__ int key_head(const S &s, int bh)
+{
+    if constexpr (MASK == kMaskSink)
+        return bh / s.group;
+    else
+        return bh;
+}
 
 // Separate-P order (S_{j+1} issued while the softmax of step j runs): always
 // at D = 64; at D = 128 when no CTA tile has a second Q tile.
-template <int D>
-__device__ __forceinline__ bool separate_p(const FwdParams &p)
+template <int D, class P>
+__device__ __forceinline__ bool separate_p(const P &p)
 {
     return Cfg<D>::kSeparateP || p.N <= kBM;
 }
 
 // K and V of a stage on separate barriers (D = 128, separate-P order).
-template <int D>
-__device__ __forceinline__ bool split_kv(const FwdParams &p)
+template <int D, class P>
+__device__ __forceinline__ bool split_kv(const P &p)
 {
     return Cfg<D>::kSplitKV && p.N <= kBM;
 }
@@ -381,9 +415,9 @@ struct Bars {
 // carry an L2 evict-first hint (the partial results, the merge's code and
 // the next launch's data stay; measured 116.8 -> 108.5 us on 4 queries x
 // 32768 keys x 32 heads with L2 flushed).
-template <int D, int MASK, bool SPLIT, bool SKV>
+template <int D, int MASK, bool SPLIT, bool SKV, class P>
 __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const CUtensorMap *tmV,
-                          const FwdParams &p, uint32_t sQ, uint32_t sStage, Bars<D> b, Ctl c)
+                          const P &p, uint32_t sQ, uint32_t sStage, Bars<D> b, Ctl c)
 {
     using C = Cfg<D>;
     int step = 0;   // K/V stages filled so far (K halves when split)
@@ -410,9 +444,9 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (ok && parts.next_t<SPLIT, MASK == kMaskBand>(p.sch, pt)) {
+    while (ok && parts.next_t<SPLIT, kBanded<MASK>>(p.sch, pt)) {
         int bh, ct;
-        sched_decode_t<SPLIT, MASK == kMaskBand>(p.sch, pt.tile, bh, ct);
+        sched_decode_t<SPLIT, kBanded<MASK>>(p.sch, pt.tile, bh, ct);
         // The previous part's last V before the Q buffer is waited for: the
         // MMA warp frees that buffer only after the part's last P.V.
         if (SKV && nv < step && !load_v()) { ok = false; break; }
@@ -429,7 +463,8 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
         }
         __syncwarp();
         ++it;
-        const int ks = (MASK == kMaskBand) ? sched_kv_start(p.sch, ct) : 0;   // the tile's first key step
+        const auto keys = step_keys<MASK>(p.sch, ct);   // the tile's key steps
+        const int kvh = key_head<MASK>(p.sch, bh);
         for (int j = pt.kb; j < pt.ke; ++j, ++step) {
             const int st = step % C::kStages;
             const uint32_t use = (uint32_t)(step / C::kStages);
@@ -439,20 +474,20 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
                 ptx::mbar_arrive_expect_tx(b.full(st), SKV ? C::kTileBytes : C::kStageBytes);
                 for (int x = 0; x < C::kBoxes; ++x) {
                     if (SKV)
-                        ptx::tma_load_3d_hint(dst + x * C::kBoxBytes, tmK, b.full(st), x * 64, (ks + j) * kBN, bh, kv_policy);
+                        ptx::tma_load_3d_hint(dst + x * C::kBoxBytes, tmK, b.full(st), x * 64, keys.first_key(j), kvh, kv_policy);
                     else
-                        ptx::tma_load_3d(dst + x * C::kBoxBytes, tmK, b.full(st), x * 64, (ks + j) * kBN, bh);
+                        ptx::tma_load_3d(dst + x * C::kBoxBytes, tmK, b.full(st), x * 64, keys.first_key(j), kvh);
                 }
                 if (!SKV)
                     for (int x = 0; x < C::kBoxes; ++x)
                         ptx::tma_load_3d(dst + C::kTileBytes + x * C::kBoxBytes, tmV, b.full(st), x * 64,
-                                         (ks + j) * kBN, bh);
+                                         keys.first_key(j), kvh);
             }
             __syncwarp();
             if (SKV) {   // V of the previous step, then this step's V becomes the pending one
                 if (nv < step && !load_v()) { ++step; ok = false; break; }
-                pv_bh = bh;
-                pv_row = (ks + j) * kBN;
+                pv_bh = kvh;
+                pv_row = keys.first_key(j);
             }
         }
     }
@@ -680,8 +715,8 @@ __device__ bool tile_interleaved(MmaIssuer<D, BF16, false> &m0, MmaIssuer<D, BF1
 
 // SEP: separate-P order (always at D = 64; at D = 128 for heads of one Q
 // tile, P_0 in tile 1's S columns), else the two-tile interleaved order.
-template <int D, bool BF16, int MASK, bool SPLIT, bool SEP>
-__device__ void mma_role(int w, const FwdParams &p, uint32_t sQ, uint32_t sStage, uint32_t tmem, Bars<D> b, Ctl c)
+template <int D, bool BF16, int MASK, bool SPLIT, bool SEP, class P>
+__device__ void mma_role(int w, const P &p, uint32_t sQ, uint32_t sStage, uint32_t tmem, Bars<D> b, Ctl c)
 {
     using C = Cfg<D>;
     auto make = [&](int q) {
@@ -704,10 +739,10 @@ __device__ void mma_role(int w, const FwdParams &p, uint32_t sQ, uint32_t sStage
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (parts.next_t<SPLIT, MASK == kMaskBand>(p.sch, pt)) {
+    while (parts.next_t<SPLIT, kBanded<MASK>>(p.sch, pt)) {
         int bh, ct;
-        sched_decode_t<SPLIT, MASK == kMaskBand>(p.sch, pt.tile, bh, ct);
-        const int n0 = part_steps(pt, sched_kv_tiles_t<MASK == kMaskBand>(p.sch, ct, 0)), n1 = part_steps(pt, sched_kv_tiles_t<MASK == kMaskBand>(p.sch, ct, 1));
+        sched_decode_t<SPLIT, kBanded<MASK>>(p.sch, pt.tile, bh, ct);
+        const int n0 = part_steps(pt, sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, 0)), n1 = part_steps(pt, sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, 1));
         const int n = pt.ke - pt.kb;
         const int qb = it % C::kQBufs;
         if (!warp_wait(b.q_full(qb), (uint32_t)(it / C::kQBufs) & 1u, c, kSiteMmaQFull))
@@ -774,8 +809,8 @@ static __device__ __noinline__ void mask_s_tail(uint32_t tS, int hi)
 // SEP as in mma_role.  At D = 128 its waits record a timeout inline: they
 // hold S, P or O rescale registers, which a call made the balanced variant
 // spill (1.3 % slower); at D = 64 the inline form measured 1.4 % slower.
-template <int D, bool BF16, int MASK, bool SPLIT, bool SEP>
-__device__ void softmax_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl c, float2 *handoff)
+template <int D, bool BF16, int MASK, bool SPLIT, bool SEP, class P>
+__device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2 *handoff)
 {
     using C = Cfg<D>;
     constexpr bool CAUSAL = MASK != kMaskNone;
@@ -792,10 +827,10 @@ __device__ void softmax_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl c
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (parts.next_t<SPLIT, MASK == kMaskBand>(p.sch, pt)) {
+    while (parts.next_t<SPLIT, kBanded<MASK>>(p.sch, pt)) {
         int bh, ct;
-        sched_decode_t<SPLIT, MASK == kMaskBand>(p.sch, pt.tile, bh, ct);
-        const int nw = sched_kv_tiles_t<MASK == kMaskBand>(p.sch, ct, w);    // steps of this Q tile in the whole tile
+        sched_decode_t<SPLIT, kBanded<MASK>>(p.sch, pt.tile, bh, ct);
+        const int nw = sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, w);    // steps of this Q tile in the whole tile
         const int np = part_steps(pt, nw);              // ... of which this part holds steps kb .. kb + np - 1
         if (np == 0)
             continue;
@@ -804,13 +839,13 @@ __device__ void softmax_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl c
         // step needs masking where some row's band edge or the key count ends
         // inside it: past the Q tile's first row's upper edge, before its last
         // row's lower edge (kMaskBand only), or past Nkv.
-        const int ks = (MASK == kMaskBand) ? sched_kv_start(p.sch, ct) : 0;   // the tile's first key step
+        const auto keys = step_keys<MASK>(p.sch, ct);   // the tile's key steps
         int row_lo = 0, row_hi = p.Nkv, edge_lo = 0, edge_hi = p.Nkv;
         if (CAUSAL) {
             const int first = ct * kCtaRows + w * kBM, r = min(row, p.N - 1);
             row_hi = sched_row_hi(p.sch, r);
             edge_hi = sched_row_hi(p.sch, first);
-            if (MASK == kMaskBand) {
+            if (kBanded<MASK>) {
                 row_lo = sched_row_lo(p.sch, r);
                 edge_lo = sched_row_lo(p.sch, min(first + kBM - 1, p.N - 1));
             }
@@ -831,7 +866,7 @@ __device__ void softmax_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl c
                 return false;
             ++s_phase;
             ptx::tc_fence_after_sync();
-            constexpr bool TMEM_MASK = (D == 64 && MASK != kMaskBand);
+            constexpr bool TMEM_MASK = (D == 64 && !kBanded<MASK>);
             if (TMEM_MASK && masked)
                 mask_s_tail(tS, row_hi - kb0);   // keys kb0 + i with i < row_hi - kb0 are visible
 
@@ -850,7 +885,14 @@ __device__ void softmax_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl c
                 s[i] = __uint_as_float(r[i / 64][i % 64]);
 
             if (!TMEM_MASK && masked) {
-                if (MASK == kMaskBand) {
+                if constexpr (MASK == kMaskSink) {
+                    // in the band, or a sink before the row's upper edge
+                    const int lo = row_lo - kb0, sink = min(p.sch.sinks, row_hi) - kb0;
+                    const uint32_t width = (uint32_t)(row_hi - row_lo);
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        s[i] = ((uint32_t)(i - lo) < width || i < sink) ? s[i] : -INFINITY;
+                } else if (MASK == kMaskBand) {
                     // key kb0 + i is visible iff row_lo <= kb0 + i < row_hi (one unsigned compare)
                     const int lo = row_lo - kb0;
                     const uint32_t width = (uint32_t)(row_hi - row_lo);
@@ -959,10 +1001,14 @@ __device__ void softmax_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl c
         };
 
         for (int jr = 0; jr < np; ++jr) {
-            const int kb0 = (ks + pt.kb + jr) * kBN;   // this step's first key
+            const int kb0 = keys.first_key(pt.kb + jr);   // this step's first key
             // masked where some row's band edge or the key count ends inside the step
-            const bool masked = (MASK == kMaskBand) ? (kb0 < edge_lo || kb0 + kBN > edge_hi)   // (edge_hi <= Nkv)
-                                                    : ((CAUSAL && kb0 + kBN > edge_hi) || kb0 + kBN > p.Nkv);
+            bool masked;
+            if constexpr (MASK == kMaskSink)   // (steps of sinks alone have no lower edge)
+                masked = (kb0 < edge_lo && kb0 + kBN > p.sch.sinks) || kb0 + kBN > edge_hi;
+            else
+                masked = (MASK == kMaskBand) ? (kb0 < edge_lo || kb0 + kBN > edge_hi)   // (edge_hi <= Nkv)
+                                             : ((CAUSAL && kb0 + kBN > edge_hi) || kb0 + kBN > p.Nkv);
             if (!step(jr, kb0, masked))
                 return;
         }
@@ -1046,8 +1092,8 @@ __device__ __forceinline__ float2 ld_cg_f2(const float2 *p)
 // part, in the order row block, part), each lane adding weight x O for 4
 // columns of 8 rows of a chunk, and writes O.  Every wait is bounded; on a
 // failed wait the copies in flight are let land and the warp stops.
-template <int D, bool BF16>
-__device__ void merge_role(const FwdParams &p, uint32_t sbuf, uint32_t sml, const MergeJob *jobs, Bars<D> b, Ctl c)
+template <int D, bool BF16, class P>
+__device__ void merge_role(const P &p, uint32_t sbuf, uint32_t sml, const MergeJob *jobs, Bars<D> b, Ctl c)
 {
     using C = Cfg<D>;
     constexpr int R = C::kMergeRows;              // 16 or 8 rows per chunk
@@ -1196,8 +1242,8 @@ __device__ void merge_role(const FwdParams &p, uint32_t sbuf, uint32_t sml, cons
 // writes O = acc / l in the input type and LSE = (m + log2 l) ln 2; a part of
 // a split tile writes its partial result to its workspace slot, and the part
 // that finishes last hands the merge of that Q tile to the merge warp.
-template <int D, bool BF16, int MASK, bool SPLIT>
-__device__ void epilogue_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl c, uint32_t s_handoff, uint32_t s_flag,
+template <int D, bool BF16, int MASK, bool SPLIT, class P>
+__device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint32_t s_handoff, uint32_t s_flag,
                               uint32_t s_jobs)
 {
     using C = Cfg<D>;
@@ -1242,13 +1288,13 @@ __device__ void epilogue_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl 
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (parts.next_t<SPLIT, MASK == kMaskBand>(p.sch, pt)) {
+    while (parts.next_t<SPLIT, kBanded<MASK>>(p.sch, pt)) {
         int bh, ct;
-        sched_decode_t<SPLIT, MASK == kMaskBand>(p.sch, pt.tile, bh, ct);
+        sched_decode_t<SPLIT, kBanded<MASK>>(p.sch, pt.tile, bh, ct);
         uint32_t published = 0;                   // bit w: Q tile w wrote a partial result
 #pragma unroll
         for (int w = 0; w < kQTiles; ++w) {
-            const int nw = sched_kv_tiles_t<MASK == kMaskBand>(p.sch, ct, w);
+            const int nw = sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, w);
             const int np = part_steps(pt, nw);
             if (np == 0)
                 continue;
@@ -1336,7 +1382,7 @@ __device__ void epilogue_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl 
             for (int w = 0; w < kQTiles; ++w) {
                 if (!(published >> w & 1u))
                     continue;
-                const int nw = sched_kv_tiles_t<MASK == kMaskBand>(p.sch, ct, w);
+                const int nw = sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, w);
                 int expected = 0, slot;
                 for (int cc = clo; cc <= chi; ++cc)
                     expected += sched_part_slot(p.sch, pt.ts, n, nw, cc, slot) ? 1 : 0;
@@ -1355,7 +1401,7 @@ __device__ void epilogue_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl 
         for (int w = 0; w < kQTiles; ++w) {
             if (!(last >> w & 1))
                 continue;
-            const int nw = sched_kv_tiles_t<MASK == kMaskBand>(p.sch, ct, w);
+            const int nw = sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, w);
             int nparts = 0, slot;
             for (int cc = clo; cc <= chi; ++cc)
                 nparts += sched_part_slot(p.sch, pt.ts, n, nw, cc, slot) ? 1 : 0;
@@ -1374,7 +1420,7 @@ __device__ void epilogue_role(const FwdParams &p, uint32_t tmem, Bars<D> b, Ctl 
 template <int D, bool BF16, int MASK, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd_sm103(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdParams p)
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ParamsOf<MASK> p)
 {
     using C = Cfg<D>;
     constexpr bool CAUSAL = MASK != kMaskNone;

@@ -1,9 +1,10 @@
-// fa_launch.cuh -- kernel selection and launch, shared by the three
+// fa_launch.cuh -- kernel selection and launch, shared by the four
 // translation units that instantiate the kernels: fa_api.cu (whole-tile
 // variants without a mask or with the causal one, and the C ABI), fa_split.cu
-// (the same for the balanced schedule) and fa_band.cu (left-bounded band
-// masks, both schedules).  Three units keep each nvcc run to eight kernels and
-// let the build compile them in parallel.
+// (the same for the balanced schedule), fa_band.cu (left-bounded band masks,
+// both schedules) and fa_sink.cu (windows with sinks, both schedules).  Four
+// units keep each nvcc run to eight kernels and let the build compile them in
+// parallel.
 #pragma once
 
 #include <cuda.h>
@@ -27,7 +28,7 @@ namespace {
 // Launch one variant on `grid` CTAs.  The dynamic shared-memory limit is
 // raised once per device and variant.
 template <int D, bool BF16, int MASK, bool SPLIT>
-fa_status launch_variant(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const fa::FwdParams &p,
+fa_status launch_variant(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const fa::ParamsOf<MASK> &p,
                          int grid, cudaStream_t stream, int dev)
 {
     static std::mutex mu;
@@ -52,10 +53,10 @@ fa_status launch_variant(const CUtensorMap &q, const CUtensorMap &k, const CUten
     return FA_OK;
 }
 
-// The variants of one mask (kMaskNone, kMaskCausal or kMaskBand) and schedule.
+// The variants of one mask (kMaskNone, kMaskCausal, kMaskBand or kMaskSink) and schedule.
 template <int MASK, bool SPLIT>
 fa_status launch_mask(int D, bool bf16, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                      const fa::FwdParams &p, int grid, cudaStream_t s, int dev)
+                      const fa::ParamsOf<MASK> &p, int grid, cudaStream_t s, int dev)
 {
     if (D == 64)
         return bf16 ? launch_variant<64, true, MASK, SPLIT>(q, k, v, p, grid, s, dev)
@@ -66,7 +67,7 @@ fa_status launch_mask(int D, bool bf16, const CUtensorMap &q, const CUtensorMap 
 
 }  // namespace
 
-// Defined in fa_api.cu, fa_split.cu and fa_band.cu respectively; `causal`
+// Defined in fa_api.cu, fa_split.cu, fa_band.cu and fa_sink.cu respectively; `causal`
 // selects kMaskCausal over kMaskNone, `split` the balanced schedule.
 fa_status launch_whole(int D, bool bf16, bool causal, const CUtensorMap &q, const CUtensorMap &k,
                        const CUtensorMap &v, const fa::FwdParams &p, int grid, cudaStream_t s, int dev);
@@ -74,9 +75,12 @@ fa_status launch_split(int D, bool bf16, bool causal, const CUtensorMap &q, cons
                        const CUtensorMap &v, const fa::FwdParams &p, int grid, cudaStream_t s, int dev);
 fa_status launch_band(int D, bool bf16, bool split, const CUtensorMap &q, const CUtensorMap &k,
                       const CUtensorMap &v, const fa::FwdParams &p, int grid, cudaStream_t s, int dev);
+fa_status launch_sink(int D, bool bf16, bool split, const CUtensorMap &q, const CUtensorMap &k,
+                      const CUtensorMap &v, const fa::SinkParams &p, int grid, cudaStream_t s, int dev);
 bool take_status_word_whole(cudaStream_t s, unsigned int *word);
 bool take_status_word_split(cudaStream_t s, unsigned int *word);
 bool take_status_word_band(cudaStream_t s, unsigned int *word);
+bool take_status_word_sink(cudaStream_t s, unsigned int *word);
 
 // The static workspace of fa_fwd_noalloc (fa_split.cu): points p's partial
 // buffers into it for schedule `sc` and head size D, and clears the counters

@@ -77,6 +77,17 @@ struct Schedule {
     int range[kSchedMaxGrid + 1];   // balanced: range[c] = floor(U c / G), filled by sched_fill_ranges
 };
 
+// A band with sinks: the first `sinks` keys stay visible to every query at or
+// behind them, whatever the band's left bound (wr = 0: causal).  A CTA tile's
+// steps are then the sinks' [0, min(ss, ke)) followed by the band's from
+// max(ks, that) on.  A type of its own, so that the functions below compile to
+// the same code as before for schedules without sinks.
+struct SinkSchedule : Schedule {
+    int sinks;      // at most Nkv; 0 where the band has no left bound
+    int ss;         // K/V steps that hold sinks: ceil(sinks / 128)
+    int group;      // query heads per key head
+};
+
 // Band bounds that cannot bind become kSchedUnbounded: with off = Nkv - N,
 // query rows sit at positions off .. Nkv - 1, so wl >= Nkv clips nothing on
 // the left and wr >= N - 1 nothing on the right.  After this, r + off - wl
@@ -151,6 +162,49 @@ FA_HD int sched_kv_tiles(const Schedule &s, int ct, int w)
     return ke - sched_kv_start(s, ct);
 }
 
+// With sinks: the tile's sink steps, and its band's first and last steps.
+struct SinkSteps {
+    int ssz, ks, ke;   // steps [0, ssz), then [ks, ke), ssz <= ks
+};
+
+FA_HD SinkSteps sched_sink_range(const SinkSchedule &s, int ct)
+{
+    const int first = ct * kSchedCtaRows;
+    const int last = (first + kSchedCtaRows - 1 < s.N - 1) ? first + kSchedCtaRows - 1 : s.N - 1;
+    SinkSteps r;
+    sched_band_steps(s, first, last, r.ks, r.ke);
+    r.ssz = s.ss < r.ke ? s.ss : r.ke;
+    r.ks = r.ks < r.ssz ? r.ssz : r.ks;
+    return r;
+}
+
+FA_HD int sched_kv_tiles(const SinkSchedule &s, int ct, int w)
+{
+    const int r0 = ct * kSchedCtaRows + w * kSchedBM;
+    if (r0 >= s.N)
+        return 0;
+    const SinkSteps r = sched_sink_range(s, ct);
+    const int last = (r0 + kSchedBM - 1 < s.N - 1) ? r0 + kSchedBM - 1 : s.N - 1;
+    int ks, ke;
+    sched_band_steps(s, r0, last, ks, ke);
+    if (ke <= r.ssz)
+        return ke;
+    return r.ssz + (ke > r.ks ? ke - r.ks : 0);
+}
+
+// First key of step j of a tile: without sinks its steps follow one another
+// from sched_kv_start on; with them they jump from the sinks to the band.
+struct TileKeys {
+    int ssz, ks;
+    FA_HD int first_key(int j) const { return (j < ssz ? j : j - ssz + ks) * kSchedBN; }
+};
+
+FA_HD TileKeys sched_tile_keys(const SinkSchedule &s, int ct)
+{
+    const SinkSteps r = sched_sink_range(s, ct);
+    return TileKeys{r.ssz, r.ks};
+}
+
 // Masks without a left bound start every row's steps at 0: the steps of rows
 // up to `last` end at this step (the end half of sched_band_steps alone).
 FA_HD int sched_step_end(const Schedule &s, int last)
@@ -161,8 +215,8 @@ FA_HD int sched_step_end(const Schedule &s, int last)
 
 // sched_kv_tiles in the kernel: BAND (a left bound) takes the general form,
 // other masks the step end alone.
-template <bool BAND>
-FA_HD int sched_kv_tiles_t(const Schedule &s, int ct, int w)
+template <bool BAND, class S>
+FA_HD int sched_kv_tiles_t(const S &s, int ct, int w)
 {
     if (BAND)
         return sched_kv_tiles(s, ct, w);
@@ -184,6 +238,12 @@ FA_HD int sched_steps_ct(const Schedule &s, int ct)
     int ks, ke;
     sched_band_steps(s, first, last, ks, ke);
     return ke - ks;
+}
+
+FA_HD int sched_steps_ct(const SinkSchedule &s, int ct)
+{
+    const SinkSteps r = sched_sink_range(s, ct);
+    return r.ssz + r.ke - r.ks;
 }
 
 // Parts a tile of this schedule may be cut into: decoding-sized heads take
@@ -247,7 +307,8 @@ FA_HD void sched_decode_rr(const Schedule &s, int t, int &bh, int &ct)
     }
 }
 
-FA_HD int sched_steps_rr(const Schedule &s, int t)
+template <class S>
+FA_HD int sched_steps_rr(const S &s, int t)
 {
     if (!s.causal)
         return s.nkv;
@@ -272,8 +333,8 @@ FA_HD void sched_decode_t(const Schedule &s, int t, int &bh, int &ct)
     }
 }
 
-template <bool BAND>
-FA_HD int sched_steps_rr_t(const Schedule &s, int t)
+template <bool BAND, class S>
+FA_HD int sched_steps_rr_t(const S &s, int t)
 {
     if (BAND)
         return sched_steps_rr(s, t);
@@ -283,7 +344,8 @@ FA_HD int sched_steps_rr_t(const Schedule &s, int t)
     return sched_step_end(s, (first + kSchedCtaRows - 1 < s.N - 1) ? first + kSchedCtaRows - 1 : s.N - 1);
 }
 
-FA_HD int sched_steps(const Schedule &s, int t)
+template <class S>
+FA_HD int sched_steps(const S &s, int t)
 {
     int bh, ct;
     sched_decode(s, t, bh, ct);
@@ -292,7 +354,8 @@ FA_HD int sched_steps(const Schedule &s, int t)
 
 // Units of all tiles before tile t (tail split: the tail's tiles before t,
 // for t >= WG).
-FA_HD long long sched_prefix(const Schedule &s, int t)
+template <class S>
+FA_HD long long sched_prefix(const S &s, int t)
 {
     if (!s.causal)
         return (long long)(t - s.W * s.G) * s.nkv;
@@ -315,7 +378,8 @@ FA_HD long long sched_prefix(const Schedule &s, int t)
     return acc + (long long)(t - g * s.BH) * sched_steps_ct(s, sched_long_row(s, g));
 }
 
-FA_HD long long sched_total_units(const Schedule &s)
+template <class S>
+FA_HD long long sched_total_units(const S &s)
 {
     return sched_prefix(s, s.T - 1) + sched_steps(s, s.T - 1);
 }
@@ -348,7 +412,8 @@ FA_HD int sched_cta_of_unit(const Schedule &s, int u)
 }
 
 // Tile containing unit u (balanced schedule), with its first unit.
-FA_HD int sched_tile_of_unit(const Schedule &s, int u, int &tstart)
+template <class S>
+FA_HD int sched_tile_of_unit(const S &s, int u, int &tstart)
 {
     if (!s.causal) {   // (tail split: the tail's tiles follow the WG whole ones)
         const int t = u / s.nkv;
@@ -401,8 +466,8 @@ struct PartIter {
 
     // The kernel knows its schedule at compile time (SPLIT = s.split) and
     // takes only that path; init / next decide at run time (host code).
-    template <bool SPLIT>
-    FA_HD void init_t(const Schedule &s, int c_)
+    template <bool SPLIT, class S>
+    FA_HD void init_t(const S &s, int c_)
     {
         c = c_;
         lt = -1;
@@ -435,8 +500,8 @@ struct PartIter {
         }
     }
 
-    template <bool SPLIT, bool BAND = true>
-    FA_HD bool next_t(const Schedule &s, Part &p)
+    template <bool SPLIT, bool BAND = true, class S>
+    FA_HD bool next_t(const S &s, Part &p)
     {
         if (SPLIT) {
             if (lt >= 0) {
@@ -484,7 +549,8 @@ struct PartIter {
         return true;
     }
 
-    FA_HD void init(const Schedule &s, int c_)
+    template <class S>
+    FA_HD void init(const S &s, int c_)
     {
         if (s.split)
             init_t<true>(s, c_);
@@ -492,14 +558,16 @@ struct PartIter {
             init_t<false>(s, c_);
     }
 
-    FA_HD bool next(const Schedule &s, Part &p)
+    template <class S>
+    FA_HD bool next(const S &s, Part &p)
     {
         return s.split ? next_t<true>(s, p) : next_t<false>(s, p);
     }
 };
 
 // The CTAs that may hold parts of tile t (first unit pt, n units): clo .. chi.
-FA_HD void sched_tile_ctas(const Schedule &s, int t, int &pt, int &n, int &clo, int &chi)
+template <class S>
+FA_HD void sched_tile_ctas(const S &s, int t, int &pt, int &n, int &clo, int &chi)
 {
     pt = (int)sched_prefix(s, t);
     n = sched_steps(s, t);
@@ -532,7 +600,8 @@ FA_HD bool sched_part_slot(const Schedule &s, int pt, int n, int nw, int c, int 
 
 // Parts of tile t in which Q tile w (visiting nw steps) has work, for the
 // merge: returns their count and writes up to `max_slots` of their slots.
-FA_HD int sched_part_slots(const Schedule &s, int t, int nw, int *slots, int max_slots)
+template <class S>
+FA_HD int sched_part_slots(const S &s, int t, int nw, int *slots, int max_slots)
 {
     int pt, n, clo, chi;
     sched_tile_ctas(s, t, pt, n, clo, chi);
@@ -570,10 +639,10 @@ constexpr int kSchedTailSteps = 64;
 // mode: 0 = as above, 1 = round-robin, 2 = balanced wherever it can be built.
 // N query rows against Nkv keys per head; `causal` here means masked by the
 // band [i + off - wl, i + off + wr] (causal proper: wl unbounded, wr = 0).
-inline Schedule sched_plan(int N, int Nkv, int BH, bool causal, int sms, int mode = 0, int wl = kSchedUnbounded,
-                           int wr = 0)
+// Fills s (whose sinks, if it has any, are set).
+template <class S>
+inline void sched_plan_into(S &s, int N, int Nkv, int BH, bool causal, int sms, int mode, int wl, int wr)
 {
-    Schedule s{};
     s.N = N;
     s.Nkv = Nkv;
     s.off = causal ? Nkv - N : 0;
@@ -628,7 +697,7 @@ inline Schedule sched_plan(int N, int Nkv, int BH, bool causal, int sms, int mod
             rr = load[c] > rr ? load[c] : rr;
     }
     if (s.U > kSchedMaxUnits || mode == 1)
-        return s;
+        return;
     long long G = (s.U < sms) ? s.U : sms;
     if (G > kSchedMaxGrid)
         G = kSchedMaxGrid;
@@ -639,26 +708,26 @@ inline Schedule sched_plan(int N, int Nkv, int BH, bool causal, int sms, int mod
     if (need > 0 && s.U / G < need)
         G = s.U / need;
     if (G < 1)
-        return s;
+        return;
     const long long balanced = (s.U + G - 1) / G;
     if (mode == 0 && !causal && s.T > s.G) {   // the tail split, or whole tiles
         const int W = s.T / s.G, L = s.T - W * s.G;
         if (L == 0 || (W < 2 && s.nkv < kSchedTailSteps))
-            return s;
+            return;
         const long long ut = (long long)L * s.nkv;
         long long gt = s.G;
         if (need > 0 && ut / gt < need)
             gt = ut / need;
         if (gt < 1)
-            return s;
+            return;
         const long long tail = (long long)W * s.nkv + (ut + gt - 1) / gt;
         if (!(rr * 100 > tail * 104 && rr - tail >= kSchedMinGain))
-            return s;
+            return;
         s.split = 1;
         s.W = W;
         s.U = ut;
         sched_fill_ranges(s, (int)gt);
-        return s;
+        return;
     }
     const bool few_long_tiles = 2LL * s.T <= sms && max_steps >= 32 && rr >= 2 * balanced;
     // decoding-sized heads (at most 64 query rows) merge cheaply: balance
@@ -671,6 +740,27 @@ inline Schedule sched_plan(int N, int Nkv, int BH, bool causal, int sms, int mod
         s.U = sched_total_units(s);   // the same total in the balanced order
         sched_fill_ranges(s);
     }
+}
+
+inline Schedule sched_plan(int N, int Nkv, int BH, bool causal, int sms, int mode = 0, int wl = kSchedUnbounded,
+                           int wr = 0)
+{
+    Schedule s{};
+    sched_plan_into(s, N, Nkv, BH, causal, sms, mode, wl, wr);
+    return s;
+}
+
+// The plan of a causal window of `wl` earlier keys (kSchedUnbounded: none)
+// with `sinks` first keys that stay visible.
+inline SinkSchedule sched_plan_sink(int N, int Nkv, int BH, int group, int sms, int mode, int wl, int sinks)
+{
+    SinkSchedule s{};
+    s.group = group;
+    int wr = 0;
+    sched_band_normalize(N, Nkv, wl, wr);
+    s.sinks = wl >= kSchedUnbounded ? 0 : (sinks < Nkv ? sinks : Nkv);
+    s.ss = (s.sinks + kSchedBN - 1) / kSchedBN;
+    sched_plan_into(s, N, Nkv, BH, true, sms, mode, wl, 0);
     return s;
 }
 

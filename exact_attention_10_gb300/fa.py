@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 from functools import lru_cache
-from typing import NamedTuple
+from operator import itemgetter
 
 from .build import LIB_PATH
 
@@ -17,9 +17,9 @@ FA_BF16, FA_FP16 = 0, 1
 FA_BWD_DETERMINISTIC = 1
 STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_VALUE", 2: "FA_ERR_MISALIGNED", 3: "FA_ERR_UNSUPPORTED_DEVICE",
           4: "FA_ERR_CUDA", 5: "FA_ERR_DEVICE_TIMEOUT", 6: "FA_ERR_NO_ALLOC_LIMIT"}
-EXPORTS = ("fa_bwd", "fa_bwd_band", "fa_bwd_ex", "fa_cache_append", "fa_cache_evict", "fa_cache_fwd", "fa_cache_read",
+EXPORTS = ("fa_bwd", "fa_bwd_band", "fa_bwd_ex", "fa_bwd_sink", "fa_bwd_sink_workspace", "fa_cache_append", "fa_cache_evict", "fa_cache_fwd", "fa_cache_read",
            "fa_cache_weights", "fa_cache_workspace", "fa_fwd", "fa_fwd_band", "fa_fwd_ex", "fa_fwd_noalloc",
-           "fa_fwd_qkv", "fa_sync_status", "fa_status_string")
+           "fa_fwd_qkv", "fa_fwd_sink", "fa_fwd_sink_workspace", "fa_sync_status", "fa_status_string")
 SCHEDULES = {"auto": 0, "whole_tiles": 1, "balanced": 2}
 
 _lib = None
@@ -58,6 +58,14 @@ def load(path: str = LIB_PATH):
     lib.fa_bwd_band.restype = c_int
     lib.fa_bwd_ex.argtypes = [vp] * 9 + [c_int] * 7 + [ctypes.c_float, c_int, ctypes.c_uint, vp]
     lib.fa_bwd_ex.restype = c_int
+    lib.fa_fwd_sink.argtypes = [vp] * 5 + [c_int] * 8 + [ctypes.c_float, c_int, c_int, vp, ctypes.c_size_t, vp]
+    lib.fa_fwd_sink.restype = c_int
+    lib.fa_fwd_sink_workspace.argtypes = [c_int] * 9 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_fwd_sink_workspace.restype = c_int
+    lib.fa_bwd_sink.argtypes = [vp] * 9 + [c_int] * 8 + [ctypes.c_float, c_int, ctypes.c_uint, vp, ctypes.c_size_t, vp]
+    lib.fa_bwd_sink.restype = c_int
+    lib.fa_bwd_sink_workspace.argtypes = [c_int] * 8 + [ctypes.c_uint, ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_bwd_sink_workspace.restype = c_int
     lib.fa_cache_append.argtypes = [vp] * 8 + [c_int] * 6 + [vp]
     lib.fa_cache_append.restype = c_int
     lib.fa_cache_read.argtypes = [vp] * 8 + [c_int] * 6 + [vp]
@@ -109,18 +117,23 @@ def _dtype_code(t) -> int:
 
 
 def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse=None, stream=None,
-            schedule: str = "auto", window: tuple[int, int] | None = None):
+            schedule: str = "auto", window: tuple[int, int] | None = None, sinks: int | None = None):
     """Attention forward on CUDA tensors q [B, H, Nq, D], k and v [B, H, Nkv, D];
     returns (O [B, H, Nq, D], LSE [B, H, Nq]).  With Nq != Nkv the causal mask
     is aligned bottom-right (fa_fwd_qkv).  ``window = (left, right)`` masks
     with a band instead (fa_fwd_band; a negative bound is unbounded; causal
-    is ignored then).
+    is ignored then).  With ``sinks`` (0 or more) the mask is the causal
+    window (left, 0), without one plain causal, in which the first ``sinks``
+    keys stay visible, and k and v may have fewer heads, [B, Hkv, Nkv, D] with
+    H a multiple of Hkv (fa_fwd_sink).
 
     ``out`` / ``lse`` may be given to write into existing buffers.
     ``schedule`` is "auto", "whole_tiles" or "balanced" (fa_schedule).
     Raises FAError on any non-OK status.  Asynchronous on ``stream``
     (default: the current torch stream).
     """
+    if sinks is not None:
+        return _forward_sink(q, k, v, scale, out, lse, stream, schedule, window, sinks)
     import torch
     if q.dim() != 4 or k.shape != v.shape or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
         raise ValueError("q must be [B, H, Nq, D] and k, v [B, H, Nkv, D]")
@@ -156,19 +169,70 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     return out, lse
 
 
+@lru_cache(maxsize=4096)
+def _sink_workspace(device: int, *sizes) -> int:
+    n = ctypes.c_size_t()
+    rc = load().fa_fwd_sink_workspace(*sizes, ctypes.byref(n))
+    if rc != 0:
+        raise FAError(rc, "fa_fwd_sink_workspace")
+    return n.value
+
+
+def _sink_shapes(q, k, v):
+    """(B, H, Hkv, Nq, Nkv, D, dtype code) of tensors that go together."""
+    sq, sk = q.shape, k.shape
+    if len(sq) != 4 or len(sk) != 4 or v.shape != sk or sq[0] != sk[0] or sq[3] != sk[3] or sk[1] < 1 or sq[1] % sk[1]:
+        raise ValueError("q must be [B, H, Nq, D] and k, v [B, Hkv, Nkv, D], H a multiple of Hkv")
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("q, k, v must be contiguous")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k, v must share a dtype")
+    return sq[0], sq[1], sk[1], sq[2], sk[2], sq[3], _dtype_code(q)
+
+
+def _forward_sink(q, k, v, scale, out, lse, stream, schedule, window, sinks):
+    import torch
+    B, H, Hkv, Nq, Nkv, D, code = _sink_shapes(q, k, v)
+    left = _left_of(window, sinks)
+    if schedule not in SCHEDULES:
+        raise ValueError(f"schedule must be one of {sorted(SCHEDULES)}")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, H, Nq]")
+    sched = SCHEDULES[schedule]
+    nbytes = _sink_workspace(q.get_device(), B, H, Hkv, Nq, Nkv, D, left, sinks, sched)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    rc = load().fa_fwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
+                            Nkv, D, left, sinks, D ** -0.5 if scale is None else scale, code, sched,
+                            ws.data_ptr() if nbytes else None, nbytes, _stream_of(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_fwd_sink")
+    if stream is not None and nbytes:
+        _keep_until_done(ws, stream)
+    return out, lse
+
+
 def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = None, dq=None, dk=None, dv=None,
-             stream=None, window: tuple[int, int] | None = None, deterministic: bool = False):
+             stream=None, window: tuple[int, int] | None = None, deterministic: bool = False, sinks: int | None = None):
     """Attention backward on CUDA tensors: q, o, do [B, H, Nq, D], k, v
     [B, H, Nkv, D] and lse [B, H, Nq] as ``forward`` returned them (same
     causal / window); returns (dQ, dK, dV).  Square unmasked or causal calls
     go to fa_bwd; a window, or Nq != Nkv (bottom-right causal), to fa_bwd_band;
     ``deterministic`` (dQ by the second pass, the same bits on every call) to
-    fa_bwd_ex with FA_BWD_DETERMINISTIC.
+    fa_bwd_ex with FA_BWD_DETERMINISTIC; ``sinks`` (k, v [B, Hkv, Nkv, D], the
+    mask of ``forward`` with sinks) to fa_bwd_sink.
 
     ``dq`` / ``dk`` / ``dv`` may be given to write into existing buffers.
     Raises FAError on any non-OK status.  Asynchronous on ``stream``
     (default: the current torch stream).
     """
+    if sinks is not None:
+        return _backward_sink(q, k, v, o, do, lse, scale, dq, dk, dv, stream, window, deterministic, sinks)
     import torch
     if (q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or o.shape != q.shape or do.shape != q.shape
             or lse.shape != q.shape[:3] or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]):
@@ -203,17 +267,71 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     return dq, dk, dv
 
 
+@lru_cache(maxsize=4096)
+def _sink_bwd_workspace(device: int, *sizes) -> int:
+    n = ctypes.c_size_t()
+    rc = load().fa_bwd_sink_workspace(*sizes, ctypes.byref(n))
+    if rc != 0:
+        raise FAError(rc, "fa_bwd_sink_workspace")
+    return n.value
+
+
+def _backward_sink(q, k, v, o, do, lse, scale, dq, dk, dv, stream, window, deterministic, sinks):
+    import torch
+    B, H, Hkv, Nq, Nkv, D, code = _sink_shapes(q, k, v)
+    left = _left_of(window, sinks)
+    if o.shape != q.shape or do.shape != q.shape or lse.shape != (B, H, Nq):
+        raise ValueError("o, do must be of q's shape and lse [B, H, Nq]")
+    if not (o.is_contiguous() and do.is_contiguous() and lse.is_contiguous()):
+        raise ValueError("o, do, lse must be contiguous")
+    if o.dtype != q.dtype or do.dtype != q.dtype or lse.dtype != torch.float32:
+        raise TypeError("o, do must be of q's type, lse float32")
+    outs = [torch.empty_like(x) if d is None else d for d, x in ((dq, q), (dk, k), (dv, v))]
+    for d, x in zip(outs, (q, k, v)):
+        if d.shape != x.shape or d.dtype != x.dtype or not d.is_contiguous():
+            raise ValueError("dq, dk, dv must be contiguous, of the shapes and type of q, k, v")
+    flags = FA_BWD_DETERMINISTIC if deterministic else 0
+    nbytes = _sink_bwd_workspace(q.get_device(), B, H, Hkv, Nq, Nkv, D, left, sinks, flags)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    rc = load().fa_bwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+                            *(d.data_ptr() for d in outs), B, H, Hkv, Nq, Nkv, D, left, sinks,
+                            D ** -0.5 if scale is None else scale, code, flags, ws.data_ptr(), nbytes,
+                            _stream_of(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_bwd_sink")
+    if stream is not None:
+        _keep_until_done(ws, stream)
+    return tuple(outs)
+
+
 # ---- the 4-bit key/value cache
 
-class PackedCache(NamedTuple):
-    """K and V of [B, Hkv, C, D] held in 4 bits: codes [B, Hkv, C, D/2] uint8
-    and (scale, minimum) [B, Hkv, C, 2] in the model's type (the format is in
-    include/fa.h)."""
+class PackedCache(tuple):
+    """K and V of [B, Hkv, C, D] held in 4 bits: the tensors (k_codes,
+    k_params, v_codes, v_params), codes [B, Hkv, C, D/2] uint8 and (scale,
+    minimum) [B, Hkv, C, 2] in the model's type (the format is in
+    include/fa.h).  Checked when it is made; ``sizes`` is (B, Hkv, C, D, dtype
+    code)."""
 
-    k_codes: "torch.Tensor"
-    k_params: "torch.Tensor"
-    v_codes: "torch.Tensor"
-    v_params: "torch.Tensor"
+    k_codes, k_params, v_codes, v_params = (property(itemgetter(i)) for i in range(4))
+
+    def __new__(cls, k_codes, k_params, v_codes, v_params):
+        import torch
+        shape = k_codes.shape
+        if len(shape) != 4 or v_codes.shape != shape or k_params.shape != v_params.shape or (
+                k_params.shape != (*shape[:3], 2)):
+            raise ValueError("a cache is codes [B, Hkv, C, D/2] and params [B, Hkv, C, 2] for K and for V")
+        if k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8 or k_params.dtype != v_params.dtype:
+            raise TypeError("cache codes are uint8, the params of K and V of one type")
+        if not (k_codes.is_contiguous() and k_params.is_contiguous() and v_codes.is_contiguous()
+                and v_params.is_contiguous()):
+            raise ValueError("the cache must be contiguous")
+        self = super().__new__(cls, (k_codes, k_params, v_codes, v_params))
+        self.sizes = (*shape[:3], 2 * shape[3], _dtype_code(k_params))
+        return self
+
+    def __reduce__(self):   # (copying and pickling go through the checks)
+        return PackedCache, tuple(self)
 
 
 def cache_empty(B: int, Hkv: int, C: int, D: int, dtype=None, device="cuda") -> PackedCache:
@@ -229,33 +347,21 @@ def cache_empty(B: int, Hkv: int, C: int, D: int, dtype=None, device="cuda") -> 
                          for n, t in ((D // 2, torch.uint8), (2, dtype)) * 2))
 
 
-def _cache_sizes(cache: PackedCache):
-    """(B, Hkv, C, D, dtype code) of a cache whose parts fit together."""
-    import torch
-    kc, kp, vc, vp = cache
-    if kc.dim() != 4 or kc.shape != vc.shape or kp.shape != vp.shape or kp.shape != (*kc.shape[:3], 2):
-        raise ValueError("a cache is codes [B, Hkv, C, D/2] and params [B, Hkv, C, 2] for K and for V")
-    if kc.dtype != torch.uint8 or vc.dtype != torch.uint8 or kp.dtype != vp.dtype:
-        raise TypeError("cache codes are uint8, the params of K and V of one type")
-    if not (kc.is_contiguous() and kp.is_contiguous() and vc.is_contiguous() and vp.is_contiguous()):
-        raise ValueError("the cache must be contiguous")
-    B, Hkv, C, half = kc.shape
-    return B, Hkv, C, 2 * half, _dtype_code(kp)
-
-
-def _ints(t, B: int, name: str):
+def _ints(t, B: int, name: str) -> int:
     import torch
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
-    if t.shape != (B,) or not t.is_contiguous():
+    if t.dim() != 1 or t.numel() != B or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous [{B}]")
     return t.data_ptr()
 
 
 def _stream_of(stream, t) -> int:
+    """The stream's handle; None: torch's current stream on t's device (asked
+    for as a plain number: a Stream object would cost more than the launch)."""
     if stream is None:
         import torch
-        stream = torch.cuda.current_stream(t.device)
+        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -276,16 +382,18 @@ def cache_append(cache: PackedCache, k, v, start, count=None, stream=None) -> No
     of a sequence.  Tokens whose place lies outside the cache are not written.
     Raises FAError on any non-OK status.  Asynchronous on ``stream``
     (default: the current torch stream)."""
-    B, Hkv, C, D, code = _cache_sizes(cache)
-    if k.dim() != 4 or k.shape != v.shape or k.shape[:2] != (B, Hkv) or k.shape[3] != D:
+    kc, kp, vc, vp = cache
+    B, Hkv, C, D, code = cache.sizes
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape or shape[0] != B or shape[1] != Hkv or shape[3] != D:
         raise ValueError(f"k, v must be [{B}, {Hkv}, N, {D}]")
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError("k, v must be contiguous")
-    if k.dtype != cache.k_params.dtype or v.dtype != k.dtype:
+    if k.dtype != kp.dtype or v.dtype != k.dtype:
         raise TypeError("k, v must be of the cache's type")
-    rc = load().fa_cache_append(*(x.data_ptr() for x in cache), k.data_ptr(), v.data_ptr(), _ints(start, B, "start"),
-                                None if count is None else _ints(count, B, "count"), B, Hkv, k.shape[2], C, D, code,
-                                _stream_of(stream, k))
+    rc = load().fa_cache_append(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                _ints(start, B, "start"), None if count is None else _ints(count, B, "count"), B, Hkv,
+                                shape[2], C, D, code, _stream_of(stream, k))
     if rc != 0:
         raise FAError(rc, "fa_cache_append")
 
@@ -293,13 +401,14 @@ def cache_append(cache: PackedCache, k, v, start, count=None, stream=None) -> No
 def cache_read(cache: PackedCache, start, n: int, count=None, stream=None):
     """The values (k, v) [B, Hkv, n, D] that cache tokens start[b] + i stand
     for; rows from count[b] on, or outside the cache, are zeros."""
+    kc, kp, vc, vp = cache
+    B, Hkv, C, D, code = cache.sizes
     import torch
-    B, Hkv, C, D, code = _cache_sizes(cache)
-    k = torch.empty((B, Hkv, n, D), dtype=cache.k_params.dtype, device=cache.k_codes.device)
+    k = torch.empty((B, Hkv, n, D), dtype=kp.dtype, device=kp.device)
     v = torch.empty_like(k)
-    rc = load().fa_cache_read(*(x.data_ptr() for x in cache), k.data_ptr(), v.data_ptr(), _ints(start, B, "start"),
-                              None if count is None else _ints(count, B, "count"), B, Hkv, n, C, D, code,
-                              _stream_of(stream, k))
+    rc = load().fa_cache_read(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), k.data_ptr(), v.data_ptr(),
+                              _ints(start, B, "start"), None if count is None else _ints(count, B, "count"), B, Hkv, n,
+                              C, D, code, _stream_of(stream, k))
     if rc != 0:
         raise FAError(rc, "fa_cache_read")
     return k, v
@@ -315,14 +424,16 @@ def _cache_workspace(device: int, H: int, Hkv: int, Nq: int, D: int) -> int:
 
 
 def _cache_queries(q, cache):
-    B, Hkv, C, D, code = _cache_sizes(cache)
-    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or q.shape[1] % Hkv != 0:
+    """(H, Nq) of queries that go with the cache."""
+    B, Hkv, _, D, _ = cache.sizes
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != D or shape[1] % Hkv != 0:
         raise ValueError(f"q must be [{B}, a multiple of {Hkv}, Nq, {D}]")
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     if q.dtype != cache.k_params.dtype:
         raise TypeError("q must be of the cache's type")
-    return B, q.shape[1], Hkv, q.shape[2], C, D, code
+    return shape[1], shape[2]
 
 
 def cache_forward(q, cache: PackedCache, lens, window: tuple[int, int] | None = None, sinks: int = 0,
@@ -338,20 +449,23 @@ def cache_forward(q, cache: PackedCache, lens, window: tuple[int, int] | None = 
     the current torch stream, and a given ``stream`` must be ordered with it.
     """
     import torch
-    B, H, Hkv, Nq, C, D, code = _cache_queries(q, cache)
+    kc, kp, vc, vp = cache
+    B, Hkv, C, D, code = cache.sizes
+    H, Nq = _cache_queries(q, cache)
     left = _left_of(window, sinks)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape and type")
-    if lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, H, Nq]")
-    nbytes = _cache_workspace(q.device.index, H, Hkv, Nq, D)
+    nbytes = _cache_workspace(q.get_device(), H, Hkv, Nq, D)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    st = _stream_of(stream, q)
-    rc = load().fa_cache_fwd(q.data_ptr(), *(x.data_ptr() for x in cache), _ints(lens, B, "lens"), out.data_ptr(),
-                             lse.data_ptr(), B, H, Hkv, Nq, C, D, left, sinks,
-                             float(D ** -0.5 if scale is None else scale), code, ws.data_ptr(), nbytes, st)
+    rc = load().fa_cache_fwd(q.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(),
+                             _ints(lens, B, "lens"), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, C, D, left, sinks,
+                             D ** -0.5 if scale is None else scale, code, ws.data_ptr(), nbytes, _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_cache_fwd")
     if stream is not None:
@@ -374,19 +488,23 @@ def cache_weights(q, cache: PackedCache, lse, lens, window: tuple[int, int] | No
     head's query rows of exp(scale q.k - lse).  With ``acc`` ([B, Hkv, C]
     float32) the weights are added to it in place, and it is returned."""
     import torch
-    B, H, Hkv, Nq, C, D, code = _cache_queries(q, cache)
+    kc, kp = cache[:2]
+    B, Hkv, C, D, code = cache.sizes
+    H, Nq = _cache_queries(q, cache)
     left = _left_of(window, sinks)
     if lse.shape != (B, H, Nq) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous [B, H, Nq]")
     if lse.dtype != torch.float32 or (acc is not None and acc.dtype != torch.float32):
         raise TypeError("lse and acc must be float32")
-    out = torch.empty((B, Hkv, C), dtype=torch.float32, device=q.device) if acc is None else acc
-    if out.shape != (B, Hkv, C) or not out.is_contiguous():
+    if acc is None:
+        out = torch.empty((B, Hkv, C), dtype=torch.float32, device=q.device)
+    elif acc.shape != (B, Hkv, C) or not acc.is_contiguous():
         raise ValueError("acc must be contiguous [B, Hkv, C]")
-    rc = load().fa_cache_weights(q.data_ptr(), cache.k_codes.data_ptr(), cache.k_params.data_ptr(), lse.data_ptr(),
-                                 _ints(lens, B, "lens"), out.data_ptr(), int(acc is not None), B, H, Hkv, Nq, C, D,
-                                 left, sinks, float(D ** -0.5 if scale is None else scale), code,
-                                 _stream_of(stream, q))
+    else:
+        out = acc
+    rc = load().fa_cache_weights(q.data_ptr(), kc.data_ptr(), kp.data_ptr(), lse.data_ptr(), _ints(lens, B, "lens"),
+                                 out.data_ptr(), int(acc is not None), B, H, Hkv, Nq, C, D, left, sinks,
+                                 D ** -0.5 if scale is None else scale, code, _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_cache_weights")
     return out
@@ -403,25 +521,29 @@ def cache_evict(cache: PackedCache, acc, lens, keep: int, sinks: int = 0, recent
     weights [B, Hkv, capacity] (0 behind them), the new lengths [B] and the
     kept positions [B, Hkv, keep] (-1 behind them)."""
     import torch
-    B, Hkv, C, D, code = _cache_sizes(cache)
+    kc, kp, vc, vp = cache
+    B, Hkv, C, D, code = cache.sizes
     if acc.shape != (B, Hkv, C) or not acc.is_contiguous():
         raise ValueError("acc must be contiguous [B, Hkv, C]")
     if acc.dtype != torch.float32:
         raise TypeError("acc must be float32")
     if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep:
         raise ValueError("keep must be at least 1 and hold the sinks and the recent tokens")
-    dev = cache.k_codes.device
     if out is None:   # (its rows behind the last kept token are not written)
-        out = PackedCache(*(torch.empty((B, Hkv, keep, x.shape[3]), dtype=x.dtype, device=dev) for x in cache))
-    B2, Hkv2, C2, D2, code2 = _cache_sizes(out)
+        codes = torch.empty((B, Hkv, keep, D // 2), dtype=torch.uint8, device=kc.device)
+        params = torch.empty((B, Hkv, keep, 2), dtype=kp.dtype, device=kc.device)
+        out = PackedCache(codes, params, torch.empty_like(codes), torch.empty_like(params))
+    kc2, kp2, vc2, vp2 = out
+    B2, Hkv2, C2, D2, code2 = out.sizes
     if (B2, Hkv2, D2, code2) != (B, Hkv, D, code) or C2 < keep:
         raise ValueError("out must be a cache like the first one, of capacity keep at least")
-    acc2 = torch.empty((B, Hkv, C2), dtype=torch.float32, device=dev)
-    lens2 = torch.empty((B,), dtype=torch.int32, device=dev)
-    index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
-    rc = load().fa_cache_evict(*(x.data_ptr() for x in cache), acc.data_ptr(), _ints(lens, B, "lens"),
-                               *(x.data_ptr() for x in out), acc2.data_ptr(), lens2.data_ptr(), index.data_ptr(), B,
-                               Hkv, C, C2, D, keep, sinks, recent, _stream_of(stream, acc))
+    acc2 = torch.empty((B, Hkv, C2), dtype=torch.float32, device=kc.device)
+    lens2 = torch.empty_like(lens)
+    index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=kc.device)
+    rc = load().fa_cache_evict(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), acc.data_ptr(),
+                               _ints(lens, B, "lens"), kc2.data_ptr(), kp2.data_ptr(), vc2.data_ptr(), vp2.data_ptr(),
+                               acc2.data_ptr(), lens2.data_ptr(), index.data_ptr(), B, Hkv, C, C2, D, keep, sinks,
+                               recent, _stream_of(stream, acc))
     if rc != 0:
         raise FAError(rc, "fa_cache_evict")
     return out, acc2, lens2, index

@@ -176,6 +176,35 @@ FA_API fa_status fa_fwd_band(const void *Q, const void *K, const void *V, void *
                              float scale, fa_dtype dtype, fa_schedule schedule, fa_stream_t stream);
 
 /*
+ * fa_fwd_sink -- causal attention in a sliding window whose first tokens stay
+ * visible ("sinks"), with query heads that may share key heads.
+ *
+ * Q, O : contiguous [B, H, Nq, D];  K, V : contiguous [B, Hkv, Nkv, D], H a
+ * multiple of Hkv, query head h reading key head floor(h / (H / Hkv));  LSE :
+ * [B, H, Nq] float32.  With i' = i + (Nkv - Nq), query i sees the keys
+ * j <= i' with j >= i' - window_left (window_left < 0: no bound) or
+ * j < sinks.  A query that sees no key (i' < 0) gets O = 0 and LSE = -inf.
+ * Key tiles that hold neither a sink nor a key of some row's window are
+ * skipped, not masked.
+ *
+ * workspace : device memory, 16-byte aligned, of at least the bytes that
+ *             fa_fwd_sink_workspace gives for the same arguments (0 where the
+ *             schedule needs none; NULL is then fine).  It is the caller's:
+ *             calls that may overlap, captured graphs among them, take
+ *             different ones.  Its contents need no set-up.
+ * Other arguments and errors as for fa_fwd_ex; B*Hkv*Nkv < 2^31.
+ */
+FA_API fa_status fa_fwd_sink(const void *Q, const void *K, const void *V, void *O, float *LSE, int B, int H,
+                             int Hkv, int Nq, int Nkv, int D, int window_left, int sinks, float scale,
+                             fa_dtype dtype, fa_schedule schedule, void *workspace, size_t workspace_bytes,
+                             fa_stream_t stream);
+
+/* fa_fwd_sink_workspace -- bytes of workspace that fa_fwd_sink needs on the
+ * current device for these arguments. */
+FA_API fa_status fa_fwd_sink_workspace(int B, int H, int Hkv, int Nq, int Nkv, int D, int window_left, int sinks,
+                                       fa_schedule schedule, size_t *bytes);
+
+/*
  * fa_fwd_noalloc -- fa_fwd_ex that allocates no memory, device or host, at
  * any call.  The pages describe nothing like it: the method itself needs no
  * scratch, and this entry point only concerns where this library's balanced
@@ -286,6 +315,30 @@ FA_API fa_status fa_bwd_ex(const void *Q, const void *K, const void *V, const vo
                            const float *LSE, void *dQ, void *dK, void *dV, int B, int H, int Nq, int Nkv, int D,
                            int window_left, int window_right, float scale, fa_dtype dtype, unsigned int flags,
                            fa_stream_t stream);
+
+/*
+ * fa_bwd_sink -- the gradients of fa_fwd_sink, from that call's O and LSE.
+ *
+ * Q, O, dO, dQ : contiguous [B, H, Nq, D];  K, V, dK, dV : contiguous
+ * [B, Hkv, Nkv, D], the gradients of a shared key head summed over its query
+ * heads in fp32;  LSE : [B, H, Nq] float32.  A query that sees no key gets
+ * dQ = 0; a key that no query sees dK = dV = 0.
+ * flags : 0 or FA_BWD_DETERMINISTIC, as for fa_bwd_ex (dK and dV are the same
+ *         bits on every call either way: a sink tile's query tiles are summed
+ *         in parts, the parts added in a fixed order).
+ * workspace : at least fa_bwd_sink_workspace bytes of device memory, 16-byte
+ *         aligned, under the rules of fa_fwd_sink's.
+ * Other arguments and errors as for fa_bwd.
+ */
+FA_API fa_status fa_bwd_sink(const void *Q, const void *K, const void *V, const void *O, const void *dO,
+                             const float *LSE, void *dQ, void *dK, void *dV, int B, int H, int Hkv, int Nq, int Nkv,
+                             int D, int window_left, int sinks, float scale, fa_dtype dtype, unsigned int flags,
+                             void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* fa_bwd_sink_workspace -- bytes of workspace that fa_bwd_sink needs on the
+ * current device for these arguments. */
+FA_API fa_status fa_bwd_sink_workspace(int B, int H, int Hkv, int Nq, int Nkv, int D, int window_left, int sinks,
+                                       unsigned int flags, size_t *bytes);
 
 /*
  * ---- A key/value cache held in 4 bits ----
