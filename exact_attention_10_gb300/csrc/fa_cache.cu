@@ -123,12 +123,12 @@ extern "C" fa_status fa_cache_append(void *Kc, void *Kp, void *Vc, void *Vp, con
         kern<<<(unsigned)blocks, cache::kThreads, 0, s>>>(
             static_cast<const uint16_t *>(K), static_cast<const uint16_t *>(V), static_cast<uint8_t *>(Kc),
             static_cast<uint32_t *>(Kp), static_cast<uint8_t *>(Vc), static_cast<uint32_t *>(Vp), start, count, Hkv, N, C,
-            (long long)rows);
+            (uint32_t)rows);
         return launched();
     };
     if (D == 64)
-        return dtype == FA_BF16 ? run(cache::append_kernel<64, true>, 8) : run(cache::append_kernel<64, false>, 8);
-    return dtype == FA_BF16 ? run(cache::append_kernel<128, true>, 16) : run(cache::append_kernel<128, false>, 16);
+        return dtype == FA_BF16 ? run(cache::append_kernel<64, true>, 4) : run(cache::append_kernel<64, false>, 4);
+    return dtype == FA_BF16 ? run(cache::append_kernel<128, true>, 8) : run(cache::append_kernel<128, false>, 8);
 }
 
 extern "C" fa_status fa_cache_read(const void *Kc, const void *Kp, const void *Vc, const void *Vp, void *K, void *V,
@@ -152,7 +152,7 @@ extern "C" fa_status fa_cache_read(const void *Kc, const void *Kp, const void *V
         kern<<<(unsigned)blocks, cache::kThreads, 0, s>>>(
             static_cast<const uint8_t *>(Kc), static_cast<const uint32_t *>(Kp), static_cast<const uint8_t *>(Vc),
             static_cast<const uint32_t *>(Vp), static_cast<uint16_t *>(K), static_cast<uint16_t *>(V), start, count, Hkv, N,
-            C, (long long)rows);
+            C, (uint32_t)rows);
         return launched();
     };
     if (D == 64)

@@ -17,7 +17,7 @@
 //   O = sum_j (p_j vs_j) u'_j + sum_j p_j vmin_j  over  sum_j p_j
 // with u, u' the integer codes: scale and minimum stay outside the products,
 // so the matrix instructions see small integers (exact in 16 bits) against q
-// (exact, the input) and against w_j = p_j vs_j.
+// (exact, the input) and against w_j = p_j vs_j (rounded to 16 bits).
 //
 // What bounds it: a decoded token reads every visible row once, D/2 + 4 bytes
 // for each of K and V, and does 4 G Nq D operations on it -- HBM, at the few
@@ -46,6 +46,7 @@ constexpr int kSub = 32;       // tokens a warp takes at a time
 constexpr int kStages = 3;     // kSub-token stages per warp, two of them in flight
 constexpr int kMinUnits = 4;   // units per CTA, at least: half a round of the CTA's eight warps
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = 1.9259629911266175e-8f;   // log2(e) - kLog2e
 constexpr float kLn2f = 0.69314718055994530942f;
 // The reference maximum m of a query row moves only when a score exceeds it
 // by more than kSlack (log2 units): p stays below 2^kSlack, far inside fp32's
@@ -114,18 +115,12 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// D[16 x 8] += A[16 x 16] B[16 x 8], fp32 accumulation.
-template <bool BF16>
+// D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, fp32 accumulation.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    if (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Transpose of an 8 x 8 matrix of 16-bit values held row-wise by the warp.
@@ -136,17 +131,34 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     return y;
 }
 
-// Codes I and I + 4 of a word of eight as the 16-bit pair (16 + code I, 16 +
-// code I + 4): the code goes to the top of the significand of 16.0, so one
-// shift and one three-input logic operation unpack two codes.  The 16 is
-// taken out of the finished sums (16 rather than a larger power keeps the
-// sums, and with them fp32's rounding, small).
-template <bool BF16, int I>
-__device__ __forceinline__ uint32_t unpack2(uint32_t w)
+// Codes as fp16 operands: a code left in place in the low byte of a half is
+// the subnormal code * 2^-24 (bits 0..3) or 16 code * 2^-24 (bits 4..7), exact.
+// So one logic operation unpacks two codes, and a word of eight takes one
+// shift besides -- the integer pipe, at half the rate of the others, is what
+// unpacking is bound by.  V's codes go to the tensor core like that.  K's are
+// brought to (code - 7.5) 2^-9 by one packed multiply-add more, exact again:
+// the tensor core aligns a subnormal's product by its nominal exponent, which
+// cuts low bits off the sum (4e-7 of a weight instead of 1e-6 with it,
+// against float64), and codes centred at their middle keep the sums as small
+// as the scores.
+constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;
+constexpr float kCodeUnit = 16777216.f;   // 2^24
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
 {
-    constexpr int up = (BF16 ? 3 : 6) - 4 * I;   // from bit 4 I to the significand's top four bits
-    const uint32_t s = up >= 0 ? w << (up >= 0 ? up : 0) : w >> (up >= 0 ? 0 : -up);
-    return (s & (BF16 ? 0x00780078u : 0x03C003C0u)) | (BF16 ? 0x41804180u : 0x4C004C00u);
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t centred_even(uint32_t w)
+{
+    return hfma2(w & kEven, 0x78007800u, 0xA380A380u);   // * 2^15 - 7.5 * 2^-9
+}
+
+__device__ __forceinline__ uint32_t centred_odd(uint32_t w)
+{
+    return hfma2(w & kOdd, 0x68006800u, 0xA380A380u);    // * 2^11 - 7.5 * 2^-9
 }
 
 template <bool BF16>
@@ -161,81 +173,112 @@ __device__ __forceinline__ uint32_t from_float(float x)
     return BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x)) : (uint32_t)__half_as_ushort(__float2half_rn(x));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float exp2i(int e)
+{
+    return __int_as_float((e + 127) << 23);
 }
 
 // ------------------------------------------------------------------ append, read
 
-// What one row's codes are computed from: x (scaled by `k`, a power of two
-// that keeps the differences and the scale inside fp32's normal range; 1 but
-// for extreme rows), the scale and minimum likewise.
+// What one row's codes are computed from, multiplied by `k`, a power of two
+// that keeps differences, scale and reciprocal inside fp32's normal range (1
+// but for extreme rows).
 struct RowScale {
     float mn, sc, inv, k;
     uint32_t params;   // as held: scale, minimum
     bool flat;         // scale 0, or a row that is not finite: codes 0
+    bool exact;        // x - mn or the quotient may need more than fp32: code_of for every value
 };
 
 template <bool BF16>
-__device__ __forceinline__ RowScale row_scale(float mn, float mx, bool finite)
+__device__ __forceinline__ RowScale row_scale(float mn, float mx)
 {
     RowScale r;
     r.k = 1.f;
-    if (!finite) {   // an infinity or NaN in the row: every value it stands for is NaN
+    r.exact = false;
+    if (!(fabsf(mn) < INFINITY && fabsf(mx) < INFINITY)) {   // an infinity or NaN in the row: it stands for NaN
         r.params = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
         r.flat = true;
         r.mn = r.sc = r.inv = 0.f;
         return r;
     }
     float range = mx - mn;
-    if (range > 3.0e38f)   // (bf16) the range overflows: in quarters
-        r.k = 0.25f;
-    else if (range > 0.f && range < 8.0e-25f)
-        r.k = 1.2089258196146292e24f;   // 2^80: the scale and its reciprocal stay normal
-    if (r.k != 1.f)
-        range = mx * r.k - mn * r.k;
-    float sc = __fdiv_rn(range, 15.f);
-    if (r.k == 1.f) {
-        r.params = from_float<BF16>(sc);
-    } else {
-        r.params = from_float<BF16>(__fdiv_rn(sc, r.k));   // (exact but for a scale that ends subnormal)
+    if (BF16) {
+        if (range > 3.0e38f)   // the range overflows: in quarters
+            r.k = 0.25f;
+        else if (range > 0.f && range < 8.0e-25f)
+            r.k = 1.2089258196146292e24f;   // 2^80
+        if (r.k != 1.f)
+            range = mx * r.k - mn * r.k;
     }
+    float sc = __fdiv_rn(range, 15.f);
+    if (BF16 && r.k != 1.f)
+        sc = __fdiv_rn(sc, r.k);   // (exact but for a scale that ends subnormal)
+    r.params = from_float<BF16>(sc);
     const float held = to_float<BF16>(r.params);
     r.params |= from_float<BF16>(mn) << 16;
     r.flat = held == 0.f;
     r.sc = held * r.k;
-    r.inv = r.flat ? 0.f : __fdiv_rn(1.f, r.sc);
     r.mn = mn * r.k;
+    r.inv = __frcp_rn(r.sc);
+    // a scale so much smaller than range / 15 that codes pass 15, or a
+    // minimum so small that x - mn rounds
+    r.exact = range * r.inv > 15.49f || (mn != 0.f && fabsf(mn) < fabsf(mx) * 3.0e-5f);
     return r;
 }
 
-// round_half_even((x - mn) / sc) clamped to 0..15.  The quotient by the
-// reciprocal is off by a few units in its last place, which matters only next
-// to a border between two codes: there the residual a - (q -+ 1/2) sc decides,
+// round_half_even((x - mn) / sc) clamped to 0..15, exactly: the quotient by the
+// reciprocal, then the residual a - (q -+ 1/2) sc decides next to a border,
 // with the rounding error of a = x - mn added back.
-__device__ __forceinline__ uint32_t code_of(float x, const RowScale &r)
+__device__ __noinline__ uint32_t code_of(float x, float mn, float sc, float inv)
 {
-    const float a = x - r.mn;
-    const float f = a * r.inv;
-    float q = rintf(f);
-    if (fabsf(f - q) > 0.4999f) {
-        const float bb = a - x;
-        const float e = (x - (a - bb)) + (-r.mn - bb);
-        const float t = fmaf(-q, r.sc, a);
-        if (f > q) {
-            const float over = (t - 0.5f * r.sc) + e;
-            if (over > 0.f || (over == 0.f && ((int)q & 1)))
-                q += 1.f;
-        } else {
-            const float under = (t + 0.5f * r.sc) + e;
-            if (under < 0.f || (under == 0.f && ((int)q & 1)))
-                q -= 1.f;
-        }
-    }
+    const float a = x - mn;
+    const float bb = a - x;
+    const float e = (x - (a - bb)) + (-mn - bb);
+    float q = fminf(rintf(a * inv), 16.f);
+    const float t = fmaf(-q, sc, a);
+    const float over = (t - 0.5f * sc) + e, under = (t + 0.5f * sc) + e;
+    if (over > 0.f || (over == 0.f && ((int)q & 1)))
+        q += 1.f;
+    else if (under < 0.f || (under == 0.f && ((int)q & 1)))
+        q -= 1.f;
     return (uint32_t)fminf(fmaxf(q, 0.f), 15.f);
+}
+
+// The codes of eight values.  Where x - mn is exact (values of eleven bits at
+// most whose magnitudes are within 2^13 of one another, or zero: `exact` false),
+// the quotient a / sc corrected once by its residual -- the final step of
+// Markstein's division -- is a half-integer only if the true one is, so that
+// rounding it half to even by adding and taking off 1.5 * 2^23 gives the code.
+// (Such values are not rare: 16-bit values over a 16-bit scale hit a border
+// about once in 300.)  Four codes at a time are summed as code * 16^i in one
+// float, exact in 16 bits.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], const RowScale &r, bool exact)
+{
+    constexpr float kRound = 12582912.f;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = x[i] - r.mn, f0 = a * r.inv;
+        const float f = fmaf(fmaf(-f0, r.sc, a), r.inv, f0);
+        s[i / 4] = fmaf((f + kRound) - kRound, (float)(1 << (4 * (i % 4))), s[i / 4]);
+    }
+    uint32_t w = (uint32_t)s[0] | ((uint32_t)s[1] << 16);
+    if (exact) {
+        w = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w |= code_of(x[i], r.mn, r.sc, r.inv) << (4 * i);
+    }
+    return w;
 }
 
 // Position of new token i of sequence b in the cache, or -1: not counted in,
@@ -247,61 +290,93 @@ __device__ __forceinline__ int slot_of(const int *start, const int *count, int b
     return (i < n && at >= 0 && at < C) ? (int)at : -1;
 }
 
-template <int D, bool BF16>
-__device__ __forceinline__ void append_row(const uint4 &x4, int part, uint32_t group, uint8_t *codes, uint32_t *params)
+// Minima of two packed 16-bit values each; a NaN wins.
+template <bool BF16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
 {
-    const uint32_t xw[4] = {x4.x, x4.y, x4.z, x4.w};
-    float x[8];
-    float mn = INFINITY, mx = -INFINITY, zero = 0.f;
+    uint32_t d;
+    if (BF16)
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    if (BF16)
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// A row's 16 channels of this lane: minimum and maximum over the row's lanes
+// (the pair (min, -max) goes through the shuffles as one word), codes, stores.
+template <int D, bool BF16>
+__device__ __forceinline__ void append_row(const uint4 (&x4)[2], int part, uint32_t group, uint8_t *codes, uint32_t *params)
+{
+    const uint32_t xw[8] = {x4[0].x, x4[0].y, x4[0].z, x4[0].w, x4[1].x, x4[1].y, x4[1].z, x4[1].w};
+    uint32_t lo = xw[0], hi = xw[0], small = xw[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = to_float<BF16>((i & 1) ? xw[i / 2] >> 16 : xw[i / 2] & 0xffffu);
-        mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
-        zero = fmaf(x[i], 0.f, zero);   // NaN once an element is not finite
+    for (int i = 1; i < 8; ++i) {
+        lo = min2<BF16>(lo, xw[i]);
+        hi = max2<BF16>(hi, xw[i]);
+        small = min2<BF16>(small, xw[i] & 0x7FFF7FFFu);
     }
+    uint32_t both = min2<BF16>(__byte_perm(lo, hi ^ 0x80008000u, 0x5410), __byte_perm(lo, hi ^ 0x80008000u, 0x7632));
 #pragma unroll
-    for (int m = D / 16; m > 0; m /= 2) {
-        mn = fminf(mn, __shfl_xor_sync(group, mn, m));
-        mx = fmaxf(mx, __shfl_xor_sync(group, mx, m));
-        zero += __shfl_xor_sync(group, zero, m);
-    }
-    const RowScale r = row_scale<BF16>(mn, mx, zero == 0.f);
-    uint32_t w = 0;
+    for (int m = D / 32; m > 0; m /= 2)
+        both = min2<BF16>(both, __shfl_xor_sync(group, both, m));
+    const RowScale r = row_scale<BF16>(to_float<BF16>(both & 0xffffu), -to_float<BF16>(both >> 16));
+    uint2 w = make_uint2(0u, 0u);
     if (!r.flat) {
+        float x[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w |= code_of(x[i] * r.k, r) << (4 * i);
+        for (int i = 0; i < 16; ++i)
+            x[i / 8][i % 8] = to_float<BF16>((i & 1) ? xw[i / 2] >> 16 : xw[i / 2] & 0xffffu);
+        if (r.k != 1.f) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                x[i / 8][i % 8] *= r.k;
+        }
+        // a value far smaller than the minimum's magnitude: x - mn may round
+        const float least = fminf(to_float<BF16>(small & 0xffffu), to_float<BF16>(small >> 16));
+        const bool exact = r.exact || least * r.k < fabsf(r.mn) * 1.2e-4f;
+        w = make_uint2(codes_of(x[0], r, exact), codes_of(x[1], r, exact));
     }
-    *reinterpret_cast<uint32_t *>(codes + part * 4) = w;
+    *reinterpret_cast<uint2 *>(codes + part * 8) = w;
     if (part == 0)
         *params = r.params;
 }
 
-// One group of D / 8 lanes per new token and head, K and V both (two loads in
-// flight per lane), 8 channels a lane.  Bound by HBM: 2 x 2 D bytes read and
-// 2 x (D/2 + 4) written per token and head.
+// One group of D / 16 lanes per new token and head, K and V both (four loads
+// in flight per lane), 16 channels a lane: the row's minimum, scale and
+// reciprocal are shared by as many codes.  It reads 2 x 2 D bytes and writes
+// 2 x (D/2 + 4) per token and head, at about a dozen instructions a value.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
     append_kernel(const uint16_t *kn, const uint16_t *vn, uint8_t *kc, uint32_t *kp, uint8_t *vc, uint32_t *vp,
-                  const int *start, const int *count, int Hkv, int N, int C, long long rows)
+                  const int *start, const int *count, int Hkv, int N, int C, uint32_t rows)
 {
-    constexpr int kTpr = D / 8;
-    const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const long long row = g / kTpr;
+    constexpr int kTpr = D / 16;
+    const uint32_t row = blockIdx.x * (kThreads / kTpr) + threadIdx.x / kTpr;   // (below 2^31 + a block's rows)
     if (row >= rows)   // whole groups leave together
         return;
-    const int part = (int)(g % kTpr);
-    const long long bh = row / N;
+    const int part = threadIdx.x % kTpr;
+    const uint4 *ks = reinterpret_cast<const uint4 *>(kn + (size_t)row * D) + 2 * part;
+    const uint4 *vs = reinterpret_cast<const uint4 *>(vn + (size_t)row * D) + 2 * part;
+    const uint4 k4[2] = {__ldg(ks), __ldg(ks + 1)}, v4[2] = {__ldg(vs), __ldg(vs + 1)};
+    const uint32_t bh = row / (uint32_t)N;
     const int i = (int)(row - bh * N);
-    const int at = slot_of(start, count, (int)(bh / Hkv), i, N, C);
+    const int at = slot_of(start, count, (int)(bh / (uint32_t)Hkv), i, N, C);
     if (at < 0)
         return;
-    const uint4 k4 = __ldg(reinterpret_cast<const uint4 *>(kn + row * D) + part);
-    const uint4 v4 = __ldg(reinterpret_cast<const uint4 *>(vn + row * D) + part);
     const int lane = threadIdx.x % 32;
     const uint32_t group = ((1u << kTpr) - 1u) << (lane & ~(kTpr - 1));
-    const long long dst = bh * C + at;
+    const size_t dst = (size_t)bh * C + at;
     append_row<D, BF16>(k4, part, group, kc + dst * (D / 2), kp + dst);
     append_row<D, BF16>(v4, part, group, vc + dst * (D / 2), vp + dst);
 }
@@ -313,7 +388,10 @@ __device__ __forceinline__ uint4 values_of(uint32_t w, uint32_t params)
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float lo = fmaf((float)((w >> (8 * i)) & 15u), sc, mn), hi = fmaf((float)((w >> (8 * i + 4)) & 15u), sc, mn);
+        // (the code as the low bits of 2^23, taken off again: no conversion instruction)
+        const float a = __uint_as_float(((w >> (8 * i)) & 15u) | 0x4B000000u) - 8388608.f;
+        const float b = __uint_as_float(((w >> (8 * i + 4)) & 15u) | 0x4B000000u) - 8388608.f;
+        const float lo = fmaf(a, sc, mn), hi = fmaf(b, sc, mn);
         o[i] = from_float<BF16>(lo) | (from_float<BF16>(hi) << 16);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
@@ -324,27 +402,26 @@ __device__ __forceinline__ uint4 values_of(uint32_t w, uint32_t params)
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
     read_kernel(const uint8_t *kc, const uint32_t *kp, const uint8_t *vc, const uint32_t *vp, uint16_t *ko, uint16_t *vo,
-                const int *start, const int *count, int Hkv, int N, int C, long long rows)
+                const int *start, const int *count, int Hkv, int N, int C, uint32_t rows)
 {
     constexpr int kTpr = D / 8;
-    const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const long long row = g / kTpr;
+    const uint32_t row = blockIdx.x * (kThreads / kTpr) + threadIdx.x / kTpr;
     if (row >= rows)
         return;
-    const int part = (int)(g % kTpr);
-    const long long bh = row / N;
+    const int part = threadIdx.x % kTpr;
+    const uint32_t bh = row / (uint32_t)N;
     const int i = (int)(row - bh * N);
-    const int at = slot_of(start, count, (int)(bh / Hkv), i, N, C);
+    const int at = slot_of(start, count, (int)(bh / (uint32_t)Hkv), i, N, C);
     uint4 k4 = make_uint4(0u, 0u, 0u, 0u), v4 = k4;
     if (at >= 0) {
-        const long long src = bh * C + at;
+        const size_t src = (size_t)bh * C + at;
         const uint32_t kw = *reinterpret_cast<const uint32_t *>(kc + src * (D / 2) + part * 4);
         const uint32_t vw = *reinterpret_cast<const uint32_t *>(vc + src * (D / 2) + part * 4);
         k4 = values_of<BF16>(kw, kp[src]);
         v4 = values_of<BF16>(vw, vp[src]);
     }
-    reinterpret_cast<uint4 *>(ko + row * D)[part] = k4;
-    reinterpret_cast<uint4 *>(vo + row * D)[part] = v4;
+    reinterpret_cast<uint4 *>(ko + (size_t)row * D)[part] = k4;
+    reinterpret_cast<uint4 *>(vo + (size_t)row * D)[part] = v4;
 }
 
 // ------------------------------------------------------------------ work decomposition
@@ -469,31 +546,58 @@ __device__ __forceinline__ uint32_t v_chunk(int t, int j)
     return (uint32_t)(block * 256 + (e * 4 + k) * 32 + j * 16);
 }
 
-// Issue the loads of tokens t0 .. t0 + 31 of key head `bh` into a stage (V
-// left out for the weights); tokens from `len` on are zeros.  Always commits
-// a group.
+// One key head's rows, this lane's first bytes of a step at token 0.
+template <int D>
+struct Rows {
+    const uint8_t *kc, *vc;
+    const uint32_t *kp, *vp;
+
+    __device__ Rows(const Params &p, long long bh)
+    {
+        const int lane = threadIdx.x % 32;
+        const long long row = bh * p.C;
+        kc = p.kc + row * Layout<D>::kRow + lane * 16;
+        vc = p.vc + row * Layout<D>::kRow + lane * 16;
+        kp = p.kp + row + lane;
+        vp = p.vp + row + lane;
+    }
+};
+
+// Issue the loads of tokens t0 .. t0 + 31 into a stage (V left out for the
+// weights); tokens from `len` on are zeros.  Always commits a group.
 template <int D, bool VALUES>
-__device__ __forceinline__ void load_stage(const Params &p, uint32_t stage, long long bh, int t0, int len, bool any)
+__device__ __forceinline__ void load_stage(const Rows<D> &rows, uint32_t stage, int t0, int len, bool any)
 {
     using L = Layout<D>;
     const int lane = threadIdx.x % 32;
+    constexpr int kPer = L::kRow / 16;   // 16-byte chunks per row; 32 lanes hold 512 bytes of consecutive rows
     if (any) {
-        constexpr int kPer = L::kRow / 16;   // 16-byte chunks per row
+        const uint8_t *kc = rows.kc + (long long)t0 * L::kRow, *vc = rows.vc + (long long)t0 * L::kRow;
+        const uint32_t dk = stage + lane * 16, dv = stage + L::kCodes + v_chunk<D>(lane / kPer, lane % kPer);
+        const uint32_t par = stage + (VALUES ? 2 : 1) * L::kCodes + lane * 4;
+        if (t0 + kSub <= len) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int idx = lane + 32 * i, t = idx / kPer, j = idx % kPer;
-            const bool real = t0 + t < len;
-            const long long row = bh * p.C + (real ? t0 + t : 0);
-            cp16(stage + idx * 16, p.kc + row * L::kRow + j * 16, real);
+            for (int i = 0; i < kPer; ++i) {   // (v_chunk moves by 512 bytes per 512 bytes of rows)
+                cp16(dk + i * 512, kc + i * 512, true);
+                if (VALUES)
+                    cp16(dv + i * 512, vc + i * 512, true);
+            }
+            cp4(par, rows.kp + t0, true);
             if (VALUES)
-                cp16(stage + L::kCodes + v_chunk<D>(t, j), p.vc + row * L::kRow + j * 16, real);
+                cp4(par + kSub * 4, rows.vp + t0, true);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const bool real = t0 + lane / kPer + i * (32 / kPer) < len;
+                cp16(dk + i * 512, real ? kc + i * 512 : rows.kc, real);
+                if (VALUES)
+                    cp16(dv + i * 512, real ? vc + i * 512 : rows.vc, real);
+            }
+            const bool real = t0 + lane < len;
+            cp4(par, real ? rows.kp + t0 : rows.kp, real);
+            if (VALUES)
+                cp4(par + kSub * 4, real ? rows.vp + t0 : rows.vp, real);
         }
-        const bool real = t0 + lane < len;
-        const long long row = bh * p.C + (real ? t0 + lane : 0);
-        const uint32_t par = stage + (VALUES ? 2 : 1) * L::kCodes;
-        cp4(par + lane * 4, p.kp + row, real);
-        if (VALUES)
-            cp4(par + (kSub + lane) * 4, p.vp + row, real);
     }
     cp_commit();
 }
@@ -522,13 +626,17 @@ __device__ __forceinline__ uint4 lds128(uint32_t a)
 // The query rows as B fragments (16 channels x 8 rows each), in the channel
 // order in which K's codes come out of their words: lane (r = lane / 4, c =
 // lane % 4) holds row 8 nt + r, channels [c D/4, (c + 1) D/4); word w of them
-// gives two fragments, (0, 4 | 1, 5) and (2, 6 | 3, 7).  Also -16 sum_d q_d
-// and sum_d q_d per row, for the two rows (columns of S^T) of this lane.
+// gives two fragments, (0, 4 | 1, 5) and (2, 6 | 3, 7).  As fp16: a row is multiplied by the power of two that brings
+// its largest element to [2^14, 2^15), so a bf16 or fp16 element is exact
+// unless it is 2^-24 of the largest or less, and then off by 2^-40 of it.
+// `mul` takes the power, the codes' unit and the softmax scale (log2 units)
+// out again; `sum` is sum_d q_d in those units; both for the two rows
+// (columns of S^T) of this lane.
 template <int D, bool BF16, int NT>
 struct Queries {
     using L = Layout<D>;
     uint32_t f[NT][L::kWords * 2][2];
-    float sum[NT][2];
+    float sum[NT][2], mul[NT][2];
 
     __device__ void load(const Params &p, long long row0, int nrows)
     {
@@ -537,25 +645,44 @@ struct Queries {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int n = 8 * nt + r;
-            float s = 0.f;
+            float x[L::kWords][8];
+            float s = 0.f, mx = 0.f;
 #pragma unroll
             for (int w = 0; w < L::kWords; ++w) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (n < nrows)
-                    x = __ldg(reinterpret_cast<const uint4 *>(q + (row0 + n) * (D / 2) + (c * L::kWords + w) * 4));
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};   // channels (0,1) (2,3) (4,5) (6,7)
-                f[nt][2 * w][0] = __byte_perm(xw[0], xw[2], 0x5410);       // 0, 4
-                f[nt][2 * w][1] = __byte_perm(xw[0], xw[2], 0x7632);       // 1, 5
-                f[nt][2 * w + 1][0] = __byte_perm(xw[1], xw[3], 0x5410);   // 2, 6
-                f[nt][2 * w + 1][1] = __byte_perm(xw[1], xw[3], 0x7632);   // 3, 7
+                    v = __ldg(reinterpret_cast<const uint4 *>(q + (row0 + n) * (D / 2) + (c * L::kWords + w) * 4));
+                const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s += to_float<BF16>(xw[i] & 0xffffu) + to_float<BF16>(xw[i] >> 16);
+                for (int i = 0; i < 8; ++i) {
+                    x[w][i] = to_float<BF16>((i & 1) ? xw[i / 2] >> 16 : xw[i / 2] & 0xffffu);
+                    s += x[w][i];
+                    mx = fmaxf(mx, fabsf(x[w][i]));
+                }
             }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            sum[nt][0] = __shfl_sync(0xffffffffu, s, 8 * c);       // row 2c
-            sum[nt][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);   // row 2c + 1
+#pragma unroll
+            for (int m = 1; m < 4; m *= 2) {
+                s += __shfl_xor_sync(0xffffffffu, s, m);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+            }
+            // (queries of 2^114 and more overflow fp16, and their rows end as NaN)
+            int e = mx > 0.f ? 14 - (int)((__float_as_uint(mx) >> 23) & 255u) + 127 : 0;
+            e = e > 100 ? 100 : (e < -100 ? -100 : e);
+            const float up = exp2i(e);
+#pragma unroll
+            for (int w = 0; w < L::kWords; ++w) {
+                f[nt][2 * w][0] = pack_f16(x[w][0] * up, x[w][4] * up);
+                f[nt][2 * w][1] = pack_f16(x[w][1] * up, x[w][5] * up);
+                f[nt][2 * w + 1][0] = pack_f16(x[w][2] * up, x[w][6] * up);
+                f[nt][2 * w + 1][1] = pack_f16(x[w][3] * up, x[w][7] * up);
+            }
+            const float back = p.qk2 * exp2i(9 - e);
+            s *= p.qk2;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {   // rows 2c and 2c + 1
+                sum[nt][k] = __shfl_sync(0xffffffffu, s, 8 * c + 4 * k);
+                mul[nt][k] = __shfl_sync(0xffffffffu, back, 8 * c + 4 * k);
+            }
         }
     }
 };
@@ -563,8 +690,8 @@ struct Queries {
 // Scores of 16 tokens (rows 16 mt .. of the stage) in log2 units: x[nt][0, 1]
 // token r, columns 2c and 2c + 1; x[nt][2, 3] token r + 8.
 template <int D, bool BF16, int NT>
-__device__ __forceinline__ void scores(const Params &p, uint32_t stage, uint32_t par, int mt,
-                                       const Queries<D, BF16, NT> &q, float (&x)[NT][4])
+__device__ __forceinline__ void scores(uint32_t stage, uint32_t par, int mt, const Queries<D, BF16, NT> &q,
+                                       float (&x)[NT][4])
 {
     using L = Layout<D>;
     const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
@@ -572,8 +699,8 @@ __device__ __forceinline__ void scores(const Params &p, uint32_t stage, uint32_t
     uint32_t wa[L::kWords], wb[L::kWords];
     if constexpr (D == 128) {
         const uint4 u = lds128(a0), v = lds128(a0 + 8 * L::kRow);
-        wa[0] = u.x; wa[1] = u.y; wa[L::kWords - 2] = u.z; wa[L::kWords - 1] = u.w;
-        wb[0] = v.x; wb[1] = v.y; wb[L::kWords - 2] = v.z; wb[L::kWords - 1] = v.w;
+        wa[0] = u.x; wa[1] = u.y; wa[2] = u.z; wa[3] = u.w;
+        wb[0] = v.x; wb[1] = v.y; wb[2] = v.z; wb[3] = v.w;
     } else {
         const uint2 u = lds64(a0), v = lds64(a0 + 8 * L::kRow);
         wa[0] = u.x; wa[1] = u.y;
@@ -585,25 +712,24 @@ __device__ __forceinline__ void scores(const Params &p, uint32_t stage, uint32_t
         s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
     for (int w = 0; w < L::kWords; ++w) {
-        const uint32_t lo[4] = {unpack2<BF16, 0>(wa[w]), unpack2<BF16, 0>(wb[w]), unpack2<BF16, 1>(wa[w]),
-                                unpack2<BF16, 1>(wb[w])};
-        const uint32_t hi[4] = {unpack2<BF16, 2>(wa[w]), unpack2<BF16, 2>(wb[w]), unpack2<BF16, 3>(wa[w]),
-                                unpack2<BF16, 3>(wb[w])};
+        const uint32_t ya = wa[w] >> 8, yb = wb[w] >> 8;
+        const uint32_t lo[4] = {centred_even(wa[w]), centred_even(wb[w]), centred_odd(wa[w]), centred_odd(wb[w])};
+        const uint32_t hi[4] = {centred_even(ya), centred_even(yb), centred_odd(ya), centred_odd(yb)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            mma<BF16>(s[nt], lo, q.f[nt][2 * w][0], q.f[nt][2 * w][1]);
-            mma<BF16>(s[nt], hi, q.f[nt][2 * w + 1][0], q.f[nt][2 * w + 1][1]);
+            mma(s[nt], lo, q.f[nt][2 * w][0], q.f[nt][2 * w][1]);
+            mma(s[nt], hi, q.f[nt][2 * w + 1][0], q.f[nt][2 * w + 1][1]);
         }
     }
     const uint32_t pa = lds32(par + (uint32_t)(16 * mt + r) * 4), pb = lds32(par + (uint32_t)(16 * mt + r + 8) * 4);
-    const float sa = to_float<BF16>(pa & 0xffffu) * p.qk2, sb = to_float<BF16>(pb & 0xffffu) * p.qk2;
-    const float za = fmaf(-16.f, sa, to_float<BF16>(pa >> 16) * p.qk2), zb = fmaf(-16.f, sb, to_float<BF16>(pb >> 16) * p.qk2);
+    const float sa = to_float<BF16>(pa & 0xffffu), sb = to_float<BF16>(pb & 0xffffu);
+    const float za = fmaf(7.5f, sa, to_float<BF16>(pa >> 16)), zb = fmaf(7.5f, sb, to_float<BF16>(pb >> 16));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] = fmaf(sa, s[nt][0], za * q.sum[nt][0]);
-        x[nt][1] = fmaf(sa, s[nt][1], za * q.sum[nt][1]);
-        x[nt][2] = fmaf(sb, s[nt][2], zb * q.sum[nt][0]);
-        x[nt][3] = fmaf(sb, s[nt][3], zb * q.sum[nt][1]);
+        x[nt][0] = fmaf(s[nt][0] * q.mul[nt][0], sa, za * q.sum[nt][0]);
+        x[nt][1] = fmaf(s[nt][1] * q.mul[nt][1], sa, za * q.sum[nt][1]);
+        x[nt][2] = fmaf(s[nt][2] * q.mul[nt][0], sb, zb * q.sum[nt][0]);
+        x[nt][3] = fmaf(s[nt][3] * q.mul[nt][1], sb, zb * q.sum[nt][1]);
     }
 }
 
@@ -634,15 +760,25 @@ __device__ __forceinline__ bool sees(const Bounds &v, int t)
 }
 
 // One segment (units [ku, ke) of one tile) of the attention by one warp:
-// running m, l, z = sum p (vmin - 16 vs) and O^T per query row.
+// running m, l, z = sum p vmin and O^T per query row.  O^T is formed from
+// w = p vs as one fp16 operand: w is multiplied by the warp's power of two
+// `fac`, which keeps the largest vs so far in [2^5, 2^6), so with p <= 2^8 it
+// stays in fp16's range, and a token's 11 significand bits are whole down to
+// 2^-20 of that.  What the rounding of w takes off or adds is given back with
+// the middle code, 7.5 (w - fp16(w)) in z, so that its error meets the codes'
+// distance from their middle only: it then costs what rounding p to 16 bits
+// costs the 16-bit kernels' product with V, in either type no more than the
+// result's own rounding.  l is summed from the unrounded p.
 template <int D, bool BF16, int NT>
 struct Attend {
     using L = Layout<D>;
     float m[NT][2], l[NT][2], z[NT][2];
     float o[NT][L::kMTiles][4];
+    float fac;
 
     __device__ void reset()
     {
+        fac = exp2i(100);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -657,15 +793,22 @@ struct Attend {
     }
 
     // 32 tokens from t0 on, in `stage`.
-    __device__ void step(const Params &p, uint32_t stage, const Queries<D, BF16, NT> &q, int t0, bool masked,
-                         const Bounds (&vis)[NT][2])
+    __device__ void step(uint32_t stage, const Queries<D, BF16, NT> &q, int t0, bool masked, const Bounds (&vis)[NT][2])
     {
         const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
         const uint32_t par = stage + 2 * L::kCodes;
         float x[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
-            scores<D, BF16, NT>(p, stage, par, mt, q, x[mt]);
+            scores<D, BF16, NT>(stage, par, mt, q, x[mt]);
+        float vs[4], vm[4];   // scale and minimum of tokens r, r + 8, r + 16, r + 24
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t w = lds32(par + (uint32_t)(kSub + 8 * k + r) * 4);
+            vs[k] = to_float<BF16>(w & 0xffffu);
+            vm[k] = to_float<BF16>(w >> 16);
+        }
+        uint32_t hid = 0;   // bit 2 k' + e ...: (token, column) pairs that are hidden
         if (masked) {
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
@@ -673,13 +816,16 @@ struct Attend {
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (!sees(vis[nt][e & 1], t0 + 16 * mt + r + 8 * (e >> 1)))
+                        if (!sees(vis[nt][e & 1], t0 + 16 * mt + r + 8 * (e >> 1))) {
                             x[mt][nt][e] = -INFINITY;
+                            hid |= 1u << ((mt * NT + nt) * 4 + e);
+                        }
         }
         // Move the reference maxima where a score is kSlack above them (always
-        // at the first visible token).
+        // at the first visible token), and the factor of w where a scale has
+        // outgrown it.
         bool up = false;
-        float mx[NT][2];
+        float mx[NT][2], big = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -687,7 +833,31 @@ struct Attend {
                 mx[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
                 up |= mx[nt][e] > m[nt][e] + kSlack;
             }
+        big = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+        up |= big * fac >= 64.f;
         if (__any_sync(0xffffffffu, up)) {
+            if (masked) {   // only rows that some query sees, and finite ones, move the factor
+                big = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    bool seen = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        seen |= ((hid >> (((k >> 1) * NT + nt) * 4 + 2 * (k & 1))) & 3u) != 3u;
+                    if (seen && vs[k] < INFINITY)
+                        big = fmaxf(big, vs[k]);
+                }
+            }
+#pragma unroll
+            for (int s = 4; s < 32; s *= 2)
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
+            float df = 1.f;
+            if (big * fac >= 64.f && big < INFINITY) {
+                const int e = 5 + 127 - (int)(__float_as_uint(big) >> 23);   // big in [2^(5 - e), 2^(6 - e))
+                const float now = exp2i(e > 100 ? 100 : (e < -125 ? -125 : e));
+                df = now / fac;   // a power of two, or 0 from 2^100
+                fac = now;
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -702,40 +872,41 @@ struct Attend {
                     z[nt][e] *= al;
 #pragma unroll
                     for (int j = 0; j < L::kMTiles; ++j) {
-                        o[nt][j][e] *= al;
-                        o[nt][j][e + 2] *= al;
+                        o[nt][j][e] *= al * df;
+                        o[nt][j][e + 2] *= al * df;
                     }
                 }
         }
+        const float mid = 7.5f * (1.f / fac);
+        float mu[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                mu[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-            // Weights of the V codes, w = p vs, as bf16 pairs hi + lo (16 bits
-            // of significand together: one bf16 alone would put 2^-9 of error
-            // on every weight, more than a half-precision output's own
-            // rounding): 4 more MMAs per 16 tokens and 64 channels.
-            const uint32_t pa = lds32(par + (uint32_t)(kSub + 16 * mt + r) * 4),
-                           pb = lds32(par + (uint32_t)(kSub + 16 * mt + r + 8) * 4);
-            const float va[2] = {to_float<BF16>(pa & 0xffffu), to_float<BF16>(pb & 0xffffu)};
-            const float vb[2] = {fmaf(-16.f, va[0], to_float<BF16>(pa >> 16)), fmaf(-16.f, va[1], to_float<BF16>(pb >> 16))};
-            uint32_t hi[NT][2], lo[NT][2];
+            uint32_t wf[NT][2];   // w as B fragments
+            const float wa = vs[2 * mt] * fac, wb = vs[2 * mt + 1] * fac;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float mu = m[nt][e & 1];
-                    const float pr = ex2(x[mt][nt][e] - (mu == -INFINITY ? 0.f : mu));
+                    const float pr = ex2(x[mt][nt][e] - mu[nt][e & 1]);
                     l[nt][e & 1] += pr;
-                    // (a hidden token weighs nothing whatever its row holds)
-                    w[e] = pr == 0.f ? 0.f : pr * va[e >> 1];
-                    z[nt][e & 1] += pr == 0.f ? 0.f : pr * vb[e >> 1];
+                    w[e] = pr * ((e >> 1) ? wb : wa);
+                    float zt = pr * vm[2 * mt + (e >> 1)];
+                    if (masked && ((hid >> ((mt * NT + nt) * 4 + e)) & 1u))
+                        w[e] = zt = 0.f;   // (a hidden token weighs nothing whatever its row holds)
+                    z[nt][e & 1] += zt;
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t a = pack_bf16(w[2 * h], w[2 * h + 1]);
-                    const uint32_t b = pack_bf16(w[2 * h] - __uint_as_float(a << 16), w[2 * h + 1] - __uint_as_float(a & 0xffff0000u));
-                    hi[nt][h] = transpose8(a);
-                    lo[nt][h] = transpose8(b);
+                    const uint32_t u = pack_f16(w[2 * h], w[2 * h + 1]);
+                    wf[nt][h] = transpose8(u);
+                    z[nt][0] = fmaf(w[2 * h] - to_float<false>(u & 0xffffu), mid, z[nt][0]);
+                    z[nt][1] = fmaf(w[2 * h + 1] - to_float<false>(u >> 16), mid, z[nt][1]);
                 }
             }
             // V^T as the A operand: for channel words of this lane, tokens
@@ -747,7 +918,7 @@ struct Attend {
                 if constexpr (D == 128) {
                     const uint2 u = lds64(stage + L::kCodes + v_chunk<D>(t, r >> 1) + (r & 1) * 8);
                     vw[k][0] = u.x;
-                    vw[k][L::kVWords - 1] = u.y;
+                    vw[k][1] = u.y;
                 } else {
                     vw[k][0] = lds32(stage + L::kCodes + v_chunk<D>(t, r >> 2) + (r & 3) * 4);
                 }
@@ -756,19 +927,24 @@ struct Attend {
             for (int w = 0; w < L::kVWords; ++w) {
                 const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
                 const uint32_t a2 = __byte_perm(vw[2][w], vw[3][w], 0x5410), a3 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+                const uint32_t b0 = a0 >> 8, b1 = a1 >> 8, b2 = a2 >> 8, b3 = a3 >> 8;
                 auto tile = [&](int j, const uint32_t (&a)[4]) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma<true>(o[nt][j], a, hi[nt][0], hi[nt][1]);
-                        mma<true>(o[nt][j], a, lo[nt][0], lo[nt][1]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma(o[nt][j], a, wf[nt][0], wf[nt][1]);
                 };
-                tile(4 * w, {unpack2<true, 0>(a0), unpack2<true, 0>(a1), unpack2<true, 0>(a2), unpack2<true, 0>(a3)});
-                tile(4 * w + 1, {unpack2<true, 1>(a0), unpack2<true, 1>(a1), unpack2<true, 1>(a2), unpack2<true, 1>(a3)});
-                tile(4 * w + 2, {unpack2<true, 2>(a0), unpack2<true, 2>(a1), unpack2<true, 2>(a2), unpack2<true, 2>(a3)});
-                tile(4 * w + 3, {unpack2<true, 3>(a0), unpack2<true, 3>(a1), unpack2<true, 3>(a2), unpack2<true, 3>(a3)});
+                tile(4 * w, {a0 & kEven, a1 & kEven, a2 & kEven, a3 & kEven});
+                tile(4 * w + 1, {a0 & kOdd, a1 & kOdd, a2 & kOdd, a3 & kOdd});
+                tile(4 * w + 2, {b0 & kEven, b1 & kEven, b2 & kEven, b3 & kEven});
+                tile(4 * w + 3, {b0 & kOdd, b1 & kOdd, b2 & kOdd, b3 & kOdd});
             }
         }
+    }
+
+    // sum_t p_t vs_t code_t of an accumulator of tile j.
+    __device__ float value(int j, float acc) const
+    {
+        return acc * ((j & 1) ? kCodeUnit / 16.f : kCodeUnit) * (1.f / fac);
     }
 };
 
@@ -838,13 +1014,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const
         const long long bh = (long long)b * p.Hkv + h;
         const long long row0 = bh * p.rows + r0;   // of the [B H Nq] query rows
 
+        const Rows<D> rows(p, bh);
         const int nsub = (ke - ku) * (kUnit / kSub);
         auto token = [&](int s) { return sp.token(ku + s / (kUnit / kSub)) + (s % (kUnit / kSub)) * kSub; };
         // Two stages ahead; the query rows load behind them.
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) {
             const int s = warp + i * kWarps;
-            load_stage<D, true>(p, ring + i * L::kStage, bh, s < nsub ? token(s) : 0, sp.len, s < nsub);
+            load_stage<D, true>(rows, ring + i * L::kStage, s < nsub ? token(s) : 0, sp.len, s < nsub);
         }
         Queries<D, BF16, NT> q;
         q.load(p, row0, nrows);
@@ -872,9 +1049,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const
             __syncwarp();   // the step's tokens are here, and every lane is done with the stage refilled below
             const int next = s + (kStages - 1) * kWarps;
             const int fill = st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1;
-            load_stage<D, true>(p, ring + fill * L::kStage, bh, next < nsub ? token(next) : 0, sp.len, next < nsub);
+            load_stage<D, true>(rows, ring + fill * L::kStage, next < nsub ? token(next) : 0, sp.len, next < nsub);
             const int t0 = token(s);
-            a.step(p, ring + st * L::kStage, q, t0, t0 < edge_lo || t0 + kSub > edge_hi, vis);
+            a.step(ring + st * L::kStage, q, t0, t0 < edge_lo || t0 + kSub > edge_hi, vis);
             st = st + 1 == kStages ? 0 : st + 1;
         }
         cp_wait<0>();
@@ -898,8 +1075,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const
                     jml[n] = make_float2(a.m[nt][e], l);
 #pragma unroll
                 for (int j = 0; j < L::kMTiles; ++j) {
-                    jo[n * S::kORow + out_channel<D>(r, j, 0)] = a.o[nt][j][e] + z;
-                    jo[n * S::kORow + out_channel<D>(r, j, 1)] = a.o[nt][j][e + 2] + z;
+                    jo[n * S::kORow + out_channel<D>(r, j, 0)] = a.value(j, a.o[nt][j][e]) + z;
+                    jo[n * S::kORow + out_channel<D>(r, j, 1)] = a.value(j, a.o[nt][j][e + 2]) + z;
                 }
             }
         __syncthreads();
@@ -1021,6 +1198,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
         const int ke = (int)((long long)sp.n - ku < u1 - u ? sp.n : ku + (u1 - u));
         const long long bh = (long long)b * p.Hkv + h;
         float *acc = p.acc + bh * p.C;
+        const Rows<D> rows(p, bh);
         const int nsub = (ke - ku) * (kUnit / kSub);
         auto token = [&](int s) { return sp.token(ku + s / (kUnit / kSub)) + (s % (kUnit / kSub)) * kSub; };
         for (int r0 = 0; r0 < p.rows; r0 += 8 * NT) {
@@ -1029,12 +1207,14 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
 #pragma unroll
             for (int i = 0; i < kStages - 1; ++i) {
                 const int s = warp + i * kWarps;
-                load_stage<D, false>(p, ring + i * L::kKeyStage, bh, s < nsub ? token(s) : 0, sp.len, s < nsub);
+                load_stage<D, false>(rows, ring + i * L::kKeyStage, s < nsub ? token(s) : 0, sp.len, s < nsub);
             }
             Queries<D, BF16, NT> q;
             q.load(p, bh * p.rows + r0, nrows);
             Bounds vis[NT][2];
-            float nl[NT][2];   // -LSE in log2 units, -inf for rows that are not there or see nothing
+            // -LSE in log2 units, to about 2^-32 in two parts; -inf for rows that are
+            // not there or see nothing
+            float nl[NT][2], nl2[NT][2];
             int edge_lo = 0, edge_hi = 0x7fffffff;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -1043,6 +1223,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
                     const int n = 8 * nt + 2 * c + e;
                     const float lse = n < nrows ? p.lse[bh * p.rows + r0 + n] : -INFINITY;
                     nl[nt][e] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+                    nl2[nt][e] = lse == -INFINITY ? 0.f : fmaf(-lse, kLog2e, -nl[nt][e]) - lse * kLog2eRest;
                     vis[nt][e] = bounds_of(p, sp.len, r0 + (n < nrows ? n : nrows - 1));
                     edge_lo = max(edge_lo, vis[nt][e].lo);
                     edge_hi = min(edge_hi, vis[nt][e].hi);
@@ -1058,7 +1239,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
                 __syncwarp();
                 const int next = s + (kStages - 1) * kWarps;
                 const int fill = st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1;
-                load_stage<D, false>(p, ring + fill * L::kKeyStage, bh, next < nsub ? token(next) : 0, sp.len, next < nsub);
+                load_stage<D, false>(rows, ring + fill * L::kKeyStage, next < nsub ? token(next) : 0, sp.len, next < nsub);
                 const int t0 = token(s);
                 const bool masked = t0 < edge_lo || t0 + kSub > edge_hi;
                 const uint32_t stage = ring + st * L::kKeyStage;
@@ -1066,17 +1247,22 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     float x[NT][4];
-                    scores<D, BF16, NT>(p, stage, stage + L::kCodes, mt, q, x);
+                    scores<D, BF16, NT>(stage, stage + L::kCodes, mt, q, x);
+                    if (masked) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!sees(vis[nt][e & 1], t0 + 16 * mt + r + 8 * (e >> 1)))
+                                    x[nt][e] = -INFINITY;
+                    }
+                    // (rows that are not there or see nothing: -inf, so 0)
                     sum[2 * mt] = sum[2 * mt + 1] = 0.f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float y = x[nt][e] + nl[nt][e & 1];
-                            const bool hidden = nl[nt][e & 1] == -INFINITY ||
-                                                (masked && !sees(vis[nt][e & 1], t0 + 16 * mt + r + 8 * (e >> 1)));
-                            sum[2 * mt + (e >> 1)] += hidden ? 0.f : ex2(y);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            sum[2 * mt + (e >> 1)] += ex2((x[nt][e] + nl[nt][e & 1]) + nl2[nt][e & 1]);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {

@@ -29,7 +29,7 @@ namespace {
 namespace cg = cooperative_groups;
 using fa_host::Arg;
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;         // the portable cluster size
@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     const int lo = p.sinks + (int)min((long long)rank * slice, (long long)M), cnt = min(slice, p.sinks + M - lo);
     const bool held = slice <= p.held;
     if (held) {
-#pragma unroll 4
+#pragma unroll 16
         for (int i = t; i < cnt; i += kSelThreads)
-            keys[i] = key_of(acc[lo + i]);
+            keys[i] = key_of(__ldg(acc + lo + i));
     }
     auto key_at = [&](int i) { return held ? keys[i] : key_of(acc[lo + i]); };
 
@@ -117,19 +117,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
                 atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
         }
         cluster.sync();
-        // Counts of the bins from the top, four to a thread, over all slices.
+        // Counts of the bins from the top, two to a thread, over all slices.
         constexpr int kPer = kBins / kSelThreads;
+        static_assert(kPer == 2, "one 8-byte load per histogram");
         const int top = kBins - 1 - t * kPer;   // this thread's highest bin
         int c[kPer] = {}, sum = 0;
-        for (int r = 0; r < CS; ++r) {
-            const int *h = cluster.map_shared_rank(hist, r);
-            const int4 v = *reinterpret_cast<const int4 *>(h + top - (kPer - 1));
-            c[0] += v.w;
-            c[1] += v.z;
-            c[2] += v.y;
-            c[3] += v.x;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            if (r < CS) {
+                const int2 v = *reinterpret_cast<const int2 *>(cluster.map_shared_rank(hist, r) + top - 1);
+                c[0] += v.y;
+                c[1] += v.x;
+            }
         }
-        static_assert(kPer == 4, "one 16-byte load per histogram");
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             sum += c[i];
@@ -212,38 +212,67 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     cluster.sync();   // no CTA leaves while another may still read its counts
 }
 
-// Rows of the kept tokens into the other cache, 16 bytes a thread, and their
-// weights (0 behind the last one).  Rows behind the last one are left as they
-// are.
+// Rows of the kept tokens into the other cache, 16 bytes a thread and row, and
+// their weights (0 behind the last one).  Rows behind the last one are left as
+// they are.  Each thread takes kGatherRows rows, so that as many reads at
+// places of the index's choosing are in flight.
+constexpr int kGatherRows = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) gather_kernel(const EvictParams p)
 {
     constexpr int kHalf = D / 32;        // 16-byte chunks of codes per row, K or V
     constexpr int kTpr = 2 * kHalf;
+    constexpr uint32_t kStep = 256 / kTpr;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the selection's index
-    const long long g = (long long)blockIdx.x * 256 + threadIdx.x;
-    const long long row = g / kTpr;      // of [B Hkv C2]
-    if (row >= p.BH * p.C2)
-        return;
-    const int part = (int)(g % kTpr);
-    const long long bh = row / p.C2;
-    const int d = (int)(row - bh * p.C2);
-    const int src = d < p.keep ? p.index[bh * p.keep + d] : -1;
-    if (src < 0) {
-        if (part == 0)
-            p.acc2[row] = 0.f;
-        return;
-    }
-    const long long from = bh * p.C + src;
+    const uint32_t rows = (uint32_t)(p.BH * p.C2);       // (below 2^31)
+    const uint32_t row0 = blockIdx.x * (kStep * kGatherRows) + threadIdx.x / kTpr;
+    const int part = threadIdx.x % kTpr;
     const bool v = part >= kHalf;
     const int j = v ? part - kHalf : part;
-    const uint8_t *c = (v ? p.vc : p.kc) + from * (D / 2) + j * 16;
-    uint8_t *c2 = (v ? p.vc2 : p.kc2) + row * (D / 2) + j * 16;
-    *reinterpret_cast<uint4 *>(c2) = __ldg(reinterpret_cast<const uint4 *>(c));
-    if (j == 0)
-        (v ? p.vp2 : p.kp2)[row] = __ldg((v ? p.vp : p.kp) + from);
-    if (part == 1)
-        p.acc2[row] = p.acc[from];
+    const uint8_t *codes = v ? p.vc : p.kc;
+    const uint32_t *params = v ? p.vp : p.kp;
+    long long from[kGatherRows];
+    uint4 x[kGatherRows];
+    uint32_t y[kGatherRows];
+    float w[kGatherRows];
+#pragma unroll
+    for (int k = 0; k < kGatherRows; ++k) {
+        const uint32_t row = row0 + k * kStep;
+        from[k] = -1;
+        if (row < rows) {
+            const uint32_t bh = row / (uint32_t)p.C2;
+            const int d = (int)(row - bh * p.C2);
+            const int src = d < p.keep ? __ldg(p.index + (size_t)bh * p.keep + d) : -1;
+            if (src >= 0)
+                from[k] = (long long)bh * p.C + src;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kGatherRows; ++k) {
+        if (from[k] >= 0) {
+            x[k] = __ldg(reinterpret_cast<const uint4 *>(codes + from[k] * (D / 2)) + j);
+            if (j == 0)
+                y[k] = __ldg(params + from[k]);
+            if (part == 1)
+                w[k] = __ldg(p.acc + from[k]);
+        } else {
+            w[k] = 0.f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kGatherRows; ++k) {
+        const uint32_t row = row0 + k * kStep;
+        if (row >= rows)
+            break;
+        if (part == 1)
+            p.acc2[row] = w[k];
+        if (from[k] < 0)
+            continue;
+        reinterpret_cast<uint4 *>((v ? p.vc2 : p.kc2) + (size_t)row * (D / 2))[j] = x[k];
+        if (j == 0)
+            (v ? p.vp2 : p.kp2)[row] = y[k];
+    }
 }
 
 // CTAs per row: more while every one of them still gets kMinSlice keys and
@@ -282,9 +311,9 @@ fa_status launch_evict(const EvictParams &q, int D, int sms, cudaStream_t s, int
         cudaGetLastError();
         return FA_ERR_CUDA;
     }
-    const long long threads = p.BH * p.C2 * (D / 16);
+    const long long per = 256 / (D / 16) * kGatherRows;   // rows per block
     cudaLaunchConfig_t cg2{};
-    cg2.gridDim = dim3((unsigned)((threads + 255) / 256));
+    cg2.gridDim = dim3((unsigned)((p.BH * p.C2 + per - 1) / per));
     cg2.blockDim = dim3(256);
     cg2.stream = s;
     cudaLaunchAttribute dep[1];

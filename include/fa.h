@@ -408,10 +408,9 @@ FA_API fa_status fa_cache_workspace(int H, int Hkv, int Nq, int D, size_t *bytes
  * (p < 0) gets O = 0 and LSE = -inf.
  * workspace : fa_cache_workspace bytes; its contents need no set-up.
  *
- * K and V enter as their integer codes, exact in 16 bits, with scale and
- * minimum applied outside the products in fp32; the softmax weights times V's
- * scale are split into two 16-bit parts, so nothing but the final result is
- * rounded to 16 bits.
+ * K and V enter the products as their integer codes, exact in 16 bits, with
+ * scale and minimum applied outside them in fp32; the softmax weight times V's
+ * scale is rounded to 11 bits for the product with V's codes.
  */
 FA_API fa_status fa_cache_fwd(const void *Q, const void *Kc, const void *Kp, const void *Vc, const void *Vp,
                               const int *lens, void *O, float *LSE, int B, int H, int Hkv, int Nq, int C, int D,

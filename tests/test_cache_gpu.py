@@ -4,17 +4,16 @@ _weights, _evict) against plain float64 implementations of their definitions.
 The packed format is compared bit for bit.  Attention and weights are compared
 with tolerances that follow the arithmetic:
 
-* scores.  x = scale (ks dot + (kmin - 16 ks) sum q), where dot = sum (16 +
-  code) q is formed in fp32 from exact products in chains of at most D + 8
-  additions and sum q likewise: |dx| <= (D + 8) 2^-24 A with A = scale (ks sum
-  (16 + code) |q| + |kmin - 16 ks| sum |q|), the sum of all magnitudes; twice
-  that covers the two products and the final additions.  `delta` below is its
-  largest value over a row's visible tokens.
-* weights p: relative error delta + 2^-21 (the exponential, 2^-22, and the
-  scaling by 2^x being exact); w = p vs as two bf16 parts: 2^-16 relative to
-  31 w in the worst case, as the offset of 16 is taken out of a sum of up to 31
-  w: 2^-11 of w |code - mean| at most where codes cancel; bounded here through
-  B = sum p (31 vs + |vmin - 16 vs|), the sum of all magnitudes in O's numerator.
+* scores.  x = scale (ks dot + kmin sum q), where dot = sum code q is formed in
+  fp32 from exact products (q scaled by a power of two) in chains of at most D
+  + 8 additions, and sum q likewise: |dx| <= (D + 8) 2^-24 A with A = scale (ks
+  sum code |q| + |kmin| sum |q|), the sum of all magnitudes; twice that covers
+  the products and the final additions.  `delta` below is its largest value
+  over a row's visible tokens.
+* weights: p has the relative error delta + 2^-21 (the exponential); w = p vs
+  is rounded to fp16, 2^-11 relative, as it enters the product with the codes:
+  2^-11 of sum p vs code, part of B = sum p (vs code + |vmin|), the sum of all
+  magnitudes in O's numerator.
 * sums over n tokens in fp32: each chain has at most n / 8 + 64 additions
   (eight warps, then the joins): (n / 8 + 64) 2^-24 of the magnitudes.
 * the result: half a unit of its type, finfo(t).eps / 2.
@@ -64,7 +63,7 @@ def unpack64(codes, params):
     return c * params[..., 0:1].double() + params[..., 1:2].double()
 
 
-def random_cache(B, Hkv, C, D, dtype, seed, poison=False):
+def random_cache(B, Hkv, C, D, dtype, seed):
     """A cache of plausible rows (keys with a few large channels)."""
     g = _gen(seed)
     k = torch.randn((B, Hkv, C, D), generator=g, device="cuda")
@@ -222,15 +221,15 @@ def reference(q, cache, lens, left, sinks, scale):
                         continue
                     x = q[b, h * G + g, i].double()
                     s = (k[at] @ x) * scale
-                    mag = scale * (ks[at] * ((16 + codes[at]) @ x.abs()) + (kmin - 16 * ks)[at].abs() * x.abs().sum())
+                    mag = scale * (ks[at] * (codes[at] @ x.abs()) + kmin[at].abs() * x.abs().sum())
                     d = 2 * (D + 8) * 2.0 ** -24 * float(mag.max())
                     L = torch.logsumexp(s, 0)
                     p = torch.exp(s - L)
                     o[b, h * G + g, i] = p @ v[at]
                     lse[b, h * G + g, i] = L
                     delta[b, h * G + g, i] = d
-                    B_ = float(p @ (31 * vs + (vmin - 16 * vs).abs())[at])
-                    o_tol[b, h * G + g, i] = B_ * (2.0 ** -16 + (n / 8 + 64) * 2.0 ** -24) + (
+                    part = p @ (v - vmin[:, None])[at]
+                    o_tol[b, h * G + g, i] = part * 2.0 ** -11 + (part + p @ vmin[at].abs()) * (n / 8 + 64) * 2.0 ** -24 + (
                         2 * (d + 2.0 ** -21) * (p @ v[at].abs()))
                     w[b, h, at] += p
                     w_tol[b, h, at] += p * (d + 2.0 ** -20 + abs(float(L)) * 2.0 ** -22)
