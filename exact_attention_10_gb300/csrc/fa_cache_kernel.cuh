@@ -135,12 +135,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 // the subnormal code * 2^-24 (bits 0..3) or 16 code * 2^-24 (bits 4..7), exact.
 // So one logic operation unpacks two codes, and a word of eight takes one
 // shift besides -- the integer pipe, at half the rate of the others, is what
-// unpacking is bound by.  V's codes go to the tensor core like that.  K's are
-// brought to (code - 7.5) 2^-9 by one packed multiply-add more, exact again:
-// the tensor core aligns a subnormal's product by its nominal exponent, which
-// cuts low bits off the sum (4e-7 of a weight instead of 1e-6 with it,
-// against float64), and codes centred at their middle keep the sums as small
-// as the scores.
+// unpacking is bound by.  The attention's go to the tensor core like that,
+// the factor 16 taken out of the other operand or the result.  The weights,
+// an fp32 result, bring K's to (code - 7.5) 2^-9 by one packed multiply-add
+// more, exact again: the tensor core aligns a subnormal's product by its
+// nominal exponent, which cuts low bits off the sum, and codes centred at
+// their middle keep the sums as small as the scores (a weight's error against
+// float64: 2.8e-7 with it, 1.1e-6 without).
 constexpr uint32_t kEven = 0x000F000Fu, kOdd = 0x00F000F0u;
 constexpr float kCodeUnit = 16777216.f;   // 2^24
 
@@ -231,7 +232,7 @@ __device__ __forceinline__ RowScale row_scale(float mn, float mx)
     r.inv = __frcp_rn(r.sc);
     // a scale so much smaller than range / 15 that codes pass 15, or a
     // minimum so small that x - mn rounds
-    r.exact = range * r.inv > 15.49f || (mn != 0.f && fabsf(mn) < fabsf(mx) * 3.0e-5f);
+    r.exact = range * r.inv > 15.49f || (mn != 0.f && fabsf(mn) < fabsf(mx) * (BF16 ? 0x1p-15f : 0x1p-12f));
     return r;
 }
 
@@ -253,14 +254,14 @@ __device__ __noinline__ uint32_t code_of(float x, float mn, float sc, float inv)
     return (uint32_t)fminf(fmaxf(q, 0.f), 15.f);
 }
 
-// The codes of eight values.  Where x - mn is exact (values of eleven bits at
-// most whose magnitudes are within 2^13 of one another, or zero: `exact` false),
-// the quotient a / sc corrected once by its residual -- the final step of
-// Markstein's division -- is a half-integer only if the true one is, so that
-// rounding it half to even by adding and taking off 1.5 * 2^23 gives the code.
-// (Such values are not rare: 16-bit values over a 16-bit scale hit a border
-// about once in 300.)  Four codes at a time are summed as code * 16^i in one
-// float, exact in 16 bits.
+// The codes of eight values.  Where x - mn is exact (fp16: magnitudes within
+// 2^12 of one another, bf16: 2^15: `exact` false), the quotient a / sc
+// corrected once by its residual -- the final step of Markstein's division --
+// is a half-integer only if the true one is, so that rounding it half to even
+// by adding and taking off 1.5 * 2^23 gives the code.  (Such values are not
+// rare: 16-bit values over a 16-bit scale hit a border about once in 300.)
+// Four codes at a time are summed as code * 16^i in one float, exact in 16
+// bits.  With `exact`, values next to a border are decided by code_of.
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], const RowScale &r, bool exact)
 {
     constexpr float kRound = 12582912.f;
@@ -273,10 +274,19 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8], const RowScale
     }
     uint32_t w = (uint32_t)s[0] | ((uint32_t)s[1] << 16);
     if (exact) {
-        w = 0;
+        float far = 0.f, top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w |= code_of(x[i], r.mn, r.sc, r.inv) << (4 * i);
+        for (int i = 0; i < 8; ++i) {
+            const float f = (x[i] - r.mn) * r.inv;
+            far = fmaxf(far, fabsf(f - ((f + kRound) - kRound)));
+            top = fmaxf(top, f);
+        }
+        if (far > 0.4999f || top > 15.49f) {
+            w = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w |= code_of(x[i], r.mn, r.sc, r.inv) << (4 * i);
+        }
     }
     return w;
 }
@@ -344,7 +354,7 @@ __device__ __forceinline__ void append_row(const uint4 (&x4)[2], int part, uint3
         }
         // a value far smaller than the minimum's magnitude: x - mn may round
         const float least = fminf(to_float<BF16>(small & 0xffffu), to_float<BF16>(small >> 16));
-        const bool exact = r.exact || least * r.k < fabsf(r.mn) * 1.2e-4f;
+        const bool exact = r.exact || least * r.k < fabsf(r.mn) * (BF16 ? 0x1p-15f : 0x1p-12f);
         w = make_uint2(codes_of(x[0], r, exact), codes_of(x[1], r, exact));
     }
     *reinterpret_cast<uint2 *>(codes + part * 8) = w;
@@ -626,13 +636,14 @@ __device__ __forceinline__ uint4 lds128(uint32_t a)
 // The query rows as B fragments (16 channels x 8 rows each), in the channel
 // order in which K's codes come out of their words: lane (r = lane / 4, c =
 // lane % 4) holds row 8 nt + r, channels [c D/4, (c + 1) D/4); word w of them
-// gives two fragments, (0, 4 | 1, 5) and (2, 6 | 3, 7).  As fp16: a row is multiplied by the power of two that brings
+// gives two fragments, (0, 4 | 1, 5) and (2, 6 | 3, 7), the odd channels
+// divided by 16 where K's codes are taken as they are (not CENTRED).  As fp16: a row is multiplied by the power of two that brings
 // its largest element to [2^14, 2^15), so a bf16 or fp16 element is exact
 // unless it is 2^-24 of the largest or less, and then off by 2^-40 of it.
 // `mul` takes the power, the codes' unit and the softmax scale (log2 units)
 // out again; `sum` is sum_d q_d in those units; both for the two rows
 // (columns of S^T) of this lane.
-template <int D, bool BF16, int NT>
+template <int D, bool BF16, int NT, bool CENTRED>
 struct Queries {
     using L = Layout<D>;
     uint32_t f[NT][L::kWords * 2][2];
@@ -668,15 +679,15 @@ struct Queries {
             // (queries of 2^114 and more overflow fp16, and their rows end as NaN)
             int e = mx > 0.f ? 14 - (int)((__float_as_uint(mx) >> 23) & 255u) + 127 : 0;
             e = e > 100 ? 100 : (e < -100 ? -100 : e);
-            const float up = exp2i(e);
+            const float up = exp2i(e), up1 = CENTRED ? up : up * 0.0625f;
 #pragma unroll
             for (int w = 0; w < L::kWords; ++w) {
                 f[nt][2 * w][0] = pack_f16(x[w][0] * up, x[w][4] * up);
-                f[nt][2 * w][1] = pack_f16(x[w][1] * up, x[w][5] * up);
+                f[nt][2 * w][1] = pack_f16(x[w][1] * up1, x[w][5] * up1);
                 f[nt][2 * w + 1][0] = pack_f16(x[w][2] * up, x[w][6] * up);
-                f[nt][2 * w + 1][1] = pack_f16(x[w][3] * up, x[w][7] * up);
+                f[nt][2 * w + 1][1] = pack_f16(x[w][3] * up1, x[w][7] * up1);
             }
-            const float back = p.qk2 * exp2i(9 - e);
+            const float back = p.qk2 * exp2i((CENTRED ? 9 : 24) - e);
             s *= p.qk2;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {   // rows 2c and 2c + 1
@@ -687,11 +698,12 @@ struct Queries {
     }
 };
 
-// Scores of 16 tokens (rows 16 mt .. of the stage) in log2 units: x[nt][0, 1]
-// token r, columns 2c and 2c + 1; x[nt][2, 3] token r + 8.
-template <int D, bool BF16, int NT>
-__device__ __forceinline__ void scores(uint32_t stage, uint32_t par, int mt, const Queries<D, BF16, NT> &q,
-                                       float (&x)[NT][4])
+// Scores of 16 tokens (rows 16 mt .. of the stage) in log2 units, less the
+// column's `ref`: x[nt][0, 1] token r, columns 2c and 2c + 1; x[nt][2, 3]
+// token r + 8.
+template <int D, bool BF16, int NT, bool CENTRED>
+__device__ __forceinline__ void scores(uint32_t stage, uint32_t par, int mt, const Queries<D, BF16, NT, CENTRED> &q,
+                                       const float (&ref)[NT][2], float (&x)[NT][4])
 {
     using L = Layout<D>;
     const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
@@ -713,8 +725,10 @@ __device__ __forceinline__ void scores(uint32_t stage, uint32_t par, int mt, con
 #pragma unroll
     for (int w = 0; w < L::kWords; ++w) {
         const uint32_t ya = wa[w] >> 8, yb = wb[w] >> 8;
-        const uint32_t lo[4] = {centred_even(wa[w]), centred_even(wb[w]), centred_odd(wa[w]), centred_odd(wb[w])};
-        const uint32_t hi[4] = {centred_even(ya), centred_even(yb), centred_odd(ya), centred_odd(yb)};
+        auto even = [](uint32_t v) { return CENTRED ? centred_even(v) : v & kEven; };
+        auto odd = [](uint32_t v) { return CENTRED ? centred_odd(v) : v & kOdd; };
+        const uint32_t lo[4] = {even(wa[w]), even(wb[w]), odd(wa[w]), odd(wb[w])};
+        const uint32_t hi[4] = {even(ya), even(yb), odd(ya), odd(yb)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             mma(s[nt], lo, q.f[nt][2 * w][0], q.f[nt][2 * w][1]);
@@ -723,13 +737,17 @@ __device__ __forceinline__ void scores(uint32_t stage, uint32_t par, int mt, con
     }
     const uint32_t pa = lds32(par + (uint32_t)(16 * mt + r) * 4), pb = lds32(par + (uint32_t)(16 * mt + r + 8) * 4);
     const float sa = to_float<BF16>(pa & 0xffffu), sb = to_float<BF16>(pb & 0xffffu);
-    const float za = fmaf(7.5f, sa, to_float<BF16>(pa >> 16)), zb = fmaf(7.5f, sb, to_float<BF16>(pb >> 16));
+    float za = to_float<BF16>(pa >> 16), zb = to_float<BF16>(pb >> 16);
+    if (CENTRED) {
+        za = fmaf(7.5f, sa, za);
+        zb = fmaf(7.5f, sb, zb);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] = fmaf(s[nt][0] * q.mul[nt][0], sa, za * q.sum[nt][0]);
-        x[nt][1] = fmaf(s[nt][1] * q.mul[nt][1], sa, za * q.sum[nt][1]);
-        x[nt][2] = fmaf(s[nt][2] * q.mul[nt][0], sb, zb * q.sum[nt][0]);
-        x[nt][3] = fmaf(s[nt][3] * q.mul[nt][1], sb, zb * q.sum[nt][1]);
+        x[nt][0] = fmaf(s[nt][0] * q.mul[nt][0], sa, fmaf(za, q.sum[nt][0], -ref[nt][0]));
+        x[nt][1] = fmaf(s[nt][1] * q.mul[nt][1], sa, fmaf(za, q.sum[nt][1], -ref[nt][1]));
+        x[nt][2] = fmaf(s[nt][2] * q.mul[nt][0], sb, fmaf(zb, q.sum[nt][0], -ref[nt][0]));
+        x[nt][3] = fmaf(s[nt][3] * q.mul[nt][1], sb, fmaf(zb, q.sum[nt][1], -ref[nt][1]));
     }
 }
 
@@ -764,11 +782,13 @@ __device__ __forceinline__ bool sees(const Bounds &v, int t)
 // w = p vs as one fp16 operand: w is multiplied by the warp's power of two
 // `fac`, which keeps the largest vs so far in [2^5, 2^6), so with p <= 2^8 it
 // stays in fp16's range, and a token's 11 significand bits are whole down to
-// 2^-20 of that.  What the rounding of w takes off or adds is given back with
-// the middle code, 7.5 (w - fp16(w)) in z, so that its error meets the codes'
-// distance from their middle only: it then costs what rounding p to 16 bits
-// costs the 16-bit kernels' product with V, in either type no more than the
-// result's own rounding.  l is summed from the unrounded p.
+// 2^-20 of that.  For an fp16 result, whose own rounding is as fine, what the
+// rounding of w takes off or adds is given back with the middle code, 7.5 (w -
+// fp16(w)) in z, so that its error meets the codes' distance from their middle
+// only and costs what rounding p to 16 bits costs the 16-bit kernels' product
+// with V (error of the result against float64: 2.4e-4 with it, 3.7e-4
+// without, 2.1e-4 from the result's rounding alone); next to bf16's rounding
+// it does not show.  l is summed from the unrounded p.
 template <int D, bool BF16, int NT>
 struct Attend {
     using L = Layout<D>;
@@ -792,15 +812,23 @@ struct Attend {
         }
     }
 
-    // 32 tokens from t0 on, in `stage`.
-    __device__ void step(uint32_t stage, const Queries<D, BF16, NT> &q, int t0, bool masked, const Bounds (&vis)[NT][2])
+    // 32 tokens from t0 on, in `stage`; MASKED: some are hidden from some row.
+    template <bool MASKED>
+    __device__ __forceinline__ void step(uint32_t stage, const Queries<D, BF16, NT, false> &q, int t0,
+                                         const Bounds (&vis)[NT][2])
     {
         const int lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
         const uint32_t par = stage + 2 * L::kCodes;
+        float ref[NT][2];   // what the scores below are relative to
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                ref[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
         float x[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
-            scores<D, BF16, NT>(stage, par, mt, q, x[mt]);
+            scores<D, BF16, NT, false>(stage, par, mt, q, ref, x[mt]);
         float vs[4], vm[4];   // scale and minimum of tokens r, r + 8, r + 16, r + 24
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -808,8 +836,8 @@ struct Attend {
             vs[k] = to_float<BF16>(w & 0xffffu);
             vm[k] = to_float<BF16>(w >> 16);
         }
-        uint32_t hid = 0;   // bit 2 k' + e ...: (token, column) pairs that are hidden
-        if (masked) {
+        uint32_t hid = 0;   // (token, column) pairs that are hidden
+        if (MASKED) {
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -825,18 +853,17 @@ struct Attend {
         // at the first visible token), and the factor of w where a scale has
         // outgrown it.
         bool up = false;
-        float mx[NT][2], big = 0.f;
+        float mx[NT][2], big = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 mx[nt][e] = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
-                up |= mx[nt][e] > m[nt][e] + kSlack;
+                up |= mx[nt][e] > (m[nt][e] == -INFINITY ? -INFINITY : kSlack);
             }
-        big = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
         up |= big * fac >= 64.f;
         if (__any_sync(0xffffffffu, up)) {
-            if (masked) {   // only rows that some query sees, and finite ones, move the factor
+            if (MASKED) {   // only rows that some query sees move the factor
                 big = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -844,15 +871,18 @@ struct Attend {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         seen |= ((hid >> (((k >> 1) * NT + nt) * 4 + 2 * (k & 1))) & 3u) != 3u;
-                    if (seen && vs[k] < INFINITY)
-                        big = fmaxf(big, vs[k]);
+                    big = fmaxf(big, seen ? vs[k] : 0.f);
                 }
             }
+            big = big < INFINITY ? big : 0.f;   // (and an infinite scale none but its own token's weight)
 #pragma unroll
             for (int s = 4; s < 32; s *= 2)
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
+#pragma unroll
+            for (int s = 1; s < 4; s *= 2)   // (masked: the columns of a token's lanes differ)
+                big = MASKED ? fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s)) : big;
             float df = 1.f;
-            if (big * fac >= 64.f && big < INFINITY) {
+            if (big * fac >= 64.f) {
                 const int e = 5 + 127 - (int)(__float_as_uint(big) >> 23);   // big in [2^(5 - e), 2^(6 - e))
                 const float now = exp2i(e > 100 ? 100 : (e < -125 ? -125 : e));
                 df = now / fac;   // a power of two, or 0 from 2^100
@@ -865,9 +895,12 @@ struct Attend {
 #pragma unroll
                     for (int s = 4; s < 32; s *= 2)
                         mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], s));
-                    const float mn = fmaxf(m[nt][e], mx[nt][e]);
-                    const float al = mn == m[nt][e] ? 1.f : ex2(m[nt][e] - mn);   // 0 from m = -inf
-                    m[nt][e] = mn;
+                    const bool first = m[nt][e] == -INFINITY;
+                    // how far the reference moves (from ref = 0 at first: to the maximum itself)
+                    const float by = mx[nt][e] == -INFINITY ? 0.f : (first ? mx[nt][e] : fmaxf(mx[nt][e], 0.f));
+                    const float al = first ? 0.f : ex2(-by);
+                    if (mx[nt][e] > -INFINITY)
+                        m[nt][e] = ref[nt][e] + by;
                     l[nt][e] *= al;
                     z[nt][e] *= al;
 #pragma unroll
@@ -875,15 +908,14 @@ struct Attend {
                         o[nt][j][e] *= al * df;
                         o[nt][j][e + 2] *= al * df;
                     }
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        x[mt][nt][e] -= by;
+                        x[mt][nt][e + 2] -= by;
+                    }
                 }
         }
         const float mid = 7.5f * (1.f / fac);
-        float mu[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                mu[nt][e] = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
             uint32_t wf[NT][2];   // w as B fragments
@@ -893,20 +925,25 @@ struct Attend {
                 float w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float pr = ex2(x[mt][nt][e] - mu[nt][e & 1]);
+                    const float pr = ex2(x[mt][nt][e]);
                     l[nt][e & 1] += pr;
                     w[e] = pr * ((e >> 1) ? wb : wa);
-                    float zt = pr * vm[2 * mt + (e >> 1)];
-                    if (masked && ((hid >> ((mt * NT + nt) * 4 + e)) & 1u))
-                        w[e] = zt = 0.f;   // (a hidden token weighs nothing whatever its row holds)
-                    z[nt][e & 1] += zt;
+                    if (MASKED) {   // a hidden token weighs nothing whatever its row holds
+                        const bool h = (hid >> ((mt * NT + nt) * 4 + e)) & 1u;
+                        w[e] = h ? 0.f : w[e];
+                        z[nt][e & 1] = h ? z[nt][e & 1] : fmaf(pr, vm[2 * mt + (e >> 1)], z[nt][e & 1]);
+                    } else {
+                        z[nt][e & 1] = fmaf(pr, vm[2 * mt + (e >> 1)], z[nt][e & 1]);
+                    }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t u = pack_f16(w[2 * h], w[2 * h + 1]);
                     wf[nt][h] = transpose8(u);
-                    z[nt][0] = fmaf(w[2 * h] - to_float<false>(u & 0xffffu), mid, z[nt][0]);
-                    z[nt][1] = fmaf(w[2 * h + 1] - to_float<false>(u >> 16), mid, z[nt][1]);
+                    if (!BF16) {
+                        z[nt][0] = fmaf(w[2 * h] - to_float<false>(u & 0xffffu), mid, z[nt][0]);
+                        z[nt][1] = fmaf(w[2 * h + 1] - to_float<false>(u >> 16), mid, z[nt][1]);
+                    }
                 }
             }
             // V^T as the A operand: for channel words of this lane, tokens
@@ -1023,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const
             const int s = warp + i * kWarps;
             load_stage<D, true>(rows, ring + i * L::kStage, s < nsub ? token(s) : 0, sp.len, s < nsub);
         }
-        Queries<D, BF16, NT> q;
+        Queries<D, BF16, NT, false> q;
         q.load(p, row0, nrows);
         Bounds vis[NT][2];
         int edge_lo = 0, edge_hi = 0x7fffffff;   // tokens in [edge_lo, edge_hi) are seen by every row
@@ -1051,7 +1088,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const
             const int fill = st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1;
             load_stage<D, true>(rows, ring + fill * L::kStage, next < nsub ? token(next) : 0, sp.len, next < nsub);
             const int t0 = token(s);
-            a.step(ring + st * L::kStage, q, t0, t0 < edge_lo || t0 + kSub > edge_hi, vis);
+            if (t0 < edge_lo || t0 + kSub > edge_hi)
+                a.template step<true>(ring + st * L::kStage, q, t0, vis);
+            else
+                a.template step<false>(ring + st * L::kStage, q, t0, vis);
             st = st + 1 == kStages ? 0 : st + 1;
         }
         cp_wait<0>();
@@ -1209,8 +1249,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
                 const int s = warp + i * kWarps;
                 load_stage<D, false>(rows, ring + i * L::kKeyStage, s < nsub ? token(s) : 0, sp.len, s < nsub);
             }
-            Queries<D, BF16, NT> q;
+            Queries<D, BF16, NT, true> q;
             q.load(p, bh * p.rows + r0, nrows);
+            const float none[NT][2] = {};
             Bounds vis[NT][2];
             // -LSE in log2 units, to about 2^-32 in two parts; -inf for rows that are
             // not there or see nothing
@@ -1247,7 +1288,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     float x[NT][4];
-                    scores<D, BF16, NT>(stage, stage + L::kCodes, mt, q, x);
+                    scores<D, BF16, NT, true>(stage, stage + L::kCodes, mt, q, none, x);
                     if (masked) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)

@@ -64,19 +64,33 @@ __device__ __forceinline__ int clamped(int n, int C)
     return n < 0 ? 0 : (n > C ? C : n);
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p)
+__device__ __forceinline__ int warp_scan(int v, int lane)   // inclusive
+{
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, v, m);
+        if (lane >= m)
+            v += u;
+    }
+    return v;
+}
+
+// One cluster per sequence and key head.  Two CTAs fit an SM (32 registers);
+// one histogram per digit, so that a digit needs one cluster barrier.
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ uint32_t keys[];   // [held]
-    __shared__ __align__(16) int hist[kBins];
+    __shared__ __align__(16) int hist[3][kBins];
     __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_count[2], s_found[2];
+    static_assert(kSelWarps == 32, "one lane per warp's sum");
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const long long bh = blockIdx.x / CS;
+    const uint32_t bh = blockIdx.x / CS;
     const int t = threadIdx.x, lane = t % 32, warp = t / 32;
     const int n = clamped(p.lens[bh / p.Hkv], p.C);
-    const float *acc = p.acc + bh * p.C;
-    int *index = p.index + bh * p.keep;
+    const float *acc = p.acc + (size_t)bh * p.C;
+    int *index = p.index + (size_t)bh * p.keep;
     if (rank == 0 && t == 0 && bh % p.Hkv == 0)
         p.lens2[bh / p.Hkv] = n < p.keep ? n : p.keep;
     if (n <= p.keep) {   // (the whole cluster leaves)
@@ -96,67 +110,71 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     const int slice = (M + CS - 1) / CS;
     const int lo = p.sinks + (int)min((long long)rank * slice, (long long)M), cnt = min(slice, p.sinks + M - lo);
     const bool held = slice <= p.held;
-    if (held) {
-#pragma unroll 16
-        for (int i = t; i < cnt; i += kSelThreads)
-            keys[i] = key_of(__ldg(acc + lo + i));
+    for (int i = t; i < 3 * kBins; i += kSelThreads)
+        (&hist[0][0])[i] = 0;
+    __syncthreads();
+    // The keys, and the histogram of their first digit as they come.
+    constexpr int kBatch = 8;   // loads in flight per thread
+    for (int i0 = 0; i0 < cnt; i0 += kBatch * kSelThreads) {
+        float x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kSelThreads + t;
+            x[u] = i < cnt ? __ldg(acc + lo + i) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kSelThreads + t;
+            if (i < cnt) {
+                const uint32_t key = key_of(x[u]);
+                if (held)
+                    keys[i] = key;
+                atomicAdd(&hist[0][key >> 21], 1);
+            }
+        }
     }
-    auto key_at = [&](int i) { return held ? keys[i] : key_of(acc[lo + i]); };
+    auto key_at = [&](int i) { return held ? keys[i] : key_of(__ldg(acc + lo + i)); };
 
     uint32_t prefix = 0;   // the digits found so far
     int left = k;          // candidates still to take among the keys that share them
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-        for (int i = t; i < kBins; i += kSelThreads)
-            hist[i] = 0;
-        __syncthreads();   // (and the keys are written)
-        for (int i = t; i < cnt; i += kSelThreads) {
-            const uint32_t key = key_at(i);
-            if (pass == 0 || (key >> (shift + bits)) == prefix)
-                atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1);
-        }
+        if (pass > 0)
+            for (int i = t; i < cnt; i += kSelThreads) {
+                const uint32_t key = key_at(i);
+                if ((key >> (shift + bits)) == prefix)
+                    atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
+            }
         cluster.sync();
         // Counts of the bins from the top, two to a thread, over all slices.
         constexpr int kPer = kBins / kSelThreads;
         static_assert(kPer == 2, "one 8-byte load per histogram");
         const int top = kBins - 1 - t * kPer;   // this thread's highest bin
-        int c[kPer] = {}, sum = 0;
+        int c0 = 0, c1 = 0;
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r) {
             if (r < CS) {
-                const int2 v = *reinterpret_cast<const int2 *>(cluster.map_shared_rank(hist, r) + top - 1);
-                c[0] += v.y;
-                c[1] += v.x;
+                const int2 v = *reinterpret_cast<const int2 *>(cluster.map_shared_rank(&hist[pass][0], r) + top - 1);
+                c0 += v.y;
+                c1 += v.x;
             }
         }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            sum += c[i];
-        int inc = sum;
-#pragma unroll
-        for (int m = 1; m < 32; m *= 2) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, m);
-            if (lane >= m)
-                inc += v;
-        }
+        const int inc = warp_scan(c0 + c1, lane);
         if (lane == 31)
             s_gt[warp] = inc;
         __syncthreads();
-        int before = inc - sum;
-        for (int w = 0; w < warp; ++w)
-            before += s_gt[w];
-        if (before < left && before + sum >= left) {   // exactly one thread: the counts add up to at least `left`
-            int i = 0;
-            while (before + c[i] < left)
-                before += c[i++];
-            s_found[0] = top - i;
-            s_found[1] = left - before;
+        const int sums = warp_scan(s_gt[lane], lane);
+        const int base = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+        const int before = inc - c0 - c1 + (warp > 0 ? base : 0);
+        if (before < left && before + c0 + c1 >= left) {   // exactly one thread: the counts add up to at least `left`
+            const bool second = before + c0 < left;
+            s_found[0] = second ? top - 1 : top;
+            s_found[1] = left - before - (second ? c0 : 0);
         }
         __syncthreads();
         prefix = (prefix << bits) | (uint32_t)s_found[0];
         left = s_found[1];
-        cluster.sync();   // every histogram has been read
     }
     // prefix is the k-th largest key; `left` of the keys equal to it are taken.
 
@@ -177,25 +195,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
         s_eq[warp] = eq;
     }
     __syncthreads();
-    if (t == 0) {
-        int a = 0, b = 0;
-        for (int w = 0; w < kSelWarps; ++w) {
-            a += s_gt[w];
-            b += s_eq[w];
-        }
-        s_count[0] = a;
-        s_count[1] = b;
+    const int all_gt = warp_scan(s_gt[lane], lane), all_eq = warp_scan(s_eq[lane], lane);
+    int n_gt = __shfl_sync(0xffffffffu, all_gt, warp) - gt, n_eq = __shfl_sync(0xffffffffu, all_eq, warp) - eq;
+    if (t == 31) {
+        s_count[0] = all_gt;
+        s_count[1] = all_eq;
     }
     cluster.sync();
-    int n_gt = 0, n_eq = 0;   // taken for certain, and equal, before this warp's part
-    for (int r = 0; r < rank; ++r) {
+    for (int r = 0; r < rank; ++r) {   // taken for certain, and equal, in the slices before
         const int *o = cluster.map_shared_rank(s_count, r);
         n_gt += o[0];
         n_eq += o[1];
-    }
-    for (int w = 0; w < warp; ++w) {
-        n_gt += s_gt[w];
-        n_eq += s_eq[w];
     }
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = w0; i0 < w1; i0 += 32) {
