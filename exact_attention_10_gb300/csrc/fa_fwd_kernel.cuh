@@ -550,6 +550,7 @@ struct MmaIssuer {
     using C = Cfg<D>;
     static constexpr uint32_t kIdescQK = instr_desc_f16(BF16, kBM, kBN, false);   // S = Q K^T, both K-major
     static constexpr uint32_t kIdescPV = instr_desc_f16(BF16, kBM, D, true);      // O += P V, V is MN-major
+    static constexpr uint32_t kIdescFew = instr_desc_f16(BF16, kBM, kSchedFewSinks, false);   // S of a few sinks alone
     int w;               // Q tile served by this warp
     uint32_t q_lo;       // descriptor lower word of Q tile w in Q buffer 0
     uint32_t k_lo;       // descriptor lower word of K in stage 0, K-major (leading byte offset unused)
@@ -599,7 +600,8 @@ struct MmaIssuer {
 
     // S_w = Q_w K^T over D/16 k-steps: K-major operands advance 32 bytes per
     // step inside a 128-byte swizzle row and 16 KB per 64-column box.
-    __device__ bool issue_s(int st)
+    // `few`: of the first 16 keys of the tile alone.
+    __device__ bool issue_s(int st, bool few = false)
     {
         if (SEP && n_s > 0) {   // the softmax has loaded the previous S_w
             if (!warp_wait(b.s_free(w), (n_s - 1) & 1u, c, kSiteMmaSFree))
@@ -611,7 +613,8 @@ struct MmaIssuer {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = (uint32_t)((kk / 4) * (C::kBoxBytes >> 4) + (kk % 4) * 2);
-                ptx::mma_ss(tS, desc_from_lo(q_cur + off), desc_from_lo(ka + off), kIdescQK, kk > 0 ? 1u : 0u);
+                ptx::mma_ss(tS, desc_from_lo(q_cur + off), desc_from_lo(ka + off), few ? kIdescFew : kIdescQK,
+                            kk > 0 ? 1u : 0u);
             }
             ptx::mma_commit(b.s_full(w));
         }
@@ -622,7 +625,8 @@ struct MmaIssuer {
 
     // O_w (+)= P_w V over 128/16 k-steps: P from TMEM (8 columns per step),
     // V MN-major: 16 key rows = 2 KB per step.
-    __device__ bool issue_pv(int st, bool accumulate)
+    // `few`: of the first 16 keys alone (one k-step).
+    __device__ bool issue_pv(int st, bool accumulate, bool few = false)
     {
         if (!accumulate) {   // first P.V of a CTA tile overwrites O_w: the epilogue must have read it
             if (n_t > 0 && !warp_wait(b.o_free(w), (n_t - 1) & 1u, c, kSiteMmaOFree))
@@ -636,8 +640,9 @@ struct MmaIssuer {
         if (ptx::elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
-                ptx::mma_ts(tO, tP + kk * 8, desc_from_lo(va + kk * (2048 >> 4)), kIdescPV,
-                            (accumulate || kk > 0) ? 1u : 0u);
+                if (kk == 0 || !few)
+                    ptx::mma_ts(tO, tP + kk * 8, desc_from_lo(va + kk * (2048 >> 4)), kIdescPV,
+                                (accumulate || kk > 0) ? 1u : 0u);
             ptx::mma_commit(b.o_done(w));
         }
         __syncwarp();
@@ -713,6 +718,96 @@ __device__ bool tile_interleaved(MmaIssuer<D, BF16, false> &m0, MmaIssuer<D, BF1
     return true;
 }
 
+// A CTA's parts under a window with sinks, their steps as one sequence: a
+// window's tiles are a dozen steps long, so their ends count.  The orders are
+// those of tile() and tile_interleaved(), carried across from one part to the
+// next: the next part's first S is issued before the last P.V of this one (in
+// the interleaved order before Q tile 1's), and the Q buffer is given back as
+// soon as the part's last S has read it, so that the next Q is on its way
+// while the last P.V runs.
+template <int D, bool BF16, bool SPLIT, bool SEP, class P>
+__device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, BF16, SEP> &m1, int w)
+{
+    using C = Cfg<D>;
+    const Bars<D> b = m.b;
+    int step = 0, it = 0;   // K/V steps and parts so far
+    int prev = -1;          // stage of the step whose P.V (interleaved: Q tile 1's) is still to come, -1: none
+    bool pv = false, acc = false, pfew = false;   // whether this warp's tile has that P.V, adds to O, and is of few sinks
+    auto finish = [&]() -> bool {   // that P.V, then its stage
+        if (SEP) {
+            if (C::kSplitKV && !m.v_wait(step - 1))
+                return false;
+            if (pv && !m.issue_pv(prev, acc, pfew))
+                return false;
+            if (C::kSplitKV)
+                m.release_v(prev);
+            else
+                m.release(prev);
+        } else {
+            if (pv && !m1.issue_pv(prev, acc, pfew))
+                return false;
+            m.release(prev);
+        }
+        return true;
+    };
+    PartIter parts;
+    parts.init_t<SPLIT>(p.sch, blockIdx.x);
+    Part pt;
+    while (parts.next_t<SPLIT, true>(p.sch, pt)) {
+        int bh, ct;
+        sched_decode_t<SPLIT, true>(p.sch, pt.tile, bh, ct);
+        const int n0 = part_steps(pt, sched_kv_tiles_t<true>(p.sch, ct, 0));
+        const int n1 = part_steps(pt, sched_kv_tiles_t<true>(p.sch, ct, 1));
+        const int n = pt.ke - pt.kb;
+        const bool few0 = pt.kb == 0 && sched_tile_keys(p.sch, ct).few;   // the part's first step
+        const int qb = it % C::kQBufs;
+        if (!warp_wait(b.q_full(qb), (uint32_t)(it / C::kQBufs) & 1u, m.c, kSiteMmaQFull))
+            return;
+        ptx::tc_fence_after_sync();
+        m.q_cur = m.q_lo + (uint32_t)(qb * (C::kQBufBytes >> 4));
+        m1.q_cur = m1.q_lo + (uint32_t)(qb * (C::kQBufBytes >> 4));
+        for (int j = 0; j < n; ++j) {
+            const bool few = few0 && j == 0;
+            int st;
+            if (!m.stage_wait(step, st))
+                return;
+            if (SEP) {
+                const int nw = w ? n1 : n0;
+                if (j < nw && !m.issue_s(st, few))
+                    return;
+                if (C::kSplitKV)
+                    m.release(st);   // K read
+                if (j == n - 1 && ptx::elect_one())
+                    ptx::mma_commit(b.q_empty(qb));
+                __syncwarp();
+                if (prev >= 0 && !finish())
+                    return;
+                pv = j < nw;
+            } else {
+                if (j < n0 && !m.issue_s(st, few))
+                    return;
+                if (prev >= 0 && !finish())
+                    return;
+                if (j < n1 && !m1.issue_s(st, few))
+                    return;
+                if (j == n - 1 && ptx::elect_one())
+                    ptx::mma_commit(b.q_empty(qb));
+                __syncwarp();
+                if (j < n0 && !m.issue_pv(st, j > 0, few))
+                    return;
+                pv = j < n1;
+            }
+            prev = st;
+            acc = j > 0;
+            pfew = few;
+            ++step;
+        }
+        ++it;
+    }
+    if (prev >= 0)
+        finish();
+}
+
 // SEP: separate-P order (always at D = 64; at D = 128 for heads of one Q
 // tile, P_0 in tile 1's S columns), else the two-tile interleaved order.
 template <int D, bool BF16, int MASK, bool SPLIT, bool SEP, class P>
@@ -735,6 +830,9 @@ __device__ void mma_role(int w, const P &p, uint32_t sQ, uint32_t sStage, uint32
     MmaIssuer<D, BF16, SEP> m1 = make(1);           // tile 1 when one warp serves both
     if (!C::kSeparateP && SEP)                      // D = 128, heads of one Q tile
         m.tP = tmem + C::col_p_one_tile();
+    if constexpr (MASK == kMaskSink) {
+        mma_parts<D, BF16, SPLIT, SEP>(p, m, m1, w);
+    } else {
     int step = 0, it = 0;
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
@@ -762,6 +860,7 @@ __device__ void mma_role(int w, const P &p, uint32_t sQ, uint32_t sStage, uint32
             ptx::mma_commit(b.q_empty(qb));
         __syncwarp();
         ++it;
+    }
     }
     // Drain: all MMAs this warp issued have completed before TMEM is freed.
     if (ptx::elect_one())
@@ -802,6 +901,28 @@ static __device__ __noinline__ void mask_s_tail(uint32_t tS, int hi)
                 x[i] = (c0 + i < hi) ? x[i] : ninf;
             ptx::tmem_st32(tS + (uint32_t)c0, x);
         }
+    }
+    ptx::tmem_wait_st();
+}
+
+// The same for windows with sinks: keys i in [lo, hi) and i < sink stay (all per
+// thread, 0 <= i < 128).  The chunks that every row of the warp sees whole --
+// from its last row's lower edge to its first row's upper -- are not touched.
+static __device__ __noinline__ void mask_s_window(uint32_t tS, int lo, int hi, int sink)
+{
+    const int from = __reduce_max_sync(0xffffffffu, lo), to = __reduce_min_sync(0xffffffffu, hi);
+    const uint32_t width = (uint32_t)(hi - lo);
+#pragma unroll 1
+    for (int c0 = 0; c0 < kBN; c0 += 32) {
+        if (c0 >= from && c0 + 32 <= to)
+            continue;
+        uint32_t x[32];
+        ptx::tmem_ld32(tS + (uint32_t)c0, x);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            x[i] = ((uint32_t)(c0 + i - lo) < width || c0 + i < sink) ? x[i] : __float_as_uint(-INFINITY);
+        ptx::tmem_st32(tS + (uint32_t)c0, x);
     }
     ptx::tmem_wait_st();
 }
@@ -869,6 +990,13 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
             constexpr bool TMEM_MASK = (D == 64 && !kBanded<MASK>);
             if (TMEM_MASK && masked)
                 mask_s_tail(tS, row_hi - kb0);   // keys kb0 + i with i < row_hi - kb0 are visible
+            if constexpr (MASK == kMaskSink) {
+                // A window has as many masked steps as whole ones a few tiles long, and
+                // all but a chunk or two of a masked step's columns are seen, or not, by
+                // whole warps: masked in TMEM, chunk by chunk, at both head sizes.
+                if (masked)
+                    mask_s_window(tS, row_lo - kb0, row_hi - kb0, min(p.sch.sinks, row_hi) - kb0);
+            }
 
             uint32_t r[2][64];
             ptx::tmem_ld64(tS, r[0]);   // the whole row of S_w in two instructions
@@ -884,15 +1012,8 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
             for (int i = 0; i < 128; ++i)
                 s[i] = __uint_as_float(r[i / 64][i % 64]);
 
-            if (!TMEM_MASK && masked) {
-                if constexpr (MASK == kMaskSink) {
-                    // in the band, or a sink before the row's upper edge
-                    const int lo = row_lo - kb0, sink = min(p.sch.sinks, row_hi) - kb0;
-                    const uint32_t width = (uint32_t)(row_hi - row_lo);
-#pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        s[i] = ((uint32_t)(i - lo) < width || i < sink) ? s[i] : -INFINITY;
-                } else if (MASK == kMaskBand) {
+            if (!TMEM_MASK && MASK != kMaskSink && masked) {
+                if (MASK == kMaskBand) {
                     // key kb0 + i is visible iff row_lo <= kb0 + i < row_hi (one unsigned compare)
                     const int lo = row_lo - kb0;
                     const uint32_t width = (uint32_t)(row_hi - row_lo);
@@ -1000,7 +1121,53 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
             return true;
         };
 
-        for (int jr = 0; jr < np; ++jr) {
+        // A step of a few sinks alone, the tile's first: 16 columns of S and P.
+        auto few_step = [&]() -> bool {
+            if (!warp_wait<D == 128>(b.s_full(w), s_phase & 1u, c, kSiteSoftSFull))
+                return false;
+            ++s_phase;
+            ptx::tc_fence_after_sync();
+            uint32_t r[16];
+            ptx::tmem_ld16(tS, r);
+            ptx::tmem_wait_ld();
+            if (sep) {
+                ptx::tc_fence_before_sync();
+                ptx::mbar_arrive(b.s_free(w));
+            }
+            int sink = 0;
+            if constexpr (MASK == kMaskSink)
+                sink = min(p.sch.sinks, row_hi);
+            float s[16], top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[i] = i < sink ? __uint_as_float(r[i]) : -INFINITY;
+                top = fmaxf(top, s[i]);
+            }
+            m = top * p.qk_scale;
+            const float m_use = (m == -INFINITY) ? 0.f : m;
+            uint32_t pk[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p0 = ptx::ex2(fmaf(s[2 * i], p.qk_scale, -m_use)), p1 = ptx::ex2(fmaf(s[2 * i + 1], p.qk_scale, -m_use));
+                l += p0 + p1;
+                pk[i] = BF16 ? ptx::pack_bf16x2(p0, p1) : ptx::pack_f16x2(p0, p1);
+            }
+            ptx::tmem_st8(tP, pk);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before_sync();
+            ptx::mbar_arrive(b.p_full(w));
+            return true;
+        };
+
+        int jr0 = 0;
+        if constexpr (MASK == kMaskSink) {
+            if (keys.few && pt.kb == 0) {
+                if (!few_step())
+                    return;
+                jr0 = 1;
+            }
+        }
+        for (int jr = jr0; jr < np; ++jr) {
             const int kb0 = keys.first_key(pt.kb + jr);   // this step's first key
             // masked where some row's band edge or the key count ends inside the step
             bool masked;

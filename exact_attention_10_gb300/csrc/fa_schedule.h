@@ -165,7 +165,9 @@ FA_HD int sched_kv_tiles(const Schedule &s, int ct, int w)
 // With sinks: the tile's sink steps, and its band's first and last steps.
 struct SinkSteps {
     int ssz, ks, ke;   // steps [0, ssz), then [ks, ke), ssz <= ks
+    bool few;          // step 0 shows the tile's rows nothing but the sinks, kSchedFewSinks at most
 };
+constexpr int kSchedFewSinks = 16;   // the narrowest matrix product
 
 FA_HD SinkSteps sched_sink_range(const SinkSchedule &s, int ct)
 {
@@ -174,6 +176,7 @@ FA_HD SinkSteps sched_sink_range(const SinkSchedule &s, int ct)
     SinkSteps r;
     sched_band_steps(s, first, last, r.ks, r.ke);
     r.ssz = s.ss < r.ke ? s.ss : r.ke;
+    r.few = r.ssz == 1 && s.sinks <= kSchedFewSinks && r.ks >= 1;
     r.ks = r.ks < r.ssz ? r.ssz : r.ks;
     return r;
 }
@@ -196,13 +199,14 @@ FA_HD int sched_kv_tiles(const SinkSchedule &s, int ct, int w)
 // from sched_kv_start on; with them they jump from the sinks to the band.
 struct TileKeys {
     int ssz, ks;
+    bool few;   // step 0: see SinkSteps
     FA_HD int first_key(int j) const { return (j < ssz ? j : j - ssz + ks) * kSchedBN; }
 };
 
 FA_HD TileKeys sched_tile_keys(const SinkSchedule &s, int ct)
 {
     const SinkSteps r = sched_sink_range(s, ct);
-    return TileKeys{r.ssz, r.ks};
+    return TileKeys{r.ssz, r.ks, r.few};
 }
 
 // Masks without a left bound start every row's steps at 0: the steps of rows
