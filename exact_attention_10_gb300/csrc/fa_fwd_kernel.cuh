@@ -259,12 +259,46 @@ using SinkParams = FwdParamsT<SinkSchedule>;
 template <int MASK>
 using ParamsOf = std::conditional_t<MASK == kMaskSink, SinkParams, FwdParams>;
 
-// First key of step j of CTA tile ct, and the key head of query head bh.
+// A CTA's next part with its tile's head and row.  Windows with sinks also
+// take what sched_sink_tile gives, in one go (the other masks compute what
+// they need from the schedule where they need it, and leave `tile` alone).
+template <int MASK, bool SPLIT, class S>
+__device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, int &bh, int &ct, SinkTile &tile)
+{
+    if constexpr (MASK == kMaskSink && !SPLIT) {
+        if (it.t >= s.T)
+            return false;
+        sched_decode_fast(s, it.t, bh, ct);
+        tile = sched_sink_tile(s, ct);
+        pt = Part{it.t, 0, tile.n, -1, 0};
+        ++it.u;
+        it.t = it.u * s.G + ((it.u & 1) ? s.G - 1 - it.c : it.c);   // (serpentine rounds, as PartIter's)
+        return true;
+    } else {
+        if (!it.template next_t<SPLIT, kBanded<MASK>>(s, pt))
+            return false;
+        sched_decode_t<SPLIT, kBanded<MASK>>(s, pt.tile, bh, ct);
+        if constexpr (MASK == kMaskSink)
+            tile = sched_sink_tile(s, ct);
+        return true;
+    }
+}
+
+// Steps that Q tile w of the tile visits, and the first key of step j.
 template <int MASK, class S>
-__device__ __forceinline__ auto step_keys(const S &s, int ct)
+__device__ __forceinline__ int q_steps(const S &s, const SinkTile &tile, int ct, int w)
+{
+    if constexpr (MASK == kMaskSink)
+        return w ? tile.nw[1] : tile.nw[0];
+    else
+        return sched_kv_tiles_t<kBanded<MASK>>(s, ct, w);
+}
+
+template <int MASK, class S>
+__device__ __forceinline__ auto step_keys(const S &s, const SinkTile &tile, int ct)
 {
     if constexpr (MASK == kMaskSink) {
-        return sched_tile_keys(s, ct);
+        return TileKeys{tile.ssz, tile.ks, tile.few};
     } else {
         struct Run {
             int ks;
@@ -444,9 +478,9 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (ok && parts.next_t<SPLIT, kBanded<MASK>>(p.sch, pt)) {
-        int bh, ct;
-        sched_decode_t<SPLIT, kBanded<MASK>>(p.sch, pt.tile, bh, ct);
+    SinkTile tile;
+    int bh, ct;
+    while (ok && next_tile<MASK, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
         // The previous part's last V before the Q buffer is waited for: the
         // MMA warp frees that buffer only after the part's last P.V.
         if (SKV && nv < step && !load_v()) { ok = false; break; }
@@ -463,7 +497,7 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
         }
         __syncwarp();
         ++it;
-        const auto keys = step_keys<MASK>(p.sch, ct);   // the tile's key steps
+        const auto keys = step_keys<MASK>(p.sch, tile, ct);   // the tile's key steps
         const int kvh = key_head<MASK>(p.sch, bh);
         for (int j = pt.kb; j < pt.ke; ++j, ++step) {
             const int st = step % C::kStages;
@@ -753,13 +787,12 @@ __device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, B
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (parts.next_t<SPLIT, true>(p.sch, pt)) {
-        int bh, ct;
-        sched_decode_t<SPLIT, true>(p.sch, pt.tile, bh, ct);
-        const int n0 = part_steps(pt, sched_kv_tiles_t<true>(p.sch, ct, 0));
-        const int n1 = part_steps(pt, sched_kv_tiles_t<true>(p.sch, ct, 1));
+    SinkTile tile;
+    int bh, ct;
+    while (next_tile<kMaskSink, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
+        const int n0 = part_steps(pt, tile.nw[0]), n1 = part_steps(pt, tile.nw[1]);
         const int n = pt.ke - pt.kb;
-        const bool few0 = pt.kb == 0 && sched_tile_keys(p.sch, ct).few;   // the part's first step
+        const bool few0 = pt.kb == 0 && tile.few;   // the part's first step
         const int qb = it % C::kQBufs;
         if (!warp_wait(b.q_full(qb), (uint32_t)(it / C::kQBufs) & 1u, m.c, kSiteMmaQFull))
             return;
@@ -907,21 +940,30 @@ static __device__ __noinline__ void mask_s_tail(uint32_t tS, int hi)
 
 // The same for windows with sinks: keys i in [lo, hi) and i < sink stay (all per
 // thread, 0 <= i < 128).  The chunks that every row of the warp sees whole --
-// from its last row's lower edge to its first row's upper -- are not touched.
+// from its last row's lower edge to its first row's upper -- are not touched,
+// those that none sees overwritten without a read.
 static __device__ __noinline__ void mask_s_window(uint32_t tS, int lo, int hi, int sink)
 {
     const int from = __reduce_max_sync(0xffffffffu, lo), to = __reduce_min_sync(0xffffffffu, hi);
+    const int none_lo = __reduce_min_sync(0xffffffffu, lo), none_hi = __reduce_max_sync(0xffffffffu, hi);
+    const int any_sink = __reduce_max_sync(0xffffffffu, sink);
     const uint32_t width = (uint32_t)(hi - lo);
 #pragma unroll 1
     for (int c0 = 0; c0 < kBN; c0 += 32) {
         if (c0 >= from && c0 + 32 <= to)
             continue;
         uint32_t x[32];
-        ptx::tmem_ld32(tS + (uint32_t)c0, x);
-        ptx::tmem_wait_ld();
+        if (c0 >= any_sink && (c0 + 32 <= none_lo || c0 >= none_hi)) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            x[i] = ((uint32_t)(c0 + i - lo) < width || c0 + i < sink) ? x[i] : __float_as_uint(-INFINITY);
+            for (int i = 0; i < 32; ++i)
+                x[i] = __float_as_uint(-INFINITY);
+        } else {
+            ptx::tmem_ld32(tS + (uint32_t)c0, x);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                x[i] = ((uint32_t)(c0 + i - lo) < width || c0 + i < sink) ? x[i] : __float_as_uint(-INFINITY);
+        }
         ptx::tmem_st32(tS + (uint32_t)c0, x);
     }
     ptx::tmem_wait_st();
@@ -948,10 +990,10 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (parts.next_t<SPLIT, kBanded<MASK>>(p.sch, pt)) {
-        int bh, ct;
-        sched_decode_t<SPLIT, kBanded<MASK>>(p.sch, pt.tile, bh, ct);
-        const int nw = sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, w);    // steps of this Q tile in the whole tile
+    SinkTile tile;
+    int bh, ct;
+    while (next_tile<MASK, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
+        const int nw = q_steps<MASK>(p.sch, tile, ct, w);    // steps of this Q tile in the whole tile
         const int np = part_steps(pt, nw);              // ... of which this part holds steps kb .. kb + np - 1
         if (np == 0)
             continue;
@@ -960,7 +1002,7 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
         // step needs masking where some row's band edge or the key count ends
         // inside it: past the Q tile's first row's upper edge, before its last
         // row's lower edge (kMaskBand only), or past Nkv.
-        const auto keys = step_keys<MASK>(p.sch, ct);   // the tile's key steps
+        const auto keys = step_keys<MASK>(p.sch, tile, ct);   // the tile's key steps
         int row_lo = 0, row_hi = p.Nkv, edge_lo = 0, edge_hi = p.Nkv;
         if (CAUSAL) {
             const int first = ct * kCtaRows + w * kBM, r = min(row, p.N - 1);
@@ -990,10 +1032,9 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
             constexpr bool TMEM_MASK = (D == 64 && !kBanded<MASK>);
             if (TMEM_MASK && masked)
                 mask_s_tail(tS, row_hi - kb0);   // keys kb0 + i with i < row_hi - kb0 are visible
-            if constexpr (MASK == kMaskSink) {
-                // A window has as many masked steps as whole ones a few tiles long, and
-                // all but a chunk or two of a masked step's columns are seen, or not, by
-                // whole warps: masked in TMEM, chunk by chunk, at both head sizes.
+            constexpr bool TMEM_WINDOW = MASK == kMaskSink && (D == 64 || SPLIT);
+            if constexpr (TMEM_WINDOW) {
+                // (as there; a window has as many masked steps as whole ones)
                 if (masked)
                     mask_s_window(tS, row_lo - kb0, row_hi - kb0, min(p.sch.sinks, row_hi) - kb0);
             }
@@ -1012,8 +1053,22 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
             for (int i = 0; i < 128; ++i)
                 s[i] = __uint_as_float(r[i / 64][i % 64]);
 
-            if (!TMEM_MASK && MASK != kMaskSink && masked) {
-                if (MASK == kMaskBand) {
+            if (!TMEM_MASK && !TMEM_WINDOW && masked) {
+                if constexpr (MASK == kMaskSink) {
+                    // In the band, or a sink before the row's upper edge.  The columns
+                    // that every row of the warp sees (its last row's lower edge to its
+                    // first row's upper) are left alone.
+                    const int lo = row_lo - kb0, sink = min(p.sch.sinks, row_hi) - kb0;
+                    const uint32_t width = (uint32_t)(row_hi - row_lo);
+                    const int from = __shfl_sync(0xffffffffu, lo, 31), to = __shfl_sync(0xffffffffu, row_hi - kb0, 0);
+#pragma unroll
+                    for (int c0 = 0; c0 < 128; c0 += 32)
+                        if (c0 < from || c0 + 32 > to) {
+#pragma unroll
+                            for (int i = c0; i < c0 + 32; ++i)
+                                s[i] = ((uint32_t)(i - lo) < width || i < sink) ? s[i] : -INFINITY;
+                        }
+                } else if (MASK == kMaskBand) {
                     // key kb0 + i is visible iff row_lo <= kb0 + i < row_hi (one unsigned compare)
                     const int lo = row_lo - kb0;
                     const uint32_t width = (uint32_t)(row_hi - row_lo);
@@ -1420,6 +1475,9 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
     // 2 + w = parity of the P.V products of Q tile w done (o_done(w)).
     uint32_t ph = 0;
     uint32_t n_jobs = 0;                          // merge jobs posted
+    // O in whole 32-byte sectors where its rows start on them (a window's tiles
+    // are short, and the next one waits for this warpgroup to read O out)
+    const bool wide = MASK == kMaskSink && (reinterpret_cast<uintptr_t>(p.O) & 31u) == 0;
 
     // Post a job in the next queue slot: nparts = 0 stops the merge warp.
     // Thread k fills part k; false if the wait for a free slot gave up.
@@ -1455,13 +1513,13 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    while (parts.next_t<SPLIT, kBanded<MASK>>(p.sch, pt)) {
-        int bh, ct;
-        sched_decode_t<SPLIT, kBanded<MASK>>(p.sch, pt.tile, bh, ct);
+    SinkTile tile;
+    int bh, ct;
+    while (next_tile<MASK, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
         uint32_t published = 0;                   // bit w: Q tile w wrote a partial result
 #pragma unroll
         for (int w = 0; w < kQTiles; ++w) {
-            const int nw = sched_kv_tiles_t<kBanded<MASK>>(p.sch, ct, w);
+            const int nw = q_steps<MASK>(p.sch, tile, ct, w);
             const int np = part_steps(pt, nw);
             if (np == 0)
                 continue;
@@ -1499,7 +1557,11 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
                                        x, y);
                         o[i] = BF16 ? ptx::pack_bf16x2(x, y) : ptx::pack_f16x2(x, y);
                     }
-                    if (valid) {
+                    if (MASK == kMaskSink && valid && wide) {
+#pragma unroll
+                        for (int v = 0; v < 2; ++v)
+                            ptx::st_global_v8(orow + q * 64 + v * 32, o + 8 * v);
+                    } else if (valid) {
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
                             ptx::st_global_v4(orow + q * 64 + v * 16, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);

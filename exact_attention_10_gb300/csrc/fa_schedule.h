@@ -86,6 +86,7 @@ struct SinkSchedule : Schedule {
     int sinks;      // at most Nkv; 0 where the band has no left bound
     int ss;         // K/V steps that hold sinks: ceil(sinks / 128)
     int group;      // query heads per key head
+    unsigned long long inv;   // ceil(2^40 / BH) where T * BH < 2^40 (then t / BH = t * inv >> 40), else 0
 };
 
 // Band bounds that cannot bind become kSchedUnbounded: with off = Nkv - N,
@@ -162,50 +163,57 @@ FA_HD int sched_kv_tiles(const Schedule &s, int ct, int w)
     return ke - sched_kv_start(s, ct);
 }
 
-// With sinks: the tile's sink steps, and its band's first and last steps.
-struct SinkSteps {
-    int ssz, ks, ke;   // steps [0, ssz), then [ks, ke), ssz <= ks
-    bool few;          // step 0 shows the tile's rows nothing but the sinks, kSchedFewSinks at most
+// With sinks, all that the roles need of CTA tile ct: its steps are [0, ssz),
+// then n - ssz from ks >= ssz on; Q tile w visits the first nw[w].  (In one
+// go: the roles compute it at every tile, and a window's tiles are short.)
+struct SinkTile {
+    int ssz, ks, n;
+    int nw[2];
+    bool few;   // the sink step shows the tile's rows nothing but the sinks, kSchedFewSinks at most
 };
 constexpr int kSchedFewSinks = 16;   // the narrowest matrix product
 
-FA_HD SinkSteps sched_sink_range(const SinkSchedule &s, int ct)
+FA_HD SinkTile sched_sink_tile(const SinkSchedule &s, int ct)
 {
     const int first = ct * kSchedCtaRows;
     const int last = (first + kSchedCtaRows - 1 < s.N - 1) ? first + kSchedCtaRows - 1 : s.N - 1;
-    SinkSteps r;
-    sched_band_steps(s, first, last, r.ks, r.ke);
-    r.ssz = s.ss < r.ke ? s.ss : r.ke;
-    r.few = r.ssz == 1 && s.sinks <= kSchedFewSinks && r.ks >= 1;
-    r.ks = r.ks < r.ssz ? r.ssz : r.ks;
+    const int mid = first + kSchedBM;   // Q tile 1's first row
+    const int last0 = (mid - 1 < s.N - 1) ? mid - 1 : s.N - 1;
+    int a, e0, a1, e1;   // first step and end of Q tile 0, of Q tile 1
+    sched_band_steps(s, first, last0, a, e0);
+    a1 = a;
+    e1 = e0;
+    if (mid < s.N)
+        sched_band_steps(s, mid, last, a1, e1);
+    SinkTile r;
+    r.ssz = s.ss < e1 ? s.ss : e1;
+    r.few = r.ssz == 1 && s.sinks <= kSchedFewSinks && a >= 1;
+    r.ks = a < r.ssz ? r.ssz : a;
+    const int m0 = e0 - r.ks, m1 = e1 - r.ks;
+    r.nw[0] = e0 <= r.ssz ? e0 : r.ssz + (m0 > 0 ? m0 : 0);
+    r.nw[1] = mid >= s.N ? 0 : (e1 <= r.ssz ? e1 : r.ssz + (m1 > 0 ? m1 : 0));
+    r.n = r.ssz + (m1 > 0 ? m1 : 0);
     return r;
 }
 
 FA_HD int sched_kv_tiles(const SinkSchedule &s, int ct, int w)
 {
-    const int r0 = ct * kSchedCtaRows + w * kSchedBM;
-    if (r0 >= s.N)
+    if (ct * kSchedCtaRows + w * kSchedBM >= s.N)
         return 0;
-    const SinkSteps r = sched_sink_range(s, ct);
-    const int last = (r0 + kSchedBM - 1 < s.N - 1) ? r0 + kSchedBM - 1 : s.N - 1;
-    int ks, ke;
-    sched_band_steps(s, r0, last, ks, ke);
-    if (ke <= r.ssz)
-        return ke;
-    return r.ssz + (ke > r.ks ? ke - r.ks : 0);
+    return sched_sink_tile(s, ct).nw[w];
 }
 
 // First key of step j of a tile: without sinks its steps follow one another
 // from sched_kv_start on; with them they jump from the sinks to the band.
 struct TileKeys {
     int ssz, ks;
-    bool few;   // step 0: see SinkSteps
+    bool few;   // step 0: see SinkTile
     FA_HD int first_key(int j) const { return (j < ssz ? j : j - ssz + ks) * kSchedBN; }
 };
 
 FA_HD TileKeys sched_tile_keys(const SinkSchedule &s, int ct)
 {
-    const SinkSteps r = sched_sink_range(s, ct);
+    const SinkTile r = sched_sink_tile(s, ct);
     return TileKeys{r.ssz, r.ks, r.few};
 }
 
@@ -246,8 +254,7 @@ FA_HD int sched_steps_ct(const Schedule &s, int ct)
 
 FA_HD int sched_steps_ct(const SinkSchedule &s, int ct)
 {
-    const SinkSteps r = sched_sink_range(s, ct);
-    return r.ssz + r.ke - r.ks;
+    return sched_sink_tile(s, ct).n;
 }
 
 // Parts a tile of this schedule may be cut into: decoding-sized heads take
@@ -765,7 +772,17 @@ inline SinkSchedule sched_plan_sink(int N, int Nkv, int BH, int group, int sms, 
     s.sinks = wl >= kSchedUnbounded ? 0 : (sinks < Nkv ? sinks : Nkv);
     s.ss = (s.sinks + kSchedBN - 1) / kSchedBN;
     sched_plan_into(s, N, Nkv, BH, true, sms, mode, wl, 0);
+    if ((double)s.T * BH < 1099511627776.0)
+        s.inv = ((1ull << 40) + (unsigned long long)BH - 1) / (unsigned long long)BH;
     return s;
+}
+
+// Tile t's head and row in the round-robin order.
+FA_HD void sched_decode_fast(const SinkSchedule &s, int t, int &bh, int &ct)
+{
+    const int q = s.inv ? (int)(((unsigned long long)t * s.inv) >> 40) : t / s.BH;
+    bh = t - q * s.BH;
+    ct = s.rev ? q : s.C - 1 - q;
 }
 
 // Workspace bytes of a balanced schedule at head size D: a partial O
