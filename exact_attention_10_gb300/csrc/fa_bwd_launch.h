@@ -28,8 +28,8 @@ struct BwdLaunch {
 };
 
 // Parts that each sink tile's query tiles are cut into in the dK/dV pass, for
-// BH query and BHkv key heads: 1 where a CTA's share of the pass is at least
-// twice a sink tile's steps anyway.
+// BH query and BHkv key heads: 1 where a sink tile's steps are no more than a
+// CTA's share of the pass.
 int sink_parts_for(int BH, int BHkv, int N, int Nkv, int wl, int sinks, int sms);
 
 // Enqueue the pre-pass, then the dQ pass and the dK/dV pass, or (fused) the

@@ -91,7 +91,7 @@ int sink_parts_for(int BH, int BHkv, int N, int Nkv, int wl, int sinks, int sms)
     win = win < nqt ? win : nqt;
     const long long tall = group * nqt;                      // steps of the first sink tile
     const long long share = BHkv * (ss * group * nqt + (nkt - ss) * group * win) / sms;   // steps per CTA, about
-    if (tall * 2 <= share)
+    if (tall <= share)   // the sink tiles come first, the others fill up behind them
         return 1;
     long long per = share / 2;                               // a part: half a share, and at least an ordinary tile
     per = per < group * win ? group * win : per;
