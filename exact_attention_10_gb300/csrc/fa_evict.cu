@@ -8,13 +8,17 @@
 // all in order of position; n <= keep keeps everything.
 //
 // Selection without sorting: weights become 32-bit keys that order as the
-// weights do, and the k-th largest key is found digit by digit (11 + 11 + 10
+// weights do, and the k-th largest key is found digit by digit (four of 8
 // bits, a histogram of the candidates per digit); one more pass ranks what is
 // above it, and the first of those equal to it, by position.  A cluster of
 // CTAs shares a row, each holding its slice of the keys in shared memory and
 // adding the others' histograms through distributed shared memory, so the
 // weights are read from memory once and a few long rows still occupy many
-// SMs.
+// SMs.  What it takes is a chain of short steps (8 rows of 130001 weights, 8
+// CTAs each: 2 us of reading, then per digit a pass over 16 keys a thread, a
+// cluster barrier, a histogram of 8 x 1 KB read from the neighbours, a scan),
+// hence small histograms: 2048 bins took three digits instead of four, but
+// 4100 cycles of reading each.
 #include "fa.h"
 
 #include <cooperative_groups.h>
@@ -31,7 +35,7 @@ using fa_host::Arg;
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 constexpr int kMaxCluster = 8;         // the portable cluster size
 constexpr int kMaxHeld = 40960;        // keys held in shared memory per CTA (160 KB); longer slices are read again
 constexpr int kMinSlice = 2048;        // keys per CTA below which a row is not split further
@@ -80,8 +84,8 @@ __device__ __forceinline__ int warp_scan(int v, int lane)   // inclusive
 __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictParams p)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    extern __shared__ uint32_t keys[];   // [held]
-    __shared__ __align__(16) int hist[3][kBins];
+    extern __shared__ __align__(16) uint32_t keys[];   // [held, rounded up to 4]
+    __shared__ int hist[4][kBins];
     __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_count[2], s_found[2];
     static_assert(kSelWarps == 32, "one lane per warp's sum");
     cg::cluster_group cluster = cg::this_cluster();
@@ -110,8 +114,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictParam
     const int slice = (M + CS - 1) / CS;
     const int lo = p.sinks + (int)min((long long)rank * slice, (long long)M), cnt = min(slice, p.sinks + M - lo);
     const bool held = slice <= p.held;
-    for (int i = t; i < 3 * kBins; i += kSelThreads)
-        (&hist[0][0])[i] = 0;
+    (&hist[0][0])[t] = 0;
+    static_assert(4 * kBins == kSelThreads, "one bin per thread");
     __syncthreads();
     // The keys, and the histogram of their first digit as they come.
     constexpr int kBatch = 8;   // loads in flight per thread
@@ -129,74 +133,97 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictParam
                 const uint32_t key = key_of(x[u]);
                 if (held)
                     keys[i] = key;
-                atomicAdd(&hist[0][key >> 21], 1);
+                atomicAdd(&hist[0][key >> 24], 1);
             }
         }
     }
-    auto key_at = [&](int i) { return held ? keys[i] : key_of(__ldg(acc + lo + i)); };
+    // Keys 4 v .. 4 v + 3 of the slice (what lies behind its end is not looked at).
+    auto keys_at = [&](int v) -> uint4 {
+        if (held)
+            return reinterpret_cast<const uint4 *>(keys)[v];
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        x.x = key_of(__ldg(acc + lo + 4 * v));
+        if (4 * v + 1 < cnt)
+            x.y = key_of(__ldg(acc + lo + 4 * v + 1));
+        if (4 * v + 2 < cnt)
+            x.z = key_of(__ldg(acc + lo + 4 * v + 2));
+        if (4 * v + 3 < cnt)
+            x.w = key_of(__ldg(acc + lo + 4 * v + 3));
+        return x;
+    };
+    const int vecs = (cnt + 3) / 4;
 
     uint32_t prefix = 0;   // the digits found so far
     int left = k;          // candidates still to take among the keys that share them
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-        if (pass > 0)
-            for (int i = t; i < cnt; i += kSelThreads) {
-                const uint32_t key = key_at(i);
-                if ((key >> (shift + bits)) == prefix)
-                    atomicAdd(&hist[pass][(key >> shift) & ((1u << bits) - 1)], 1);
-            }
-        cluster.sync();
-        // Counts of the bins from the top, two to a thread, over all slices.
-        constexpr int kPer = kBins / kSelThreads;
-        static_assert(kPer == 2, "one 8-byte load per histogram");
-        const int top = kBins - 1 - t * kPer;   // this thread's highest bin
-        int c0 = 0, c1 = 0;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        if (pass > 0) {
+            __syncthreads();   // (pass 1: the keys are written)
+            for (int v = t; v < vecs; v += kSelThreads) {
+                const uint4 x = keys_at(v);
+                const uint32_t key[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-            if (r < CS) {
-                const int2 v = *reinterpret_cast<const int2 *>(cluster.map_shared_rank(&hist[pass][0], r) + top - 1);
-                c0 += v.y;
-                c1 += v.x;
+                for (int u = 0; u < 4; ++u)
+                    if ((key[u] >> (shift + 8)) == prefix && 4 * v + u < cnt)
+                        atomicAdd(&hist[pass][(key[u] >> shift) & 255u], 1);
             }
         }
-        const int inc = warp_scan(c0 + c1, lane);
-        if (lane == 31)
-            s_gt[warp] = inc;
-        __syncthreads();
-        const int sums = warp_scan(s_gt[lane], lane);
-        const int base = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
-        const int before = inc - c0 - c1 + (warp > 0 ? base : 0);
-        if (before < left && before + c0 + c1 >= left) {   // exactly one thread: the counts add up to at least `left`
-            const bool second = before + c0 < left;
-            s_found[0] = second ? top - 1 : top;
-            s_found[1] = left - before - (second ? c0 : 0);
+        cluster.sync();
+        // Counts of the bins from the top, one to each of 256 threads, over all slices.
+        int c = 0, inc = 0;
+        if (t < kBins) {
+            const int bin = kBins - 1 - t;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < CS)
+                    c += *cluster.map_shared_rank(&hist[pass][bin], r);
+            inc = warp_scan(c, lane);
+            if (lane == 31)
+                s_gt[warp] = inc;
         }
         __syncthreads();
-        prefix = (prefix << bits) | (uint32_t)s_found[0];
+        if (t < kBins) {
+            int before = inc - c;
+#pragma unroll
+            for (int w = 0; w < kBins / 32; ++w)
+                before += w < warp ? s_gt[w] : 0;
+            if (before < left && before + c >= left) {   // exactly one thread: the counts add up to at least `left`
+                s_found[0] = kBins - 1 - t;
+                s_found[1] = left - before;
+            }
+        }
+        __syncthreads();
+        prefix = (prefix << 8) | (uint32_t)s_found[0];
         left = s_found[1];
     }
     // prefix is the k-th largest key; `left` of the keys equal to it are taken.
 
-    // Rank by position: each warp counts its own consecutive part of the slice,
-    // then the slices and the warps before it give its first rank.
-    const int per = ((cnt + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int w0 = min(warp * per, cnt), w1 = min(w0 + per, cnt);
+    // Rank by position: each thread counts its own consecutive part of the
+    // slice; the slices, warps and lanes before it give its first rank.
+    const int per = (vecs + kSelThreads - 1) / kSelThreads;
+    const int v0 = min(t * per, vecs), v1 = min(v0 + per, vecs);
     int gt = 0, eq = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t key = key_at(i);
-        gt += key > prefix;
-        eq += key == prefix;
+    for (int v = v0; v < v1; ++v) {
+        const uint4 x = keys_at(v);
+        const uint32_t key[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool in = 4 * v + u < cnt;
+            gt += in && key[u] > prefix;
+            eq += in && key[u] == prefix;
+        }
     }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        s_gt[warp] = gt;
-        s_eq[warp] = eq;
+    const int gt_inc = warp_scan(gt, lane), eq_inc = warp_scan(eq, lane);
+    if (lane == 31) {
+        s_gt[warp] = gt_inc;
+        s_eq[warp] = eq_inc;
     }
     __syncthreads();
     const int all_gt = warp_scan(s_gt[lane], lane), all_eq = warp_scan(s_eq[lane], lane);
-    int n_gt = __shfl_sync(0xffffffffu, all_gt, warp) - gt, n_eq = __shfl_sync(0xffffffffu, all_eq, warp) - eq;
+    // (of the warps before this one: the sums up to and with it, less its own)
+    int n_gt = __shfl_sync(0xffffffffu, all_gt, warp) - s_gt[warp] + gt_inc - gt;
+    int n_eq = __shfl_sync(0xffffffffu, all_eq, warp) - s_eq[warp] + eq_inc - eq;
     if (t == 31) {
         s_count[0] = all_gt;
         s_count[1] = all_eq;
@@ -207,17 +234,21 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const EvictParam
         n_gt += o[0];
         n_eq += o[1];
     }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t key = i < w1 ? key_at(i) : 0u;
-        const bool g = i < w1 && key > prefix, e = i < w1 && key == prefix;
-        const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-        const int my_eq = n_eq + __popc(be & below);
-        if (g || (e && my_eq < left))
-            index[p.sinks + n_gt + __popc(bg & below) + min(my_eq, left)] = lo + i;
-        n_gt += __popc(bg);
-        n_eq += __popc(be);
+    if (gt + eq > 0) {
+        for (int v = v0; v < v1; ++v) {
+            const uint4 x = keys_at(v);
+            const uint32_t key[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (4 * v + u >= cnt || key[u] < prefix)
+                    continue;
+                const bool g = key[u] > prefix;
+                if (g || n_eq < left)
+                    index[p.sinks + n_gt + min(n_eq, left)] = lo + 4 * v + u;
+                n_gt += g;
+                n_eq += !g;
+            }
+        }
     }
     cluster.sync();   // no CTA leaves while another may still read its counts
 }
@@ -308,7 +339,7 @@ fa_status launch_evict(const EvictParams &q, int D, int sms, cudaStream_t s, int
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.BH * cs));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = (size_t)p.held * 4;
+    cfg.dynamicSmemBytes = ((size_t)p.held + 3) / 4 * 16;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
