@@ -68,6 +68,7 @@ struct Params {
     int rows;                 // query rows per key head: (H / Hkv) * Nq
     int Nq;
     int RB;                   // row blocks per key head (tiles of 8 NT rows); weights: 1
+    int whole;                // attention: no tile is cut (short caches)
     int left, sinks;          // left < 0: no window
     int accumulate;           // weights: add to acc instead of writing it
     float qk2;                // scale * log2(e)
@@ -1021,7 +1022,8 @@ __device__ __forceinline__ void store_out(const Params &p, long long row, int ch
 // may be partial (slots 2c, 2c + 1); merge_kernel joins those.  Within a CTA
 // the eight warps take 32-token steps in turn, each through its own ring of
 // cp.async stages, so no barrier stands between loads and products; they join
-// their running sums through shared memory at the end of a tile.
+// their running sums through shared memory at the end of a tile.  Where `whole`
+// is set the CTAs share out whole tiles instead.
 template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const Params p)
 {
@@ -1033,18 +1035,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)(warp * kStages * L::kStage);
 
-    const Where w = locate(p, blockIdx.x, gridDim.x, scratch);
-    if ((long long)blockIdx.x >= w.parts)
-        return;
-    const long long u0 = w.first, u1 = w.total * (blockIdx.x + 1) / w.parts;
-    int b = w.b;
-    Span sp = span_of(p, b);
     const int HR = p.Hkv * p.RB;
-    int hr = (int)((u0 - w.before) / sp.n);
-    int ku = (int)((u0 - w.before) - (long long)hr * sp.n);
+    long long u0, u1;   // units, or tiles where none is cut
+    int b, hr, ku = 0;
+    Span sp;
+    if (p.whole) {
+        const long long tiles = (long long)p.B * HR;
+        u0 = tiles * blockIdx.x / gridDim.x;
+        u1 = tiles * (blockIdx.x + 1) / gridDim.x;
+        if (u0 == u1)
+            return;
+        b = (int)(u0 / HR);
+        hr = (int)(u0 - (long long)b * HR);
+        sp = span_of(p, b);
+    } else {
+        const Where w = locate(p, blockIdx.x, gridDim.x, scratch);
+        if ((long long)blockIdx.x >= w.parts)
+            return;
+        u0 = w.first;
+        u1 = w.total * (blockIdx.x + 1) / w.parts;
+        b = w.b;
+        sp = span_of(p, b);
+        hr = (int)((u0 - w.before) / sp.n);
+        ku = (int)((u0 - w.before) - (long long)hr * sp.n);
+    }
 
     for (long long u = u0; u < u1;) {
-        const int ke = (int)((long long)sp.n - ku < u1 - u ? sp.n : ku + (u1 - u));
+        const int ke = p.whole || (long long)sp.n - ku < u1 - u ? sp.n : (int)(ku + (u1 - u));
         const bool whole = ku == 0 && ke == sp.n;
         const int h = hr / p.RB, r0 = (hr - h * p.RB) * (8 * NT);
         const int nrows = p.rows - r0 < 8 * NT ? p.rows - r0 : 8 * NT;
@@ -1154,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) attend_kernel(const
             }
         }
         __syncthreads();   // read before the next tile's loads overwrite it
-        u += ke - ku;
+        u += p.whole ? 1 : ke - ku;
         ku = 0;
         if (++hr == HR && u < u1) {
             hr = 0;

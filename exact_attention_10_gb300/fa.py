@@ -70,7 +70,7 @@ def load(path: str = LIB_PATH):
     lib.fa_cache_append.restype = c_int
     lib.fa_cache_read.argtypes = [vp] * 8 + [c_int] * 6 + [vp]
     lib.fa_cache_read.restype = c_int
-    lib.fa_cache_workspace.argtypes = [c_int] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.fa_cache_workspace.argtypes = [c_int] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.fa_cache_workspace.restype = c_int
     lib.fa_cache_fwd.argtypes = [vp] * 8 + [c_int] * 8 + [ctypes.c_float, c_int, vp, ctypes.c_size_t, vp]
     lib.fa_cache_fwd.restype = c_int
@@ -414,10 +414,10 @@ def cache_read(cache: PackedCache, start, n: int, count=None, stream=None):
     return k, v
 
 
-@lru_cache(maxsize=None)
-def _cache_workspace(device: int, H: int, Hkv: int, Nq: int, D: int) -> int:
+@lru_cache(maxsize=4096)
+def _cache_workspace(device: int, *sizes) -> int:
     n = ctypes.c_size_t()
-    rc = load().fa_cache_workspace(H, Hkv, Nq, D, ctypes.byref(n))
+    rc = load().fa_cache_workspace(*sizes, ctypes.byref(n))
     if rc != 0:
         raise FAError(rc, "fa_cache_workspace")
     return n.value
@@ -461,14 +461,15 @@ def cache_forward(q, cache: PackedCache, lens, window: tuple[int, int] | None = 
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, H, Nq]")
-    nbytes = _cache_workspace(q.get_device(), H, Hkv, Nq, D)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    nbytes = _cache_workspace(q.get_device(), B, H, Hkv, Nq, C, D)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     rc = load().fa_cache_fwd(q.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(),
                              _ints(lens, B, "lens"), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, C, D, left, sinks,
-                             D ** -0.5 if scale is None else scale, code, ws.data_ptr(), nbytes, _stream_of(stream, q))
+                             D ** -0.5 if scale is None else scale, code, ws.data_ptr() if nbytes else None, nbytes,
+                             _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_cache_fwd")
-    if stream is not None:
+    if stream is not None and nbytes:
         _keep_until_done(ws, stream)
     return out, lse
 

@@ -393,8 +393,8 @@ FA_API fa_status fa_cache_read(const void *Kc, const void *Kp, const void *Vc, c
                                fa_dtype dtype, fa_stream_t stream);
 
 /* fa_cache_workspace -- bytes of workspace that fa_cache_fwd needs on the
- * current device for these sizes (any B and C). */
-FA_API fa_status fa_cache_workspace(int H, int Hkv, int Nq, int D, size_t *bytes);
+ * current device for these sizes (0 for short caches). */
+FA_API fa_status fa_cache_workspace(int B, int H, int Hkv, int Nq, int C, int D, size_t *bytes);
 
 /*
  * fa_cache_fwd -- attention of each sequence's last Nq tokens against the
@@ -406,7 +406,8 @@ FA_API fa_status fa_cache_workspace(int H, int Hkv, int Nq, int D, size_t *bytes
  * in the cache) and sees the tokens j <= p with j >= p - window_left
  * (window_left < 0: no bound) or j < sinks.  A query that sees no token
  * (p < 0) gets O = 0 and LSE = -inf.
- * workspace : fa_cache_workspace bytes; its contents need no set-up.
+ * workspace : fa_cache_workspace bytes (NULL where they are 0); its contents
+ *        need no set-up.
  *
  * K and V enter the products as their integer codes, exact in 16 bits, with
  * scale and minimum applied outside them in fp32; the softmax weight times V's
