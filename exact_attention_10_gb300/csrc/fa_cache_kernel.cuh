@@ -1268,11 +1268,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
             }
             Queries<D, BF16, NT, true> q;
             q.load(p, bh * p.rows + r0, nrows);
-            const float none[NT][2] = {};
             Bounds vis[NT][2];
-            // -LSE in log2 units, to about 2^-32 in two parts; -inf for rows that are
-            // not there or see nothing
-            float nl[NT][2], nl2[NT][2];
+            // LSE in log2 units, what the scores are taken relative to, and 2 to the
+            // power of what its rounding to fp32 left out (1 + 1e-6 at most, but the
+            // same for a whole row); +inf for rows that are not there or see nothing
+            float ref[NT][2], rest[NT][2];
             int edge_lo = 0, edge_hi = 0x7fffffff;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -1280,8 +1280,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
                 for (int e = 0; e < 2; ++e) {
                     const int n = 8 * nt + 2 * c + e;
                     const float lse = n < nrows ? p.lse[bh * p.rows + r0 + n] : -INFINITY;
-                    nl[nt][e] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-                    nl2[nt][e] = lse == -INFINITY ? 0.f : fmaf(-lse, kLog2e, -nl[nt][e]) - lse * kLog2eRest;
+                    ref[nt][e] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+                    rest[nt][e] = lse == -INFINITY ? 1.f : exp2f(-fmaf(lse, kLog2e, -ref[nt][e]) - lse * kLog2eRest);
                     vis[nt][e] = bounds_of(p, sp.len, r0 + (n < nrows ? n : nrows - 1));
                     edge_lo = max(edge_lo, vis[nt][e].lo);
                     edge_hi = min(edge_hi, vis[nt][e].hi);
@@ -1305,7 +1305,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
                     float x[NT][4];
-                    scores<D, BF16, NT, true>(stage, stage + L::kCodes, mt, q, none, x);
+                    scores<D, BF16, NT, true>(stage, stage + L::kCodes, mt, q, ref, x);
                     if (masked) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -1320,7 +1320,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) weights_kernel(cons
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            sum[2 * mt + (e >> 1)] += ex2((x[nt][e] + nl[nt][e & 1]) + nl2[nt][e & 1]);
+                            sum[2 * mt + (e >> 1)] = fmaf(ex2(x[nt][e]), rest[nt][e & 1], sum[2 * mt + (e >> 1)]);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
