@@ -178,6 +178,21 @@ def _sink_workspace(device: int, *sizes) -> int:
     return n.value
 
 
+def _workspace(nbytes: int, t, stream):
+    """Workspace for a call on ``stream`` (None: torch's current one) from
+    torch's allocator, on that very stream: when it is dropped after the call,
+    torch hands it on to later work of the same stream only."""
+    import torch
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+
+
 def _sink_shapes(q, k, v):
     """(B, H, Hkv, Nq, Nkv, D, dtype code) of tensors that go together."""
     sq, sk = q.shape, k.shape
@@ -206,14 +221,12 @@ def _forward_sink(q, k, v, scale, out, lse, stream, schedule, window, sinks):
         raise ValueError("lse must be contiguous float32 [B, H, Nq]")
     sched = SCHEDULES[schedule]
     nbytes = _sink_workspace(q.get_device(), B, H, Hkv, Nq, Nkv, D, left, sinks, sched)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    ws = _workspace(nbytes, q, stream)
     rc = load().fa_fwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
                             Nkv, D, left, sinks, D ** -0.5 if scale is None else scale, code, sched,
                             ws.data_ptr() if nbytes else None, nbytes, _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_fwd_sink")
-    if stream is not None and nbytes:
-        _keep_until_done(ws, stream)
     return out, lse
 
 
@@ -292,15 +305,13 @@ def _backward_sink(q, k, v, o, do, lse, scale, dq, dk, dv, stream, window, deter
             raise ValueError("dq, dk, dv must be contiguous, of the shapes and type of q, k, v")
     flags = FA_BWD_DETERMINISTIC if deterministic else 0
     nbytes = _sink_bwd_workspace(q.get_device(), B, H, Hkv, Nq, Nkv, D, left, sinks, flags)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    ws = _workspace(nbytes, q, stream)
     rc = load().fa_bwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                             *(d.data_ptr() for d in outs), B, H, Hkv, Nq, Nkv, D, left, sinks,
                             D ** -0.5 if scale is None else scale, code, flags, ws.data_ptr(), nbytes,
                             _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_bwd_sink")
-    if stream is not None:
-        _keep_until_done(ws, stream)
     return tuple(outs)
 
 
@@ -367,8 +378,8 @@ def _stream_of(stream, t) -> int:
 
 def _left_of(window, sinks) -> int:
     """window_left of ``window`` = (left, 0) or None (no window)."""
-    if sinks < 0:
-        raise ValueError("sinks must not be negative")
+    if not 0 <= sinks <= 0x7FFFFFFF:
+        raise ValueError("sinks must be a 32-bit count")
     if window is None:
         return -1
     if window[1] != 0:
@@ -401,6 +412,8 @@ def cache_append(cache: PackedCache, k, v, start, count=None, stream=None) -> No
 def cache_read(cache: PackedCache, start, n: int, count=None, stream=None):
     """The values (k, v) [B, Hkv, n, D] that cache tokens start[b] + i stand
     for; rows from count[b] on, or outside the cache, are zeros."""
+    if not 1 <= n <= 0x7FFFFFFF:
+        raise ValueError("n must be a 32-bit count of at least 1")
     kc, kp, vc, vp = cache
     B, Hkv, C, D, code = cache.sizes
     import torch
@@ -445,8 +458,8 @@ def cache_forward(q, cache: PackedCache, lens, window: tuple[int, int] | None = 
     from p - left on, but for the first ``sinks`` tokens, which stay visible.
 
     Raises FAError on any non-OK status.  Asynchronous on ``stream``
-    (default: the current torch stream); the workspace comes from torch, on
-    the current torch stream, and a given ``stream`` must be ordered with it.
+    (default: the current torch stream; the outputs that are not given are
+    allocated on the current one, which a given ``stream`` must follow).
     """
     import torch
     kc, kp, vc, vp = cache
@@ -462,24 +475,14 @@ def cache_forward(q, cache: PackedCache, lens, window: tuple[int, int] | None = 
     elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, H, Nq]")
     nbytes = _cache_workspace(q.get_device(), B, H, Hkv, Nq, C, D)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    ws = _workspace(nbytes, q, stream)
     rc = load().fa_cache_fwd(q.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(),
                              _ints(lens, B, "lens"), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, C, D, left, sinks,
                              D ** -0.5 if scale is None else scale, code, ws.data_ptr() if nbytes else None, nbytes,
                              _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_cache_fwd")
-    if stream is not None and nbytes:
-        _keep_until_done(ws, stream)
     return out, lse
-
-
-def _keep_until_done(t, stream) -> None:
-    """Let torch reuse ``t``'s memory only after the work queued on ``stream``."""
-    import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-    t.record_stream(stream)
 
 
 def cache_weights(q, cache: PackedCache, lse, lens, window: tuple[int, int] | None = None, sinks: int = 0,
@@ -528,7 +531,7 @@ def cache_evict(cache: PackedCache, acc, lens, keep: int, sinks: int = 0, recent
         raise ValueError("acc must be contiguous [B, Hkv, C]")
     if acc.dtype != torch.float32:
         raise TypeError("acc must be float32")
-    if keep < 1 or sinks < 0 or recent < 0 or sinks + recent > keep:
+    if not 1 <= keep <= 0x7FFFFFFF or sinks < 0 or recent < 0 or sinks + recent > keep:
         raise ValueError("keep must be at least 1 and hold the sinks and the recent tokens")
     if out is None:   # (its rows behind the last kept token are not written)
         codes = torch.empty((B, Hkv, keep, D // 2), dtype=torch.uint8, device=kc.device)

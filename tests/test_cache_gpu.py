@@ -495,6 +495,7 @@ EVICT = [  # (B, Hkv, C, lens, keep, sinks, recent)
     (1, 2, 400000, [399999], 3000, 4, 100),   # slices longer than shared memory holds
     (70, 8, 300, None, 100, 1, 20),           # more rows than SMs
     (2, 1, 64, [70, -3], 32, 1, 1),           # lengths outside [0, C]
+    (2, 1, 20, [20, 7], 33, 1, 1),            # a budget that no sequence can reach
 ]
 
 
@@ -556,6 +557,68 @@ def test_evict_into_a_new_cache():
     at = index.clamp(min=0).long()
     picked = fa.PackedCache(*(x.gather(2, at[..., None].expand(2, 2, 64, x.shape[3])).contiguous() for x in cache))
     assert torch.equal(o, fa.cache_forward(q, picked, lens2)[0])
+
+
+def test_serving_step_with_eviction_captured():
+    """Append, attention, weights, eviction and read-out in one captured graph,
+    replayed on other lengths and contents: what the eager calls give."""
+    B, H, Hkv, C, D = 2, 8, 2, 3000, 64
+    q, cache, lens, _, _ = _attention_case((B, H, Hkv, 1, C, [2900, 50], -1, 0), D, "fp16", seed=31)
+    k = torch.randn((B, Hkv, 1, D), generator=_gen(6), device="cuda").half()
+    zero = torch.zeros_like(lens)
+
+    def step():
+        fa.cache_append(cache, k, k, lens)
+        n = lens + 1
+        o, lse = fa.cache_forward(q, cache, n, window=(2000, 0), sinks=4)
+        acc = fa.cache_weights(q, cache, lse, n, window=(2000, 0), sinks=4)
+        kept, acc2, n2, index = fa.cache_evict(cache, acc, n, 700, sinks=4, recent=200)
+        return (o, lse, acc, acc2, n2, index, *fa.cache_read(kept, zero, 700, count=n2))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for new in ([1500, 2999], [0, 699]):
+        lens.copy_(torch.tensor(new, dtype=torch.int32))
+        k.copy_(torch.randn((B, Hkv, 1, D), generator=_gen(new[0]), device="cuda").half())
+        graph.replay()
+        got = [x.clone() for x in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+    _ok()
+
+
+def test_many_query_rows():
+    """A prompt's last 100 tokens: 400 query rows per key head, in row blocks."""
+    case = (1, 4, 1, 100, 600, [555], 300, 7)
+    for D, dtype in ((64, "fp16"), (128, "bf16")):
+        q, cache, lens, left, sinks = _attention_case(case, D, dtype, seed=13)
+        o, lse = fa.cache_forward(q, cache, lens, window=(left, 0), sinks=sinks)
+        ref = reference(q, cache, lens, left, sinks, D ** -0.5)
+        check_attention(q, cache, lens, left, sinks, D ** -0.5, o, lse, ref)
+        w = fa.cache_weights(q, cache, lse, lens, window=(left, 0), sinks=sinks)
+        _ok()
+        assert abs(float(w.sum()) - 400) <= 400 * 2.0 ** -14   # every query's weights sum to 1
+        assert bool(((w.double() - ref[2]).abs() <= 4 * ref[4] + ref[2] * 2.0 ** -14).all())
+
+
+def test_same_tensor_for_keys_and_values_and_queries_that_are_not_finite():
+    q, cache, lens, _, _ = _attention_case((2, 4, 2, 1, 300, [300, 100], -1, 0), 128, "bf16", seed=17)
+    want = fa.cache_forward(q, cache, lens)
+    bad = q.clone()
+    bad[0, 1, 0, 3], bad[1, 2, 0, 0] = math.nan, math.inf
+    o, lse = fa.cache_forward(bad, cache, lens)
+    _ok()
+    hit = torch.zeros((2, 4, 1), dtype=torch.bool, device="cuda")
+    hit[0, 1], hit[1, 2] = True, True
+    assert bool(torch.isnan(o[hit]).all()) and torch.equal(o[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
+    x = torch.randn((2, 2, 5, 128), device="cuda").bfloat16()
+    fa.cache_append(cache, x, x, lens - 5)
+    got = fa.cache_read(cache, lens - 5, 5)
+    _ok()
+    assert torch.equal(got[0], got[1])
 
 
 # ------------------------------------------------------------------ refusals that need device memory
