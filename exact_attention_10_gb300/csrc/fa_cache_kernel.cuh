@@ -783,13 +783,12 @@ __device__ __forceinline__ bool sees(const Bounds &v, int t)
 // w = p vs as one fp16 operand: w is multiplied by the warp's power of two
 // `fac`, which keeps the largest vs so far in [2^5, 2^6), so with p <= 2^8 it
 // stays in fp16's range, and a token's 11 significand bits are whole down to
-// 2^-20 of that.  For an fp16 result, whose own rounding is as fine, what the
-// rounding of w takes off or adds is given back with the middle code, 7.5 (w -
-// fp16(w)) in z, so that its error meets the codes' distance from their middle
-// only and costs what rounding p to 16 bits costs the 16-bit kernels' product
-// with V (error of the result against float64: 2.4e-4 with it, 3.7e-4
-// without, 2.1e-4 from the result's rounding alone); next to bf16's rounding
-// it does not show.  l is summed from the unrounded p.
+// 2^-20 of that.  Next to a bf16 result's rounding w's does not show (1.7e-3
+// against float64 with and without it).  For an fp16 result, whose own
+// rounding is as fine, w is two fp16 operands, the second what the first left
+// out (3.7e-4 with one, 2.1e-4 with two, 2.1e-4 from the result's rounding
+// alone): 8 more MMAs per 16 tokens at D = 128.  l is summed from the
+// unrounded p.
 template <int D, bool BF16, int NT>
 struct Attend {
     using L = Layout<D>;
@@ -916,10 +915,9 @@ struct Attend {
                     }
                 }
         }
-        const float mid = 7.5f * (1.f / fac);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-            uint32_t wf[NT][2];   // w as B fragments
+            uint32_t wf[NT][2], wl[NT][2];   // w as B fragments; fp16 results: what they leave out
             const float wa = vs[2 * mt] * fac, wb = vs[2 * mt + 1] * fac;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -941,10 +939,9 @@ struct Attend {
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t u = pack_f16(w[2 * h], w[2 * h + 1]);
                     wf[nt][h] = transpose8(u);
-                    if (!BF16) {
-                        z[nt][0] = fmaf(w[2 * h] - to_float<false>(u & 0xffffu), mid, z[nt][0]);
-                        z[nt][1] = fmaf(w[2 * h + 1] - to_float<false>(u >> 16), mid, z[nt][1]);
-                    }
+                    if (!BF16)
+                        wl[nt][h] = transpose8(pack_f16(w[2 * h] - to_float<false>(u & 0xffffu),
+                                                        w[2 * h + 1] - to_float<false>(u >> 16)));
                 }
             }
             // V^T as the A operand: for channel words of this lane, tokens
@@ -968,8 +965,11 @@ struct Attend {
                 const uint32_t b0 = a0 >> 8, b1 = a1 >> 8, b2 = a2 >> 8, b3 = a3 >> 8;
                 auto tile = [&](int j, const uint32_t (&a)[4]) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
                         mma(o[nt][j], a, wf[nt][0], wf[nt][1]);
+                        if (!BF16)
+                            mma(o[nt][j], a, wl[nt][0], wl[nt][1]);
+                    }
                 };
                 tile(4 * w, {a0 & kEven, a1 & kEven, a2 & kEven, a3 & kEven});
                 tile(4 * w + 1, {a0 & kOdd, a1 & kOdd, a2 & kOdd, a3 & kOdd});

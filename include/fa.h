@@ -411,7 +411,8 @@ FA_API fa_status fa_cache_workspace(int B, int H, int Hkv, int Nq, int C, int D,
  *
  * K and V enter the products as their integer codes, exact in 16 bits, with
  * scale and minimum applied outside them in fp32; the softmax weight times V's
- * scale is rounded to 11 bits for the product with V's codes.
+ * scale is rounded to 11 bits for the product with V's codes, to 22 for an
+ * fp16 result.
  */
 FA_API fa_status fa_cache_fwd(const void *Q, const void *Kc, const void *Kp, const void *Vc, const void *Vp,
                               const int *lens, void *O, float *LSE, int B, int H, int Hkv, int Nq, int C, int D,

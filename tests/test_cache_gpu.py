@@ -12,8 +12,8 @@ with tolerances that follow the arithmetic:
   over a row's visible tokens.
 * weights: p has the relative error delta + 2^-21 (the exponential); w = p vs
   is rounded to fp16, 2^-11 relative, as it enters the product with the codes:
-  2^-11 of sum p vs code, part of B = sum p (vs code + |vmin|), the sum of all
-  magnitudes in O's numerator.
+  2^-11 of sum p vs code (2^-22 for fp16 results), part of B = sum p (vs code +
+  |vmin|), the sum of all magnitudes in O's numerator.
 * sums over n tokens in fp32: each chain has at most n / 8 + 64 additions
   (eight warps, then the joins): (n / 8 + 64) 2^-24 of the magnitudes.
 * the result: half a unit of its type, finfo(t).eps / 2.
