@@ -117,7 +117,19 @@ fa_status launch_weights_t(const cache::Params &p, int sms, cudaStream_t s, int 
     const fa_status st = fa_host::allow_smem(reinterpret_cast<const void *>(&cache::weights_kernel<D, BF16, NT>), smem, dev, set);
     if (st != FA_OK)
         return st;
-    cache::weights_kernel<D, BF16, NT><<<sms * (NT <= 2 ? 2 : 1), cache::kThreads, smem, s>>>(p);
+    cache::weights_kernel<D, BF16, NT><<<sms * 2, cache::kThreads, smem, s>>>(p);
+    return launched();
+}
+
+template <int D, bool BF16>
+fa_status launch_weights_rows(const cache::Params &p, int sms, cudaStream_t s, int dev)
+{
+    constexpr int smem = cache::RowsSmem<D>::kBytes;
+    static bool set[fa_host::kMaxDevices] = {};
+    const fa_status st = fa_host::allow_smem(reinterpret_cast<const void *>(&cache::weights_rows_kernel<D, BF16>), smem, dev, set);
+    if (st != FA_OK)
+        return st;
+    cache::weights_rows_kernel<D, BF16><<<sms * 2, cache::kThreads, smem, s>>>(p);
     return launched();
 }
 
@@ -292,13 +304,12 @@ extern "C" fa_status fa_cache_weights(const void *Q, const void *Kc, const void 
     p.qk2 = scale * cache::kLog2e;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == FA_BF16;
-    const int nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);   // rows of one pass over the keys
     auto run = [&](auto d, auto b) -> fa_status {
         constexpr int DD = decltype(d)::value;
         constexpr bool BB = decltype(b)::value;
-        if (nt == 1)
+        if (rows <= 8)
             return launch_weights_t<DD, BB, 1>(p, di->sms, s, dev);
-        return nt == 2 ? launch_weights_t<DD, BB, 2>(p, di->sms, s, dev) : launch_weights_t<DD, BB, 4>(p, di->sms, s, dev);
+        return rows <= 16 ? launch_weights_t<DD, BB, 2>(p, di->sms, s, dev) : launch_weights_rows<DD, BB>(p, di->sms, s, dev);
     };
     using T = std::true_type;
     using F = std::false_type;
