@@ -413,7 +413,7 @@ bool sink_sizes_ok(int B, int H, int Hkv, int Nq, int Nkv, int D, int window_lef
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nkv < 1 || sinks < 0)
         return false;
     const long long BH = (long long)B * H;
-    if (BH >= (1ll << 31) || BH * Nq >= (1ll << 31) || (long long)B * Hkv * Nkv >= (1ll << 31))
+    if (BH > fa_host::kMaxRows || BH * Nq > fa_host::kMaxRows || (long long)B * Hkv * Nkv > fa_host::kMaxRows)
         return false;
     int wr = 0;
     *wl = window_left;

@@ -31,14 +31,14 @@ bool sizes_ok(int B, int Hkv, long long N, int C, int D, fa_dtype dtype)
     if (B < 1 || Hkv < 1 || N < 1 || C < 1)
         return false;
     const long long BH = (long long)B * Hkv;
-    return BH < (1ll << 31) && BH * N < (1ll << 31) && BH * C < (1ll << 31);
+    return BH <= fa_host::kMaxRows && BH * N <= fa_host::kMaxRows && BH * C <= fa_host::kMaxRows;
 }
 
 bool queries_ok(int B, int H, int Hkv, int Nq)
 {
     if (H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1)
         return false;
-    return (long long)B * H < (1ll << 31) && (long long)B * H * Nq < (1ll << 31);
+    return (long long)B * H <= fa_host::kMaxRows && (long long)B * H * Nq <= fa_host::kMaxRows;
 }
 
 // Query rows per tile: 8 where a key head has no more, else 16 (a tile's rows

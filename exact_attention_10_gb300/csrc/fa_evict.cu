@@ -385,7 +385,7 @@ extern "C" fa_status fa_cache_evict(const void *Kc, const void *Kp, const void *
         return FA_ERR_INVALID_VALUE;
     const long long BH = (long long)B * Hkv;
     // (kMaxCluster CTAs per row at most, in one grid dimension)
-    if (BH >= (1ll << 31) / kMaxCluster || BH * C >= (1ll << 31) || BH * C2 >= (1ll << 31))
+    if (BH >= (1ll << 31) / kMaxCluster || BH * C > fa_host::kMaxRows || BH * C2 > fa_host::kMaxRows)
         return FA_ERR_INVALID_VALUE;
     const size_t from = (size_t)BH * C, to = (size_t)BH * C2;
     const Arg args[13] = {{Kc, from * D / 2, false, 16}, {Kp, from * 4, false, 4}, {Vc, from * D / 2, false, 16},

@@ -19,6 +19,10 @@ const DeviceInfo *device_info(int dev);
 
 bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb);
 
+// Rows (tokens) of one tensor, at most: kernels index them with 32 bits, and a
+// block's or cluster's stride past the last one must not wrap.
+constexpr long long kMaxRows = (1ll << 31) - 65536;
+
 // Device (or managed) memory of device `dev`.
 bool is_device_pointer(const void *p, int dev);
 

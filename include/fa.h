@@ -192,7 +192,8 @@ FA_API fa_status fa_fwd_band(const void *Q, const void *K, const void *V, void *
  *             schedule needs none; NULL is then fine).  It is the caller's:
  *             calls that may overlap, captured graphs among them, take
  *             different ones.  Its contents need no set-up.
- * Other arguments and errors as for fa_fwd_ex; B*Hkv*Nkv < 2^31.
+ * Other arguments and errors as for fa_fwd_ex; B*H*Nq and B*Hkv*Nkv at most
+ * 2^31 - 65536.
  */
 FA_API fa_status fa_fwd_sink(const void *Q, const void *K, const void *V, void *O, float *LSE, int B, int H,
                              int Hkv, int Nq, int Nkv, int D, int window_left, int sinks, float scale,
@@ -361,7 +362,7 @@ FA_API fa_status fa_bwd_sink_workspace(int B, int H, int Hkv, int Nq, int Nkv, i
  * neither read nor written unless said otherwise.
  *
  * Arguments of all cache calls: device pointers to contiguous tensors;
- * B, Hkv, C >= 1 with B*Hkv*C < 2^31; D = 64 or 128; codes, Q, K, V, O and
+ * B, Hkv, C >= 1; B*Hkv*C (B*Hkv*N, B*H*Nq) at most 2^31 - 65536; D = 64 or 128; codes, Q, K, V, O and
  * workspaces 16-byte aligned, everything else to its element (params 4).
  * Outputs overlap no other argument.  Errors as for fa_fwd, nothing enqueued
  * on any of them.  The calls allocate nothing and keep nothing between calls:

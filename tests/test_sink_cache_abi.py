@@ -113,6 +113,25 @@ def test_cache_refusals(lib, fn, base, bad):
                 assert _call(f, base, base, {name: base[name] + 4}) == UNSUPPORTED, name
 
 
+@pytest.mark.parametrize("fn,base,sizes", [
+    ("fa_cache_append", APPEND, ("C", "N")), ("fa_cache_read", APPEND, ("C", "N")), ("fa_cache_fwd", CACHE, ("C",)),
+    ("fa_cache_weights", WEIGHTS, ("C",)), ("fa_cache_evict", EVICT, ("C", "C2")),
+    ("fa_fwd_sink", FWD, ("Nkv", "Nq")), ("fa_bwd_sink", BWD, ("Nkv", "Nq"))])
+def test_sizes_next_to_the_32_bit_limit(lib, fn, base, sizes):
+    """Lengths whose last block's or cluster's indices would pass 2^31 are
+    refused, the ones below them are not (pointers 2^40 bytes apart, so that no
+    tensor overlaps another)."""
+    f = getattr(lib, fn)
+    far = {name: (i + 1) << 40 for i, name in enumerate(n for n in base if base[n] in P)}
+    one = dict(B=1, Hkv=1) | ({"H": 1} if "H" in base else {})
+    small = {n: 64 for n in ("N", "C", "C2", "Nq", "Nkv", "keep") if n in base}
+    for name in sizes:
+        for n in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 65535):
+            assert _call(f, base, base, far | one | small | {name: n}) == INVALID, (name, n)
+        if _no_gpu() and name != "Nq":   # (its rows are not the largest tensor of every call)
+            assert _call(f, base, base, far | one | small | {name: 2 ** 31 - 65536}) == UNSUPPORTED, name
+
+
 def test_python_refusals_before_the_library():
     torch = pytest.importorskip("torch")
     c = fa.cache_empty(2, 2, 16, 64, torch.bfloat16, device="cpu")
