@@ -284,7 +284,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const EvictParams p)
         if (row < rows) {
             const uint32_t bh = row / (uint32_t)p.C2;
             const int d = (int)(row - bh * p.C2);
-            const int src = d < p.keep ? __ldg(p.index + (size_t)bh * p.keep + d) : -1;
+            // (not through the read-only path: the index was written while this grid was already there)
+            const int src = d < p.keep ? __ldcg(p.index + (size_t)bh * p.keep + d) : -1;
             if (src >= 0)
                 from[k] = (long long)bh * p.C + src;
         }
