@@ -21,8 +21,8 @@
 //
 // What bounds it: a decoded token reads every visible row once, D/2 + 4 bytes
 // for each of K and V, and does 4 G Nq D operations on it -- HBM, at the few
-// query rows per key head of decoding, if unpacking keeps up: 64 codes per
-// lane and 16 tokens for each of K and V, about one integer operation each.
+// query rows per key head of decoding, if unpacking keeps up: 16 tokens are 64
+// codes per lane for each of K and V, about five integer operations per eight.
 // Hence mma.sync and not tcgen05: the codes go from shared memory through
 // registers (unpacking) straight into A fragments (16 tokens or channels x 16)
 // with the 8 query rows as the N dimension, where tcgen05 would want the
