@@ -329,9 +329,9 @@ class PackedCache(tuple):
     def __new__(cls, k_codes, k_params, v_codes, v_params):
         import torch
         shape = k_codes.shape
-        if len(shape) != 4 or v_codes.shape != shape or k_params.shape != v_params.shape or (
+        if len(shape) != 4 or 0 in shape or v_codes.shape != shape or k_params.shape != v_params.shape or (
                 k_params.shape != (*shape[:3], 2)):
-            raise ValueError("a cache is codes [B, Hkv, C, D/2] and params [B, Hkv, C, 2] for K and for V")
+            raise ValueError("a cache is codes [B, Hkv, C, D/2] and params [B, Hkv, C, 2] for K and for V, none empty")
         if k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8 or k_params.dtype != v_params.dtype:
             raise TypeError("cache codes are uint8, the params of K and V of one type")
         if not (k_codes.is_contiguous() and k_params.is_contiguous() and v_codes.is_contiguous()

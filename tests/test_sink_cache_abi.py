@@ -166,3 +166,10 @@ def test_python_refusals_before_the_library():
             fa.forward(q, k, k, sinks=bad.get("sinks", 0), window=bad.get("window", (3, 0)))
     with pytest.raises(ValueError):
         fa.cache_evict(c, torch.zeros(2, 2, 16), ints, 4, sinks=3, recent=2)
+
+
+@pytest.mark.parametrize("sizes", [(0, 2, 16), (2, 0, 16), (2, 2, 0)], ids=str)
+def test_empty_caches_are_refused(sizes):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError):
+        fa.cache_empty(*sizes, 64, torch.bfloat16, device="cpu")
