@@ -184,8 +184,10 @@ FA_API fa_status fa_fwd_band(const void *Q, const void *K, const void *V, void *
  * [B, H, Nq] float32.  With i' = i + (Nkv - Nq), query i sees the keys
  * j <= i' with j >= i' - window_left (window_left < 0: no bound) or
  * j < sinks.  A query that sees no key (i' < 0) gets O = 0 and LSE = -inf.
- * Key tiles that hold neither a sink nor a key of some row's window are
- * skipped, not masked.
+ * Key tiles (128 keys) that hold neither a sink nor a key of some row's window
+ * are skipped, not masked.  What K holds at a key does not reach the queries
+ * that do not see it; V must be finite in every tile that is visited, as a
+ * hidden key's weight 0 still multiplies it.
  *
  * workspace : device memory, 16-byte aligned, of at least the bytes that
  *             fa_fwd_sink_workspace gives for the same arguments (0 where the
@@ -323,7 +325,8 @@ FA_API fa_status fa_bwd_ex(const void *Q, const void *K, const void *V, const vo
  * Q, O, dO, dQ : contiguous [B, H, Nq, D];  K, V, dK, dV : contiguous
  * [B, Hkv, Nkv, D], the gradients of a shared key head summed over its query
  * heads in fp32;  LSE : [B, H, Nq] float32.  A query that sees no key gets
- * dQ = 0; a key that no query sees dK = dV = 0.
+ * dQ = 0; a key that no query sees dK = dV = 0.  Q, K, V, O and dO must be
+ * finite in every tile that is visited.
  * flags : 0 or FA_BWD_DETERMINISTIC, as for fa_bwd_ex (dK and dV are the same
  *         bits on every call either way: a sink tile's query tiles are summed
  *         in parts, the parts added in a fixed order).

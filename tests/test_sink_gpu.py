@@ -236,6 +236,27 @@ def test_hidden_keys_may_hold_anything(D):
     assert torch.equal(a[1][:, :, :128], b[1][:, :, :128]) and torch.equal(a[1][:, :, 1024:], b[1][:, :, 1024:])
 
 
+@pytest.mark.parametrize("schedule", ["whole_tiles", "balanced"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_that_are_not_finite_reach_only_their_queries(D, schedule):
+    """Keys of visited tiles -- one next to the sinks, two in the windows -- that
+    hold NaN or infinities: the rows that do not see them keep every bit."""
+    N, left, sinks = 1200, 200, 4
+    q, k, v, _ = _inputs(1, 4, 2, N, N, D, "bf16", seed=6)
+    dirty = k.clone()
+    rows = torch.arange(N, device="cuda")
+    blind = torch.ones(N, dtype=torch.bool, device="cuda")
+    for j, x in ((10, math.nan), (500, math.inf), (900, -math.inf)):
+        dirty[:, :, j] = x
+        blind &= ~((rows >= j) & (rows - left <= j))
+    want = fa.forward(q, k, v, window=(left, 0), sinks=sinks, schedule=schedule)
+    got = fa.forward(q, dirty, v, window=(left, 0), sinks=sinks, schedule=schedule)
+    _ok()
+    assert int(blind.sum()) == N - 3 * (left + 1)
+    assert torch.equal(want[0][:, :, blind], got[0][:, :, blind])
+    assert torch.equal(want[1][:, :, blind], got[1][:, :, blind])
+
+
 def test_graphs_and_streams():
     """Captured forward and backward, two graphs replayed at once on two
     streams while eager calls run on a third: the same bits."""
