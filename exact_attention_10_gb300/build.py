@@ -1,11 +1,12 @@
 """Build the CUDA library (libfa_gb300.so) in-tree with nvcc for sm_103a.
 
-Eight translation units, compiled in parallel and linked into one shared
+Nine translation units, compiled in parallel and linked into one shared
 library: csrc/fa_api.cu (the C ABI and the whole-tile kernel variants without
 a mask or with the causal one), csrc/fa_split.cu (the same for the balanced
 schedule), csrc/fa_band.cu (left-bounded band masks, both schedules),
 csrc/fa_sink.cu (windows with sinks, both schedules),
-csrc/fa_bwd.cu and fa_bwd_sink.cu (the backward), csrc/fa_cache.cu (the 4-bit cache) and
+csrc/fa_bwd.cu and fa_bwd_sink.cu (the backward), csrc/fa_cache.cu (the 4-bit cache),
+csrc/fa_cache_rows.cu (the weights of its tokens for many query rows) and
 csrc/fa_evict.cu (eviction from it), so the build stays quick on both the
 x86_64 build machine and the aarch64 GPU host.
 The runtime is linked statically and the driver's tensor-map encoder is
@@ -21,7 +22,8 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f) for f in ("fa_api.cu", "fa_split.cu", "fa_band.cu", "fa_sink.cu", "fa_bwd.cu",
-                                               "fa_bwd_sink.cu", "fa_cache.cu", "fa_evict.cu")]
+                                               "fa_bwd_sink.cu", "fa_cache.cu", "fa_cache_rows.cu",
+                                               "fa_evict.cu")]
 LIB_PATH = os.path.join(PKG, "libfa_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

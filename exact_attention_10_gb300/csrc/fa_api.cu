@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "fa_bwd_launch.h"
+#include "fa_cache_rows.h"
 #include "fa_host.h"
 #include "fa_launch.cuh"
 
@@ -811,12 +812,13 @@ extern "C" fa_status fa_sync_status(fa_stream_t stream)
         return FA_ERR_CUDA;
     }
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned int w_whole = 0, w_split = 0, w_band = 0, w_bwd = 0, w_sink = 0, w_bsink = 0;
+    unsigned int w_whole = 0, w_split = 0, w_band = 0, w_bwd = 0, w_sink = 0, w_bsink = 0, w_rows = 0;
     if (!fa_launch::take_status_word_whole(s, &w_whole) || !fa_launch::take_status_word_split(s, &w_split) ||
         !fa_launch::take_status_word_band(s, &w_band) || !fa_launch::take_status_word_bwd(s, &w_bwd) ||
-        !fa_launch::take_status_word_sink(s, &w_sink) || !fa_launch::take_status_word_bwd_sink(s, &w_bsink))
+        !fa_launch::take_status_word_sink(s, &w_sink) || !fa_launch::take_status_word_bwd_sink(s, &w_bsink) ||
+        !fa_launch::take_status_word_rows(s, &w_rows))
         return FA_ERR_CUDA;
-    if ((w_whole | w_split | w_band | w_bwd | w_sink | w_bsink) != 0) {
+    if ((w_whole | w_split | w_band | w_bwd | w_sink | w_bsink | w_rows) != 0) {
         // an aborted launch may have left split-tile counters non-zero
         int dev = -1;
         cudaGetDevice(&dev);

@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "fa_cache_kernel.cuh"
+#include "fa_cache_rows.h"
 #include "fa_host.h"
 
 namespace {
@@ -118,18 +119,6 @@ fa_status launch_weights_t(const cache::Params &p, int sms, cudaStream_t s, int 
     if (st != FA_OK)
         return st;
     cache::weights_kernel<D, BF16, NT><<<sms * 2, cache::kThreads, smem, s>>>(p);
-    return launched();
-}
-
-template <int D, bool BF16>
-fa_status launch_weights_rows(const cache::Params &p, int sms, cudaStream_t s, int dev)
-{
-    constexpr int smem = cache::RowsSmem<D>::kBytes;
-    static bool set[fa_host::kMaxDevices] = {};
-    const fa_status st = fa_host::allow_smem(reinterpret_cast<const void *>(&cache::weights_rows_kernel<D, BF16>), smem, dev, set);
-    if (st != FA_OK)
-        return st;
-    cache::weights_rows_kernel<D, BF16><<<sms * 2, cache::kThreads, smem, s>>>(p);
     return launched();
 }
 
@@ -309,7 +298,7 @@ extern "C" fa_status fa_cache_weights(const void *Q, const void *Kc, const void 
         constexpr bool BB = decltype(b)::value;
         if (rows <= 8)
             return launch_weights_t<DD, BB, 1>(p, di->sms, s, dev);
-        return rows <= 16 ? launch_weights_t<DD, BB, 2>(p, di->sms, s, dev) : launch_weights_rows<DD, BB>(p, di->sms, s, dev);
+        return rows <= 16 ? launch_weights_t<DD, BB, 2>(p, di->sms, s, dev) : fa_launch::launch_weights_rows(p, DD, BB, di->sms, s, dev);
     };
     using T = std::true_type;
     using F = std::false_type;

@@ -240,7 +240,7 @@ __device__ __forceinline__ RowScale row_scale(float mn, float mx)
 // round_half_even((x - mn) / sc) clamped to 0..15, exactly: the quotient by the
 // reciprocal, then the residual a - (q -+ 1/2) sc decides next to a border,
 // with the rounding error of a = x - mn added back.
-__device__ __noinline__ uint32_t code_of(float x, float mn, float sc, float inv)
+static __device__ __noinline__ uint32_t code_of(float x, float mn, float sc, float inv)
 {
     const float a = x - mn;
     const float bb = a - x;
@@ -484,8 +484,8 @@ struct Where {
     int b;                    // the sequence that holds unit `first`
 };
 
-// Called by every thread of the block (it reads all of lens); `scratch` holds
-// kWarps + 2 values.  Threads take consecutive sequences; an exclusive scan
+// Called by every thread of the block, kThreads or more (it reads all of lens);
+// `scratch` holds kWarps + 2 values.  The first kThreads threads take consecutive sequences; an exclusive scan
 // over the threads' sums, then the owning thread walks its own.
 __device__ inline Where locate(const Params &p, int k, int grid, long long *scratch)
 {
@@ -493,8 +493,9 @@ __device__ inline Where locate(const Params &p, int k, int grid, long long *scra
     const int per = (p.B + kThreads - 1) / kThreads;
     const long long HR = (long long)p.Hkv * p.RB;
     long long sum = 0;
-    for (int i = t * per; i < (t + 1) * per && i < p.B; ++i)
-        sum += span_of(p, i).n * HR;
+    if (t < kThreads)
+        for (int i = t * per; i < (t + 1) * per && i < p.B; ++i)
+            sum += span_of(p, i).n * HR;
     long long inc = sum;
 #pragma unroll
     for (int m = 1; m < 32; m *= 2) {
@@ -502,7 +503,7 @@ __device__ inline Where locate(const Params &p, int k, int grid, long long *scra
         if (lane >= m)
             inc += v;
     }
-    if (lane == 31)
+    if (lane == 31 && warp < kWarps)
         scratch[warp] = inc;
     __syncthreads();
     Where w{0, 0, 0, 0, 0};
@@ -1246,7 +1247,7 @@ __device__ __forceinline__ void zero_rest(const Params &p, float *acc, const Spa
 // scores again, K alone, with the LSE that the attention returned.  A token's
 // sum is formed by one warp, in a fixed order, and every entry of acc has one
 // writer, so nothing is added by atomics.  This kernel takes up to 8 NT query
-// rows, held as fragments in registers (decoding).
+// rows, held as fragments in registers (decoding); more go to fa_cache_rows.cu.
 template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, 2) weights_kernel(const Params p)
 {
@@ -1345,202 +1346,6 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(const Params p)
         }
         cp_wait<0>();
         __syncwarp();
-        if (!p.accumulate)
-            zero_rest(p, acc, sp, ku, ke);
-        u += ke - ku;
-        ku = 0;
-        if (++h == p.Hkv && u < u1) {
-            h = 0;
-            sp = span_of(p, ++b);
-        }
-    }
-}
-
-// The same for more query rows than a warp holds in registers (a prompt's last
-// tokens): blocks of 64, their fragments and columns' constants in shared
-// memory, filled by the eight warps together.  A block's 16 products per 16
-// tokens and 16 channels share the unpacked codes; each fragment read from
-// shared memory serves two of them (32 tokens).  Further blocks go through the
-// cache again, from L2, and add.  (2 x 8 key heads, 20000 and 32768 tokens, 64
-// rows, D = 128: 31 us; with 32 rows in registers at a time, which leaves one CTA
-// per SM, 45.)
-constexpr int kRowBlock = 64;
-
-template <int D>
-struct RowsSmem {
-    static constexpr int kFrag = kRowBlock / 8 * (D / 16) * 32 * 8;   // [nt][k-step][lane] two words
-    static constexpr int kPipe = kWarps * kStages * Layout<D>::kKeyStage;
-    static constexpr int kConst = kRowBlock * 16;                      // mul, sum, ref, rest per row
-    static constexpr int kBounds = kRowBlock * 16;                     // lo, hi, sink per row
-    static constexpr int kBytes = kPipe + kFrag + kConst + kBounds;
-};
-
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) weights_rows_kernel(const Params p)
-{
-    using L = Layout<D>;
-    using S = RowsSmem<D>;
-    constexpr int kSteps = D / 16, kNT = kRowBlock / 8;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long scratch[kWarps + 2];
-    __shared__ int s_edge[2][kWarps];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-    const uint32_t ring = base + (uint32_t)(warp * kStages * L::kKeyStage);
-    const uint32_t frag = base + S::kPipe + lane * 8;
-    float4 *s_const = reinterpret_cast<float4 *>(smem + S::kPipe + S::kFrag);
-    int4 *s_bounds = reinterpret_cast<int4 *>(smem + S::kPipe + S::kFrag + S::kConst);
-    const Where w = locate(p, blockIdx.x, gridDim.x, scratch);
-    if ((long long)blockIdx.x >= w.parts)
-        return;
-    const long long u0 = w.first, u1 = w.total * (blockIdx.x + 1) / w.parts;
-    int b = w.b;
-    Span sp = span_of(p, b);
-    int h = (int)((u0 - w.before) / sp.n);
-    int ku = (int)((u0 - w.before) - (long long)h * sp.n);
-    for (long long u = u0; u < u1;) {
-        const int ke = (int)((long long)sp.n - ku < u1 - u ? sp.n : ku + (u1 - u));
-        const long long bh = (long long)b * p.Hkv + h;
-        float *acc = p.acc + bh * p.C;
-        const Rows<D> rows(p, bh);
-        const int nsub = (ke - ku) * (kUnit / kSub);
-        auto token = [&](int s) { return sp.token(ku + s / (kUnit / kSub)) + (s % (kUnit / kSub)) * kSub; };
-        for (int r0 = 0; r0 < p.rows; r0 += kRowBlock) {
-            const bool add = p.accumulate || r0 > 0;
-#pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) {
-                const int s = warp + i * kWarps;
-                load_stage<D, false>(rows, ring + i * L::kKeyStage, s < nsub ? token(s) : 0, sp.len, s < nsub);
-            }
-            __syncthreads();   // the block before has been used by every warp
-            {   // rows 8 warp .. of the block
-                const int first = r0 + 8 * warp;
-                Queries<D, BF16, 1, true> q;
-                q.load(p, bh * p.rows + first, p.rows - first);
-#pragma unroll
-                for (int k = 0; k < kSteps; ++k)
-                    *reinterpret_cast<uint2 *>(smem + S::kPipe + ((warp * kSteps + k) * 32 + lane) * 8) =
-                        make_uint2(q.f[0][k][0], q.f[0][k][1]);
-                int lo = 0, hi = 0x7fffffff;
-                if (r == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int n = first + 2 * c + e;
-                        const float lse = n < p.rows ? p.lse[bh * p.rows + n] : -INFINITY;
-                        const float ref = lse * kLog2e;
-                        s_const[8 * warp + 2 * c + e] =
-                            lse == -INFINITY ? make_float4(q.mul[0][e], q.sum[0][e], INFINITY, 1.f)
-                                             : make_float4(q.mul[0][e], q.sum[0][e], ref,
-                                                           exp2f(-fmaf(lse, kLog2e, -ref) - lse * kLog2eRest));
-                        const Bounds v = bounds_of(p, sp.len, n < p.rows ? n : p.rows - 1);
-                        s_bounds[8 * warp + 2 * c + e] = make_int4(v.lo, v.hi, v.sink, 0);
-                        lo = max(lo, v.lo);
-                        hi = min(hi, v.hi);
-                    }
-                }
-                lo = __reduce_max_sync(0xffffffffu, lo);
-                hi = __reduce_min_sync(0xffffffffu, hi);
-                if (lane == 0) {
-                    s_edge[0][warp] = lo;
-                    s_edge[1][warp] = hi;
-                }
-            }
-            __syncthreads();
-            int edge_lo = 0, edge_hi = 0x7fffffff;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                edge_lo = max(edge_lo, s_edge[0][i]);
-                edge_hi = min(edge_hi, s_edge[1][i]);
-            }
-            int st = 0;
-            for (int s = warp; s < nsub; s += kWarps) {
-                cp_wait<kStages - 2>();
-                __syncwarp();
-                const int next = s + (kStages - 1) * kWarps;
-                const int fill = st + kStages - 1 >= kStages ? st - 1 : st + kStages - 1;
-                load_stage<D, false>(rows, ring + fill * L::kKeyStage, next < nsub ? token(next) : 0, sp.len, next < nsub);
-                const int t0 = token(s);
-                const bool masked = t0 < edge_lo || t0 + kSub > edge_hi;
-                const uint32_t stage = ring + st * L::kKeyStage;
-                float x[kNT][2][4];
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[nt][e / 4][e % 4] = 0.f;
-#pragma unroll
-                for (int w2 = 0; w2 < L::kWords / 2; ++w2) {   // two words of every row: four k-steps
-                    uint2 k[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        k[i] = lds64(stage + (uint32_t)((8 * i + r) * L::kRow + (c * L::kWords + 2 * w2) * 4));
-#pragma unroll
-                    for (int w1 = 0; w1 < 2; ++w1) {
-                        uint32_t a[2][2][4];   // [k-step][16 tokens]
-#pragma unroll
-                        for (int mt = 0; mt < 2; ++mt) {
-                            const uint32_t wa = w1 ? k[2 * mt].y : k[2 * mt].x, wb = w1 ? k[2 * mt + 1].y : k[2 * mt + 1].x;
-                            a[0][mt][0] = centred_even(wa);
-                            a[0][mt][1] = centred_even(wb);
-                            a[0][mt][2] = centred_odd(wa);
-                            a[0][mt][3] = centred_odd(wb);
-                            a[1][mt][0] = centred_even(wa >> 8);
-                            a[1][mt][1] = centred_even(wb >> 8);
-                            a[1][mt][2] = centred_odd(wa >> 8);
-                            a[1][mt][3] = centred_odd(wb >> 8);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint2 f = lds64(frag + (uint32_t)((nt * kSteps + 2 * (2 * w2 + w1) + i) * 256));
-                                mma(x[nt][0], a[i][0], f.x, f.y);
-                                mma(x[nt][1], a[i][1], f.x, f.y);
-                            }
-                    }
-                }
-                float sa[4], za[4], sum[4];   // tokens r, r + 8, r + 16, r + 24
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t v = lds32(stage + L::kCodes + (uint32_t)(8 * k + r) * 4);
-                    sa[k] = to_float<BF16>(v & 0xffffu);
-                    za[k] = fmaf(7.5f, sa[k], to_float<BF16>(v >> 16));
-                    sum[k] = 0.f;
-                }
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float4 k4 = s_const[8 * nt + 2 * c + e];
-                        float y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y[k] = fmaf(x[nt][k >> 1][e + 2 * (k & 1)] * k4.x, sa[k], fmaf(za[k], k4.y, -k4.z));
-                        if (masked) {
-                            const int4 v = s_bounds[8 * nt + 2 * c + e];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (!sees(Bounds{v.x, v.y, v.z}, t0 + 8 * k + r))
-                                    y[k] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            sum[k] = fmaf(ex2(y[k]), k4.w, sum[k]);
-                    }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-                    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-                }
-                const float mine = c == 0 ? sum[0] : (c == 1 ? sum[1] : (c == 2 ? sum[2] : sum[3]));
-                const int t = t0 + r + 8 * c;
-                if (t < sp.len)
-                    acc[t] = add ? acc[t] + mine : mine;
-                st = st + 1 == kStages ? 0 : st + 1;
-            }
-            cp_wait<0>();
-            __syncwarp();
-        }
         if (!p.accumulate)
             zero_rest(p, acc, sp, ku, ke);
         u += ke - ku;

@@ -1,0 +1,443 @@
+// fa_cache_rows.cu -- the weights of cached tokens (fa_cache_weights) for more
+// than 16 query rows per key head: a prompt's last tokens, or several drafted
+// tokens of many query heads.
+//
+//   acc[b, h, t] (+)= sum over the key head's rows n that see t of
+//                     exp(scale q_n . k_t - LSE_n)
+//
+// With 64 rows the scores are a matrix product of some size (K [tokens, D]
+// against Q^T), so they go through the tensor core proper: K's codes, centred
+// and exact in fp16 ((code - 7.5) 2^-9, as in fa_cache_kernel.cuh), are
+// unpacked into swizzled shared memory as the A operand of tcgen05.mma, 128
+// tokens a tile, against up to 64 query rows as B; the scores come back from
+// tensor memory one token to a thread, so that a token's sum needs no shuffle.
+//
+// Per 128 tokens and 64 rows at D = 128: 256 cycles of MMA, 512 of
+// exponentials (16 a cycle), and about 2000 warp instructions -- 500 cycles of
+// the four schedulers -- half unpacking, half the multiply-adds around the
+// exponentials, two columns at a time.  So the roles run beside one another:
+//   warps 0-3  the scores' exponentials and sums (TMEM lane = token)
+//   warps 4-7  unpacking: codes two tiles ahead in registers, fp16 to one of
+//              two stages
+//   warp 8     issues the MMAs
+// with two CTAs per SM.  Rows are taken 64 at a time; further blocks go
+// through the cache again, from L2, and add to what the first wrote.
+#include <cuda_runtime.h>
+
+#include "fa_cache_kernel.cuh"
+#include "fa_cache_rows.h"
+#include "fa_fwd_kernel.cuh"
+#include "fa_host.h"
+
+namespace fa {
+namespace cache {
+
+namespace {
+
+constexpr int kRowBlock = 64;       // query rows per pass over the cache
+constexpr int kTileTokens = 128;    // tokens per MMA tile: two units
+constexpr int kRowsThreads = 288;
+constexpr int kUnpackWarp = 4;      // the first of the four
+constexpr int kIssueWarp = 8;
+constexpr uint32_t kTmemCols = 2 * kRowBlock;
+
+// Wait sites for the status word.
+enum : uint32_t { kSiteRowsFull = 64, kSiteRowsFree, kSiteRowsDone, kSiteRowsReuse, kSiteRowsDrain };
+
+template <int D>
+struct RowsSmem {
+    static constexpr int kBoxes = D / 64;                        // 64 channels: a 128-byte swizzled row
+    static constexpr int kKBox = kTileTokens * 128;
+    static constexpr int kKStage = kBoxes * kKBox;
+    static constexpr int kQBox = kRowBlock * 128;
+    static constexpr int kQOff = 2 * kKStage;
+    static constexpr int kConstOff = kQOff + kBoxes * kQBox;     // mul, sum, -ref, rest of every row
+    static constexpr int kBoundsOff = kConstOff + 4 * kRowBlock * 4;
+    static constexpr int kEdgeOff = kBoundsOff + kRowBlock * 16;
+    static constexpr int kBarOff = kEdgeOff + 2 * kWarps * 4;
+    static constexpr int kScratchOff = kBarOff + 8 * 8;
+    static constexpr int kMiscOff = kScratchOff + (kWarps + 2) * 8;
+    static constexpr int kBytes = kMiscOff + 16 + 1024;          // (1024: alignment of the swizzle)
+};
+
+struct RowsBars {
+    uint32_t base;
+    __device__ uint32_t full(int s) const { return base + 8u * s; }         // unpacking -> MMA: stage s holds a tile
+    __device__ uint32_t done(int s) const { return base + 8u * (2 + s); }   // MMA: stage s read, scores s final
+    __device__ uint32_t free_(int s) const { return base + 8u * (4 + s); }  // sums -> MMA: scores s read out
+    __device__ uint32_t drain() const { return base + 8u * 6; }
+};
+
+// Token of row `r` of tile i of a segment (units [ku, ke)), -1: none.
+__device__ __forceinline__ int tile_token(const Span &sp, int ku, int ke, int i, int r)
+{
+    const int u = ku + 2 * i + r / kUnit;
+    if (u >= ke)
+        return -1;
+    const int t = sp.token(u) + r % kUnit;
+    return t < sp.len ? t : -1;
+}
+
+// Row `row` (of a tile or of the query block), 16-byte chunk `ch` of its fp16
+// values: 8 channels of one word of codes, as the pairs (0, 4), (1, 5), (2, 6),
+// (3, 7) in which they come out of it.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t box0, uint32_t box_bytes, int row, int ch)
+{
+    return box0 + (uint32_t)(ch / 8) * box_bytes + (uint32_t)row * 128u + (uint32_t)(((ch & 7) ^ (row & 7)) * 16);
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Rows 8 warp + r of the query block (r = lane / 4; channels [c D/4, (c + 1)
+// D/4) of lane c): fp16 times a power of two, as Queries::load does it, and
+// the row's constants and bounds.  Rows that are not there weigh nothing.
+template <int D, bool BF16>
+__device__ __forceinline__ void load_rows(const Params &p, long long bh, int r0, int len, uint32_t base, uint8_t *base_ptr)
+{
+    using S = RowsSmem<D>;
+    constexpr int kWords = D / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
+    const int n = 8 * warp + r;
+    const bool there = r0 + n < p.rows;
+    float x[kWords][8], s = 0.f, mx = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (there)
+            v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint32_t *>(p.q) + (bh * p.rows + r0 + n) * (D / 2)) +
+                      c * kWords + w);
+        const uint32_t xw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[w][i] = to_float<BF16>((i & 1) ? xw[i / 2] >> 16 : xw[i / 2] & 0xffffu);
+            s += x[w][i];
+            mx = fmaxf(mx, fabsf(x[w][i]));
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 4; m *= 2) {
+        s += __shfl_xor_sync(0xffffffffu, s, m);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+    }
+    int e = mx > 0.f ? 14 - (int)((__float_as_uint(mx) >> 23) & 255u) + 127 : 0;
+    e = e > 100 ? 100 : (e < -100 ? -100 : e);
+    const float up = exp2i(e);
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+        sts128(chunk_at(base + S::kQOff, S::kQBox, n, c * kWords + w), pack_f16(x[w][0] * up, x[w][4] * up),
+               pack_f16(x[w][1] * up, x[w][5] * up), pack_f16(x[w][2] * up, x[w][6] * up),
+               pack_f16(x[w][3] * up, x[w][7] * up));
+    int lo = 0, hi = 0x7fffffff;
+    if (c == 0) {
+        const float lse = there ? p.lse[bh * p.rows + r0 + n] : -INFINITY;
+        const float ref = lse * kLog2e;
+        float *k = reinterpret_cast<float *>(base_ptr + S::kConstOff) + n;
+        k[0] = p.qk2 * exp2i(9 - e);
+        k[kRowBlock] = s * p.qk2;
+        // what the scores are taken relative to; -inf where the row is not there or sees nothing
+        k[2 * kRowBlock] = lse == -INFINITY ? -INFINITY : -ref;
+        // 2 to the power of what its rounding left out
+        k[3 * kRowBlock] = lse == -INFINITY ? 1.f : exp2f(-fmaf(lse, kLog2e, -ref) - lse * kLog2eRest);
+        const Bounds v = bounds_of(p, len, there ? r0 + n : p.rows - 1);
+        reinterpret_cast<int4 *>(base_ptr + S::kBoundsOff)[n] = make_int4(v.lo, v.hi, v.sink, 0);
+        lo = v.lo;
+        hi = v.hi;
+    }
+    lo = __reduce_max_sync(0xffffffffu, lo);
+    hi = __reduce_min_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        int *edge = reinterpret_cast<int *>(base_ptr + S::kEdgeOff);
+        edge[warp] = lo;
+        edge[kWarps + warp] = hi;
+    }
+}
+
+// Unpacking: thread -> row tr of the tile and code chunk cc (16 bytes, 32
+// channels), so that the eight rows of a quarter warp store to different banks.
+template <int D>
+struct Unpacker {
+    static constexpr int kChunks = D / 32;      // of 16 bytes, codes of a token: 4 or 2
+    static constexpr int kRows = 32 / kChunks;  // rows per warp and round
+    static constexpr int kRounds = 32 / kRows;  // a warp has 32 of the tile's rows
+    uint4 next[2][kRounds];
+
+    __device__ __forceinline__ void fetch(uint4 (&x)[kRounds], const uint8_t *kc, const Span &sp, int ku, int ke, int i)
+    {
+        const int warp = threadIdx.x / 32 - kUnpackWarp, lane = threadIdx.x % 32;
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+            const int t = tile_token(sp, ku, ke, i, warp * 32 + k * kRows + lane % kRows);
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (t >= 0)
+                x[k] = __ldg(reinterpret_cast<const uint4 *>(kc + (long long)t * (D / 2)) + lane / kRows);
+        }
+    }
+
+    __device__ __forceinline__ void store(const uint4 (&x)[kRounds], uint32_t stage)
+    {
+        using S = RowsSmem<D>;
+        const int warp = threadIdx.x / 32 - kUnpackWarp, lane = threadIdx.x % 32;
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+            const int row = warp * 32 + k * kRows + lane % kRows;
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t y = w[j] >> 8;
+                sts128(chunk_at(stage, S::kKBox, row, 4 * (lane / kRows) + j), centred_even(w[j]), centred_odd(w[j]),
+                       centred_even(y), centred_odd(y));
+            }
+        }
+        ptx::fence_proxy_async_smem();
+    }
+};
+
+// One token's sum over the columns [c0, c0 + 16) of its scores; x holds those
+// from x0 on.
+template <bool MASKED>
+__device__ __forceinline__ void add_columns(const uint32_t (&x)[32], int c0, int x0, const float *k, const int4 *bounds, int t,
+                                            float sa, float za, uint64_t (&sum)[2])
+{
+    const uint64_t sa2 = ptx::f2_pack(sa, sa), za2 = ptx::f2_pack(za, za);
+#pragma unroll
+    for (int i = c0; i < c0 + 16; i += 4) {
+        const float4 mul = *reinterpret_cast<const float4 *>(k + i);
+        const float4 qs = *reinterpret_cast<const float4 *>(k + kRowBlock + i);
+        const float4 nref = *reinterpret_cast<const float4 *>(k + 2 * kRowBlock + i);
+        const float4 rest = *reinterpret_cast<const float4 *>(k + 3 * kRowBlock + i);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint64_t m2 = h ? ptx::f2_pack(mul.z, mul.w) : ptx::f2_pack(mul.x, mul.y);
+            const uint64_t q2 = h ? ptx::f2_pack(qs.z, qs.w) : ptx::f2_pack(qs.x, qs.y);
+            const uint64_t n2 = h ? ptx::f2_pack(nref.z, nref.w) : ptx::f2_pack(nref.x, nref.y);
+            const uint64_t r2 = h ? ptx::f2_pack(rest.z, rest.w) : ptx::f2_pack(rest.x, rest.y);
+            const uint64_t s2 = ptx::f2_pack(__uint_as_float(x[i - x0 + 2 * h]), __uint_as_float(x[i - x0 + 2 * h + 1]));
+            float y0, y1;
+            ptx::f2_unpack(ptx::f2_fma(ptx::f2_mul(s2, m2), sa2, ptx::f2_fma(za2, q2, n2)), y0, y1);
+            if (MASKED) {
+                const int4 a = bounds[i + 2 * h], b = bounds[i + 2 * h + 1];
+                y0 = sees(Bounds{a.x, a.y, a.z}, t) ? y0 : -INFINITY;
+                y1 = sees(Bounds{b.x, b.y, b.z}, t) ? y1 : -INFINITY;
+            }
+            sum[h] = ptx::f2_fma(ptx::f2_pack(ex2(y0), ex2(y1)), r2, sum[h]);
+        }
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Params p)
+{
+    using S = RowsSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *base_ptr = smem_raw + (base - raw);
+    const RowsBars b{base + S::kBarOff};
+    uint32_t *misc = reinterpret_cast<uint32_t *>(base_ptr + S::kMiscOff);
+    const Ctl c{reinterpret_cast<volatile int *>(misc + 1)};
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    const Where w = locate(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(base_ptr + S::kScratchOff));
+    if ((long long)blockIdx.x >= w.parts)
+        return;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(b.full(s), 4);
+            ptx::mbar_init(b.done(s), 1);
+            ptx::mbar_init(b.free_(s), 4);
+        }
+        ptx::mbar_init(b.drain(), 1);
+        *c.abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == kIssueWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(misc), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc);
+
+    const long long u0 = w.first, u1 = w.total * (blockIdx.x + 1) / w.parts;
+    int bb = w.b;
+    Span sp = span_of(p, bb);
+    int h = (int)((u0 - w.before) / sp.n);
+    int ku = (int)((u0 - w.before) - (long long)h * sp.n);
+    uint32_t it = 0;   // tiles before this pass: tile j of it is number it + j, in stage (it + j) % 2
+    bool ok = true;
+    for (long long u = u0; u < u1 && ok;) {
+        const int ke = (int)((long long)sp.n - ku < u1 - u ? sp.n : ku + (u1 - u));
+        const long long bh = (long long)bb * p.Hkv + h;
+        float *acc = p.acc + bh * p.C;
+        const int nt = (ke - ku + 1) / 2;
+        for (int r0 = 0; r0 < p.rows && ok; r0 += kRowBlock) {
+            const int nrows = p.rows - r0 < kRowBlock ? p.rows - r0 : kRowBlock;
+            const int cols = (nrows + 15) & ~15;
+            // (every role is through with the block before: its last MMA is
+            // read out, and the sums have its constants behind them)
+            if (warp < kWarps) {
+                load_rows<D, BF16>(p, bh, r0, sp.len, base, base_ptr);
+                ptx::fence_proxy_async_smem();
+            }
+            __syncthreads();
+            if (warp == kIssueWarp) {
+                const uint32_t idesc = instr_desc_f16(false, kTileTokens, cols, false);
+                for (int i = 0; i < nt && ok; ++i) {
+                    const uint32_t n = it + i, s = n & 1u;
+                    ok = warp_wait(b.full(s), (n >> 1) & 1u, c, kSiteRowsFull) &&
+                         (n < 2 || warp_wait(b.free_(s), ((n >> 1) - 1u) & 1u, c, kSiteRowsFree));
+                    if (!ok)
+                        break;
+                    ptx::tc_fence_after_sync();
+                    if (ptx::elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            ptx::mma_ss(tmem + s * kRowBlock,
+                                        smem_desc_sw128(base + s * S::kKStage + (kk / 4) * S::kKBox + (kk % 4) * 32, 16),
+                                        smem_desc_sw128(base + S::kQOff + (kk / 4) * S::kQBox + (kk % 4) * 32, 16), idesc,
+                                        kk > 0 ? 1u : 0u);
+                        ptx::mma_commit(b.done(s));
+                    }
+                    __syncwarp();
+                }
+            } else if (warp >= kUnpackWarp) {
+                Unpacker<D> x;
+                const uint8_t *kc = p.kc + bh * p.C * (D / 2);
+                x.fetch(x.next[0], kc, sp, ku, ke, 0);
+                x.fetch(x.next[1], kc, sp, ku, ke, 1);
+                for (int i = 0; i < nt && ok; i += 2) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t n = it + i + e, s = n & 1u;
+                        if (i + e >= nt)
+                            break;
+                        if (n >= 2 && !warp_wait(b.done(s), ((n >> 1) - 1u) & 1u, c, kSiteRowsReuse)) {
+                            ok = false;
+                            break;
+                        }
+                        x.store(x.next[e], base + s * S::kKStage);
+                        __syncwarp();
+                        if (lane == 0)
+                            ptx::mbar_arrive(b.full(s));
+                        x.fetch(x.next[e], kc, sp, ku, ke, i + e + 2);
+                    }
+                }
+            } else {
+                const bool add = p.accumulate || r0 > 0;
+                const float *k = reinterpret_cast<const float *>(base_ptr + S::kConstOff);
+                const int4 *bounds = reinterpret_cast<const int4 *>(base_ptr + S::kBoundsOff);
+                const int *edge = reinterpret_cast<const int *>(base_ptr + S::kEdgeOff);
+                int edge_lo = 0, edge_hi = 0x7fffffff;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) {
+                    edge_lo = max(edge_lo, edge[i]);
+                    edge_hi = min(edge_hi, edge[kWarps + i]);
+                }
+                const uint32_t *kp = p.kp + bh * p.C;
+                int t = tile_token(sp, ku, ke, 0, threadIdx.x);
+                uint32_t par = t >= 0 ? __ldg(kp + t) : 0u;
+                for (int i = 0; i < nt; ++i) {
+                    const uint32_t n = it + i, s = n & 1u;
+                    const float sa = to_float<BF16>(par & 0xffffu), za = fmaf(7.5f, sa, to_float<BF16>(par >> 16));
+                    const int now = t;
+                    t = tile_token(sp, ku, ke, i + 1, threadIdx.x);
+                    par = t >= 0 ? __ldg(kp + t) : 0u;
+                    const float old = add && now >= 0 ? acc[now] : 0.f;
+                    if (!warp_wait(b.done(s), (n >> 1) & 1u, c, kSiteRowsDone)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after_sync();
+                    // (a tile's absent tokens, -1 here, are not looked at)
+                    const bool masked = __any_sync(0xffffffffu, now >= 0 && (now < edge_lo || now >= edge_hi));
+                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int x0 = 0; x0 < kRowBlock; x0 += 32) {
+                        if (x0 >= cols)
+                            break;
+                        uint32_t x[32];
+                        ptx::tmem_ld32(tmem + s * kRowBlock + x0 + ((uint32_t)warp << 21), x);
+                        ptx::tmem_wait_ld();
+                        if (x0 + 32 >= cols) {   // all read out
+                            ptx::tc_fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0)
+                                ptx::mbar_arrive(b.free_(s));
+                        }
+#pragma unroll
+                        for (int c0 = x0; c0 < x0 + 32; c0 += 16)
+                            if (c0 < cols) {
+                                if (masked)
+                                    add_columns<true>(x, c0, x0, k, bounds, now, sa, za, sum);
+                                else
+                                    add_columns<false>(x, c0, x0, k, bounds, now, sa, za, sum);
+                            }
+                    }
+                    float a0, a1;
+                    ptx::f2_unpack(ptx::f2_add(sum[0], sum[1]), a0, a1);
+                    if (now >= 0)
+                        acc[now] = old + (a0 + a1);
+                }
+            }
+            it += (uint32_t)nt;
+            ok = __syncthreads_and(ok);
+        }
+        if (!p.accumulate && warp < kWarps)
+            zero_rest(p, acc, sp, ku, ke);
+        u += ke - ku;
+        ku = 0;
+        if (++h == p.Hkv && u < u1) {
+            h = 0;
+            sp = span_of(p, ++bb);
+        }
+    }
+    if (warp == kIssueWarp) {   // every MMA has completed before its TMEM is given back
+        if (ptx::elect_one())
+            ptx::mma_commit(b.drain());
+        __syncwarp();
+        wait_landed(b.drain(), 0u, c, kSiteRowsDrain);
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kIssueWarp) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool BF16>
+fa_status launch(const Params &p, int sms, cudaStream_t s, int dev)
+{
+    constexpr int smem = RowsSmem<D>::kBytes;
+    static bool set[fa_host::kMaxDevices] = {};
+    const fa_status st = fa_host::allow_smem(reinterpret_cast<const void *>(&weights_rows_kernel<D, BF16>), smem, dev, set);
+    if (st != FA_OK)
+        return st;
+    weights_rows_kernel<D, BF16><<<sms * 2, kRowsThreads, smem, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace cache
+}  // namespace fa
+
+namespace fa_launch {
+
+fa_status launch_weights_rows(const fa::cache::Params &p, int D, bool bf16, int sms, cudaStream_t s, int dev)
+{
+    if (D == 64)
+        return bf16 ? fa::cache::launch<64, true>(p, sms, s, dev) : fa::cache::launch<64, false>(p, sms, s, dev);
+    return bf16 ? fa::cache::launch<128, true>(p, sms, s, dev) : fa::cache::launch<128, false>(p, sms, s, dev);
+}
+
+bool take_status_word_rows(cudaStream_t s, unsigned int *word)
+{
+    return fa::take_status_word_on(s, word);
+}
+
+}  // namespace fa_launch

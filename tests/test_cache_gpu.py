@@ -312,6 +312,57 @@ def test_attention_and_weights(case, D, dtype):
     assert bool(((acc - 3.0).double() - w_ref).abs().le(tol + 2.0 ** -21).all())
 
 
+ROWS = [  # as above, with more than 16 query rows per key head
+    (1, 17, 1, 1, 1, [1], -1, 0),
+    (1, 4, 1, 5, 64, [64], -1, 0),
+    (2, 8, 2, 8, 200, [65, 200], -1, 0),                # 32 rows; an odd number of units
+    (1, 3, 1, 11, 500, [500], -1, 0),                   # 33
+    (1, 8, 1, 8, 1000, [937], -1, 0),                   # 64, one whole block
+    (2, 5, 1, 13, 700, [700, 129], -1, 0),              # 65: a second block of one row
+    (2, 8, 1, 20, 600, [600, 10], 64, 5),               # 160; some queries see nothing
+    (3, 20, 1, 1, 300, [0, 400, -5], 20, 3),            # no tokens; lengths outside [0, C]
+    (1, 8, 2, 5, 3001, [2999], 255, 4),                 # units left out between sinks and window: tiles of two places
+    (2, 16, 4, 6, 2000, [1500, 130], 64, 70),
+    (1, 24, 1, 1, 4000, [3999], 1000, 65),
+    (1, 6, 1, 3, 40000, [39990], -1, 0),                # shared out over many CTAs
+    (40, 18, 1, 1, 200, None, -1, 0),
+    (300, 20, 1, 1, 70, None, 20, 3),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", ROWS, ids=lambda c: "-".join(map(str, c[:5])) + f"-w{c[6]}s{c[7]}")
+def test_attention_and_weights_of_many_rows(case, D, dtype):
+    test_attention_and_weights(case, D, dtype)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_of_many_rows_run_to_run_and_hidden(D):
+    """The same bits on every call and beside another stream's calls; rows that a
+    query does not see, and those behind the sequence, may hold anything."""
+    q, cache, lens, left, sinks = _attention_case((3, 12, 2, 9, 3000, [2900, 64, 1501], 700, 9), D, "bf16", seed=21)
+    _, lse = fa.cache_forward(q, cache, lens, window=(left, 0), sinks=sinks)
+    want = fa.cache_weights(q, cache, lse, lens, window=(left, 0), sinks=sinks)
+    dirty = fa.PackedCache(*(x.clone() for x in cache))
+    for b, n in enumerate(lens.tolist()):
+        dirty[0][b, :, n:] = 255
+        dirty[1][b, :, n:] = math.nan
+        first = max(0, n - 9 - left)   # the first query's window
+        if first > sinks:
+            dirty[1][b, :, sinks:first] = math.inf
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = fa.cache_weights(q, dirty, lse, lens, window=(left, 0), sinks=sinks)
+        with torch.cuda.stream(side):
+            other = fa.cache_weights(q, cache, lse, lens, window=(left, 0), sinks=sinks)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(other, want)
+    _ok()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_large_scores(D):
     """Queries four times larger: the maximum moves often, single tokens dominate."""
