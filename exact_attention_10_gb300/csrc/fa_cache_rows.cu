@@ -8,18 +8,21 @@
 // With 64 rows the scores are a matrix product of some size (K [tokens, D]
 // against Q^T), so they go through the tensor core proper: K's codes, centred
 // and exact in fp16 ((code - 7.5) 2^-9, as in fa_cache_kernel.cuh), are
-// unpacked into swizzled shared memory as the A operand of tcgen05.mma, 128
-// tokens a tile, against up to 64 query rows as B; the scores come back from
-// tensor memory one token to a thread, so that a token's sum needs no shuffle.
+// unpacked into tensor memory, one token to a thread, as the A operand of
+// tcgen05.mma, 128 tokens a tile, against up to 64 query rows as B; the scores
+// come back from tensor memory as fragments, four tokens and a quarter of the
+// columns to a thread, so that a column's constants serve four tokens.
 //
-// Per 128 tokens and 64 rows at D = 128: 256 cycles of MMA, 512 of
-// exponentials (16 a cycle), and about 2000 warp instructions -- 500 cycles of
-// the four schedulers -- half unpacking, half the multiply-adds around the
-// exponentials, two columns at a time.  So the roles run beside one another:
-//   warps 0-3  the scores' exponentials and sums (TMEM lane = token)
-//   warps 4-7  unpacking: codes two tiles ahead in registers, fp16 to one of
-//              two stages
-//   warp 8     issues the MMAs
+// (Shared memory is what bound this with K unpacked there and a token's scores
+// to a thread: per 128 tokens, 64 rows and D = 128, 280 cycles of stores, 380 of
+// the MMA's reads and 730 of constants, of the 1400 that a tile took.)
+//
+// Roles, beside one another:
+//   warps 0-7   the scores' exponentials and sums, two groups of four that take
+//               every other tile
+//   warps 8-11  unpacking: codes two tiles ahead in registers, fp16 to one of
+//               two stages
+//   warp 12     issues the MMAs
 // with two CTAs per SM.  Rows are taken 64 at a time; further blocks go
 // through the cache again, from L2, and add to what the first wrote.
 #include <cuda_runtime.h>
@@ -36,10 +39,11 @@ namespace {
 
 constexpr int kRowBlock = 64;       // query rows per pass over the cache
 constexpr int kTileTokens = 128;    // tokens per MMA tile: two units
-constexpr int kRowsThreads = 288;
-constexpr int kUnpackWarp = 4;      // the first of the four
-constexpr int kIssueWarp = 8;
-constexpr uint32_t kTmemCols = 2 * kRowBlock;
+constexpr int kRowsThreads = 416;
+constexpr int kUnpackWarp = 8;      // the first of the four
+constexpr int kIssueWarp = 12;
+constexpr int kScoreCols = 2 * kRowBlock;   // TMEM: two stages of scores, then two of K (D / 2 columns each)
+constexpr uint32_t kTmemCols = 256;         // (two CTAs per SM share 512)
 
 // Wait sites for the status word.
 enum : uint32_t { kSiteRowsFull = 64, kSiteRowsFree, kSiteRowsDone, kSiteRowsReuse, kSiteRowsDrain };
@@ -47,11 +51,8 @@ enum : uint32_t { kSiteRowsFull = 64, kSiteRowsFree, kSiteRowsDone, kSiteRowsReu
 template <int D>
 struct RowsSmem {
     static constexpr int kBoxes = D / 64;                        // 64 channels: a 128-byte swizzled row
-    static constexpr int kKBox = kTileTokens * 128;
-    static constexpr int kKStage = kBoxes * kKBox;
     static constexpr int kQBox = kRowBlock * 128;
-    static constexpr int kQOff = 2 * kKStage;
-    static constexpr int kConstOff = kQOff + kBoxes * kQBox;     // mul, sum, -ref, rest of every row
+    static constexpr int kConstOff = kBoxes * kQBox;             // the rows' constants, see load_rows
     static constexpr int kBoundsOff = kConstOff + 4 * kRowBlock * 4;
     static constexpr int kEdgeOff = kBoundsOff + kRowBlock * 16;
     static constexpr int kBarOff = kEdgeOff + 2 * kWarps * 4;
@@ -62,25 +63,39 @@ struct RowsSmem {
 
 struct RowsBars {
     uint32_t base;
-    __device__ uint32_t full(int s) const { return base + 8u * s; }         // unpacking -> MMA: stage s holds a tile
-    __device__ uint32_t done(int s) const { return base + 8u * (2 + s); }   // MMA: stage s read, scores s final
+    __device__ uint32_t full(int s) const { return base + 8u * s; }         // unpacking -> MMA: stage s of K holds a tile
+    __device__ uint32_t done(int s) const { return base + 8u * (2 + s); }   // MMA: K s read, scores s final
     __device__ uint32_t free_(int s) const { return base + 8u * (4 + s); }  // sums -> MMA: scores s read out
     __device__ uint32_t drain() const { return base + 8u * 6; }
 };
 
-// Token of row `r` of tile i of a segment (units [ku, ke)), -1: none.
-__device__ __forceinline__ int tile_token(const Span &sp, int ku, int ke, int i, int r)
+// The 32 tokens of tile i of a segment (units [ku, ke)) that a warp of quadrant
+// `quad` has: t0 .., of which those before `end` are there.
+__device__ __forceinline__ int tile_tokens(const Span &sp, int ku, int ke, int i, int quad, int &end)
 {
-    const int u = ku + 2 * i + r / kUnit;
-    if (u >= ke)
-        return -1;
-    const int t = sp.token(u) + r % kUnit;
-    return t < sp.len ? t : -1;
+    const int u = ku + 2 * i + quad / 2;
+    end = u < ke ? sp.len : 0;
+    return sp.token(u) + quad % 2 * kSub;
 }
 
-// Row `row` (of a tile or of the query block), 16-byte chunk `ch` of its fp16
-// values: 8 channels of one word of codes, as the pairs (0, 4), (1, 5), (2, 6),
-// (3, 7) in which they come out of it.
+// Loads that stay where they are written: ahead of their use.
+__device__ __forceinline__ uint4 ld_ahead(const uint4 *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_ahead(const uint32_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// Row `row` of the query block, 16-byte chunk `ch` of its fp16 values: 8
+// channels, in the order in which K's come out of a word of codes, the pairs
+// (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ uint32_t chunk_at(uint32_t box0, uint32_t box_bytes, int row, int ch)
 {
     return box0 + (uint32_t)(ch / 8) * box_bytes + (uint32_t)row * 128u + (uint32_t)(((ch & 7) ^ (row & 7)) * 16);
@@ -93,7 +108,8 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 
 // Rows 8 warp + r of the query block (r = lane / 4; channels [c D/4, (c + 1)
 // D/4) of lane c): fp16 times a power of two, as Queries::load does it, and
-// the row's constants and bounds.  Rows that are not there weigh nothing.
+// the row's constants and bounds.  Rows that are not there weigh nothing.  The
+// constants of rows 2 i and 2 i + 1 are eight floats: mul, sum, -ref, rest of both.
 template <int D, bool BF16>
 __device__ __forceinline__ void load_rows(const Params &p, long long bh, int r0, int len, uint32_t base, uint8_t *base_ptr)
 {
@@ -127,20 +143,20 @@ __device__ __forceinline__ void load_rows(const Params &p, long long bh, int r0,
     const float up = exp2i(e);
 #pragma unroll
     for (int w = 0; w < kWords; ++w)
-        sts128(chunk_at(base + S::kQOff, S::kQBox, n, c * kWords + w), pack_f16(x[w][0] * up, x[w][4] * up),
+        sts128(chunk_at(base, S::kQBox, n, c * kWords + w), pack_f16(x[w][0] * up, x[w][4] * up),
                pack_f16(x[w][1] * up, x[w][5] * up), pack_f16(x[w][2] * up, x[w][6] * up),
                pack_f16(x[w][3] * up, x[w][7] * up));
     int lo = 0, hi = 0x7fffffff;
     if (c == 0) {
         const float lse = there ? p.lse[bh * p.rows + r0 + n] : -INFINITY;
         const float ref = lse * kLog2e;
-        float *k = reinterpret_cast<float *>(base_ptr + S::kConstOff) + n;
+        float *k = reinterpret_cast<float *>(base_ptr + S::kConstOff) + n / 2 * 8 + n % 2;
         k[0] = p.qk2 * exp2i(9 - e);
-        k[kRowBlock] = s * p.qk2;
+        k[2] = s * p.qk2;
         // what the scores are taken relative to; -inf where the row is not there or sees nothing
-        k[2 * kRowBlock] = lse == -INFINITY ? -INFINITY : -ref;
+        k[4] = lse == -INFINITY ? -INFINITY : -ref;
         // 2 to the power of what its rounding left out
-        k[3 * kRowBlock] = lse == -INFINITY ? 1.f : exp2f(-fmaf(lse, kLog2e, -ref) - lse * kLog2eRest);
+        k[6] = lse == -INFINITY ? 1.f : exp2f(-fmaf(lse, kLog2e, -ref) - lse * kLog2eRest);
         const Bounds v = bounds_of(p, len, there ? r0 + n : p.rows - 1);
         reinterpret_cast<int4 *>(base_ptr + S::kBoundsOff)[n] = make_int4(v.lo, v.hi, v.sink, 0);
         lo = v.lo;
@@ -155,74 +171,70 @@ __device__ __forceinline__ void load_rows(const Params &p, long long bh, int r0,
     }
 }
 
-// Unpacking: thread -> row tr of the tile and code chunk cc (16 bytes, 32
-// channels), so that the eight rows of a quarter warp store to different banks.
+// Unpacking: a thread has one token of the tile (its TMEM lane), whose codes it
+// loads two tiles ahead.
 template <int D>
 struct Unpacker {
-    static constexpr int kChunks = D / 32;      // of 16 bytes, codes of a token: 4 or 2
-    static constexpr int kRows = 32 / kChunks;  // rows per warp and round
-    static constexpr int kRounds = 32 / kRows;  // a warp has 32 of the tile's rows
-    uint4 next[2][kRounds];
+    static constexpr int kChunks = D / 32;   // of 16 bytes, codes of a token
+    uint4 next[2][kChunks];
 
-    __device__ __forceinline__ void fetch(uint4 (&x)[kRounds], const uint8_t *kc, const Span &sp, int ku, int ke, int i)
+    __device__ __forceinline__ void fetch(uint4 (&x)[kChunks], const uint8_t *kc, const Span &sp, int ku, int ke, int i)
     {
-        const int warp = threadIdx.x / 32 - kUnpackWarp, lane = threadIdx.x % 32;
+        int end;
+        const int t = tile_tokens(sp, ku, ke, i, threadIdx.x / 32 % 4, end) + threadIdx.x % 32;
+        const uint4 *src = reinterpret_cast<const uint4 *>(kc + (long long)t * (D / 2));
 #pragma unroll
-        for (int k = 0; k < kRounds; ++k) {
-            const int t = tile_token(sp, ku, ke, i, warp * 32 + k * kRows + lane % kRows);
+        for (int k = 0; k < kChunks; ++k) {
             x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (t >= 0)
-                x[k] = __ldg(reinterpret_cast<const uint4 *>(kc + (long long)t * (D / 2)) + lane / kRows);
+            if (t < end)
+                x[k] = ld_ahead(src + k);
         }
     }
 
-    __device__ __forceinline__ void store(const uint4 (&x)[kRounds], uint32_t stage)
+    // fp16 pairs, 16 columns per chunk, to `stage` (the warp's lanes).
+    __device__ __forceinline__ void store(const uint4 (&x)[kChunks], uint32_t stage)
     {
-        using S = RowsSmem<D>;
-        const int warp = threadIdx.x / 32 - kUnpackWarp, lane = threadIdx.x % 32;
 #pragma unroll
-        for (int k = 0; k < kRounds; ++k) {
-            const int row = warp * 32 + k * kRows + lane % kRows;
+        for (int k = 0; k < kChunks; ++k) {
             const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t v[16];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t y = w[j] >> 8;
-                sts128(chunk_at(stage, S::kKBox, row, 4 * (lane / kRows) + j), centred_even(w[j]), centred_odd(w[j]),
-                       centred_even(y), centred_odd(y));
+                v[4 * j] = centred_even(w[j]);
+                v[4 * j + 1] = centred_odd(w[j]);
+                v[4 * j + 2] = centred_even(w[j] >> 8);
+                v[4 * j + 3] = centred_odd(w[j] >> 8);
             }
+            ptx::tmem_st16(stage + 16 * k, v);
         }
-        ptx::fence_proxy_async_smem();
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before_sync();
     }
 };
 
-// One token's sum over the columns [c0, c0 + 16) of its scores; x holds those
-// from x0 on.
+// Adds to the sums of four tokens (t, t + 8: lo; t + 16, t + 24: hi) this
+// thread's columns of a group of 16: two of each eight.
 template <bool MASKED>
-__device__ __forceinline__ void add_columns(const uint32_t (&x)[32], int c0, int x0, const float *k, const int4 *bounds, int t,
-                                            float sa, float za, uint64_t (&sum)[2])
+__device__ __forceinline__ void add_columns(const uint32_t (&lo)[8], const uint32_t (&hi)[8], const float *k,
+                                            const int4 *bounds, int t, const uint64_t (&sa)[4], const uint64_t (&za)[4],
+                                            uint64_t (&sum)[4])
 {
-    const uint64_t sa2 = ptx::f2_pack(sa, sa), za2 = ptx::f2_pack(za, za);
 #pragma unroll
-    for (int i = c0; i < c0 + 16; i += 4) {
-        const float4 mul = *reinterpret_cast<const float4 *>(k + i);
-        const float4 qs = *reinterpret_cast<const float4 *>(k + kRowBlock + i);
-        const float4 nref = *reinterpret_cast<const float4 *>(k + 2 * kRowBlock + i);
-        const float4 rest = *reinterpret_cast<const float4 *>(k + 3 * kRowBlock + i);
+    for (int q = 0; q < 2; ++q) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(k + 32 * q);       // mul, sum
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(k + 32 * q + 4);   // -ref, rest
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint64_t m2 = h ? ptx::f2_pack(mul.z, mul.w) : ptx::f2_pack(mul.x, mul.y);
-            const uint64_t q2 = h ? ptx::f2_pack(qs.z, qs.w) : ptx::f2_pack(qs.x, qs.y);
-            const uint64_t n2 = h ? ptx::f2_pack(nref.z, nref.w) : ptx::f2_pack(nref.x, nref.y);
-            const uint64_t r2 = h ? ptx::f2_pack(rest.z, rest.w) : ptx::f2_pack(rest.x, rest.y);
-            const uint64_t s2 = ptx::f2_pack(__uint_as_float(x[i - x0 + 2 * h]), __uint_as_float(x[i - x0 + 2 * h + 1]));
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t *x = j < 2 ? lo + 4 * q + 2 * j : hi + 4 * q + 2 * (j - 2);
+            const uint64_t s2 = ptx::f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1]));
             float y0, y1;
-            ptx::f2_unpack(ptx::f2_fma(ptx::f2_mul(s2, m2), sa2, ptx::f2_fma(za2, q2, n2)), y0, y1);
+            ptx::f2_unpack(ptx::f2_fma(ptx::f2_mul(s2, a.x), sa[j], ptx::f2_fma(za[j], a.y, b.x)), y0, y1);
             if (MASKED) {
-                const int4 a = bounds[i + 2 * h], b = bounds[i + 2 * h + 1];
-                y0 = sees(Bounds{a.x, a.y, a.z}, t) ? y0 : -INFINITY;
-                y1 = sees(Bounds{b.x, b.y, b.z}, t) ? y1 : -INFINITY;
+                const int4 v0 = bounds[8 * q], v1 = bounds[8 * q + 1];
+                y0 = sees(Bounds{v0.x, v0.y, v0.z}, t + 8 * j) ? y0 : -INFINITY;
+                y1 = sees(Bounds{v1.x, v1.y, v1.z}, t + 8 * j) ? y1 : -INFINITY;
             }
-            sum[h] = ptx::f2_fma(ptx::f2_pack(ex2(y0), ex2(y1)), r2, sum[h]);
+            sum[j] = ptx::f2_fma(ptx::f2_pack(ex2(y0), ex2(y1)), b.y, sum[j]);
         }
     }
 }
@@ -296,9 +308,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                     if (ptx::elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
-                            ptx::mma_ss(tmem + s * kRowBlock,
-                                        smem_desc_sw128(base + s * S::kKStage + (kk / 4) * S::kKBox + (kk % 4) * 32, 16),
-                                        smem_desc_sw128(base + S::kQOff + (kk / 4) * S::kQBox + (kk % 4) * 32, 16), idesc,
+                            ptx::mma_ts(tmem + s * kRowBlock, tmem + kScoreCols + s * (D / 2) + kk * 8,
+                                        smem_desc_sw128(base + (kk / 4) * S::kQBox + (kk % 4) * 32, 16), idesc,
                                         kk > 0 ? 1u : 0u);
                         ptx::mma_commit(b.done(s));
                     }
@@ -319,7 +330,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                             ok = false;
                             break;
                         }
-                        x.store(x.next[e], base + s * S::kKStage);
+                        ptx::tc_fence_after_sync();
+                        x.store(x.next[e], tmem + kScoreCols + s * (D / 2) + ((uint32_t)(warp % 4) << 21));
                         __syncwarp();
                         if (lane == 0)
                             ptx::mbar_arrive(b.full(s));
@@ -338,49 +350,67 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                     edge_hi = min(edge_hi, edge[kWarps + i]);
                 }
                 const uint32_t *kp = p.kp + bh * p.C;
-                int t = tile_token(sp, ku, ke, 0, threadIdx.x);
-                uint32_t par = t >= 0 ? __ldg(kp + t) : 0u;
-                for (int i = 0; i < nt; ++i) {
-                    const uint32_t n = it + i, s = n & 1u;
-                    const float sa = to_float<BF16>(par & 0xffffu), za = fmaf(7.5f, sa, to_float<BF16>(par >> 16));
-                    const int now = t;
-                    t = tile_token(sp, ku, ke, i + 1, threadIdx.x);
-                    par = t >= 0 ? __ldg(kp + t) : 0u;
-                    const float old = add && now >= 0 ? acc[now] : 0.f;
-                    if (!warp_wait(b.done(s), (n >> 1) & 1u, c, kSiteRowsDone)) {
+                const int g = warp / 4, quad = warp % 4;   // of the two groups: the tiles of stage g
+                const int r = lane / 4, cl = lane % 4;
+                const uint32_t scores_at = tmem + g * kRowBlock + ((uint32_t)quad << 21);
+                const int first = (int)((g ^ it) & 1u);
+                int end, t0 = tile_tokens(sp, ku, ke, first, quad, end);
+                uint32_t par = t0 + lane < end ? ld_ahead(kp + t0 + lane) : 0u;
+                for (int i = first; i < nt; i += 2) {
+                    const uint32_t n = it + i;
+                    uint64_t sa[4], za[4], sum[4];   // of tokens r, r + 8, r + 16, r + 24
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t v = __shfl_sync(0xffffffffu, par, r + 8 * j);
+                        const float a = to_float<BF16>(v & 0xffffu), z = fmaf(7.5f, a, to_float<BF16>(v >> 16));
+                        sa[j] = ptx::f2_pack(a, a);
+                        za[j] = ptx::f2_pack(z, z);
+                        sum[j] = 0ull;
+                    }
+                    const bool masked = t0 < edge_lo || t0 + kSub > edge_hi;
+                    const int t = t0 + r;
+                    // lane (r, cl) writes token r + 8 cl
+                    float *to = t + 8 * cl < end ? acc + t + 8 * cl : nullptr;
+                    const float old = add && to ? *to : 0.f;
+                    t0 = tile_tokens(sp, ku, ke, i + 2, quad, end);
+                    par = t0 + lane < end ? ld_ahead(kp + t0 + lane) : 0u;
+                    if (!warp_wait(b.done(g), (n >> 1) & 1u, c, kSiteRowsDone)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after_sync();
-                    // (a tile's absent tokens, -1 here, are not looked at)
-                    const bool masked = __any_sync(0xffffffffu, now >= 0 && (now < edge_lo || now >= edge_hi));
-                    uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int x0 = 0; x0 < kRowBlock; x0 += 32) {
-                        if (x0 >= cols)
+                    for (int c0 = 0; c0 < kRowBlock; c0 += 16) {
+                        if (c0 >= cols)
                             break;
-                        uint32_t x[32];
-                        ptx::tmem_ld32(tmem + s * kRowBlock + x0 + ((uint32_t)warp << 21), x);
+                        uint32_t lo[8], hi[8];   // tokens 0 .. 15 and 16 .. 31 of the warp's
+                        ptx::tmem_ld_frag16(scores_at + c0, lo);
+                        ptx::tmem_ld_frag16(scores_at + c0 + (16u << 16), hi);
                         ptx::tmem_wait_ld();
-                        if (x0 + 32 >= cols) {   // all read out
+                        if (c0 + 16 >= cols) {   // all read out
                             ptx::tc_fence_before_sync();
                             __syncwarp();
                             if (lane == 0)
-                                ptx::mbar_arrive(b.free_(s));
+                                ptx::mbar_arrive(b.free_(g));
                         }
-#pragma unroll
-                        for (int c0 = x0; c0 < x0 + 32; c0 += 16)
-                            if (c0 < cols) {
-                                if (masked)
-                                    add_columns<true>(x, c0, x0, k, bounds, now, sa, za, sum);
-                                else
-                                    add_columns<false>(x, c0, x0, k, bounds, now, sa, za, sum);
-                            }
+                        const float *kc = k + 4 * c0 + 8 * cl;
+                        const int4 *vis = bounds + c0 + 2 * cl;
+                        if (masked)
+                            add_columns<true>(lo, hi, kc, vis, t, sa, za, sum);
+                        else
+                            add_columns<false>(lo, hi, kc, vis, t, sa, za, sum);
                     }
-                    float a0, a1;
-                    ptx::f2_unpack(ptx::f2_add(sum[0], sum[1]), a0, a1);
-                    if (now >= 0)
-                        acc[now] = old + (a0 + a1);
+                    float total[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float a0, a1;
+                        ptx::f2_unpack(sum[j], a0, a1);
+                        total[j] = a0 + a1;
+                        total[j] += __shfl_xor_sync(0xffffffffu, total[j], 1);
+                        total[j] += __shfl_xor_sync(0xffffffffu, total[j], 2);
+                    }
+                    if (to)
+                        *to = old + (cl == 0 ? total[0] : (cl == 1 ? total[1] : (cl == 2 ? total[2] : total[3])));
                 }
             }
             it += (uint32_t)nt;
