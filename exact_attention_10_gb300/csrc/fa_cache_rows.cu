@@ -10,8 +10,9 @@
 // and exact in fp16 ((code - 7.5) 2^-9, as in fa_cache_kernel.cuh), are
 // unpacked into tensor memory, one token to a thread, as the A operand of
 // tcgen05.mma, 128 tokens a tile, against up to 64 query rows as B; the scores
-// come back from tensor memory as fragments, four tokens and a quarter of the
-// columns to a thread, so that a column's constants serve four tokens.
+// come back from tensor memory as fragments, 16 tokens at a time, two of them
+// and a quarter of the columns to a thread, so that a column's constants are
+// read for two and a warp's reads of them are few.
 //
 // (Shared memory is what bound this with K unpacked there and a token's scores
 // to a thread: per 128 tokens, 64 rows and D = 128, 280 cycles of stores, 380 of
@@ -21,8 +22,8 @@
 //   warps 0-7   the scores' exponentials and sums, two groups of four that take
 //               every other tile
 //   warps 8-11  unpacking: codes two tiles ahead in registers, fp16 to one of
-//               two stages
-//   warp 12     issues the MMAs
+//               two stages; warp 8 issues the MMAs besides (a warp for that
+//               alone would leave the others 72 registers)
 // with two CTAs per SM.  Rows are taken 64 at a time; further blocks go
 // through the cache again, from L2, and add to what the first wrote.
 #include <cuda_runtime.h>
@@ -39,9 +40,8 @@ namespace {
 
 constexpr int kRowBlock = 64;       // query rows per pass over the cache
 constexpr int kTileTokens = 128;    // tokens per MMA tile: two units
-constexpr int kRowsThreads = 416;
-constexpr int kUnpackWarp = 8;      // the first of the four
-constexpr int kIssueWarp = 12;
+constexpr int kRowsThreads = 384;
+constexpr int kUnpackWarp = 8;      // the first of the four, which also issues the MMAs
 constexpr int kScoreCols = 2 * kRowBlock;   // TMEM: two stages of scores, then two of K (D / 2 columns each)
 constexpr uint32_t kTmemCols = 256;         // (two CTAs per SM share 512)
 
@@ -212,29 +212,77 @@ struct Unpacker {
     }
 };
 
-// Adds to the sums of four tokens (t, t + 8: lo; t + 16, t + 24: hi) this
-// thread's columns of a group of 16: two of each eight.
-template <bool MASKED>
-__device__ __forceinline__ void add_columns(const uint32_t (&lo)[8], const uint32_t (&hi)[8], const float *k,
-                                            const int4 *bounds, int t, const uint64_t (&sa)[4], const uint64_t (&za)[4],
-                                            uint64_t (&sum)[4])
+// Adds to the sums of two tokens (t and t + 8) this thread's columns, two of
+// each eight, of x, whose first column's constants and bounds are at k and vis.
+template <int N, bool MASKED>
+__device__ __forceinline__ void add_columns(const uint32_t (&x)[N], int cols, const float *k, const int4 *vis, int t,
+                                            const uint64_t (&sa)[2], const uint64_t (&za)[2], uint64_t (&sum)[2])
 {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < N / 4; ++q) {
+        if (q % 2 == 0 && 8 * q >= cols)
+            break;
         const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(k + 32 * q);       // mul, sum
         const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(k + 32 * q + 4);   // -ref, rest
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t *x = j < 2 ? lo + 4 * q + 2 * j : hi + 4 * q + 2 * (j - 2);
-            const uint64_t s2 = ptx::f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1]));
+        for (int j = 0; j < 2; ++j) {
+            const uint64_t s2 = ptx::f2_pack(__uint_as_float(x[4 * q + 2 * j]), __uint_as_float(x[4 * q + 2 * j + 1]));
             float y0, y1;
             ptx::f2_unpack(ptx::f2_fma(ptx::f2_mul(s2, a.x), sa[j], ptx::f2_fma(za[j], a.y, b.x)), y0, y1);
             if (MASKED) {
-                const int4 v0 = bounds[8 * q], v1 = bounds[8 * q + 1];
+                const int4 v0 = vis[8 * q], v1 = vis[8 * q + 1];
                 y0 = sees(Bounds{v0.x, v0.y, v0.z}, t + 8 * j) ? y0 : -INFINITY;
                 y1 = sees(Bounds{v1.x, v1.y, v1.z}, t + 8 * j) ? y1 : -INFINITY;
             }
             sum[j] = ptx::f2_fma(ptx::f2_pack(ex2(y0), ex2(y1)), b.y, sum[j]);
+        }
+    }
+}
+
+// The sums of a warp's 32 tokens from t0 on, over `cols` columns (at most 2 W)
+// of scores at `at`: total[j] of token t0 + lane / 4 + 8 j.  The next 16 tokens'
+// or columns' scores load while these are worked on; `bar` is arrived on once
+// all have been read.
+template <bool BF16, int W, bool MASKED>
+__device__ __forceinline__ void tile_sums(uint32_t at, int cols, uint32_t par, const float *k, const int4 *vis, int t0,
+                                          uint32_t bar, float (&total)[4])
+{
+    const int lane = threadIdx.x % 32, r = lane / 4, cl = lane % 4;
+    k += 8 * cl;
+    vis += 2 * cl;
+    uint32_t x[W / 2], y[W / 2];
+    ptx::tmem_ld_frag(at, x);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint64_t sa[2], za[2], sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t v = __shfl_sync(0xffffffffu, par, r + 16 * half + 8 * j);
+            const float a = to_float<BF16>(v & 0xffffu), z = fmaf(7.5f, a, to_float<BF16>(v >> 16));
+            sa[j] = ptx::f2_pack(a, a);
+            za[j] = ptx::f2_pack(z, z);
+        }
+        const int t = t0 + 16 * half + r;
+        ptx::tmem_wait_ld();
+        ptx::tmem_ld_frag(at + (half << 20) + W, y);
+        add_columns<W / 2, MASKED>(x, W, k, vis, t, sa, za, sum);
+        ptx::tmem_wait_ld();
+        if (half == 0) {
+            ptx::tmem_ld_frag(at + (1u << 20), x);
+        } else {
+            ptx::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(bar);
+        }
+        add_columns<W / 2, MASKED>(y, cols - W, k + 4 * W, vis + W, t, sa, za, sum);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float a, b;
+            ptx::f2_unpack(sum[j], a, b);
+            a += b;
+            a += __shfl_xor_sync(0xffffffffu, a, 1);
+            total[2 * half + j] = a + __shfl_xor_sync(0xffffffffu, a, 2);
         }
     }
 }
@@ -265,7 +313,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
         *c.abort_flag = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == kIssueWarp) {
+    if (warp == kUnpackWarp) {
         ptx::tmem_alloc(ptx::smem_addr(misc), kTmemCols);
         ptx::tmem_relinquish();
     }
@@ -296,26 +344,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                 ptx::fence_proxy_async_smem();
             }
             __syncthreads();
-            if (warp == kIssueWarp) {
+            if (warp >= kUnpackWarp) {
                 const uint32_t idesc = instr_desc_f16(false, kTileTokens, cols, false);
-                for (int i = 0; i < nt && ok; ++i) {
-                    const uint32_t n = it + i, s = n & 1u;
-                    ok = warp_wait(b.full(s), (n >> 1) & 1u, c, kSiteRowsFull) &&
-                         (n < 2 || warp_wait(b.free_(s), ((n >> 1) - 1u) & 1u, c, kSiteRowsFree));
-                    if (!ok)
-                        break;
-                    ptx::tc_fence_after_sync();
-                    if (ptx::elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk)
-                            ptx::mma_ts(tmem + s * kRowBlock, tmem + kScoreCols + s * (D / 2) + kk * 8,
-                                        smem_desc_sw128(base + (kk / 4) * S::kQBox + (kk % 4) * 32, 16), idesc,
-                                        kk > 0 ? 1u : 0u);
-                        ptx::mma_commit(b.done(s));
-                    }
-                    __syncwarp();
-                }
-            } else if (warp >= kUnpackWarp) {
                 Unpacker<D> x;
                 const uint8_t *kc = p.kc + bh * p.C * (D / 2);
                 x.fetch(x.next[0], kc, sp, ku, ke, 0);
@@ -324,6 +354,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t n = it + i + e, s = n & 1u;
+                        const uint32_t k_at = tmem + kScoreCols + s * (D / 2);
                         if (i + e >= nt)
                             break;
                         if (n >= 2 && !warp_wait(b.done(s), ((n >> 1) - 1u) & 1u, c, kSiteRowsReuse)) {
@@ -331,11 +362,27 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                             break;
                         }
                         ptx::tc_fence_after_sync();
-                        x.store(x.next[e], tmem + kScoreCols + s * (D / 2) + ((uint32_t)(warp % 4) << 21));
+                        x.store(x.next[e], k_at + ((uint32_t)(warp % 4) << 21));
                         __syncwarp();
                         if (lane == 0)
                             ptx::mbar_arrive(b.full(s));
                         x.fetch(x.next[e], kc, sp, ku, ke, i + e + 2);
+                        if (warp > kUnpackWarp)
+                            continue;
+                        ok = warp_wait(b.full(s), (n >> 1) & 1u, c, kSiteRowsFull) &&
+                             (n < 2 || warp_wait(b.free_(s), ((n >> 1) - 1u) & 1u, c, kSiteRowsFree));
+                        if (!ok)
+                            break;
+                        ptx::tc_fence_after_sync();
+                        if (ptx::elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                ptx::mma_ts(tmem + s * kRowBlock, k_at + kk * 8,
+                                            smem_desc_sw128(base + (kk / 4) * S::kQBox + (kk % 4) * 32, 16), idesc,
+                                            kk > 0 ? 1u : 0u);
+                            ptx::mma_commit(b.done(s));
+                        }
+                        __syncwarp();
                     }
                 }
             } else {
@@ -357,20 +404,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                 int end, t0 = tile_tokens(sp, ku, ke, first, quad, end);
                 uint32_t par = t0 + lane < end ? ld_ahead(kp + t0 + lane) : 0u;
                 for (int i = first; i < nt; i += 2) {
-                    const uint32_t n = it + i;
-                    uint64_t sa[4], za[4], sum[4];   // of tokens r, r + 8, r + 16, r + 24
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t v = __shfl_sync(0xffffffffu, par, r + 8 * j);
-                        const float a = to_float<BF16>(v & 0xffffu), z = fmaf(7.5f, a, to_float<BF16>(v >> 16));
-                        sa[j] = ptx::f2_pack(a, a);
-                        za[j] = ptx::f2_pack(z, z);
-                        sum[j] = 0ull;
-                    }
-                    const bool masked = t0 < edge_lo || t0 + kSub > edge_hi;
-                    const int t = t0 + r;
+                    const uint32_t n = it + i, now = par;
+                    const int t = t0;
                     // lane (r, cl) writes token r + 8 cl
-                    float *to = t + 8 * cl < end ? acc + t + 8 * cl : nullptr;
+                    float *to = t + r + 8 * cl < end ? acc + t + r + 8 * cl : nullptr;
                     const float old = add && to ? *to : 0.f;
                     t0 = tile_tokens(sp, ku, ke, i + 2, quad, end);
                     par = t0 + lane < end ? ld_ahead(kp + t0 + lane) : 0u;
@@ -379,35 +416,18 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                         break;
                     }
                     ptx::tc_fence_after_sync();
-#pragma unroll
-                    for (int c0 = 0; c0 < kRowBlock; c0 += 16) {
-                        if (c0 >= cols)
-                            break;
-                        uint32_t lo[8], hi[8];   // tokens 0 .. 15 and 16 .. 31 of the warp's
-                        ptx::tmem_ld_frag16(scores_at + c0, lo);
-                        ptx::tmem_ld_frag16(scores_at + c0 + (16u << 16), hi);
-                        ptx::tmem_wait_ld();
-                        if (c0 + 16 >= cols) {   // all read out
-                            ptx::tc_fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0)
-                                ptx::mbar_arrive(b.free_(g));
-                        }
-                        const float *kc = k + 4 * c0 + 8 * cl;
-                        const int4 *vis = bounds + c0 + 2 * cl;
-                        if (masked)
-                            add_columns<true>(lo, hi, kc, vis, t, sa, za, sum);
-                        else
-                            add_columns<false>(lo, hi, kc, vis, t, sa, za, sum);
-                    }
+                    const bool masked = t < edge_lo || t + kSub > edge_hi;
                     float total[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float a0, a1;
-                        ptx::f2_unpack(sum[j], a0, a1);
-                        total[j] = a0 + a1;
-                        total[j] += __shfl_xor_sync(0xffffffffu, total[j], 1);
-                        total[j] += __shfl_xor_sync(0xffffffffu, total[j], 2);
+                    if (cols > 32) {
+                        if (masked)
+                            tile_sums<BF16, 32, true>(scores_at, cols, now, k, bounds, t, b.free_(g), total);
+                        else
+                            tile_sums<BF16, 32, false>(scores_at, cols, now, k, bounds, t, b.free_(g), total);
+                    } else {
+                        if (masked)
+                            tile_sums<BF16, 16, true>(scores_at, cols, now, k, bounds, t, b.free_(g), total);
+                        else
+                            tile_sums<BF16, 16, false>(scores_at, cols, now, k, bounds, t, b.free_(g), total);
                     }
                     if (to)
                         *to = old + (cl == 0 ? total[0] : (cl == 1 ? total[1] : (cl == 2 ? total[2] : total[3])));
@@ -425,7 +445,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
             sp = span_of(p, ++bb);
         }
     }
-    if (warp == kIssueWarp) {   // every MMA has completed before its TMEM is given back
+    if (warp == kUnpackWarp) {   // every MMA has completed before its TMEM is given back
         if (ptx::elect_one())
             ptx::mma_commit(b.drain());
         __syncwarp();
@@ -433,7 +453,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
-    if (warp == kIssueWarp) {
+    if (warp == kUnpackWarp) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc(tmem, kTmemCols);
     }

@@ -232,14 +232,24 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr));
 }
 
-// 16 lanes x 16 columns -> 8 registers per thread, as fragments: registers 4 q
-// and 4 q + 1 are columns 8 q + 2 (thread % 4) and the next of lane thread / 4,
-// 4 q + 2 and 4 q + 3 those of the lane eight further.
-__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, uint32_t (&r)[8])
+// 16 lanes x 16 (32) columns -> 8 (16) registers per thread, as fragments:
+// registers 4 q and 4 q + 1 are columns 8 q + 2 (thread % 4) and the next of
+// lane thread / 4, 4 q + 2 and 4 q + 3 those of the lane eight further.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 // 8 columns of this thread's lane.
