@@ -14,9 +14,15 @@
 // and a quarter of the columns to a thread, so that a column's constants are
 // read for two and a warp's reads of them are few.
 //
-// (Shared memory is what bound this with K unpacked there and a token's scores
-// to a thread: per 128 tokens, 64 rows and D = 128, 280 cycles of stores, 380 of
-// the MMA's reads and 730 of constants, of the 1400 that a tile took.)
+// What bounds it: issue slots.  Per 128 tokens, 64 rows and D = 128, about 2000
+// warp instructions of sums (five per score and thread) and 800 of unpacking,
+// 1300 cycles a tile in all, against 256 of the MMAs and 256 of exponentials.
+// (With K unpacked into shared memory and one token's scores to a thread it was
+// shared memory: 280 cycles of stores, 380 of the MMA's reads and 730 of
+// constants of 1400 a tile.  Packed pairs of multiply-adds took as long as
+// single ones; 88 registers for the sums and 64 for the unpacking spilled.)
+// 2 x 8 key heads, 20000 and 32768 tokens, 64 rows, D = 128: 24.0 us; through
+// mma.sync with the rows' fragments in shared memory 30.6.
 //
 // Roles, beside one another:
 //   warps 0-7   the scores' exponentials and sums, two groups of four that take
@@ -46,7 +52,7 @@ constexpr int kScoreCols = 2 * kRowBlock;   // TMEM: two stages of scores, then 
 constexpr uint32_t kTmemCols = 256;         // (two CTAs per SM share 512)
 
 // Wait sites for the status word.
-enum : uint32_t { kSiteRowsFull = 64, kSiteRowsFree, kSiteRowsDone, kSiteRowsReuse, kSiteRowsDrain };
+enum : uint32_t { kSiteRowsQueries = 64, kSiteRowsFull, kSiteRowsFree, kSiteRowsDone, kSiteRowsReuse, kSiteRowsDrain };
 
 template <int D>
 struct RowsSmem {
@@ -66,6 +72,7 @@ struct RowsBars {
     __device__ uint32_t full(int s) const { return base + 8u * s; }         // unpacking -> MMA: stage s of K holds a tile
     __device__ uint32_t done(int s) const { return base + 8u * (2 + s); }   // MMA: K s read, scores s final
     __device__ uint32_t free_(int s) const { return base + 8u * (4 + s); }  // sums -> MMA: scores s read out
+    __device__ uint32_t rows() const { return base + 8u * 7; }              // queries -> MMA: the block of rows is there
     __device__ uint32_t drain() const { return base + 8u * 6; }
 };
 
@@ -118,6 +125,7 @@ __device__ __forceinline__ void load_rows(const Params &p, long long bh, int r0,
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
     const int n = 8 * warp + r;
     const bool there = r0 + n < p.rows;
+    const float lse = there ? __uint_as_float(ld_ahead(reinterpret_cast<const uint32_t *>(p.lse) + bh * p.rows + r0 + n)) : -INFINITY;
     float x[kWords][8], s = 0.f, mx = 0.f;
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
@@ -148,7 +156,6 @@ __device__ __forceinline__ void load_rows(const Params &p, long long bh, int r0,
                pack_f16(x[w][3] * up, x[w][7] * up));
     int lo = 0, hi = 0x7fffffff;
     if (c == 0) {
-        const float lse = there ? p.lse[bh * p.rows + r0 + n] : -INFINITY;
         const float ref = lse * kLog2e;
         float *k = reinterpret_cast<float *>(base_ptr + S::kConstOff) + n / 2 * 8 + n % 2;
         k[0] = p.qk2 * exp2i(9 - e);
@@ -216,25 +223,25 @@ struct Unpacker {
 // each eight, of x, whose first column's constants and bounds are at k and vis.
 template <int N, bool MASKED>
 __device__ __forceinline__ void add_columns(const uint32_t (&x)[N], int cols, const float *k, const int4 *vis, int t,
-                                            const uint64_t (&sa)[2], const uint64_t (&za)[2], uint64_t (&sum)[2])
+                                            const float (&sa)[2], const float (&za)[2], float (&sum)[2])
 {
 #pragma unroll
     for (int q = 0; q < N / 4; ++q) {
         if (q % 2 == 0 && 8 * q >= cols)
             break;
-        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(k + 32 * q);       // mul, sum
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(k + 32 * q + 4);   // -ref, rest
+        const float4 a = *reinterpret_cast<const float4 *>(k + 32 * q);       // mul, sum
+        const float4 b = *reinterpret_cast<const float4 *>(k + 32 * q + 4);   // -ref, rest
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint64_t s2 = ptx::f2_pack(__uint_as_float(x[4 * q + 2 * j]), __uint_as_float(x[4 * q + 2 * j + 1]));
-            float y0, y1;
-            ptx::f2_unpack(ptx::f2_fma(ptx::f2_mul(s2, a.x), sa[j], ptx::f2_fma(za[j], a.y, b.x)), y0, y1);
+            float y0 = fmaf(__uint_as_float(x[4 * q + 2 * j]) * a.x, sa[j], fmaf(za[j], a.z, b.x));
+            float y1 = fmaf(__uint_as_float(x[4 * q + 2 * j + 1]) * a.y, sa[j], fmaf(za[j], a.w, b.y));
             if (MASKED) {
                 const int4 v0 = vis[8 * q], v1 = vis[8 * q + 1];
                 y0 = sees(Bounds{v0.x, v0.y, v0.z}, t + 8 * j) ? y0 : -INFINITY;
                 y1 = sees(Bounds{v1.x, v1.y, v1.z}, t + 8 * j) ? y1 : -INFINITY;
             }
-            sum[j] = ptx::f2_fma(ptx::f2_pack(ex2(y0), ex2(y1)), b.y, sum[j]);
+            sum[j] = fmaf(ex2(y0), b.z, sum[j]);
+            sum[j] = fmaf(ex2(y1), b.w, sum[j]);
         }
     }
 }
@@ -254,13 +261,13 @@ __device__ __forceinline__ void tile_sums(uint32_t at, int cols, uint32_t par, c
     ptx::tmem_ld_frag(at, x);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        uint64_t sa[2], za[2], sum[2] = {0ull, 0ull};
+        float sa[2], za[2], sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t v = __shfl_sync(0xffffffffu, par, r + 16 * half + 8 * j);
             const float a = to_float<BF16>(v & 0xffffu), z = fmaf(7.5f, a, to_float<BF16>(v >> 16));
-            sa[j] = ptx::f2_pack(a, a);
-            za[j] = ptx::f2_pack(z, z);
+            sa[j] = a;
+            za[j] = z;
         }
         const int t = t0 + 16 * half + r;
         ptx::tmem_wait_ld();
@@ -278,9 +285,7 @@ __device__ __forceinline__ void tile_sums(uint32_t at, int cols, uint32_t par, c
         add_columns<W / 2, MASKED>(y, cols - W, k + 4 * W, vis + W, t, sa, za, sum);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            float a, b;
-            ptx::f2_unpack(sum[j], a, b);
-            a += b;
+            float a = sum[j];
             a += __shfl_xor_sync(0xffffffffu, a, 1);
             total[2 * half + j] = a + __shfl_xor_sync(0xffffffffu, a, 2);
         }
@@ -309,6 +314,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
             ptx::mbar_init(b.done(s), 1);
             ptx::mbar_init(b.free_(s), 4);
         }
+        ptx::mbar_init(b.rows(), kWarps);
         ptx::mbar_init(b.drain(), 1);
         *c.abort_flag = 0;
         ptx::fence_barrier_init();
@@ -328,6 +334,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
     int h = (int)((u0 - w.before) / sp.n);
     int ku = (int)((u0 - w.before) - (long long)h * sp.n);
     uint32_t it = 0;   // tiles before this pass: tile j of it is number it + j, in stage (it + j) % 2
+    uint32_t pass = 0;
     bool ok = true;
     for (long long u = u0; u < u1 && ok;) {
         const int ke = (int)((long long)sp.n - ku < u1 - u ? sp.n : ku + (u1 - u));
@@ -337,13 +344,16 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
         for (int r0 = 0; r0 < p.rows && ok; r0 += kRowBlock) {
             const int nrows = p.rows - r0 < kRowBlock ? p.rows - r0 : kRowBlock;
             const int cols = (nrows + 15) & ~15;
-            // (every role is through with the block before: its last MMA is
-            // read out, and the sums have its constants behind them)
+            // Every role is through with the block before.  The sums' warps bring
+            // the next rows while the others unpack the first tiles.
             if (warp < kWarps) {
                 load_rows<D, BF16>(p, bh, r0, sp.len, base, base_ptr);
                 ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(b.rows());
+                asm volatile("bar.sync 1, 256;" ::: "memory");   // the sums' warps have the constants
             }
-            __syncthreads();
             if (warp >= kUnpackWarp) {
                 const uint32_t idesc = instr_desc_f16(false, kTileTokens, cols, false);
                 Unpacker<D> x;
@@ -369,6 +379,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                         x.fetch(x.next[e], kc, sp, ku, ke, i + e + 2);
                         if (warp > kUnpackWarp)
                             continue;
+                        if (i + e == 0 && !(ok = warp_wait(b.rows(), pass & 1u, c, kSiteRowsQueries)))
+                            break;
                         ok = warp_wait(b.full(s), (n >> 1) & 1u, c, kSiteRowsFull) &&
                              (n < 2 || warp_wait(b.free_(s), ((n >> 1) - 1u) & 1u, c, kSiteRowsFree));
                         if (!ok)
@@ -433,6 +445,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
                         *to = old + (cl == 0 ? total[0] : (cl == 1 ? total[1] : (cl == 2 ? total[2] : total[3])));
                 }
             }
+            ++pass;
             it += (uint32_t)nt;
             ok = __syncthreads_and(ok);
         }
