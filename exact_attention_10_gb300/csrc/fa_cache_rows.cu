@@ -21,8 +21,11 @@
 // shared memory: 280 cycles of stores, 380 of the MMA's reads and 730 of
 // constants of 1400 a tile.  Packed pairs of multiply-adds took as long as
 // single ones; 88 registers for the sums and 64 for the unpacking spilled.)
-// 2 x 8 key heads, 20000 and 32768 tokens, 64 rows, D = 128: 24.0 us; through
-// mma.sync with the rows' fragments in shared memory 30.6.
+// 2 x 8 key heads, 20000 and 32768 tokens, 64 rows, D = 128: 24.7 us; through
+// mma.sync with the rows' fragments in shared memory 30.6.  8 x 8 key heads of
+// up to 8192 tokens, D = 128, 18 / 40 / 128 rows: 20.1 / 22.1 / 41.6 us against
+// 28.6 / 29.0 / 54.4; 2 x 8 of up to 1024, 18 / 64 rows: 6.9 / 8.0 against 7.1 /
+// 7.3, the longer chain of steps.
 //
 // Roles, beside one another:
 //   warps 0-7   the scores' exponentials and sums, two groups of four that take
