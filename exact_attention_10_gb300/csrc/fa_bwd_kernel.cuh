@@ -1516,8 +1516,11 @@ __global__ void __launch_bounds__(256)
     const int part = (int)(g % kTpr);
     if (row >= rows)   // whole row groups leave together (kTpr divides the warp)
         return;
-    const long long bh = row / Npad;
-    const int i = (int)(row - bh * Npad);
+    const uint32_t bh = (uint32_t)row / (uint32_t)Npad;   // (rows < 2^31)
+    const int i = (int)((uint32_t)row - bh * (uint32_t)Npad);
+    float lse = -INFINITY;   // (loaded beside O and dO: one memory latency, not two)
+    if (part == 0 && i < N)
+        lse = LSE[(size_t)bh * N + i];
     if (dqa) {
         float4 *z = reinterpret_cast<float4 *>(dqa + row * D + 8 * part);
         z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1555,7 +1558,6 @@ __global__ void __launch_bounds__(256)
     if (part == 0) {   // negated, as the passes add them
         float l = -INFINITY;
         if (i < N) {
-            const float lse = LSE[(size_t)bh * N + i];
             l = (lse == -INFINITY) ? -INFINITY : -(lse * 1.4426950408889634f);   // a row without keys: P = 0
         }
         lg[row] = l;
