@@ -484,9 +484,26 @@ struct Where {
     int b;                    // the sequence that holds unit `first`
 };
 
+// U k / G for k <= G (in 32 bits where it fits: a 64-bit division is some
+// hundred instructions).
+__device__ __forceinline__ long long share_of(const Where &w, int k)
+{
+    if (w.total < (1ll << 22))   // (k is below 2^10)
+        return (uint32_t)w.total * (uint32_t)k / (uint32_t)w.parts;
+    return w.total * k / w.parts;
+}
+
+// Tile (key head and row block) of its sequence, of `n` units a tile, that holds
+// unit d of the sequence's.
+__device__ __forceinline__ int tile_of(long long d, int n)
+{
+    return d < (1ll << 31) ? (int)((uint32_t)d / (uint32_t)n) : (int)(d / n);
+}
+
 // Called by every thread of the block, kThreads or more (it reads all of lens);
-// `scratch` holds kWarps + 2 values.  The first kThreads threads take consecutive sequences; an exclusive scan
-// over the threads' sums, then the owning thread walks its own.
+// `scratch` holds kWarps + 2 values.  The first kThreads threads take
+// consecutive sequences; an exclusive scan over the threads' sums, then the
+// owning thread walks its own.
 __device__ inline Where locate(const Params &p, int k, int grid, long long *scratch)
 {
     const int t = threadIdx.x, lane = t % 32, warp = t / 32;
@@ -529,6 +546,32 @@ __device__ inline Where locate(const Params &p, int k, int grid, long long *scra
     __syncthreads();
     w.before = scratch[kWarps];
     w.b = (int)scratch[kWarps + 1];
+    return w;
+}
+
+// The same, quicker where a warp can hold a sequence to a lane: every warp for
+// itself, without the barriers (the weights, 8 sequences: 17.4 -> 17.1 us, 64
+// rows 24.6 -> 23.7).  Not for the attention, whose registers are full: it
+// spilled 116 bytes and took 80.4 us for 78.2.
+__device__ inline Where locate_quick(const Params &p, int k, int grid, long long *scratch)
+{
+    if (p.B > 32)
+        return locate(p, k, grid, scratch);
+    const int lane = threadIdx.x % 32;
+    const long long sum = lane < p.B ? span_of(p, lane).n * ((long long)p.Hkv * p.RB) : 0;
+    long long inc = sum;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m)
+            inc += v;
+    }
+    Where w;
+    w.total = __shfl_sync(0xffffffffu, inc, 31);
+    w.parts = parts_of(w.total, grid);
+    w.first = k < w.parts ? share_of(w, k) : 0;
+    w.b = __ffs(__ballot_sync(0xffffffffu, w.first < inc)) - 1;   // (inc never falls, and ends above `first`)
+    w.before = __shfl_sync(0xffffffffu, inc - sum, w.b);
     return w;
 }
 
@@ -1191,22 +1234,23 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const Params p, int gri
     __shared__ long long scratch[kWarps + 2];
     // (lens are inputs: the search may run before the attention has ended)
     const int k = blockIdx.x;
-    const Where w = locate(p, k + 1, grid, scratch);
+    const Where w = locate_quick(p, k + 1, grid, scratch);
     grid_wait();   // by every block, so that this grid ends after the attention has
     const long long G = w.parts, U = w.total;
     if (k + 1 >= G)
         return;
     const long long edge = w.first;   // first unit of CTA k + 1
     const Span sp = span_of(p, w.b);
-    const int hr = (int)((edge - w.before) / sp.n);
+    const int hr = tile_of(edge - w.before, sp.n);
     const long long t0 = w.before + (long long)hr * sp.n, t1 = t0 + sp.n;   // the tile's units
-    if (t0 == edge || U * k / G > t0)   // not inside a tile, or not its first boundary
+    const long long start = share_of(w, k);   // of CTA k's units
+    if (t0 == edge || start > t0)   // not inside a tile, or not its first boundary
         return;
     const long long last = (t1 * G - 1) / U;   // CTA holding unit t1 - 1: the largest x with U x / G < t1
     const int h = hr / p.RB, r0 = (hr - h * p.RB) * (8 * NT);
     const int nrows = p.rows - r0 < 8 * NT ? p.rows - r0 : 8 * NT;
     const long long row0 = ((long long)w.b * p.Hkv + h) * p.rows + r0;
-    const long long slot0 = 2 * k + (U * k / G == t0 ? 0 : 1);   // CTA k's part: its only one, or its last
+    const long long slot0 = 2 * k + (start == t0 ? 0 : 1);   // CTA k's part: its only one, or its last
     for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
         const int n = i / (D / 4), ch = (i % (D / 4)) * 4;
         float M = -INFINITY;
@@ -1256,13 +1300,13 @@ __global__ void __launch_bounds__(kThreads, 2) weights_kernel(const Params p)
     __shared__ long long scratch[kWarps + 2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, c = lane % 4;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)(warp * kStages * L::kKeyStage);
-    const Where w = locate(p, blockIdx.x, gridDim.x, scratch);
+    const Where w = locate_quick(p, blockIdx.x, gridDim.x, scratch);
     if ((long long)blockIdx.x >= w.parts)
         return;
-    const long long u0 = w.first, u1 = w.total * (blockIdx.x + 1) / w.parts;
+    const long long u0 = w.first, u1 = share_of(w, blockIdx.x + 1);
     int b = w.b;
     Span sp = span_of(p, b);
-    int h = (int)((u0 - w.before) / sp.n);
+    int h = tile_of(u0 - w.before, sp.n);
     int ku = (int)((u0 - w.before) - (long long)h * sp.n);
     for (long long u = u0; u < u1;) {
         const int ke = (int)((long long)sp.n - ku < u1 - u ? sp.n : ku + (u1 - u));

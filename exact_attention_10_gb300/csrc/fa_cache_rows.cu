@@ -21,7 +21,7 @@
 // shared memory: 280 cycles of stores, 380 of the MMA's reads and 730 of
 // constants of 1400 a tile.  Packed pairs of multiply-adds took as long as
 // single ones; 88 registers for the sums and 64 for the unpacking spilled.)
-// 2 x 8 key heads, 20000 and 32768 tokens, 64 rows, D = 128: 24.7 us; through
+// 2 x 8 key heads, 20000 and 32768 tokens, 64 rows, D = 128: 23.7 us; through
 // mma.sync with the rows' fragments in shared memory 30.6.  8 x 8 key heads of
 // up to 8192 tokens, D = 128, 18 / 40 / 128 rows: 20.1 / 22.1 / 41.6 us against
 // 28.6 / 29.0 / 54.4; 2 x 8 of up to 1024, 18 / 64 rows: 6.9 / 8.0 against 7.1 /
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
     const Ctl c{reinterpret_cast<volatile int *>(misc + 1)};
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-    const Where w = locate(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(base_ptr + S::kScratchOff));
+    const Where w = locate_quick(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(base_ptr + S::kScratchOff));
     if ((long long)blockIdx.x >= w.parts)
         return;
     if (threadIdx.x == 0) {
@@ -331,10 +331,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) weights_rows_kernel(const Par
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(misc);
 
-    const long long u0 = w.first, u1 = w.total * (blockIdx.x + 1) / w.parts;
+    const long long u0 = w.first, u1 = share_of(w, blockIdx.x + 1);
     int bb = w.b;
     Span sp = span_of(p, bb);
-    int h = (int)((u0 - w.before) / sp.n);
+    int h = tile_of(u0 - w.before, sp.n);
     int ku = (int)((u0 - w.before) - (long long)h * sp.n);
     uint32_t it = 0;   // tiles before this pass: tile j of it is number it + j, in stage (it + j) % 2
     uint32_t pass = 0;

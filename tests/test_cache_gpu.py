@@ -337,6 +337,15 @@ def test_attention_and_weights_of_many_rows(case, D, dtype):
     test_attention_and_weights(case, D, dtype)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 256, 257])
+@pytest.mark.parametrize("H", [2, 20])
+def test_batches_around_what_a_warp_or_a_block_holds(B, H):
+    """The search for a CTA's share of the tokens takes a sequence to a lane, or
+    several to a thread; empty sequences among them, at either end."""
+    for lens in (None, [0] * (B - 1) + [900], [900] + [0] * (B - 1)):
+        test_attention_and_weights((B, H, 1, 1, 1500, lens, -1, 0), 64, "bf16")
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_weights_of_many_rows_run_to_run_and_hidden(D):
     """The same bits on every call and beside another stream's calls; rows that a
