@@ -523,7 +523,12 @@ def cache_evict(cache: PackedCache, acc, lens, keep: int, sinks: int = 0, recent
     Returns (cache, acc, lens, index): another cache (``out``, of any capacity
     from ``keep`` on, or a new one of capacity ``keep``), the kept tokens'
     weights [B, Hkv, capacity] (0 behind them), the new lengths [B] and the
-    kept positions [B, Hkv, keep] (-1 behind them)."""
+    kept positions [B, Hkv, keep] (-1 behind them).
+
+    The kept tokens move together: in the new cache positions, lengths, windows
+    and sinks count them alone (a window hides the kept tokens before it; none
+    sees them all).  A new cache is full once a sequence was cut; to append to
+    it, give ``out`` a capacity with room (two caches in turn)."""
     import torch
     kc, kp, vc, vp = cache
     B, Hkv, C, D, code = cache.sizes

@@ -445,6 +445,14 @@ FA_API fa_status fa_cache_weights(const void *Q, const void *Kc, const void *Kp,
  * -0 equals 0; NaN is below every number), in order of position.  A sequence
  * of at most `keep` tokens keeps them all.
  *
+ * The kept tokens move together: the j-th of them is token j of the other
+ * cache, and every later call counts positions, lengths, windows and sinks
+ * there.  window_left then reaches back over that many kept tokens, however
+ * far apart they once were, and hides the heavy ones before them: attention
+ * that is to see every kept token takes no window.  To append
+ * further tokens C2 must have room for them: a sequence that was cut fills the
+ * first `keep` rows.
+ *
  * Kc2, Kp2, Vc2, Vp2 : the other cache; rows behind the last kept token are
  *                      left as they are.
  * acc2  : [B, Hkv, C2] float32: the kept tokens' weights, then zeros.
