@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from contextlib import nullcontext
 from functools import lru_cache
 from operator import itemgetter
 
@@ -116,6 +117,25 @@ def _dtype_code(t) -> int:
     raise TypeError(f"fa_fwd takes bfloat16 or float16 tensors, got {t.dtype}")
 
 
+def _on(stream, t):
+    """Where a call on ``stream`` (None: torch's current one) has torch allocate
+    its results and workspace: on that very stream, so that no earlier work of
+    another stream still uses the memory, and what is dropped after the call is
+    handed on to later work of the same stream only."""
+    if stream is None:
+        return nullcontext()
+    import torch
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(nbytes: int, t):
+    """Device memory from torch's allocator (None: none needed)."""
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=t.device) if nbytes else None
+
+
 def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse=None, stream=None,
             schedule: str = "auto", window: tuple[int, int] | None = None, sinks: int | None = None):
     """Attention forward on CUDA tensors q [B, H, Nq, D], k and v [B, H, Nkv, D];
@@ -130,7 +150,10 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     ``out`` / ``lse`` may be given to write into existing buffers.
     ``schedule`` is "auto", "whole_tiles" or "balanced" (fa_schedule).
     Raises FAError on any non-OK status.  Asynchronous on ``stream``
-    (default: the current torch stream).
+    (default: the current torch stream).  In every call here the results that
+    are not given are allocated on that stream and belong to it, as in torch:
+    another stream waits for it before it uses them (``wait_stream``), and
+    holds them by ``record_stream``.
     """
     if sinks is not None:
         return _forward_sink(q, k, v, scale, out, lse, stream, schedule, window, sinks)
@@ -145,10 +168,10 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     B, H, N, D = q.shape
     if scale is None:
         scale = D ** -0.5
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    if out is None or lse is None:
+        with _on(stream, q):
+            out = torch.empty_like(q) if out is None else out
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device) if lse is None else lse
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -178,21 +201,6 @@ def _sink_workspace(device: int, *sizes) -> int:
     return n.value
 
 
-def _workspace(nbytes: int, t, stream):
-    """Workspace for a call on ``stream`` (None: torch's current one) from
-    torch's allocator, on that very stream: when it is dropped after the call,
-    torch hands it on to later work of the same stream only."""
-    import torch
-    if nbytes == 0:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-
-
 def _sink_shapes(q, k, v):
     """(B, H, Hkv, Nq, Nkv, D, dtype code) of tensors that go together."""
     sq, sk = q.shape, k.shape
@@ -211,17 +219,16 @@ def _forward_sink(q, k, v, scale, out, lse, stream, schedule, window, sinks):
     left = _left_of(window, sinks)
     if schedule not in SCHEDULES:
         raise ValueError(f"schedule must be one of {sorted(SCHEDULES)}")
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
         raise ValueError("out must be contiguous, of q's shape and type")
-    if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [B, H, Nq]")
     sched = SCHEDULES[schedule]
     nbytes = _sink_workspace(q.get_device(), B, H, Hkv, Nq, Nkv, D, left, sinks, sched)
-    ws = _workspace(nbytes, q, stream)
+    with _on(stream, q):
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = _workspace(nbytes, q)
     rc = load().fa_fwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq,
                             Nkv, D, left, sinks, D ** -0.5 if scale is None else scale, code, sched,
                             ws.data_ptr() if nbytes else None, nbytes, _stream_of(stream, q))
@@ -259,9 +266,9 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     Nkv = k.shape[2]
     if scale is None:
         scale = D ** -0.5
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    if dq is None or dk is None or dv is None:
+        with _on(stream, q):
+            dq, dk, dv = (torch.empty_like(x) if d is None else d for d, x in ((dq, q), (dk, k), (dv, v)))
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -299,13 +306,14 @@ def _backward_sink(q, k, v, o, do, lse, scale, dq, dk, dv, stream, window, deter
         raise ValueError("o, do, lse must be contiguous")
     if o.dtype != q.dtype or do.dtype != q.dtype or lse.dtype != torch.float32:
         raise TypeError("o, do must be of q's type, lse float32")
-    outs = [torch.empty_like(x) if d is None else d for d, x in ((dq, q), (dk, k), (dv, v))]
-    for d, x in zip(outs, (q, k, v)):
-        if d.shape != x.shape or d.dtype != x.dtype or not d.is_contiguous():
+    for d, x in ((dq, q), (dk, k), (dv, v)):
+        if d is not None and (d.shape != x.shape or d.dtype != x.dtype or not d.is_contiguous()):
             raise ValueError("dq, dk, dv must be contiguous, of the shapes and type of q, k, v")
     flags = FA_BWD_DETERMINISTIC if deterministic else 0
     nbytes = _sink_bwd_workspace(q.get_device(), B, H, Hkv, Nq, Nkv, D, left, sinks, flags)
-    ws = _workspace(nbytes, q, stream)
+    with _on(stream, q):
+        outs = [torch.empty_like(x) if d is None else d for d, x in ((dq, q), (dk, k), (dv, v))]
+        ws = _workspace(nbytes, q)
     rc = load().fa_bwd_sink(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                             *(d.data_ptr() for d in outs), B, H, Hkv, Nq, Nkv, D, left, sinks,
                             D ** -0.5 if scale is None else scale, code, flags, ws.data_ptr(), nbytes,
@@ -411,14 +419,16 @@ def cache_append(cache: PackedCache, k, v, start, count=None, stream=None) -> No
 
 def cache_read(cache: PackedCache, start, n: int, count=None, stream=None):
     """The values (k, v) [B, Hkv, n, D] that cache tokens start[b] + i stand
-    for; rows from count[b] on, or outside the cache, are zeros."""
+    for; rows from count[b] on, or outside the cache, are zeros.
+    Asynchronous on ``stream``, which the results belong to (see ``forward``)."""
     if not 1 <= n <= 0x7FFFFFFF:
         raise ValueError("n must be a 32-bit count of at least 1")
     kc, kp, vc, vp = cache
     B, Hkv, C, D, code = cache.sizes
     import torch
-    k = torch.empty((B, Hkv, n, D), dtype=kp.dtype, device=kp.device)
-    v = torch.empty_like(k)
+    with _on(stream, kp):
+        k = torch.empty((B, Hkv, n, D), dtype=kp.dtype, device=kp.device)
+        v = torch.empty_like(k)
     rc = load().fa_cache_read(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), k.data_ptr(), v.data_ptr(),
                               _ints(start, B, "start"), None if count is None else _ints(count, B, "count"), B, Hkv, n,
                               C, D, code, _stream_of(stream, k))
@@ -458,24 +468,23 @@ def cache_forward(q, cache: PackedCache, lens, window: tuple[int, int] | None = 
     from p - left on, but for the first ``sinks`` tokens, which stay visible.
 
     Raises FAError on any non-OK status.  Asynchronous on ``stream``
-    (default: the current torch stream; the outputs that are not given are
-    allocated on the current one, which a given ``stream`` must follow).
+    (default: the current torch stream), which the results that are not given
+    belong to (see ``forward``).
     """
     import torch
     kc, kp, vc, vp = cache
     B, Hkv, C, D, code = cache.sizes
     H, Nq = _cache_queries(q, cache)
     left = _left_of(window, sinks)
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
         raise ValueError("out must be contiguous, of q's shape and type")
-    if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [B, H, Nq]")
     nbytes = _cache_workspace(q.get_device(), B, H, Hkv, Nq, C, D)
-    ws = _workspace(nbytes, q, stream)
+    with _on(stream, q):
+        out = torch.empty_like(q) if out is None else out
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = _workspace(nbytes, q)
     rc = load().fa_cache_fwd(q.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(),
                              _ints(lens, B, "lens"), out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, C, D, left, sinks,
                              D ** -0.5 if scale is None else scale, code, ws.data_ptr() if nbytes else None, nbytes,
@@ -490,7 +499,9 @@ def cache_weights(q, cache: PackedCache, lse, lens, window: tuple[int, int] | No
     """What each cached token weighs in ``cache_forward`` of the same arguments
     (``lse`` as it returned it): [B, Hkv, C] float32, the sum over a key
     head's query rows of exp(scale q.k - lse).  With ``acc`` ([B, Hkv, C]
-    float32) the weights are added to it in place, and it is returned."""
+    float32) the weights are added to it in place, and it is returned.
+    Asynchronous on ``stream``, which a result that is not given belongs to (see
+    ``forward``)."""
     import torch
     kc, kp = cache[:2]
     B, Hkv, C, D, code = cache.sizes
@@ -501,7 +512,8 @@ def cache_weights(q, cache: PackedCache, lse, lens, window: tuple[int, int] | No
     if lse.dtype != torch.float32 or (acc is not None and acc.dtype != torch.float32):
         raise TypeError("lse and acc must be float32")
     if acc is None:
-        out = torch.empty((B, Hkv, C), dtype=torch.float32, device=q.device)
+        with _on(stream, q):
+            out = torch.empty((B, Hkv, C), dtype=torch.float32, device=q.device)
     elif acc.shape != (B, Hkv, C) or not acc.is_contiguous():
         raise ValueError("acc must be contiguous [B, Hkv, C]")
     else:
@@ -528,7 +540,8 @@ def cache_evict(cache: PackedCache, acc, lens, keep: int, sinks: int = 0, recent
     The kept tokens move together: in the new cache positions, lengths, windows
     and sinks count them alone (a window hides the kept tokens before it; none
     sees them all).  A new cache is full once a sequence was cut; to append to
-    it, give ``out`` a capacity with room (two caches in turn)."""
+    it, give ``out`` a capacity with room (two caches in turn).  Asynchronous on
+    ``stream``, which the results belong to (see ``forward``)."""
     import torch
     kc, kp, vc, vp = cache
     B, Hkv, C, D, code = cache.sizes
@@ -539,16 +552,18 @@ def cache_evict(cache: PackedCache, acc, lens, keep: int, sinks: int = 0, recent
     if not 1 <= keep <= 0x7FFFFFFF or sinks < 0 or recent < 0 or sinks + recent > keep:
         raise ValueError("keep must be at least 1 and hold the sinks and the recent tokens")
     if out is None:   # (its rows behind the last kept token are not written)
-        codes = torch.empty((B, Hkv, keep, D // 2), dtype=torch.uint8, device=kc.device)
-        params = torch.empty((B, Hkv, keep, 2), dtype=kp.dtype, device=kc.device)
-        out = PackedCache(codes, params, torch.empty_like(codes), torch.empty_like(params))
+        with _on(stream, kc):
+            codes = torch.empty((B, Hkv, keep, D // 2), dtype=torch.uint8, device=kc.device)
+            params = torch.empty((B, Hkv, keep, 2), dtype=kp.dtype, device=kc.device)
+            out = PackedCache(codes, params, torch.empty_like(codes), torch.empty_like(params))
     kc2, kp2, vc2, vp2 = out
     B2, Hkv2, C2, D2, code2 = out.sizes
     if (B2, Hkv2, D2, code2) != (B, Hkv, D, code) or C2 < keep:
         raise ValueError("out must be a cache like the first one, of capacity keep at least")
-    acc2 = torch.empty((B, Hkv, C2), dtype=torch.float32, device=kc.device)
-    lens2 = torch.empty_like(lens)
-    index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=kc.device)
+    with _on(stream, kc):
+        acc2 = torch.empty((B, Hkv, C2), dtype=torch.float32, device=kc.device)
+        lens2 = torch.empty_like(lens)
+        index = torch.empty((B, Hkv, keep), dtype=torch.int32, device=kc.device)
     rc = load().fa_cache_evict(kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), acc.data_ptr(),
                                _ints(lens, B, "lens"), kc2.data_ptr(), kp2.data_ptr(), vc2.data_ptr(), vp2.data_ptr(),
                                acc2.data_ptr(), lens2.data_ptr(), index.data_ptr(), B, Hkv, C, C2, D, keep, sinks,
