@@ -10,6 +10,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -305,9 +306,9 @@ fa_status launch_whole(int D, bool bf16, bool causal, const CUtensorMap &q, cons
                   : launch_mask<fa::kMaskNone, false>(D, bf16, q, k, v, p, grid, s, dev);
 }
 
-bool take_status_word_whole(cudaStream_t s, unsigned int *word)
+unsigned int *status_word_whole()
 {
-    return fa::take_status_word_on(s, word);
+    return fa::status_word_address();
 }
 
 }  // namespace fa_launch
@@ -805,20 +806,69 @@ extern "C" fa_status fa_bwd_sink(const void *Q, const void *K, const void *V, co
     return fa_launch::launch_bwd_sink(a, reinterpret_cast<cudaStream_t>(stream), dev);
 }
 
+namespace {
+
+// The status words of every unit with bounded waits, and where one read of
+// them leaves what it found: a slot of its own for each of the calls that may
+// be under way at a time (one after another, round robin).
+constexpr int kStatusWords = 7;
+constexpr unsigned int kStatusSlots = 64;
+struct StatusWords {
+    unsigned int *word[kStatusWords];
+};
+__device__ unsigned int g_status_taken[kStatusSlots];
+
+// One thread takes each word and clears it in a single atomic exchange, so a
+// timeout that a kernel on another stream records meanwhile is kept for the
+// next read, never lost.
+__global__ void take_status_kernel(StatusWords w, unsigned int slot)
+{
+    unsigned int any = 0;
+#pragma unroll
+    for (int i = 0; i < kStatusWords; ++i)
+        any |= atomicExch(w.word[i], 0u);
+    g_status_taken[slot] = any;
+}
+
+// Read and clear all words on stream `s` into *any: one launch, one copy and
+// one wait, however many units there are (a launch, copy and wait for each of
+// the seven took 130 us).  False if something failed.
+bool take_status(cudaStream_t s, unsigned int *any)
+{
+    static std::atomic<unsigned int> calls{0};
+    const StatusWords w = {{fa_launch::status_word_whole(), fa_launch::status_word_split(), fa_launch::status_word_band(),
+                            fa_launch::status_word_bwd(), fa_launch::status_word_sink(), fa_launch::status_word_bwd_sink(),
+                            fa_launch::status_word_rows()}};
+    *any = 0;
+    for (unsigned int *p : w.word)
+        if (!p)
+            return false;
+    const unsigned int slot = calls++ % kStatusSlots;
+    take_status_kernel<<<1, 1, 0, s>>>(w, slot);
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(any, g_status_taken, sizeof *any, slot * sizeof *any, cudaMemcpyDeviceToHost, s) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess) {
+        cudaGetLastError();
+        *any = 0;
+        return false;
+    }
+    return true;
+}
+
+}  // namespace
+
 extern "C" fa_status fa_sync_status(fa_stream_t stream)
 {
-    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (cudaStreamSynchronize(s) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_CUDA;
     }
-    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    unsigned int w_whole = 0, w_split = 0, w_band = 0, w_bwd = 0, w_sink = 0, w_bsink = 0, w_rows = 0;
-    if (!fa_launch::take_status_word_whole(s, &w_whole) || !fa_launch::take_status_word_split(s, &w_split) ||
-        !fa_launch::take_status_word_band(s, &w_band) || !fa_launch::take_status_word_bwd(s, &w_bwd) ||
-        !fa_launch::take_status_word_sink(s, &w_sink) || !fa_launch::take_status_word_bwd_sink(s, &w_bsink) ||
-        !fa_launch::take_status_word_rows(s, &w_rows))
+    unsigned int any;
+    if (!take_status(s, &any))
         return FA_ERR_CUDA;
-    if ((w_whole | w_split | w_band | w_bwd | w_sink | w_bsink | w_rows) != 0) {
+    if (any != 0) {
         // an aborted launch may have left split-tile counters non-zero
         int dev = -1;
         cudaGetDevice(&dev);

@@ -83,9 +83,9 @@ fa_status launch_bwd(const BwdLaunch &a, cudaStream_t s, int dev)
     return a.causal ? launch_all<128, false, true>(a, s, dev) : launch_all<128, false, false>(a, s, dev);
 }
 
-bool take_status_word_bwd(cudaStream_t s, unsigned int *word)
+unsigned int *status_word_bwd()
 {
-    return fa::take_status_word_on(s, word);
+    return fa::status_word_address();
 }
 
 }  // namespace fa_launch

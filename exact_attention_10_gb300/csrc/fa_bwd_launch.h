@@ -35,10 +35,10 @@ int sink_parts_for(int BH, int BHkv, int N, int Nkv, int wl, int sinks, int sms)
 // Enqueue the pre-pass, then the dQ pass and the dK/dV pass, or (fused) the
 // one pass and the conversion of the dQ accumulator, on `s`.
 fa_status launch_bwd(const BwdLaunch &a, cudaStream_t s, int dev);
-bool take_status_word_bwd(cudaStream_t s, unsigned int *word);
+unsigned int *status_word_bwd();
 
 // The same for a causal window with sinks and shared key heads (fa_bwd_sink.cu).
 fa_status launch_bwd_sink(const BwdLaunch &a, cudaStream_t s, int dev);
-bool take_status_word_bwd_sink(cudaStream_t s, unsigned int *word);
+unsigned int *status_word_bwd_sink();
 
 }  // namespace fa_launch

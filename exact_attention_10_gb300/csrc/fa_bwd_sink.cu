@@ -106,9 +106,9 @@ fa_status launch_bwd_sink(const BwdLaunch &a, cudaStream_t s, int dev)
     return a.bf16 ? launch_all<128, true>(a, s, dev) : launch_all<128, false>(a, s, dev);
 }
 
-bool take_status_word_bwd_sink(cudaStream_t s, unsigned int *word)
+unsigned int *status_word_bwd_sink()
 {
-    return fa::take_status_word_on(s, word);
+    return fa::status_word_address();
 }
 
 }  // namespace fa_launch

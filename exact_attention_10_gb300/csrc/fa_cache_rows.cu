@@ -501,9 +501,9 @@ fa_status launch_weights_rows(const fa::cache::Params &p, int D, bool bf16, int 
     return bf16 ? fa::cache::launch<128, true>(p, sms, s, dev) : fa::cache::launch<128, false>(p, sms, s, dev);
 }
 
-bool take_status_word_rows(cudaStream_t s, unsigned int *word)
+unsigned int *status_word_rows()
 {
-    return fa::take_status_word_on(s, word);
+    return fa::status_word_address();
 }
 
 }  // namespace fa_launch

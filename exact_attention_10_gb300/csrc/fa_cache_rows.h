@@ -15,6 +15,6 @@ struct Params;
 namespace fa_launch {
 
 fa_status launch_weights_rows(const fa::cache::Params &p, int D, bool bf16, int sms, cudaStream_t s, int dev);
-bool take_status_word_rows(cudaStream_t s, unsigned int *word);
+unsigned int *status_word_rows();
 
 }  // namespace fa_launch

@@ -87,32 +87,18 @@ namespace fa {
 // Device status word: 0 = fine; otherwise 1 | (site << 8) of the first wait
 // that expired.  Each translation unit that includes this header has its own
 // (device code is not linked across units); fa_sync_status() reads and clears
-// every unit's word (take_status_word_on).
+// them all in one kernel, by their addresses.
 static __device__ unsigned int g_status_word;
 
-// fa_sync_status's read of this unit's status word: one thread takes the
-// word and clears it in a single atomic exchange, so a timeout that a kernel
-// on another stream records meanwhile is kept for the next read, never lost.
-static __device__ unsigned int g_status_taken;
-static __global__ void take_status_kernel()
+// Host: this unit's status word on the current device; null on an error.
+static inline unsigned int *status_word_address()
 {
-    g_status_taken = atomicExch(&g_status_word, 0u);
-}
-
-// Host: read and clear this unit's status word (current device) on stream
-// `s` into *word; false if a launch or copy failed.
-static inline bool take_status_word_on(cudaStream_t s, unsigned int *word)
-{
-    *word = 0;
-    take_status_kernel<<<1, 1, 0, s>>>();
-    if (cudaGetLastError() != cudaSuccess ||
-        cudaMemcpyFromSymbolAsync(word, g_status_taken, sizeof *word, 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess) {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) {
         cudaGetLastError();
-        *word = 0;
-        return false;
+        return nullptr;
     }
-    return true;
+    return static_cast<unsigned int *>(p);
 }
 
 constexpr int kBM = 128;        // query rows per Q tile (one TMEM lane each)

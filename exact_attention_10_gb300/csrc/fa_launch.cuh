@@ -77,10 +77,10 @@ fa_status launch_band(int D, bool bf16, bool split, const CUtensorMap &q, const 
                       const CUtensorMap &v, const fa::FwdParams &p, int grid, cudaStream_t s, int dev);
 fa_status launch_sink(int D, bool bf16, bool split, const CUtensorMap &q, const CUtensorMap &k,
                       const CUtensorMap &v, const fa::SinkParams &p, int grid, cudaStream_t s, int dev);
-bool take_status_word_whole(cudaStream_t s, unsigned int *word);
-bool take_status_word_split(cudaStream_t s, unsigned int *word);
-bool take_status_word_band(cudaStream_t s, unsigned int *word);
-bool take_status_word_sink(cudaStream_t s, unsigned int *word);
+unsigned int *status_word_whole();
+unsigned int *status_word_split();
+unsigned int *status_word_band();
+unsigned int *status_word_sink();
 
 // The static workspace of fa_fwd_noalloc (fa_split.cu): points p's partial
 // buffers into it for schedule `sc` and head size D, and clears the counters

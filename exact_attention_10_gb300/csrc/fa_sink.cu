@@ -11,9 +11,9 @@ fa_status launch_sink(int D, bool bf16, bool split, const CUtensorMap &q, const 
                  : launch_mask<fa::kMaskSink, false>(D, bf16, q, k, v, p, grid, s, dev);
 }
 
-bool take_status_word_sink(cudaStream_t s, unsigned int *word)
+unsigned int *status_word_sink()
 {
-    return fa::take_status_word_on(s, word);
+    return fa::status_word_address();
 }
 
 }  // namespace fa_launch

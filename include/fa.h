@@ -472,8 +472,9 @@ FA_API fa_status fa_cache_evict(const void *Kc, const void *Kp, const void *Vc, 
  * itself failed.
  *
  * The word is read and cleared in one atomic exchange by a one-thread kernel
- * on `stream`, so a timeout recorded meanwhile is never lost.  There is one
- * word per device, shared by all streams: a timeout from a kernel on another
+ * on `stream`, so a timeout recorded meanwhile is never lost.  (One launch, one
+ * copy and one wait a call.)  There is one word per device, shared by all
+ * streams: a timeout from a kernel on another
  * stream is reported by whichever call reads the word first, and a timeout
  * from a kernel on another stream that has not finished yet is reported only
  * by a later call.  To attribute a timeout to a stream, synchronise the
