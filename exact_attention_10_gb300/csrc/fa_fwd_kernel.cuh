@@ -252,14 +252,7 @@ template <int MASK, bool SPLIT, class S>
 __device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, int &bh, int &ct, SinkTile &tile)
 {
     if constexpr (MASK == kMaskSink && !SPLIT) {
-        if (it.t >= s.T)
-            return false;
-        sched_decode_fast(s, it.t, bh, ct);
-        tile = sched_sink_tile(s, ct);
-        pt = Part{it.t, 0, tile.n, -1, 0};
-        ++it.u;
-        it.t = it.u * s.G + ((it.u & 1) ? s.G - 1 - it.c : it.c);   // (serpentine rounds, as PartIter's)
-        return true;
+        return sched_next_whole(s, it, pt, bh, ct, tile);
     } else {
         if (!it.template next_t<SPLIT, kBanded<MASK>>(s, pt))
             return false;

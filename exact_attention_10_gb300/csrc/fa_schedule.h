@@ -785,6 +785,20 @@ FA_HD void sched_decode_fast(const SinkSchedule &s, int t, int &bh, int &ct)
     ct = s.rev ? q : s.C - 1 - q;
 }
 
+// PartIter's next part of a whole-tile schedule (serpentine rounds) with its
+// head, row and steps, as the kernel's roles take it: without a division.
+FA_HD bool sched_next_whole(const SinkSchedule &s, PartIter &it, Part &pt, int &bh, int &ct, SinkTile &tile)
+{
+    if (it.t >= s.T)
+        return false;
+    sched_decode_fast(s, it.t, bh, ct);
+    tile = sched_sink_tile(s, ct);
+    pt = Part{it.t, 0, tile.n, -1, 0};
+    ++it.u;
+    it.t = it.u * s.G + ((it.u & 1) ? s.G - 1 - it.c : it.c);
+    return true;
+}
+
 // Workspace bytes of a balanced schedule at head size D: a partial O
 // ([256 rows][D] fp32) and (m, l) per row for two slots per CTA, then two
 // int counters per CTA tile (one per Q tile).  Whole tiles need none.
