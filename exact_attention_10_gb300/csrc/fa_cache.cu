@@ -43,8 +43,9 @@ bool queries_ok(int B, int H, int Hkv, int Nq)
 }
 
 // Query rows per tile: 8 where a key head has no more, else 16 (a tile's rows
-// share the unpacked codes, so 16 rows cost little more than 8; their
-// accumulators fill the registers of one CTA per SM instead of two).
+// share the unpacked codes, but their accumulators fill the registers of one CTA
+// per SM instead of two: 108 us for 16 rows against 79 for 8, see
+// fa_cache_kernel.cuh, which also says what more rows cost).
 int row_tiles(int rows)
 {
     return rows <= 8 ? 1 : 2;

@@ -23,11 +23,17 @@
 // for each of K and V, and does 4 G Nq D operations on it -- HBM, at the few
 // query rows per key head of decoding, if unpacking keeps up: 16 tokens are 64
 // codes per lane for each of K and V, about five integer operations per eight.
-// Hence mma.sync and not tcgen05: the codes go from shared memory through
-// registers (unpacking) straight into A fragments (16 tokens or channels x 16)
-// with the 8 query rows as the N dimension, where tcgen05 would want the
+// Hence mma.sync and not tcgen05 at those: the codes go from shared memory
+// through registers (unpacking) straight into A fragments (16 tokens or channels
+// x 16) with the 8 query rows as the N dimension, where tcgen05 would want the
 // unpacked operand written back to shared memory or TMEM first, and its M =
 // 128 rows are 16 times what a decode step has.
+// More rows per key head (drafted tokens, the end of a prompt) come in blocks
+// of 16, each of which reads and unpacks the key head's rows again, so the time
+// grows with them: 16 sequences of 16001 to 32768 tokens, 8 key heads, D = 128,
+// 8 / 16 / 32 / 64 rows: 79 / 108 / 196 / 376 us, where the bytes take 63 at
+// each.  One pass for all rows would be a product for tcgen05, as the weights
+// have it (fa_cache_rows.cu); the attention has none.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -143,9 +143,10 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     is aligned bottom-right (fa_fwd_qkv).  ``window = (left, right)`` masks
     with a band instead (fa_fwd_band; a negative bound is unbounded; causal
     is ignored then).  With ``sinks`` (0 or more) the mask is the causal
-    window (left, 0), without one plain causal, in which the first ``sinks``
-    keys stay visible, and k and v may have fewer heads, [B, Hkv, Nkv, D] with
-    H a multiple of Hkv (fa_fwd_sink).
+    window (left, 0), without one plain causal, whatever ``causal`` says, in
+    which the first ``sinks`` keys stay visible, and k and v may have fewer
+    heads, [B, Hkv, Nkv, D] with H a multiple of Hkv (fa_fwd_sink); shared heads
+    without sinks take ``sinks=0``, other masks have none.
 
     ``out`` / ``lse`` may be given to write into existing buffers.
     ``schedule`` is "auto", "whole_tiles" or "balanced" (fa_schedule).
@@ -245,7 +246,7 @@ def backward(q, k, v, o, do, lse, causal: bool = False, scale: float | None = No
     go to fa_bwd; a window, or Nq != Nkv (bottom-right causal), to fa_bwd_band;
     ``deterministic`` (dQ by the second pass, the same bits on every call) to
     fa_bwd_ex with FA_BWD_DETERMINISTIC; ``sinks`` (k, v [B, Hkv, Nkv, D], the
-    mask of ``forward`` with sinks) to fa_bwd_sink.
+    mask of ``forward`` with sinks, ``causal`` or not) to fa_bwd_sink.
 
     ``dq`` / ``dk`` / ``dv`` may be given to write into existing buffers.
     Raises FAError on any non-OK status.  Asynchronous on ``stream``

@@ -404,14 +404,16 @@ FA_API fa_status fa_cache_workspace(int B, int H, int Hkv, int Nq, int C, int D,
  * fa_cache_fwd -- attention of each sequence's last Nq tokens against the
  * cache: decoding (Nq = 1), speculative decoding, or the end of a prompt.
  *
- * Q, O : [B, H, Nq, D] of `dtype`; H a multiple of Hkv, query heads h Hkv/H
- *        sharing key head floor(h / (H / Hkv)).  LSE : [B, H, Nq] float32.
+ * Q, O : [B, H, Nq, D] of `dtype`; H a multiple of Hkv, query head h reading
+ *        key head floor(h / (H / Hkv)).  LSE : [B, H, Nq] float32.
  * Query i of sequence b sits at position p = lens[b] - Nq + i (its own key is
  * in the cache) and sees the tokens j <= p with j >= p - window_left
  * (window_left < 0: no bound) or j < sinks.  A query that sees no token
  * (p < 0) gets O = 0 and LSE = -inf.
  * workspace : fa_cache_workspace bytes (NULL where they are 0); its contents
  *        need no set-up.
+ * The (H / Hkv) Nq query rows of a key head are taken 16 at a time, each block
+ * with a pass of its own over the cache.
  *
  * K and V enter the products as their integer codes, exact in 16 bits, with
  * scale and minimum applied outside them in fp32; the softmax weight times V's
