@@ -125,8 +125,8 @@ def _on(stream, t):
     if stream is None:
         return nullcontext()
     import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    if not isinstance(stream, torch.cuda.Stream):   # a handle, or another library's stream with one
+        stream = torch.cuda.ExternalStream(_stream_of(stream, t), device=t.device)
     return torch.cuda.stream(stream)
 
 

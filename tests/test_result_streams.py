@@ -51,8 +51,11 @@ def _calls(dev, dtype, B=2, H=4, Hkv=2, N=40, D=64, C=48):
 NAMES = list(_calls("cpu", torch.bfloat16))
 
 
-class _Stream:
-    cuda_stream = 77
+class _Foreign:
+    """Another library's stream: nothing but a handle."""
+
+    def __init__(self, handle=77):
+        self.cuda_stream = handle
 
 
 class _Lib:
@@ -66,8 +69,9 @@ class _Lib:
         return call
 
 
+@pytest.mark.parametrize("stream", [_Foreign(), 77], ids=["object", "handle"])
 @pytest.mark.parametrize("name", NAMES)
-def test_allocations_are_on_the_given_stream(name, monkeypatch):
+def test_allocations_are_on_the_given_stream(name, stream, monkeypatch):
     call = _calls("cpu", torch.bfloat16)[name]
     on, made = [], []
 
@@ -95,11 +99,11 @@ def test_allocations_are_on_the_given_stream(name, monkeypatch):
             lib = _Lib()
             m.setattr(fa, "load", lambda *a: lib)
             m.setattr(torch.cuda, "stream", Context)
+            m.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
             m.setattr(torch, "empty", recorded(torch.empty))
             m.setattr(torch, "empty_like", recorded(torch.empty_like))
-            s = _Stream()
-            call(s)
-            assert made and all(x is s for x in made), made
+            call(stream)
+            assert made and all(x == ("external", 77) for x in made), made
     finally:
         for x in queries:
             x.cache_clear()
@@ -130,3 +134,21 @@ def test_results_do_not_take_memory_that_is_still_written(name):
     assert fa.sync_status(side.cuda_stream) == 0
     for a, b in zip(got, want):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NAMES)
+def test_streams_of_every_kind(name):
+    """torch's streams, plain handles (the legacy default stream's 0 among them)
+    and objects with nothing but a handle."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    call = _calls("cuda", torch.bfloat16)[name]
+    want = call(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream, _Foreign(side.cuda_stream), 0):
+        got = call(stream)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
