@@ -20,6 +20,7 @@
 #include "fa_cache_rows.h"
 #include "fa_host.h"
 #include "fa_launch.cuh"
+#include "fa_packed_launch.h"
 
 namespace {
 
@@ -141,6 +142,7 @@ fa_status allow_smem(const void *kern, int smem, int dev, bool *set)
 
 namespace {
 
+using fa_host::current_device;
 using fa_host::device_info;
 using fa_host::DeviceInfo;
 using fa_host::is_device_pointer;
@@ -182,6 +184,46 @@ bool encode_map_f32(CUtensorMap *m, float *ptr, long long rows, int D)
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+namespace fa_host {
+
+fa_status current_device(int *dev, const DeviceInfo **di)
+{
+    *dev = -1;
+    if (cudaGetDevice(dev) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_UNSUPPORTED_DEVICE;
+    }
+    *di = device_info(*dev);
+    return (*di && (*di)->supported) ? FA_OK : FA_ERR_UNSUPPORTED_DEVICE;
+}
+
+bool encode_rows_f32(CUtensorMap *m, float *ptr, long long rows, int D)
+{
+    return encode_map_f32(m, ptr, rows, D);
+}
+
+bool encode_packed(CUtensorMap *m, const void *ptr, int rows, int heads, int D, long long row, long long head, bool bf16)
+{
+    EncodeTiledFn enc = encode_tiled();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {(cuuint64_t)row * 2, (cuuint64_t)head * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)fa::kBM, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                           const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+}  // namespace fa_host
+
+namespace {
 
 // Per-(device, stream) workspace for split tiles: partial O and (m, l) for
 // two slots per CTA, and one counter per (tile, Q tile) that must be zero
@@ -421,18 +463,6 @@ bool sink_sizes_ok(int B, int H, int Hkv, int Nq, int Nkv, int D, int window_lef
     *wl = window_left;
     fa::sched_band_normalize(Nq, Nkv, *wl, wr);
     return true;
-}
-
-// The current device, if it is one this library runs on.
-fa_status current_device(int *dev, const DeviceInfo **di)
-{
-    *dev = -1;
-    if (cudaGetDevice(dev) != cudaSuccess) {
-        cudaGetLastError();
-        return FA_ERR_UNSUPPORTED_DEVICE;
-    }
-    *di = device_info(*dev);
-    return (*di && (*di)->supported) ? FA_OK : FA_ERR_UNSUPPORTED_DEVICE;
 }
 
 }  // namespace
@@ -811,7 +841,7 @@ namespace {
 // The status words of every unit with bounded waits, and where one read of
 // them leaves what it found: a slot of its own for each of the calls that may
 // be under way at a time (one after another, round robin).
-constexpr int kStatusWords = 7;
+constexpr int kStatusWords = 9;
 constexpr unsigned int kStatusSlots = 64;
 struct StatusWords {
     unsigned int *word[kStatusWords];
@@ -832,13 +862,14 @@ __global__ void take_status_kernel(StatusWords w, unsigned int slot)
 
 // Read and clear all words on stream `s` into *any: one launch, one copy and
 // one wait, however many units there are (a launch, copy and wait for each of
-// the seven took 130 us).  False if something failed.
+// seven took 130 us).  False if something failed.
 bool take_status(cudaStream_t s, unsigned int *any)
 {
     static std::atomic<unsigned int> calls{0};
     const StatusWords w = {{fa_launch::status_word_whole(), fa_launch::status_word_split(), fa_launch::status_word_band(),
                             fa_launch::status_word_bwd(), fa_launch::status_word_sink(), fa_launch::status_word_bwd_sink(),
-                            fa_launch::status_word_rows()}};
+                            fa_launch::status_word_rows(), fa_launch::status_word_packed(),
+                            fa_launch::status_word_bwd_packed()}};
     *any = 0;
     for (unsigned int *p : w.word)
         if (!p)

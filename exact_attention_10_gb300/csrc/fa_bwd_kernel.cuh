@@ -131,6 +131,34 @@ struct SinkParams : Params {
     float *part;    // KV, nc > 1: the parts' dK and dV, [BHkv * ss * nc][2][128][D] fp32, not yet scaled
 };
 
+// Packed sequences (fa_packed.h): tiles and lengths come from the plan's list
+// of the pass, N is the tokens, Npad the rows of the statistics per head.
+struct PackedParams : Params {
+    const int4 *header, *list;
+    int H, group;           // query heads, and those per key head
+    int heads;              // of a tile: H (dQ pass) or H / group (KV)
+    int causal;
+    long long a_row, a_head, b_row, b_head;   // bytes between rows and heads of dA and dB
+};
+
+template <class P>
+constexpr bool kPackedPass = false;
+template <>
+constexpr bool kPackedPass<PackedParams> = true;
+
+// Work tiles of the pass.
+template <bool KV>
+__device__ __forceinline__ int work_tiles(const Params &p)
+{
+    return p.T;
+}
+template <bool KV>
+__device__ __forceinline__ int work_tiles(const PackedParams &p)
+{
+    const int4 h = ld_plan(p.header);
+    return (KV ? h.z : h.y) * p.heads;
+}
+
 template <class P>
 constexpr bool kSinkPass = false;
 template <>
@@ -376,6 +404,53 @@ __device__ __forceinline__ SinkWork<KV> bwd_work(const SinkParams &p, bool, int 
     return w;
 }
 
+// Packed sequences.  dK/dV pass: a key tile streams the query tiles of its
+// sequence that see it, of each of the group's query heads in turn; one that no
+// query sees takes one step with an empty query tile, which writes its zeros.
+// dQ pass: a query tile streams the key tiles its rows see.
+template <bool KV>
+struct PackedWork {
+    int rh, rt, n;
+    int q0, Lq, k0, Lk;    // the sequence
+    int qt0;               // its first query tile among all sequences'
+    int per, s0, group;    // KV: as in SinkWork; per = 0: the empty tile
+    int empty;             // the empty query tile
+    __device__ int head(int j) const { return KV ? rh * group + (per ? j / per : 0) : rh / group; }
+    __device__ int tile(int j) const { return KV ? (per ? s0 + j % per : 0) : j; }
+    __device__ int slot() const { return -1; }
+    __device__ int rows(int j) const { return (KV ? Lq : Lk) - tile(j) * kTile; }   // of step j's tile (128 or more: all)
+    __device__ int qtile(int t) const { return KV && per == 0 ? empty : qt0 + t; }   // among all sequences', of tile t
+};
+
+template <bool KV>
+__device__ __forceinline__ PackedWork<KV> bwd_work(const PackedParams &p, bool, int t)
+{
+    PackedWork<KV> w;
+    const int e = (int)((uint32_t)t / (uint32_t)p.heads);
+    w.rh = t - e * p.heads;
+    const int4 seq = ld_plan(p.list + 2 * (size_t)e), at = ld_plan(p.list + 2 * (size_t)e + 1);
+    w.q0 = seq.x;
+    w.Lq = seq.y;
+    w.k0 = seq.z;
+    w.Lk = seq.w;
+    w.rt = at.x;
+    w.qt0 = at.y;
+    w.group = p.group;
+    w.empty = ld_plan(p.header).y;
+    w.per = w.s0 = 0;
+    if (KV) {
+        const int s0 = packed::first_query_tile(w.rt, w.Lq, w.Lk, p.causal);
+        if (s0 >= 0) {
+            w.s0 = s0;
+            w.per = (w.Lq + kTile - 1) / kTile - s0;
+        }
+        w.n = w.per ? w.per * p.group : 1;
+    } else {
+        w.n = packed::key_steps(w.rt * kTile, w.Lq, w.Lk, p.causal);
+    }
+    return w;
+}
+
 // The band mask of one step, in terms of d = key - query: with (kt, qt) the
 // step's key and query tiles, d = 128 (kt - qt) + x where x = lane - column
 // (KV) or column - lane (dQ pass), and key j is visible from query i iff
@@ -434,6 +509,39 @@ __device__ __forceinline__ StepMask bwd_step_mask(const SinkParams &p, bool, int
         m.whole = m.e_hi >= kTile - 1;
     }
     return m;
+}
+
+// The mask of a step of work `wk`.  Packed: the sequence's diagonal, and in the
+// dK/dV pass the key rows behind its end: their P would reach dQ in the fused
+// pass.
+template <bool KV, class P, class W>
+__device__ __forceinline__ StepMask work_mask(const P &p, const W &wk, bool causal, int kt, int qt)
+{
+    if constexpr (kPackedPass<P>) {
+        StepMask m{-1024, 1024, true};
+        if (p.causal) {
+            const long long e = (long long)wk.Lk - wk.Lq - (long long)kTile * (kt - qt);
+            m.e_hi = (int)(e < -1024 ? -1024 : (e > 1024 ? 1024 : e));
+            m.whole = m.e_hi >= kTile - 1;
+        }
+        if (KV && wk.Lk - kt * kTile < kTile)
+            m.whole = false;
+        return m;
+    } else {
+        return bwd_step_mask(p, causal, kt, qt);
+    }
+}
+
+// ... and what it hides from key row `row` (KV).
+template <bool KV, class P, class W>
+__device__ __forceinline__ void work_mask_row(const P &, const W &wk, StepMask &m, int kt, int row)
+{
+    if constexpr (kPackedPass<P> && KV) {
+        if (kt * kTile + row >= wk.Lk) {
+            m.e_lo = 1024;
+            m.e_hi = -1024;
+        }
+    }
 }
 
 __device__ __forceinline__ void sink_row(const Params &, StepMask &, int, int) {}
@@ -546,6 +654,39 @@ __device__ __forceinline__ bool warp_wait_all(uint32_t b0, uint32_t p0, bool u0,
 
 // ------------------------------------------------------------------ producer
 
+// One box of a tile of keys (KEYS) or query rows of the work's sequence (load_box).
+template <bool KEYS, class P, class W>
+__device__ __forceinline__ void bwd_box(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int x, int row, int head,
+                                        const P &, const W &wk)
+{
+    if constexpr (kPackedPass<P>)
+        load_box<true>(dst, tm, bar, x, row, head, KEYS ? wk.k0 : wk.q0);
+    else
+        load_box<false>(dst, tm, bar, x, row, head, 0);
+}
+
+// The rows behind its sequence in step j's pair of streamed tiles, global step g,
+// zeroed as far as the products over them go (packed::tail_ksteps), by the MMA
+// warp; and those products' k-steps.
+template <int D, bool KV, bool FQ = false, class P, class W>
+__device__ __forceinline__ void zero_streamed(const P &, const W &wk, int j, uint32_t sStage, int g)
+{
+    if constexpr (kPackedPass<P>) {
+        const int n = wk.rows(j);
+        zero_tail<D>(BCfg<D, KV, FQ>::slot0(sStage, g), n);
+        zero_tail<D>(BCfg<D, KV, FQ>::slot1(sStage, g), n);
+    }
+}
+
+template <class P, class W>
+__device__ __forceinline__ int streamed_ksteps(const P &, const W &wk, int j)
+{
+    if constexpr (kPackedPass<P>)
+        return packed::tail_ksteps(wk.rows(j));
+    else
+        return kTile / 16;
+}
+
 template <int D, bool KV, bool FQ, class P>
 __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const CUtensorMap *tmS0,
                          const CUtensorMap *tmS1, const P &p, bool causal, uint32_t sRes, uint32_t sStage,
@@ -556,7 +697,7 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
     bool ok = true;
     for (int r = 0; ok; ++r) {
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= p.T)
+        if (t >= work_tiles<KV>(p))
             break;
         const auto wk = bwd_work<KV>(p, causal, t);
         const int n = wk.n;
@@ -567,8 +708,8 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
         if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(b.res_full(), 2 * C::kTileBytes);
             for (int x = 0; x < C::kBoxes; ++x) {
-                ptx::tma_load_3d(sRes + x * C::kBoxBytes, tmR0, b.res_full(), x * 64, wk.rt * kTile, wk.rh);
-                ptx::tma_load_3d(sRes + C::kTileBytes + x * C::kBoxBytes, tmR1, b.res_full(), x * 64, wk.rt * kTile, wk.rh);
+                bwd_box<KV>(sRes + x * C::kBoxBytes, tmR0, b.res_full(), x * 64, wk.rt * kTile, wk.rh, p, wk);
+                bwd_box<KV>(sRes + C::kTileBytes + x * C::kBoxBytes, tmR1, b.res_full(), x * 64, wk.rt * kTile, wk.rh, p, wk);
             }
         }
         __syncwarp();
@@ -587,8 +728,8 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
                     ptx::mbar_arrive_expect_tx(b.full(k0), C::kTileBytes);
                     ptx::mbar_arrive_expect_tx(b.full1(k1), C::kTileBytes);
                     for (int x = 0; x < C::kBoxes; ++x) {
-                        ptx::tma_load_3d(d0 + x * C::kBoxBytes, tmS0, b.full(k0), x * 64, row, bh);
-                        ptx::tma_load_3d(d1 + x * C::kBoxBytes, tmS1, b.full1(k1), x * 64, row, bh);
+                        bwd_box<!KV>(d0 + x * C::kBoxBytes, tmS0, b.full(k0), x * 64, row, bh, p, wk);
+                        bwd_box<!KV>(d1 + x * C::kBoxBytes, tmS1, b.full1(k1), x * 64, row, bh, p, wk);
                     }
                 }
                 __syncwarp();
@@ -604,11 +745,13 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
                 const uint32_t dst = sStage + st * C::kStageBytes;
                 ptx::mbar_arrive_expect_tx(b.full(st), C::kStageBytes);
                 for (int x = 0; x < C::kBoxes; ++x) {
-                    ptx::tma_load_3d(dst + x * C::kBoxBytes, tmS0, b.full(st), x * 64, row, bh);
-                    ptx::tma_load_3d(dst + C::kTileBytes + x * C::kBoxBytes, tmS1, b.full(st), x * 64, row, bh);
+                    bwd_box<!KV>(dst + x * C::kBoxBytes, tmS0, b.full(st), x * 64, row, bh, p, wk);
+                    bwd_box<!KV>(dst + C::kTileBytes + x * C::kBoxBytes, tmS1, b.full(st), x * 64, row, bh, p, wk);
                 }
                 if (KV) {   // the query tile's lg and delta: 512 bytes each, 16-byte aligned (Npad % 128 == 0)
-                    const size_t off = (size_t)bh * p.Npad + row;
+                    size_t off = (size_t)bh * p.Npad + row;
+                    if constexpr (kPackedPass<P>)
+                        off = (size_t)bh * p.Npad + (size_t)wk.qtile(wk.tile(j)) * kTile;
                     ptx::bulk_load(dst + 2 * C::kTileBytes, p.lg + off, kTile * 4, b.full(st));
                     ptx::bulk_load(dst + 2 * C::kTileBytes + kTile * 4, p.dl + off, kTile * 4, b.full(st));
                 }
@@ -679,7 +822,7 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
 
     for (int r = 0; ok; ++r) {
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= p.T)
+        if (t >= work_tiles<KV>(p))
             break;
         const auto wk = bwd_work<KV>(p, causal, t);
         const int n = wk.n;
@@ -690,6 +833,7 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
         ptx::tc_fence_after_sync();
         if (!stage_ready(g))
             break;
+        zero_streamed<D, KV>(p, wk, 0, sStage, g);
         issue_sd(g, r0_lo, 0u, tS, b.sd_full());
         issue_sd(g, r1_lo, (uint32_t)C::kTileBytes, tDP, b.dp_full());
         for (int j = 0; j < n; ++j, ++g) {
@@ -711,11 +855,13 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
             const uint32_t sa = sStage + (uint32_t)(st * C::kStageBytes);
             const uint32_t m0_lo = desc_lo(sa + C::kTileBytes, C::kBoxBytes);   // dO
             const uint32_t m1_lo = desc_lo(sa, C::kBoxBytes);                   // Q
+            const int ks = streamed_ksteps(p, wk, j);
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    ptx::mma_ts(tAcc0, tS + a_col(kk), desc_from_lo(m0_lo + kk * (2048 >> 4)), kIdescTS,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+                    if (!kPackedPass<P> || kk < ks)
+                        ptx::mma_ts(tAcc0, tS + a_col(kk), desc_from_lo(m0_lo + kk * (2048 >> 4)), kIdescTS,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
             }
             __syncwarp();
             if (j + 1 < n) {   // S_{g+1} over P^T_g, behind dV_g
@@ -723,13 +869,15 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
                     ok = false;
                     break;
                 }
+                zero_streamed<D, KV>(p, wk, j + 1, sStage, g + 1);
                 issue_sd(g + 1, r0_lo, 0u, tS, b.sd_full());
             }
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    ptx::mma_ts(tAcc1, tDP + a_col(kk), desc_from_lo(m1_lo + kk * (2048 >> 4)), kIdescTS,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+                    if (!kPackedPass<P> || kk < ks)
+                        ptx::mma_ts(tAcc1, tDP + a_col(kk), desc_from_lo(m1_lo + kk * (2048 >> 4)), kIdescTS,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
                 ptx::mma_commit(b.empty(st));
                 if (j == n - 1) {
                     ptx::mma_commit(b.acc_full());
@@ -807,7 +955,7 @@ __device__ void bwd_compute(const P &p, uint32_t tmem, uint32_t sStage, BBars<D,
     int step = 0, tiles = 0;
     for (int r = 0;; ++r) {
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= p.T)
+        if (t >= work_tiles<KV>(p))
             break;
         const auto wk = bwd_work<KV>(p, CAUSAL, t);
         const int bh = wk.rh, rt = wk.rt, n = wk.n;
@@ -823,9 +971,10 @@ __device__ void bwd_compute(const P &p, uint32_t tmem, uint32_t sStage, BBars<D,
             // Masks: the band's edges (the causal diagonal); padding queries
             // and queries without keys have lg = +inf (stored as -lg = -inf),
             // so their P is already 0.
-            StepMask sm = bwd_step_mask(p, CAUSAL, rt, si);
+            StepMask sm = work_mask<KV>(p, wk, CAUSAL, rt, si);
             const bool masked = !sm.whole;   // warp-uniform
             sink_row(p, sm, rt, lane_row);
+            work_mask_row<KV>(p, wk, sm, rt, lane_row);
             uint32_t pv[64];   // S, then P (fp32)
             ptx::tmem_ld64(tS, pv);
             ptx::tmem_wait_ld();
@@ -902,6 +1051,12 @@ __device__ void bwd_compute(const P &p, uint32_t tmem, uint32_t sStage, BBars<D,
         if (KV) {
             const uint32_t tA = tmem + (h ? C::kColAcc1 : C::kColAcc0) + lane_off;
             char *dst = static_cast<char *>(h ? p.dA : p.dB) + ((size_t)bh * p.Nkv + grow) * D * 2;
+            int end = p.Nkv;
+            if constexpr (kPackedPass<P>) {
+                dst = static_cast<char *>(h ? p.dA : p.dB) + (long long)(wk.k0 + grow) * (h ? p.a_row : p.b_row) +
+                      (long long)bh * (h ? p.a_head : p.b_head);
+                end = wk.Lk;
+            }
             const float mul = h ? p.scale : 1.f;
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
@@ -910,7 +1065,7 @@ __device__ void bwd_compute(const P &p, uint32_t tmem, uint32_t sStage, BBars<D,
                 ptx::tmem_wait_ld();
                 if (kSinkPass<P> && wk.slot() >= 0)
                     store_part32(part_row<D>(p, wk.slot(), h, lane_row) + 32 * cc, v);
-                else if (grow < p.Nkv)
+                else if (grow < end)
                     store_row32<BF16>(dst + cc * 64, v, mul);
             }
         } else {
@@ -972,7 +1127,8 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
 
     // S_g = R0 S0_g^T and dP_g = R1 S1_g^T into their columns (the previous
     // step's S and dP must have been loaded by the compute warps).
-    auto issue_sd = [&](int gs) -> bool {
+    // `z`: packed: zeroes what the step's tiles hold behind their sequence.
+    auto issue_sd = [&](int gs, auto z) -> bool {
         if (C::kSplitRing) {   // the dQ pass at D = 128 (measured 1.4-4 % faster; neutral in the fused pass)
             if (!warp_wait_all(b.sd_free(), (uint32_t)(gs - 1) & 1u, gs > 0, b.full(gs % C::kRing0),
                                (uint32_t)(gs / C::kRing0) & 1u, true, b.full1(gs % C::kRing1),
@@ -985,6 +1141,7 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
                 return false;
         }
         ptx::tc_fence_after_sync();
+        z();
         const uint32_t s0_lo = desc_lo(C::slot0(sStage, gs), 16), s1_lo = desc_lo(C::slot1(sStage, gs), 16);
         if (ptx::elect_one()) {
 #pragma unroll
@@ -1007,7 +1164,7 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
 
     for (int r = 0; ok; ++r) {
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= p.T)
+        if (t >= work_tiles<KV>(p))
             break;
         const auto wk = bwd_work<KV>(p, causal, t);
         const int n = wk.n;
@@ -1016,10 +1173,17 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
         if (!warp_wait(b.res_full(), (uint32_t)tiles & 1u, c, kSiteBwdResFull))
             break;
         ptx::tc_fence_after_sync();
-        if (!issue_sd(g))
+        auto tails = [&](int js, int gs) {
+            return [&, js, gs]() { zero_streamed<D, KV, FQ>(p, wk, js, sStage, gs); };
+        };
+        if constexpr (kPackedPass<P> && FQ) {   // the resident tiles' rows, which dQ sums over
+            zero_tail<D>(sRes, wk.Lk - wk.rt * kTile);
+            zero_tail<D>(sRes + C::kTileBytes, wk.Lk - wk.rt * kTile);
+        }
+        if (!issue_sd(g, tails(0, g)))
             break;
         for (int j = 0; j < n; ++j, ++g) {
-            if (j + 1 < n && !issue_sd(g + 1)) {
+            if (j + 1 < n && !issue_sd(g + 1, tails(j + 1, g + 1))) {
                 ok = false;
                 break;
             }
@@ -1044,23 +1208,27 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
             const uint32_t m1_lo = desc_lo(C::slot0(sStage, g), C::kBoxBytes);                               // KV: Q
             const uint32_t tA0 = tmem + (KV ? C::kColP : C::kColDS + 64u * (uint32_t)(g & 1));
             const uint32_t tA1 = tmem + C::kColDS;
+            const int ks = streamed_ksteps(p, wk, j);
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    ptx::mma_ts(tAcc0, tA0 + 8 * kk, desc_from_lo(m0_lo + kk * (2048 >> 4)), kIdescTS,
-                                (j > 0 || kk > 0) ? 1u : 0u);
+                    if (!kPackedPass<P> || kk < ks)
+                        ptx::mma_ts(tAcc0, tA0 + 8 * kk, desc_from_lo(m0_lo + kk * (2048 >> 4)), kIdescTS,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
                 if (KV && FQ) {   // dS^T K-major in shared memory: 32 bytes per k-step, a box per 64 queries
                     const uint32_t ds_lo = desc_lo(sDs, 16);
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        ptx::mma_ss(tAcc1, desc_from_lo(ds_lo + (uint32_t)((kk / 4) * (C::kBoxBytes >> 4) + (kk % 4) * 2)),
-                                    desc_from_lo(m1_lo + kk * (2048 >> 4)), kIdescTS, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (!kPackedPass<P> || kk < ks)
+                            ptx::mma_ss(tAcc1, desc_from_lo(ds_lo + (uint32_t)((kk / 4) * (C::kBoxBytes >> 4) + (kk % 4) * 2)),
+                                        desc_from_lo(m1_lo + kk * (2048 >> 4)), kIdescTS, (j > 0 || kk > 0) ? 1u : 0u);
                     ptx::mma_commit(b.pd_free());
                 } else if (KV) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        ptx::mma_ts(tAcc1, tA1 + 8 * kk, desc_from_lo(m1_lo + kk * (2048 >> 4)), kIdescTS,
-                                    (j > 0 || kk > 0) ? 1u : 0u);
+                        if (!kPackedPass<P> || kk < ks)
+                            ptx::mma_ts(tAcc1, tA1 + 8 * kk, desc_from_lo(m1_lo + kk * (2048 >> 4)), kIdescTS,
+                                        (j > 0 || kk > 0) ? 1u : 0u);
                     ptx::mma_commit(b.pd_free());
                 }
                 ptx::mma_commit(b.empty(st));
@@ -1094,7 +1262,7 @@ __device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uin
     int g = 0, tiles = 0;
     for (int r = 0;; ++r) {
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= p.T)
+        if (t >= work_tiles<KV>(p))
             break;
         const auto wk = bwd_work<KV>(p, CAUSAL, t);
         const int bh = wk.rh, rt = wk.rt, n = wk.n;
@@ -1102,7 +1270,9 @@ __device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uin
             continue;
         uint64_t nlg = 0, ndl = 0;   // dQ pass: this thread's query row's -lg and -delta
         if (!KV) {
-            const size_t off = (size_t)bh * p.Npad + (size_t)rt * kTile + row;
+            size_t off = (size_t)bh * p.Npad + (size_t)rt * kTile + row;
+            if constexpr (kPackedPass<P>)
+                off = (size_t)bh * p.Npad + (size_t)wk.qtile(rt) * kTile + row;
             nlg = ptx::f2_pack(p.lg[off], p.lg[off]);
             ndl = ptx::f2_pack(p.dl[off], p.dl[off]);
         }
@@ -1122,11 +1292,15 @@ __device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uin
             // edges (the causal diagonal), and in the dQ pass keys past Nkv
             // (padding queries and queries without keys have lg = +inf, stored as -inf).
             const uint32_t vec = sStage + (g % C::kStages) * C::kStageBytes + 2 * C::kTileBytes;
-            const int limit = KV ? kTile : p.Nkv - si * kTile;   // dQ pass: columns >= limit past Nkv
-            StepMask sm = bwd_step_mask(p, CAUSAL, KV ? rt : si, KV ? si : rt);
+            int limit = KV ? kTile : p.Nkv - si * kTile;   // dQ pass: columns >= limit past Nkv
+            if constexpr (kPackedPass<P> && !KV)
+                limit = wk.Lk - si * kTile;
+            StepMask sm = work_mask<KV>(p, wk, CAUSAL, KV ? rt : si, KV ? si : rt);
             const bool masked = !sm.whole || limit < 64 * h + 64;
-            if (KV)
+            if (KV) {
                 sink_row(p, sm, rt, row);
+                work_mask_row<KV>(p, wk, sm, rt, row);
+            }
             const LaneMask lm = bwd_lane_mask<KV>(sm, row, limit);
             // Scaled scores x = S * s log2(e) - lg in place; masked steps then set
             // hidden scores to -inf (exp2 gives 0) in a separate pass, so the
@@ -1216,6 +1390,12 @@ __device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uin
         if (KV) {
             const uint32_t tA = tmem + (h ? C::kColAcc1 : C::kColAcc0) + lane_off;
             char *dst = static_cast<char *>(h ? p.dA : p.dB) + ((size_t)bh * p.Nkv + grow) * D * 2;
+            int end = p.Nkv;
+            if constexpr (kPackedPass<P>) {
+                dst = static_cast<char *>(h ? p.dA : p.dB) + (long long)(wk.k0 + grow) * (h ? p.a_row : p.b_row) +
+                      (long long)bh * (h ? p.a_head : p.b_head);
+                end = wk.Lk;
+            }
             const float mul = h ? p.scale : 1.f;
 #pragma unroll
             for (int cc = 0; cc < D / 32; ++cc) {
@@ -1224,18 +1404,23 @@ __device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uin
                 ptx::tmem_wait_ld();
                 if (kSinkPass<P> && wk.slot() >= 0)
                     store_part32(part_row<D>(p, wk.slot(), h, row) + 32 * cc, v);
-                else if (grow < p.Nkv)
+                else if (grow < end)
                     store_row32<BF16>(dst + cc * 64, v, mul);
             }
         } else {
             char *dst = static_cast<char *>(p.dA) + ((size_t)bh * p.N + grow) * D * 2;
+            int end = p.N;
+            if constexpr (kPackedPass<P>) {
+                dst = static_cast<char *>(p.dA) + (long long)(wk.q0 + grow) * p.a_row + (long long)bh * p.a_head;
+                end = wk.Lq;
+            }
 #pragma unroll
             for (int cc = 0; cc < D / 64; ++cc) {
                 const int col = h * (D / 2) + 32 * cc;
                 uint32_t v[32];
                 ptx::tmem_ld32(tmem + C::kColAcc0 + lane_off + col, v);
                 ptx::tmem_wait_ld();
-                if (grow < p.N)
+                if (grow < end)
                     store_row32<BF16>(dst + col * 2, v, p.scale);
             }
         }
@@ -1267,7 +1452,7 @@ __device__ void bwd_mma_dq(const P &p, uint32_t sRes, uint32_t sDs, uint32_t tme
     bool ok = true;
     for (int r = 0; ok; ++r) {
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= p.T)
+        if (t >= work_tiles<true>(p))
             break;
         const auto wk = bwd_work<true>(p, CAUSAL, t);
         const int n = wk.n;
@@ -1275,6 +1460,9 @@ __device__ void bwd_mma_dq(const P &p, uint32_t sRes, uint32_t sDs, uint32_t tme
             continue;
         if (!warp_wait(b.res_full(), (uint32_t)tiles & 1u, c, kSiteBwdResFull))
             break;
+        int ks = kTile / 16;   // of the keys (packed: the tile's rows behind its sequence are left out)
+        if constexpr (kPackedPass<P>)
+            ks = packed::tail_ksteps(wk.Lk - wk.rt * kTile);
         for (int j = 0; j < n; ++j, ++g) {
             if (!warp_wait(b.p_full(), (uint32_t)g & 1u, c, kSiteBwdPFull) ||
                 (g > 0 && !warp_wait(b.dq_free(), (uint32_t)(g - 1) & 1u, c, kSiteBwdDqFree))) {
@@ -1285,8 +1473,9 @@ __device__ void bwd_mma_dq(const P &p, uint32_t sRes, uint32_t sDs, uint32_t tme
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                    ptx::mma_ss(tDQ, desc_from_lo(a_lo + kk * (2048 >> 4)), desc_from_lo(k_lo + kk * (2048 >> 4)), kIdesc,
-                                kk > 0 ? 1u : 0u);
+                    if (!kPackedPass<P> || kk < ks)
+                        ptx::mma_ss(tDQ, desc_from_lo(a_lo + kk * (2048 >> 4)), desc_from_lo(k_lo + kk * (2048 >> 4)), kIdesc,
+                                    kk > 0 ? 1u : 0u);
                 ptx::mma_commit(b.dq_full());
                 ptx::mma_commit(b.pd_free());
                 if (j == n - 1)
@@ -1341,7 +1530,7 @@ __device__ void bwd_dq_out(const CUtensorMap *tmDQ, const P &p, uint32_t tmem, u
     bool ok = true;
     for (int r = 0; ok; ++r) {
         const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= p.T)
+        if (t >= work_tiles<true>(p))
             break;
         const auto wk = bwd_work<true>(p, CAUSAL, t);
         const int n = wk.n;
@@ -1379,7 +1568,9 @@ __device__ void bwd_dq_out(const CUtensorMap *tmDQ, const P &p, uint32_t tmem, u
             ptx::fence_proxy_async_smem();   // the staging, visible to the reductions
             dq_sync();
             if (leader) {
-                const int y = wk.head(j) * p.Npad + wk.tile(j) * kTile;
+                int y = wk.head(j) * p.Npad + wk.tile(j) * kTile;
+                if constexpr (kPackedPass<P>)
+                    y = wk.head(j) * p.Npad + wk.qtile(wk.tile(j)) * kTile;
                 fq::tma_reduce_add_2d(tmDQ, sDq, 0, y);
                 fq::tma_reduce_add_2d(tmDQ, sDq + C::kDqBoxBytes, 32, y);
                 fq::bulk_commit_group();
@@ -1562,6 +1753,104 @@ __global__ void __launch_bounds__(256)
         }
         lg[row] = l;
         dl[row] = (i < N) ? -acc : 0.f;
+    }
+}
+
+// The same for packed sequences: a row of the statistics is row i of query tile
+// i / 128, which the plan's table places; `row` and `head` are bytes of O and dO.
+struct PackedRows {
+    const int4 *header, *table;
+    int Tq, Npad, H;
+    long long o_row, o_head, d_row, d_head;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float dot8(const uint4 &o4, const uint4 &d4)
+{
+    const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w}, dw[4] = {d4.x, d4.y, d4.z, d4.w};
+    float acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float o0, o1, d0, d1;
+        if (BF16) {
+            o0 = __uint_as_float(ow[k] << 16);
+            o1 = __uint_as_float(ow[k] & 0xffff0000u);
+            d0 = __uint_as_float(dw[k] << 16);
+            d1 = __uint_as_float(dw[k] & 0xffff0000u);
+        } else {
+            o0 = __half2float(__ushort_as_half((unsigned short)(ow[k] & 0xffffu)));
+            o1 = __half2float(__ushort_as_half((unsigned short)(ow[k] >> 16)));
+            d0 = __half2float(__ushort_as_half((unsigned short)(dw[k] & 0xffffu)));
+            d1 = __half2float(__ushort_as_half((unsigned short)(dw[k] >> 16)));
+        }
+        acc = fmaf(o0, d0, acc);
+        acc = fmaf(o1, d1, acc);
+    }
+    return acc;
+}
+
+// blockIdx.x: query tile, blockIdx.y: head.  The tiles behind the empty one are left.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256)
+    fa_bwd_prep_packed(const char *O, const char *dO, const float *LSE, float *lg, float *dl, float *dqa,
+                       const __grid_constant__ PackedRows p)
+{
+    fq::grid_launch_dependents();
+    constexpr int kTpr = D / 8, kRows = 256 / kTpr;   // threads per row, rows at a time
+    const int tile = blockIdx.x, h = blockIdx.y;
+    if (tile > ld_plan(p.header).y)
+        return;
+    const int4 at = ld_plan(p.table + tile);
+    const int part = threadIdx.x % kTpr, lane = threadIdx.x % 32;
+    const uint32_t group = ((1u << kTpr) - 1u) << (lane & ~(kTpr - 1));
+#pragma unroll 4
+    for (int i = threadIdx.x / kTpr; i < kTile; i += kRows) {
+        const size_t row = (size_t)h * p.Npad + (size_t)tile * kTile + i;
+        const bool real = i < at.y;
+        float lse = -INFINITY;
+        if (part == 0 && real)
+            lse = LSE[(size_t)h * p.Tq + at.x + i];
+        if (dqa) {
+            float4 *z = reinterpret_cast<float4 *>(dqa + row * D + 8 * part);
+            z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+            z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float acc = 0.f;
+        if (real)
+            acc = dot8<BF16>(
+                *reinterpret_cast<const uint4 *>(O + (long long)(at.x + i) * p.o_row + h * p.o_head + 16 * part),
+                *reinterpret_cast<const uint4 *>(dO + (long long)(at.x + i) * p.d_row + h * p.d_head + 16 * part));
+#pragma unroll
+        for (int m = kTpr / 2; m > 0; m /= 2)
+            acc += __shfl_xor_sync(group, acc, m);
+        if (part == 0) {
+            lg[row] = (lse == -INFINITY) ? -INFINITY : -(lse * 1.4426950408889634f);   // no keys, or no row: P = 0
+            dl[row] = real ? -acc : 0.f;
+        }
+    }
+}
+
+// dQ = scale * the fp32 accumulator for packed sequences; grid as above.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    fa_bwd_dq_convert_packed(const float *dqa, char *dQ, const __grid_constant__ PackedRows p, int D, float scale)
+{
+    fq::grid_wait();
+    const int tile = blockIdx.x, h = blockIdx.y;
+    if (tile >= ld_plan(p.header).y)
+        return;
+    const int4 at = ld_plan(p.table + tile);
+    const int tpr = D / 8, part = threadIdx.x % tpr;
+    for (int i = threadIdx.x / tpr; i < at.y; i += 256 / tpr) {
+        const float4 *src =
+            reinterpret_cast<const float4 *>(dqa + ((size_t)h * p.Npad + (size_t)tile * kTile + i) * D + 8 * part);
+        const float4 a = src[0], b = src[1];
+        uint4 o;
+        o.x = BF16 ? ptx::pack_bf16x2(a.x * scale, a.y * scale) : ptx::pack_f16x2(a.x * scale, a.y * scale);
+        o.y = BF16 ? ptx::pack_bf16x2(a.z * scale, a.w * scale) : ptx::pack_f16x2(a.z * scale, a.w * scale);
+        o.z = BF16 ? ptx::pack_bf16x2(b.x * scale, b.y * scale) : ptx::pack_f16x2(b.x * scale, b.y * scale);
+        o.w = BF16 ? ptx::pack_bf16x2(b.z * scale, b.w * scale) : ptx::pack_f16x2(b.z * scale, b.w * scale);
+        *reinterpret_cast<uint4 *>(dQ + (long long)(at.x + i) * p.o_row + h * p.o_head + 16 * part) = o;
     }
 }
 

@@ -1,0 +1,95 @@
+// fa_bwd_packed.cu -- the backward for packed sequences: the passes of
+// fa_bwd_kernel.cuh with PackedParams, between their own row statistics and
+// conversion of dQ.
+#include "fa_bwd_pass.cuh"
+#include "fa_packed_launch.h"
+
+namespace fa_launch {
+
+namespace {
+
+template <int D, bool BF16>
+fa_status launch_all(const PackedBwdLaunch &a, cudaStream_t s, int dev)
+{
+    namespace pk = fa::packed;
+    using P = fa::bwd::PackedParams;
+    const int4 *plan = static_cast<const int4 *>(a.plan);
+    const bool fused = D == 64 && a.fused;
+    const long long npad = pk::padded_rows(a.z);
+    fa::bwd::PackedRows rows{plan, plan + pk::table_word(a.z), a.z.Tq, (int)npad, a.z.H,
+                             a.o.row * 2, a.o.head * 2, a.dO.row * 2, a.dO.head * 2};
+    const dim3 grid((unsigned)(npad / pk::kTile), (unsigned)a.z.H);
+    fa::bwd::fa_bwd_prep_packed<D, BF16><<<grid, 256, 0, s>>>(static_cast<const char *>(a.o.ptr),
+                                                              static_cast<const char *>(a.dO.ptr), a.LSE, a.lg, a.dl,
+                                                              fused ? a.dqa : nullptr, rows);
+    if (cudaGetLastError() != cudaSuccess)
+        return FA_ERR_CUDA;
+    P p{};
+    p.lg = a.lg;
+    p.dl = a.dl;
+    p.N = a.z.Tq;
+    p.Nkv = a.z.Tk;
+    p.Npad = (int)npad;
+    p.BH = a.z.H;
+    p.qk2 = a.scale * 1.4426950408889634f;
+    p.scale = a.scale;
+    p.header = plan;
+    p.H = a.z.H;
+    p.group = a.z.H / a.z.Hkv;
+    p.causal = a.causal;
+    auto blocks = [&](int list, int heads) {
+        const long long t = pk::capacity(a.z, list) * heads;
+        return (int)(t < a.sms ? t : a.sms);
+    };
+    fa_status st;
+    if (!fused) {   // dQ in a pass of its own
+        p.list = plan + pk::list_word(a.z, 1);
+        p.heads = a.z.H;
+        p.dA = a.dq.ptr;
+        p.a_row = a.dq.row * 2;
+        p.a_head = a.dq.head * 2;
+        st = launch_pass<D, BF16, true, false, false, P>(a.tq, a.tdo, a.tk, a.tv, a.tq, p, blocks(1, a.z.H), s, dev);
+        if (st != FA_OK)
+            return st;
+    }
+    p.list = plan + pk::list_word(a.z, 2);
+    p.heads = a.z.Hkv;
+    p.dA = a.dk.ptr;
+    p.dB = a.dv.ptr;
+    p.a_row = a.dk.row * 2;
+    p.a_head = a.dk.head * 2;
+    p.b_row = a.dv.row * 2;
+    p.b_head = a.dv.head * 2;
+    const int g = blocks(2, a.z.Hkv);
+    if constexpr (D == 64)
+        st = fused ? launch_pass<D, BF16, true, true, true, P>(a.tk, a.tv, a.tq, a.tdo, a.tdqa, p, g, s, dev)
+                   : launch_pass<D, BF16, true, true, false, P>(a.tk, a.tv, a.tq, a.tdo, a.tq, p, g, s, dev);
+    else
+        st = launch_pass<D, BF16, true, true, false, P>(a.tk, a.tv, a.tq, a.tdo, a.tq, p, g, s, dev);
+    if (st != FA_OK || !fused)
+        return st;
+    rows.o_row = a.dq.row * 2;
+    rows.o_head = a.dq.head * 2;
+    if (launch_dependent(fa::bwd::fa_bwd_dq_convert_packed<BF16>, grid, dim3(256), 0, s, (const float *)a.dqa,
+                         static_cast<char *>(a.dq.ptr), rows, D, a.scale) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+}  // namespace
+
+fa_status launch_bwd_packed(const PackedBwdLaunch &a, cudaStream_t s, int dev)
+{
+    if (a.D == 64)
+        return a.bf16 ? launch_all<64, true>(a, s, dev) : launch_all<64, false>(a, s, dev);
+    return a.bf16 ? launch_all<128, true>(a, s, dev) : launch_all<128, false>(a, s, dev);
+}
+
+unsigned int *status_word_bwd_packed()
+{
+    return fa::status_word_address();
+}
+
+}  // namespace fa_launch

@@ -79,6 +79,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "fa_packed.h"
 #include "fa_schedule.h"
 #include "sm103_ptx.cuh"
 
@@ -117,6 +118,9 @@ constexpr int kMaskBand = 2;
 // A causal window with sinks: the steps of the first keys, which every query
 // behind them sees, then the band's; query heads may share key heads.
 constexpr int kMaskSink = 3;
+// Packed sequences (fa_packed.h), causal or not: tiles, lengths and bounds come
+// from the batch's plan.
+constexpr int kMaskPacked = 4;
 template <int MASK>
 constexpr bool kBanded = MASK == kMaskBand || MASK == kMaskSink;   // a left bound
 constexpr int kEpilogueWarpgroup = 2;
@@ -242,16 +246,42 @@ struct FwdParamsT {
 };
 using FwdParams = FwdParamsT<Schedule>;
 using SinkParams = FwdParamsT<SinkSchedule>;
+struct PackedParams : FwdParamsT<PackedSchedule> {   // N: tokens, causal in sch
+    long long o_row, o_head;   // bytes between O's rows and heads
+    int wide;                  // O's rows start on 32 bytes
+};
 template <int MASK>
-using ParamsOf = std::conditional_t<MASK == kMaskSink, SinkParams, FwdParams>;
+using ParamsOf =
+    std::conditional_t<MASK == kMaskSink, SinkParams, std::conditional_t<MASK == kMaskPacked, PackedParams, FwdParams>>;
+template <int MASK>
+using TileOf = std::conditional_t<MASK == kMaskPacked, PackedTile, SinkTile>;
 
 // A CTA's next part with its tile's head and row.  Windows with sinks also
 // take what sched_sink_tile gives, in one go (the other masks compute what
 // they need from the schedule where they need it, and leave `tile` alone).
 template <int MASK, bool SPLIT, class S>
-__device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, int &bh, int &ct, SinkTile &tile)
+__device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, int &bh, int &ct, TileOf<MASK> &tile)
 {
-    if constexpr (MASK == kMaskSink && !SPLIT) {
+    if constexpr (MASK == kMaskPacked) {
+        static_assert(!SPLIT, "packed sequences run whole tiles");
+        if (it.t >= __ldg(s.count) * s.H)
+            return false;
+        const int e = (int)((uint32_t)it.t / (uint32_t)s.H);
+        bh = it.t - e * s.H;   // the query head
+        const int4 seq = ld_plan(s.list + 2 * (size_t)e), at = ld_plan(s.list + 2 * (size_t)e + 1);
+        tile.q0 = seq.x;
+        tile.Lq = seq.y;
+        tile.k0 = seq.z;
+        tile.Lk = seq.w;
+        ct = at.x;
+        tile.nw[0] = packed::key_steps(ct * kCtaRows, seq.y, seq.w, s.causal);
+        tile.nw[1] = packed::key_steps(ct * kCtaRows + kBM, seq.y, seq.w, s.causal);
+        pt.kb = 0;
+        pt.ke = tile.nw[0] > tile.nw[1] ? tile.nw[0] : tile.nw[1];
+        ++it.u;
+        it.t = it.u * s.G + ((it.u & 1) ? s.G - 1 - it.c : it.c);
+        return true;
+    } else if constexpr (MASK == kMaskSink && !SPLIT) {
         return sched_next_whole(s, it, pt, bh, ct, tile);
     } else {
         if (!it.template next_t<SPLIT, kBanded<MASK>>(s, pt))
@@ -265,16 +295,16 @@ __device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, in
 
 // Steps that Q tile w of the tile visits, and the first key of step j.
 template <int MASK, class S>
-__device__ __forceinline__ int q_steps(const S &s, const SinkTile &tile, int ct, int w)
+__device__ __forceinline__ int q_steps(const S &s, const TileOf<MASK> &tile, int ct, int w)
 {
-    if constexpr (MASK == kMaskSink)
+    if constexpr (MASK == kMaskSink || MASK == kMaskPacked)
         return w ? tile.nw[1] : tile.nw[0];
     else
         return sched_kv_tiles_t<kBanded<MASK>>(s, ct, w);
 }
 
 template <int MASK, class S>
-__device__ __forceinline__ auto step_keys(const S &s, const SinkTile &tile, int ct)
+__device__ __forceinline__ auto step_keys(const S &s, const TileOf<MASK> &tile, int ct)
 {
     if constexpr (MASK == kMaskSink) {
         return TileKeys{tile.ssz, tile.ks, tile.few};
@@ -290,7 +320,7 @@ __device__ __forceinline__ auto step_keys(const S &s, const SinkTile &tile, int 
 template <int MASK, class S>
 __device__ __forceinline__ int key_head(const S &s, int bh)
 {
-    if constexpr (MASK == kMaskSink)
+    if constexpr (MASK == kMaskSink || MASK == kMaskPacked)
         return bh / s.group;
     else
         return bh;
@@ -418,6 +448,35 @@ struct Bars {
 
 // ------------------------------------------------------------------ producer
 
+// One box of a tile: 64 columns from x on of rows first .. first + 127 of head
+// `head`; packed sequences: of the sequence whose first row is `start` (rows
+// behind its last are the next one's, zeros behind the tensor's: zero_tail).
+template <bool PACKED>
+__device__ __forceinline__ void load_box(uint32_t dst, const void *tm, uint32_t bar, int x, int first, int head, int start)
+{
+    ptx::tma_load_3d(dst, tm, bar, x, PACKED ? start + first : first, head);
+}
+
+// Packed sequences: zero the rows of a [128, D] tile in shared memory from its
+// sequence's last, the n-th, to the next multiple of 16 (packed::tail_ksteps),
+// by a whole warp, before the products that it issues next read them.  (A row
+// is 128 bytes of each box, whatever its swizzle.)
+template <int D>
+__device__ __forceinline__ void zero_tail(uint32_t tile, int n)
+{
+    n = n < 0 ? 0 : n;
+    const int end = packed::tail_ksteps(n) * 16;
+    if (n >= end)   // (a whole tile, or a multiple of 16)
+        return;
+    const int lane = threadIdx.x % 32;
+    for (int r = n + lane / 8; r < end; r += 4)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+            ptx::st_shared_zero16(tile + (uint32_t)(x * kBM * 128 + r * 128 + (lane % 8) * 16));
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // TMA producer, run by a whole warp; one elected lane issues the copies.
 // Per CTA tile: both Q tiles into the Q buffer, then for each step j the
 // pair K_j, V_j into the next stage of the ring.  With K and V split, the
@@ -437,6 +496,8 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
     int it = 0;     // parts started by this CTA (one Q load each)
     int nv = 0;     // split: V halves filled so far; V of step nv is pending while nv < step
     int pv_bh = 0, pv_row = 0;   // ... its head and first key
+    [[maybe_unused]] int pv_k0 = 0;   // ... packed: its sequence's first key row
+    constexpr bool PACKED = MASK == kMaskPacked;
     bool ok = true;
     const uint64_t kv_policy = ptx::l2_policy_evict_first();   // split K/V (decoding): each K/V tile is read once
     auto load_v = [&]() -> bool {
@@ -447,8 +508,12 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
         if (ptx::elect_one()) {
             const uint32_t dst = sStage + st * C::kStageBytes + C::kTileBytes;
             ptx::mbar_arrive_expect_tx(b.v_full(st), C::kTileBytes);
-            for (int x = 0; x < C::kBoxes; ++x)
-                ptx::tma_load_3d_hint(dst + x * C::kBoxBytes, tmV, b.v_full(st), x * 64, pv_row, pv_bh, kv_policy);
+            for (int x = 0; x < C::kBoxes; ++x) {
+                if constexpr (PACKED)
+                    load_box<true>(dst + x * C::kBoxBytes, tmV, b.v_full(st), x * 64, pv_row, pv_bh, pv_k0);
+                else
+                    ptx::tma_load_3d_hint(dst + x * C::kBoxBytes, tmV, b.v_full(st), x * 64, pv_row, pv_bh, kv_policy);
+            }
         }
         __syncwarp();
         ++nv;
@@ -457,7 +522,7 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    SinkTile tile;
+    TileOf<MASK> tile;
     int bh, ct;
     while (ok && next_tile<MASK, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
         // The previous part's last V before the Q buffer is waited for: the
@@ -470,9 +535,14 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
             const uint32_t dst = sQ + qb * C::kQBufBytes;
             ptx::mbar_arrive_expect_tx(b.q_full(qb), kQTiles * C::kTileBytes);
             for (int w = 0; w < kQTiles; ++w)
-                for (int x = 0; x < C::kBoxes; ++x)
-                    ptx::tma_load_3d(dst + w * C::kTileBytes + x * C::kBoxBytes, tmQ, b.q_full(qb), x * 64,
-                                     ct * kCtaRows + w * kBM, bh);
+                for (int x = 0; x < C::kBoxes; ++x) {
+                    if constexpr (PACKED)
+                        load_box<true>(dst + w * C::kTileBytes + x * C::kBoxBytes, tmQ, b.q_full(qb), x * 64,
+                                       ct * kCtaRows + w * kBM, bh, tile.q0);
+                    else
+                        ptx::tma_load_3d(dst + w * C::kTileBytes + x * C::kBoxBytes, tmQ, b.q_full(qb), x * 64,
+                                         ct * kCtaRows + w * kBM, bh);
+                }
         }
         __syncwarp();
         ++it;
@@ -486,21 +556,30 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
                 const uint32_t dst = sStage + st * C::kStageBytes;
                 ptx::mbar_arrive_expect_tx(b.full(st), SKV ? C::kTileBytes : C::kStageBytes);
                 for (int x = 0; x < C::kBoxes; ++x) {
-                    if (SKV)
+                    if constexpr (PACKED)
+                        load_box<true>(dst + x * C::kBoxBytes, tmK, b.full(st), x * 64, keys.first_key(j), kvh, tile.k0);
+                    else if (SKV)
                         ptx::tma_load_3d_hint(dst + x * C::kBoxBytes, tmK, b.full(st), x * 64, keys.first_key(j), kvh, kv_policy);
                     else
                         ptx::tma_load_3d(dst + x * C::kBoxBytes, tmK, b.full(st), x * 64, keys.first_key(j), kvh);
                 }
                 if (!SKV)
-                    for (int x = 0; x < C::kBoxes; ++x)
-                        ptx::tma_load_3d(dst + C::kTileBytes + x * C::kBoxBytes, tmV, b.full(st), x * 64,
-                                         keys.first_key(j), kvh);
+                    for (int x = 0; x < C::kBoxes; ++x) {
+                        if constexpr (PACKED)
+                            load_box<true>(dst + C::kTileBytes + x * C::kBoxBytes, tmV, b.full(st), x * 64,
+                                           keys.first_key(j), kvh, tile.k0);
+                        else
+                            ptx::tma_load_3d(dst + C::kTileBytes + x * C::kBoxBytes, tmV, b.full(st), x * 64,
+                                             keys.first_key(j), kvh);
+                    }
             }
             __syncwarp();
             if (SKV) {   // V of the previous step, then this step's V becomes the pending one
                 if (nv < step && !load_v()) { ++step; ok = false; break; }
                 pv_bh = kvh;
                 pv_row = keys.first_key(j);
+                if constexpr (PACKED)
+                    pv_k0 = tile.k0;
             }
         }
     }
@@ -638,8 +717,10 @@ struct MmaIssuer {
 
     // O_w (+)= P_w V over 128/16 k-steps: P from TMEM (8 columns per step),
     // V MN-major: 16 key rows = 2 KB per step.
-    // `few`: of the first 16 keys alone (one k-step).
-    __device__ bool issue_pv(int st, bool accumulate, bool few = false)
+    // `few`: of the first 16 keys alone (one k-step).  PACKED: the step holds
+    // `rows` of its sequence's keys.
+    template <bool PACKED = false>
+    __device__ bool issue_pv(int st, bool accumulate, bool few = false, int rows = kBN)
     {
         if (!accumulate) {   // first P.V of a CTA tile overwrites O_w: the epilogue must have read it
             if (n_t > 0 && !warp_wait(b.o_free(w), (n_t - 1) & 1u, c, kSiteMmaOFree))
@@ -650,10 +731,11 @@ struct MmaIssuer {
             return false;
         ptx::tc_fence_after_sync();
         const uint32_t va = v_lo + (uint32_t)(st * (C::kStageBytes >> 4));
+        const int ksteps = PACKED ? packed::tail_ksteps(rows) : kBN / 16;
         if (ptx::elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
-                if (kk == 0 || !few)
+                if (PACKED ? kk < ksteps : kk == 0 || !few)
                     ptx::mma_ts(tO, tP + kk * 8, desc_from_lo(va + kk * (2048 >> 4)), kIdescPV,
                                 (accumulate || kk > 0) ? 1u : 0u);
             ptx::mma_commit(b.o_done(w));
@@ -737,27 +819,31 @@ __device__ bool tile_interleaved(MmaIssuer<D, BF16, false> &m0, MmaIssuer<D, BF1
 // next: the next part's first S is issued before the last P.V of this one (in
 // the interleaved order before Q tile 1's), and the Q buffer is given back as
 // soon as the part's last S has read it, so that the next Q is on its way
-// while the last P.V runs.
-template <int D, bool BF16, bool SPLIT, bool SEP, class P>
-__device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, BF16, SEP> &m1, int w)
+// while the last P.V runs.  Packed sequences, whose tiles may be as short, too.
+template <int D, bool BF16, int MASK, bool SPLIT, bool SEP, class P>
+__device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, BF16, SEP> &m1, int w, uint32_t sV)
 {
     using C = Cfg<D>;
     const Bars<D> b = m.b;
     int step = 0, it = 0;   // K/V steps and parts so far
     int prev = -1;          // stage of the step whose P.V (interleaved: Q tile 1's) is still to come, -1: none
     bool pv = false, acc = false, pfew = false;   // whether this warp's tile has that P.V, adds to O, and is of few sinks
+    constexpr bool PACKED = MASK == kMaskPacked;
+    int prows = kBN;        // packed: keys of the sequence in that step
     auto finish = [&]() -> bool {   // that P.V, then its stage
         if (SEP) {
             if (C::kSplitKV && !m.v_wait(step - 1))
                 return false;
-            if (pv && !m.issue_pv(prev, acc, pfew))
+            if (PACKED)
+                zero_tail<D>(sV + (uint32_t)(prev * C::kStageBytes), prows);
+            if (pv && !m.template issue_pv<PACKED>(prev, acc, pfew, prows))
                 return false;
             if (C::kSplitKV)
                 m.release_v(prev);
             else
                 m.release(prev);
         } else {
-            if (pv && !m1.issue_pv(prev, acc, pfew))
+            if (pv && !m1.template issue_pv<PACKED>(prev, acc, pfew, prows))
                 return false;
             m.release(prev);
         }
@@ -766,9 +852,9 @@ __device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, B
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    SinkTile tile;
+    TileOf<MASK> tile;
     int bh, ct;
-    while (next_tile<kMaskSink, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
+    while (next_tile<MASK, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
         const int n0 = part_steps(pt, tile.nw[0]), n1 = part_steps(pt, tile.nw[1]);
         const int n = pt.ke - pt.kb;
         const bool few0 = pt.kb == 0 && tile.few;   // the part's first step
@@ -780,6 +866,9 @@ __device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, B
         m1.q_cur = m1.q_lo + (uint32_t)(qb * (C::kQBufBytes >> 4));
         for (int j = 0; j < n; ++j) {
             const bool few = few0 && j == 0;
+            int rows = kBN;
+            if constexpr (PACKED)
+                rows = tile.Lk - j * kBN;
             int st;
             if (!m.stage_wait(step, st))
                 return;
@@ -805,11 +894,14 @@ __device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, B
                 if (j == n - 1 && ptx::elect_one())
                     ptx::mma_commit(b.q_empty(qb));
                 __syncwarp();
-                if (j < n0 && !m.issue_pv(st, j > 0, few))
+                if (PACKED)
+                    zero_tail<D>(sV + (uint32_t)(st * C::kStageBytes), rows);
+                if (j < n0 && !m.template issue_pv<PACKED>(st, j > 0, few, rows))
                     return;
                 pv = j < n1;
             }
             prev = st;
+            prows = rows;
             acc = j > 0;
             pfew = few;
             ++step;
@@ -842,8 +934,8 @@ __device__ void mma_role(int w, const P &p, uint32_t sQ, uint32_t sStage, uint32
     MmaIssuer<D, BF16, SEP> m1 = make(1);           // tile 1 when one warp serves both
     if (!C::kSeparateP && SEP)                      // D = 128, heads of one Q tile
         m.tP = tmem + C::col_p_one_tile();
-    if constexpr (MASK == kMaskSink) {
-        mma_parts<D, BF16, SPLIT, SEP>(p, m, m1, w);
+    if constexpr (MASK == kMaskSink || MASK == kMaskPacked) {
+        mma_parts<D, BF16, MASK, SPLIT, SEP>(p, m, m1, w, sStage + C::kTileBytes);
     } else {
     int step = 0, it = 0;
     PartIter parts;
@@ -969,7 +1061,7 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    SinkTile tile;
+    TileOf<MASK> tile;
     int bh, ct;
     while (next_tile<MASK, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
         const int nw = q_steps<MASK>(p.sch, tile, ct, w);    // steps of this Q tile in the whole tile
@@ -983,7 +1075,11 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
         // row's lower edge (kMaskBand only), or past Nkv.
         const auto keys = step_keys<MASK>(p.sch, tile, ct);   // the tile's key steps
         int row_lo = 0, row_hi = p.Nkv, edge_lo = 0, edge_hi = p.Nkv;
-        if (CAUSAL) {
+        if constexpr (MASK == kMaskPacked) {
+            const int first = ct * kCtaRows + w * kBM;
+            row_hi = packed::row_end(min(row, tile.Lq - 1), tile.Lq, tile.Lk, p.sch.causal);
+            edge_hi = packed::row_end(first, tile.Lq, tile.Lk, p.sch.causal);   // (at most Lk)
+        } else if (CAUSAL) {
             const int first = ct * kCtaRows + w * kBM, r = min(row, p.N - 1);
             row_hi = sched_row_hi(p.sch, r);
             edge_hi = sched_row_hi(p.sch, first);
@@ -1207,6 +1303,8 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
             bool masked;
             if constexpr (MASK == kMaskSink)   // (steps of sinks alone have no lower edge)
                 masked = (kb0 < edge_lo && kb0 + kBN > p.sch.sinks) || kb0 + kBN > edge_hi;
+            else if constexpr (MASK == kMaskPacked)
+                masked = kb0 + kBN > edge_hi;
             else
                 masked = (MASK == kMaskBand) ? (kb0 < edge_lo || kb0 + kBN > edge_hi)   // (edge_hi <= Nkv)
                                              : ((CAUSAL && kb0 + kBN > edge_hi) || kb0 + kBN > p.Nkv);
@@ -1456,7 +1554,9 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
     uint32_t n_jobs = 0;                          // merge jobs posted
     // O in whole 32-byte sectors where its rows start on them (a window's tiles
     // are short, and the next one waits for this warpgroup to read O out)
-    const bool wide = MASK == kMaskSink && (reinterpret_cast<uintptr_t>(p.O) & 31u) == 0;
+    bool wide = MASK == kMaskSink && (reinterpret_cast<uintptr_t>(p.O) & 31u) == 0;
+    if constexpr (MASK == kMaskPacked)
+        wide = p.wide;
 
     // Post a job in the next queue slot: nparts = 0 stops the merge warp.
     // Thread k fills part k; false if the wait for a free slot gave up.
@@ -1492,7 +1592,7 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
-    SinkTile tile;
+    TileOf<MASK> tile;
     int bh, ct;
     while (next_tile<MASK, SPLIT>(parts, p.sch, pt, bh, ct, tile)) {
         uint32_t published = 0;                   // bit w: Q tile w wrote a partial result
@@ -1519,11 +1619,15 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
             const float inv_l = (st.y > 0.f) ? 1.f / st.y : 0.f;   // a row that saw no key: O = 0
             const uint64_t il2 = ptx::f2_pack(inv_l, inv_l);
             const int row = ct * kCtaRows + w * kBM + t;
-            const bool valid = row < p.N;
+            bool valid = row < p.N;
+            if constexpr (MASK == kMaskPacked)
+                valid = row < tile.Lq;
             const uint32_t tO = tmem + C::col_o(w) + lane_off;
             if (whole) {
                 uint8_t *orow =
                     reinterpret_cast<uint8_t *>(p.O) + ((size_t)bh * p.N + (size_t)(valid ? row : 0)) * D * 2;
+                if constexpr (MASK == kMaskPacked)
+                    orow = reinterpret_cast<uint8_t *>(p.O) + (tile.q0 + (valid ? row : 0)) * p.o_row + bh * p.o_head;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t o[32];
@@ -1536,7 +1640,7 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
                                        x, y);
                         o[i] = BF16 ? ptx::pack_bf16x2(x, y) : ptx::pack_f16x2(x, y);
                     }
-                    if (MASK == kMaskSink && valid && wide) {
+                    if ((MASK == kMaskSink || MASK == kMaskPacked) && valid && wide) {
 #pragma unroll
                         for (int v = 0; v < 2; ++v)
                             ptx::st_global_v8(orow + q * 64 + v * 32, o + 8 * v);
@@ -1546,8 +1650,12 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
                             ptx::st_global_v4(orow + q * 64 + v * 16, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                     }
                 }
-                if (valid)
-                    p.LSE[(size_t)bh * p.N + row] = (st.x + log2f(st.y)) * kLn2;
+                if (valid) {
+                    if constexpr (MASK == kMaskPacked)
+                        p.LSE[(size_t)bh * p.N + tile.q0 + row] = (st.x + log2f(st.y)) * kLn2;
+                    else
+                        p.LSE[(size_t)bh * p.N + row] = (st.x + log2f(st.y)) * kLn2;
+                }
             } else {   // a part of a split tile: the partial result of the valid rows (the merge reads no other)
                 float *prow = p.part_o + ((size_t)pt.slot * kCtaRows + w * kBM + t) * D;
 #pragma unroll
@@ -1631,7 +1739,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ ParamsOf<MASK> p)
 {
     using C = Cfg<D>;
-    constexpr bool CAUSAL = MASK != kMaskNone;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;    // 128-byte swizzle atoms need 1024-byte alignment

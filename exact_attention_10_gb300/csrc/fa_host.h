@@ -2,6 +2,8 @@
 // (defined in fa_api.cu): the current device, argument ranges, pointers.
 #pragma once
 
+#include <cuda.h>
+
 #include <cstddef>
 
 #include "fa.h"
@@ -44,5 +46,15 @@ fa_status check_args(const Arg *args, int n, int *dev, const DeviceInfo **info);
 // holds one flag per device (kMaxDevices), zero at first, for this kernel.
 constexpr int kMaxDevices = 64;
 fa_status allow_smem(const void *kern, int smem, int dev, bool *set);
+
+// The current device and its properties, if it is one this library runs on.
+fa_status current_device(int *dev, const DeviceInfo **info);
+
+// Tensor map over `rows` rows of `heads` heads, [row, head, D] with strides in
+// elements, of 64 x 128 boxes.
+bool encode_packed(CUtensorMap *m, const void *ptr, int rows, int heads, int D, long long row, long long head, bool bf16);
+
+// Rank-2 map over an fp32 [rows, D] array, 32 x 128 boxes, 128-byte swizzle.
+bool encode_rows_f32(CUtensorMap *m, float *ptr, long long rows, int D);
 
 }  // namespace fa_host

@@ -1,0 +1,425 @@
+// fa_packed.cu -- attention over packed sequences: the batch's plan, the
+// forward's kernel variants and the C entry points (include/fa.h).  The
+// backward's kernels are in fa_bwd_packed.cu.
+#include "fa_packed.h"
+
+#include <cmath>
+
+#include "fa_host.h"
+#include "fa_launch.cuh"
+#include "fa_packed_launch.h"
+
+namespace {
+
+namespace pk = fa::packed;
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kBuckets = 2048;   // of the sort by cost: longer tiles share a bucket with others as long to 1 in 2048
+
+struct PlanParams {
+    const int *cu_q, *cu_k;
+    pk::Sizes z;
+    int causal, lists;
+    int4 *plan;
+};
+
+// Exclusive scan of one value per thread over the block (a sum, or a maximum
+// of values >= 0), and the value over all threads.
+template <bool MAX>
+__device__ int block_scan(int x, int *scratch, int &total)
+{
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    auto op = [](int a, int b) { return MAX ? max(a, b) : a + b; };
+    int inc = x;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m)
+            inc = op(inc, v);
+    }
+    __syncthreads();   // scratch may still be read from the scan before
+    if (lane == 31)
+        scratch[warp] = inc;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int i = 0; i < kPlanWarps; ++i) {
+        if (i < warp)
+            before = op(before, scratch[i]);
+        total = op(total, scratch[i]);
+    }
+    const int up = __shfl_up_sync(0xffffffffu, inc, 1);
+    return lane ? op(before, up) : before;
+}
+
+__device__ __forceinline__ int clamp_to(int x, int top)
+{
+    return x < 0 ? 0 : (x > top ? top : x);
+}
+
+// One block per list.  Boundaries that leave [0, tokens] or fall are clamped
+// (each to the largest so far), so whatever cu holds, the sequences lie within
+// the tensors, apart from one another, and fit the lists.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p)
+{
+    __shared__ int scratch[kPlanWarps];
+    __shared__ int hist[kBuckets];
+    const int l = blockIdx.x, t = threadIdx.x, S = p.z.S;
+    int4 *entries = p.plan + pk::list_word(p.z, l);
+    int4 *seqs = p.plan + pk::scratch_word(p.z, l);   // two words a sequence: {q0, Lq, k0, Lk}, {first entry, first query tile}
+    const int tile = l == 0 ? 2 * pk::kTile : pk::kTile;
+
+    // sequences, `per` after one another to a thread
+    const int per = (S + kPlanThreads - 1) / kPlanThreads;
+    const int s0 = min(t * (long long)per, (long long)S), s1 = min((t + 1) * (long long)per, (long long)S);
+    int mq = 0, mk = 0, total;
+    for (int s = s0; s < s1; ++s) {
+        mq = max(mq, clamp_to(p.cu_q[s], p.z.Tq));
+        mk = max(mk, clamp_to(p.cu_k[s], p.z.Tk));
+    }
+    mq = block_scan<true>(mq, scratch, total);
+    mk = block_scan<true>(mk, scratch, total);
+    int nt = 0, nq = 0;
+    if (s0 < s1) {
+        int a = max(mq, clamp_to(p.cu_q[s0], p.z.Tq)), b = max(mk, clamp_to(p.cu_k[s0], p.z.Tk));
+        for (int s = s0; s < s1; ++s) {
+            const int a1 = max(a, clamp_to(p.cu_q[s + 1], p.z.Tq)), b1 = max(b, clamp_to(p.cu_k[s + 1], p.z.Tk));
+            seqs[2 * (size_t)s] = make_int4(a, a1 - a, b, b1 - b);
+            nt += ((l == 2 ? b1 - b : a1 - a) + tile - 1) / tile;
+            nq += (a1 - a + pk::kTile - 1) / pk::kTile;
+            a = a1;
+            b = b1;
+        }
+    }
+    int n;
+    int at = block_scan<false>(nt, scratch, n), qt = block_scan<false>(nq, scratch, total);
+    for (int s = s0; s < s1; ++s) {
+        const int4 q = seqs[2 * (size_t)s];
+        seqs[2 * (size_t)s + 1] = make_int4(at, qt, 0, 0);
+        at += ((l == 2 ? q.w : q.y) + tile - 1) / tile;
+        qt += (q.y + pk::kTile - 1) / pk::kTile;
+    }
+    if (t == 0)
+        (&p.plan[0].x)[l] = n;
+    if (l == 1) {
+        int4 *table = p.plan + pk::table_word(p.z);
+        if (t == 0)
+            table[n] = make_int4(0, 0, 0, 0);
+    }
+    for (int i = t; i < kBuckets; i += kPlanThreads)
+        hist[i] = 0;
+    __syncthreads();
+
+    auto seq_of = [&](int e) {   // the last sequence whose first entry is at most e (empty ones have the next's)
+        int lo = 0, hi = S - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (seqs[2 * (size_t)mid + 1].x <= e)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        return lo;
+    };
+    auto cost = [&](const int4 &q, int i) -> int {   // steps
+        if (l == 0)
+            return pk::key_steps(i * tile, q.y, q.w, p.causal) + pk::key_steps(i * tile + pk::kTile, q.y, q.w, p.causal);
+        if (l == 1)
+            return pk::key_steps(i * tile, q.y, q.w, p.causal);
+        const int f = pk::first_query_tile(i, q.y, q.w, p.causal);
+        return f < 0 ? 1 : (q.y + pk::kTile - 1) / pk::kTile - f;
+    };
+    int top = 0;
+    for (int e = t; e < n; e += kPlanThreads) {
+        const int s = seq_of(e);
+        top = max(top, cost(seqs[2 * (size_t)s], e - seqs[2 * (size_t)s + 1].x));
+    }
+    block_scan<true>(top, scratch, total);
+    top = total;
+    // buckets from the longest tiles to the shortest
+    auto bucket = [&](int c) { return kBuckets - 1 - (top < kBuckets ? c : (int)((long long)c * kBuckets / (top + 1ll))); };
+    for (int e = t; e < n; e += kPlanThreads) {
+        const int s = seq_of(e);
+        atomicAdd(&hist[bucket(cost(seqs[2 * (size_t)s], e - seqs[2 * (size_t)s + 1].x))], 1);
+    }
+    __syncthreads();
+    {
+        constexpr int kPer = kBuckets / kPlanThreads;
+        int v[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            v[i] = hist[t * kPer + i];
+            sum += v[i];
+        }
+        int before = block_scan<false>(sum, scratch, total);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            hist[t * kPer + i] = before;
+            before += v[i];
+        }
+    }
+    __syncthreads();
+    for (int e = t; e < n; e += kPlanThreads) {
+        const int s = seq_of(e);
+        const int4 q = seqs[2 * (size_t)s], w = seqs[2 * (size_t)s + 1];
+        const int i = e - w.x;
+        const int pos = atomicAdd(&hist[bucket(cost(q, i))], 1);   // (tiles of a bucket in any order: they are independent)
+        entries[2 * (size_t)pos] = q;
+        entries[2 * (size_t)pos + 1] = make_int4(i, w.y, 0, 0);
+        if (l == 1)
+            p.plan[pk::table_word(p.z) + e] = make_int4(q.x + i * pk::kTile, min(pk::kTile, q.y - i * pk::kTile), 0, 0);
+    }
+}
+
+// Sizes that every packed call checks: rows and padded rows within 32-bit indices.
+bool sizes_ok(const fa_packed_sizes *s, pk::Sizes *z)
+{
+    if (!s || s->seqs < 1 || s->tokens_q < 1 || s->tokens_k < 1 || s->heads < 1 || s->key_heads < 1 ||
+        s->heads % s->key_heads != 0 || (s->causal != 0 && s->causal != 1) || s->heads > 65535)
+        return false;
+    *z = pk::Sizes{s->seqs, s->tokens_q, s->tokens_k, s->heads, s->key_heads};
+    const long long pad_k = (s->tokens_k + 128ll * s->seqs) * s->key_heads;
+    const long long pad_q = pk::padded_rows(*z) * s->heads;
+    return pad_q <= fa_host::kMaxRows && pad_k <= fa_host::kMaxRows && s->seqs < (1 << 24);
+}
+
+// Strided rows of one tensor; where there is one row or head, its stride does not count.
+struct Rows {
+    const void *p;
+    long long row, head;   // elements
+    int rows, heads, D;
+    bool out;
+    size_t bytes() const { return (size_t)((rows - 1) * row + (heads - 1) * head + D) * 2; }
+    // Bytes that one row's heads span, 0 if heads are not within a row.
+    long long span() const
+    {
+        const long long s = (heads - 1) * head + D;
+        return rows == 1 || s <= row ? s * 2 : 0;
+    }
+};
+
+bool make_rows(const fa_rows *r, int rows, int heads, int D, bool out, Rows *w)
+{
+    if (!r || !r->ptr)
+        return false;
+    *w = Rows{r->ptr, r->row, r->head, rows, heads, D, out};
+    if (heads == 1)
+        w->head = D;
+    if (rows == 1)
+        w->row = heads * (w->head > 0 ? w->head : 0);
+    return w->row >= D && w->head >= D && w->row % 8 == 0 && w->head % 8 == 0 && w->row < (1ll << 38) &&
+           w->head < (1ll << 38);
+}
+
+// Elements in common, as far as the strides tell: two sets of rows whose ranges
+// cross are apart if they have the same distance between rows and lie in
+// different parts of it (slices of one buffer).
+bool rows_overlap(const Rows &a, const Rows &b)
+{
+    if (!fa_host::ranges_overlap(a.p, a.bytes(), b.p, b.bytes()))
+        return false;
+    if (a.row != b.row || !a.span() || !b.span())
+        return true;
+    const long long step = a.row * 2;
+    long long d = (reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % (unsigned long long)step;
+    if (reinterpret_cast<uintptr_t>(b.p) < reinterpret_cast<uintptr_t>(a.p)) {
+        d = (reinterpret_cast<uintptr_t>(a.p) - reinterpret_cast<uintptr_t>(b.p)) % (unsigned long long)step;
+        d = d ? step - d : 0;
+    }
+    return !(d >= a.span() && d + b.span() <= step);
+}
+
+// An output's rows are apart from one another: heads within a row, or rows
+// within a head.
+bool rows_apart(const Rows &r)
+{
+    return (r.heads - 1) * r.head + r.D <= r.row || (r.rows - 1) * r.row + r.D <= r.head || r.rows == 1;
+}
+
+// Checks of a call's tensors and its plain arguments (fa_host::check_args).
+fa_status check_rows(const Rows *rows, int n, const fa_host::Arg *args, int m, int *dev, const fa_host::DeviceInfo **di)
+{
+    for (int i = 0; i < n; ++i)
+        if (reinterpret_cast<uintptr_t>(rows[i].p) & 15u)
+            return FA_ERR_MISALIGNED;
+    for (int i = 0; i < n; ++i) {
+        if (rows[i].out && !rows_apart(rows[i]))
+            return FA_ERR_INVALID_VALUE;
+        for (int j = 0; j < n; ++j)
+            if (i != j && rows[i].out && rows_overlap(rows[i], rows[j]))
+                return FA_ERR_INVALID_VALUE;
+        for (int j = 0; j < m; ++j)
+            if ((rows[i].out || args[j].out) &&
+                fa_host::ranges_overlap(rows[i].p, rows[i].bytes(), args[j].p, args[j].bytes))
+                return FA_ERR_INVALID_VALUE;
+    }
+    const fa_status st = fa_host::check_args(args, m, dev, di);
+    if (st != FA_OK)
+        return st;
+    for (int i = 0; i < n; ++i)
+        if (!fa_host::is_device_pointer(rows[i].p, *dev))
+            return FA_ERR_INVALID_VALUE;
+    return FA_OK;
+}
+
+bool encode(CUtensorMap *m, const Rows &r, bool bf16)
+{
+    return fa_host::encode_packed(m, r.p, r.rows, r.heads, r.D, r.row, r.head, bf16);
+}
+
+bool scale_ok(float scale)
+{
+    return std::isfinite(scale) && scale > 0.f;
+}
+
+bool fused_dq(int D, unsigned flags)
+{
+    return D == 64 && !(flags & FA_BWD_DETERMINISTIC);
+}
+
+}  // namespace
+
+extern "C" fa_status fa_packed_plan_bytes(const fa_packed_sizes *sizes, int grad, size_t *bytes)
+{
+    pk::Sizes z;
+    if (!bytes || !sizes_ok(sizes, &z) || (grad != 0 && grad != 1))
+        return FA_ERR_INVALID_VALUE;
+    *bytes = (size_t)pk::plan_words(z, grad) * 16;
+    return FA_OK;
+}
+
+extern "C" fa_status fa_packed_plan(const int *cu_q, const int *cu_k, const fa_packed_sizes *sizes, int grad, void *plan,
+                                    size_t plan_bytes, fa_stream_t stream)
+{
+    pk::Sizes z;
+    if (!sizes_ok(sizes, &z) || (grad != 0 && grad != 1))
+        return FA_ERR_INVALID_VALUE;
+    if (plan_bytes < (size_t)pk::plan_words(z, grad) * 16)
+        return FA_ERR_INVALID_VALUE;
+    const size_t cu_bytes = ((size_t)z.S + 1) * 4;
+    const fa_host::Arg args[3] = {{cu_q, cu_bytes, false, 4}, {cu_k, cu_bytes, false, 4}, {plan, plan_bytes, true, 16}};
+    int dev;
+    const fa_host::DeviceInfo *di;
+    const fa_status st = fa_host::check_args(args, 3, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    const PlanParams p{cu_q, cu_k, z, sizes->causal, grad ? 3 : 1, static_cast<int4 *>(plan)};
+    plan_kernel<<<p.lists, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" fa_status fa_packed_fwd(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *o, float *LSE,
+                                   const fa_packed_sizes *sizes, int D, float scale, fa_dtype dtype, const void *plan,
+                                   size_t plan_bytes, fa_stream_t stream)
+{
+    pk::Sizes z;
+    Rows r[4];
+    if ((dtype != FA_BF16 && dtype != FA_FP16) || (D != 64 && D != 128) || !sizes_ok(sizes, &z) || !scale_ok(scale))
+        return FA_ERR_INVALID_VALUE;
+    if (!make_rows(q, z.Tq, z.H, D, false, r) || !make_rows(k, z.Tk, z.Hkv, D, false, r + 1) ||
+        !make_rows(v, z.Tk, z.Hkv, D, false, r + 2) || !make_rows(o, z.Tq, z.H, D, true, r + 3))
+        return FA_ERR_INVALID_VALUE;
+    if (plan_bytes < (size_t)pk::plan_words(z, false) * 16)
+        return FA_ERR_INVALID_VALUE;
+    const fa_host::Arg args[2] = {{LSE, (size_t)z.H * z.Tq * 4, true, 4}, {plan, plan_bytes, false, 16}};
+    int dev;
+    const fa_host::DeviceInfo *di;
+    const fa_status st = check_rows(r, 4, args, 2, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    const bool bf16 = dtype == FA_BF16;
+    alignas(64) CUtensorMap tq, tk, tv;
+    if (!encode(&tq, r[0], bf16) || !encode(&tk, r[1], bf16) || !encode(&tv, r[2], bf16))
+        return FA_ERR_CUDA;
+    fa::PackedParams p{};
+    p.O = o->ptr;
+    p.LSE = LSE;
+    p.N = z.Tq;
+    p.Nkv = z.Tk;
+    p.qk_scale = scale * 1.4426950408889634f;   // scale * log2(e)
+    p.o_row = r[3].row * 2;
+    p.o_head = r[3].head * 2;
+    p.wide = ((reinterpret_cast<uintptr_t>(o->ptr) | (uintptr_t)p.o_row | (uintptr_t)p.o_head) & 31u) == 0;
+    p.sch.causal = sizes->causal;
+    p.sch.H = z.H;
+    p.sch.group = z.H / z.Hkv;
+    p.sch.count = static_cast<const int *>(plan);
+    p.sch.list = static_cast<const int4 *>(plan) + pk::list_word(z, 0);
+    const long long tiles = pk::capacity(z, 0) * z.H;
+    p.sch.G = (int)(tiles < di->sms ? tiles : di->sms);
+    return fa_launch::launch_mask<fa::kMaskPacked, false>(D, bf16, tq, tk, tv, p, p.sch.G,
+                                                          reinterpret_cast<cudaStream_t>(stream), dev);
+}
+
+extern "C" fa_status fa_packed_bwd_workspace(const fa_packed_sizes *sizes, int D, unsigned int flags, size_t *bytes)
+{
+    pk::Sizes z;
+    if (!bytes || (D != 64 && D != 128) || (flags & ~FA_BWD_DETERMINISTIC) || !sizes_ok(sizes, &z))
+        return FA_ERR_INVALID_VALUE;
+    *bytes = (size_t)pk::padded_rows(z) * z.H * (2 + (fused_dq(D, flags) ? D : 0)) * sizeof(float);
+    return FA_OK;
+}
+
+extern "C" fa_status fa_packed_bwd(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *o,
+                                   const fa_rows *dO, const float *LSE, const fa_rows *dq, const fa_rows *dk,
+                                   const fa_rows *dv, const fa_packed_sizes *sizes, int D, float scale, fa_dtype dtype,
+                                   unsigned int flags, const void *plan, size_t plan_bytes, void *workspace,
+                                   size_t workspace_bytes, fa_stream_t stream)
+{
+    fa_launch::PackedBwdLaunch a{};
+    pk::Sizes &z = a.z;
+    Rows r[8];
+    if ((dtype != FA_BF16 && dtype != FA_FP16) || (D != 64 && D != 128) || (flags & ~FA_BWD_DETERMINISTIC) ||
+        !sizes_ok(sizes, &z) || !scale_ok(scale))
+        return FA_ERR_INVALID_VALUE;
+    if (!make_rows(q, z.Tq, z.H, D, false, r) || !make_rows(k, z.Tk, z.Hkv, D, false, r + 1) ||
+        !make_rows(v, z.Tk, z.Hkv, D, false, r + 2) || !make_rows(o, z.Tq, z.H, D, false, r + 3) ||
+        !make_rows(dO, z.Tq, z.H, D, false, r + 4) || !make_rows(dq, z.Tq, z.H, D, true, r + 5) ||
+        !make_rows(dk, z.Tk, z.Hkv, D, true, r + 6) || !make_rows(dv, z.Tk, z.Hkv, D, true, r + 7))
+        return FA_ERR_INVALID_VALUE;
+    size_t need;
+    if (plan_bytes < (size_t)pk::plan_words(z, true) * 16 || fa_packed_bwd_workspace(sizes, D, flags, &need) != FA_OK ||
+        workspace_bytes < need)
+        return FA_ERR_INVALID_VALUE;
+    const fa_host::Arg args[3] = {{LSE, (size_t)z.H * z.Tq * 4, false, 4}, {plan, plan_bytes, false, 16},
+                                  {workspace, workspace_bytes, true, 16}};
+    int dev;
+    const fa_host::DeviceInfo *di;
+    const fa_status st = check_rows(r, 8, args, 3, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    a.bf16 = dtype == FA_BF16;
+    if (!encode(&a.tq, r[0], a.bf16) || !encode(&a.tk, r[1], a.bf16) || !encode(&a.tv, r[2], a.bf16) ||
+        !encode(&a.tdo, r[4], a.bf16))
+        return FA_ERR_CUDA;
+    const size_t rows = (size_t)pk::padded_rows(z) * z.H;
+    a.fused = fused_dq(D, flags);
+    a.lg = static_cast<float *>(workspace);
+    a.dl = a.lg + rows;
+    a.dqa = a.dl + rows;
+    if (a.fused && !fa_host::encode_rows_f32(&a.tdqa, a.dqa, (long long)rows, D))
+        return FA_ERR_CUDA;
+    auto rows_of = [](const Rows &x) { return fa_rows{const_cast<void *>(x.p), x.row, x.head}; };
+    a.o = rows_of(r[3]);
+    a.dO = rows_of(r[4]);
+    a.dq = rows_of(r[5]);
+    a.dk = rows_of(r[6]);
+    a.dv = rows_of(r[7]);
+    a.LSE = LSE;
+    a.plan = plan;
+    a.D = D;
+    a.sms = di->sms;
+    a.causal = sizes->causal != 0;
+    a.scale = scale;
+    return fa_launch::launch_bwd_packed(a, reinterpret_cast<cudaStream_t>(stream), dev);
+}
+
+namespace fa_launch {
+
+unsigned int *status_word_packed()
+{
+    return fa::status_word_address();
+}
+
+}  // namespace fa_launch

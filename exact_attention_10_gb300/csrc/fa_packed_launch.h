@@ -1,0 +1,30 @@
+// fa_packed_launch.h -- interface between the packed calls (fa_packed.cu) and
+// the backward's translation unit (fa_bwd_packed.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fa.h"
+#include "fa_packed.h"
+
+namespace fa_launch {
+
+struct PackedBwdLaunch {
+    CUtensorMap tq, tk, tv, tdo;   // fa_host::encode_packed
+    CUtensorMap tdqa;              // fused: fa_host::encode_rows_f32 over dqa
+    fa_rows o, dO, dq, dk, dv;
+    const float *LSE;              // [H, Tq]
+    float *lg, *dl, *dqa;          // workspace: [H][padded rows], and with D fused
+    const void *plan;
+    fa::packed::Sizes z;
+    int D, sms;
+    bool bf16, causal, fused;
+    float scale;
+};
+
+fa_status launch_bwd_packed(const PackedBwdLaunch &a, cudaStream_t s, int dev);
+unsigned int *status_word_packed();
+unsigned int *status_word_bwd_packed();
+
+}  // namespace fa_launch

@@ -20,10 +20,21 @@ STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_VALUE", 2: "FA_ERR_MISALIGNED", 3: "FA_
           4: "FA_ERR_CUDA", 5: "FA_ERR_DEVICE_TIMEOUT", 6: "FA_ERR_NO_ALLOC_LIMIT"}
 EXPORTS = ("fa_bwd", "fa_bwd_band", "fa_bwd_ex", "fa_bwd_sink", "fa_bwd_sink_workspace", "fa_cache_append", "fa_cache_evict", "fa_cache_fwd", "fa_cache_read",
            "fa_cache_weights", "fa_cache_workspace", "fa_fwd", "fa_fwd_band", "fa_fwd_ex", "fa_fwd_noalloc",
-           "fa_fwd_qkv", "fa_fwd_sink", "fa_fwd_sink_workspace", "fa_sync_status", "fa_status_string")
+           "fa_fwd_qkv", "fa_fwd_sink", "fa_fwd_sink_workspace", "fa_packed_bwd", "fa_packed_bwd_workspace",
+           "fa_packed_fwd", "fa_packed_plan", "fa_packed_plan_bytes", "fa_sync_status", "fa_status_string")
 SCHEDULES = {"auto": 0, "whole_tiles": 1, "balanced": 2}
 
 _lib = None
+
+
+class Rows(ctypes.Structure):
+    """fa_rows: element (t, h, d) of a tensor is ptr[t * row + h * head + d]."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("row", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+class PackedSizes(ctypes.Structure):
+    """fa_packed_sizes."""
+    _fields_ = [(n, ctypes.c_int) for n in ("seqs", "tokens_q", "tokens_k", "heads", "key_heads", "causal")]
 
 
 class FAError(RuntimeError):
@@ -79,6 +90,16 @@ def load(path: str = LIB_PATH):
     lib.fa_cache_weights.restype = c_int
     lib.fa_cache_evict.argtypes = [vp] * 13 + [c_int] * 8 + [vp]
     lib.fa_cache_evict.restype = c_int
+    rows, sizes, size_t = ctypes.POINTER(Rows), ctypes.POINTER(PackedSizes), ctypes.c_size_t
+    lib.fa_packed_plan_bytes.argtypes = [sizes, c_int, ctypes.POINTER(size_t)]
+    lib.fa_packed_plan.argtypes = [vp, vp, sizes, c_int, vp, size_t, vp]
+    lib.fa_packed_fwd.argtypes = [rows] * 4 + [vp, sizes, c_int, ctypes.c_float, c_int, vp, size_t, vp]
+    lib.fa_packed_bwd_workspace.argtypes = [sizes, c_int, ctypes.c_uint, ctypes.POINTER(size_t)]
+    lib.fa_packed_bwd.argtypes = [rows] * 5 + [vp] + [rows] * 3 + [sizes, c_int, ctypes.c_float, c_int, ctypes.c_uint,
+                                                                    vp, size_t, vp, size_t, vp]
+    for f in (lib.fa_packed_plan_bytes, lib.fa_packed_plan, lib.fa_packed_fwd, lib.fa_packed_bwd_workspace,
+              lib.fa_packed_bwd):
+        f.restype = c_int
     lib.fa_sync_status.argtypes = [vp]
     lib.fa_sync_status.restype = c_int
     lib.fa_status_string.argtypes = [c_int]
@@ -322,6 +343,148 @@ def _backward_sink(q, k, v, o, do, lse, scale, dq, dk, dv, stream, window, deter
     if rc != 0:
         raise FAError(rc, "fa_bwd_sink")
     return tuple(outs)
+
+
+# ---- packed sequences
+
+class PackedPlan:
+    """A batch of packed sequences, laid out on the device (``packed_plan``
+    makes it); the calls of every layer take it.  ``buffer`` holds the layout,
+    ``sizes`` the batch's sizes."""
+
+    __slots__ = ("buffer", "sizes", "grad", "device")
+
+    def __init__(self, buffer, sizes, grad):
+        self.buffer, self.sizes, self.grad, self.device = buffer, sizes, grad, buffer.get_device()
+
+
+def packed_plan(cu, tokens: int, H: int, Hkv: int | None = None, cu_k=None, tokens_k: int | None = None,
+                causal: bool = False, grad: bool = False, stream=None) -> PackedPlan:
+    """Lay out a batch of packed sequences for ``packed_forward`` and, with
+    ``grad``, ``packed_backward``: sequence s has the query rows cu[s] ..
+    cu[s + 1] - 1 of ``tokens``, and the key rows cu_k[s] .. cu_k[s + 1] - 1 of
+    ``tokens_k`` (default: the same); H query heads share Hkv key heads.  ``cu``
+    and ``cu_k`` are int32 [S + 1] on the device, read there by a kernel on
+    ``stream`` (default: the current torch stream), so nothing waits for the
+    device; the plan keeps what it needs of them.  It belongs to that stream, as
+    results do (see ``forward``)."""
+    import torch
+    if (cu_k is None) != (tokens_k is None):
+        raise ValueError("keys of their own take both cu_k and tokens_k")
+    cu_k, tokens_k = (cu, tokens) if cu_k is None else (cu_k, tokens_k)
+    Hkv = H if Hkv is None else Hkv
+    if cu.dim() != 1 or cu.numel() < 2:
+        raise ValueError("cu must be [S + 1] of at least one sequence")
+    S = cu.numel() - 1
+    pq, pk = _ints(cu, S + 1, "cu"), _ints(cu_k, S + 1, "cu_k")
+    for n in (tokens, tokens_k, H, Hkv):
+        if not 0 <= n <= 0x7FFFFFFF:
+            raise ValueError("token and head counts must be 32-bit counts")
+    sizes = PackedSizes(S, tokens, tokens_k, H, Hkv, int(bool(causal)))
+    n = ctypes.c_size_t()
+    rc = load().fa_packed_plan_bytes(sizes, int(bool(grad)), n)
+    if rc != 0:
+        raise FAError(rc, "fa_packed_plan_bytes")
+    with _on(stream, cu):
+        buffer = torch.empty(n.value, dtype=torch.uint8, device=cu.device)
+    rc = load().fa_packed_plan(pq, pk, sizes, int(bool(grad)), buffer.data_ptr(), n.value, _stream_of(stream, cu))
+    if rc != 0:
+        raise FAError(rc, "fa_packed_plan")
+    return PackedPlan(buffer, sizes, bool(grad))
+
+
+def _rows(t, rows: int, heads: int, D: int, dtype, device: int, name: str) -> Rows:
+    if t.shape != (rows, heads, D):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {D}]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be of q's type")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the plan's device")
+    row, head, last = t.stride()
+    if last != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return Rows(t.data_ptr(), row, head)
+
+
+def _packed_check(q, plan, lse):
+    import torch
+    if not isinstance(plan, PackedPlan):
+        raise TypeError("plan must be a PackedPlan (packed_plan)")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, H, D]")
+    z = plan.sizes
+    if lse is not None:
+        if lse.shape != (z.heads, z.tokens_q) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous [{z.heads}, {z.tokens_q}]")
+        if lse.dtype != torch.float32:
+            raise TypeError("lse must be float32")
+        if lse.get_device() != plan.device:
+            raise ValueError("lse must be on the plan's device")
+    return z, q.shape[2], _dtype_code(q)
+
+
+def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=None, lse=None, stream=None):
+    """Attention inside each sequence of a planned batch: q [T, H, D], k and v
+    [Tk, Hkv, D], the last dimension contiguous and the others of any strides
+    that are multiples of 8 (slices of one projection's output, say).  Returns
+    (O [T, H, D], LSE [H, T]); rows that belong to no sequence are not written.
+    Whether it is causal is the plan's.  A query that sees no key gets O = 0 and
+    LSE = -inf.
+
+    ``out`` (of such strides) / ``lse`` may be given to write into existing
+    buffers.  Raises FAError on any non-OK status.  Asynchronous on ``stream``
+    (default: the current torch stream), which the results that are not given
+    belong to (see ``forward``).
+    """
+    import torch
+    z, D, code = _packed_check(q, plan, lse)
+    dev, t = plan.device, q.dtype
+    rq = _rows(q, z.tokens_q, z.heads, D, t, dev, "q")
+    rk, rv = (_rows(x, z.tokens_k, z.key_heads, D, t, dev, n) for x, n in ((k, "k"), (v, "v")))
+    if out is None or lse is None:
+        with _on(stream, q):
+            out = torch.empty((z.tokens_q, z.heads, D), dtype=t, device=q.device) if out is None else out
+            lse = torch.empty((z.heads, z.tokens_q), dtype=torch.float32, device=q.device) if lse is None else lse
+    ro = _rows(out, z.tokens_q, z.heads, D, t, dev, "out")
+    rc = load().fa_packed_fwd(rq, rk, rv, ro, lse.data_ptr(), z, D, D ** -0.5 if scale is None else scale, code,
+                              plan.buffer.data_ptr(), plan.buffer.numel(), _stream_of(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_packed_fwd")
+    return out, lse
+
+
+def packed_backward(q, k, v, o, do, lse, plan: PackedPlan, scale: float | None = None, dq=None, dk=None, dv=None,
+                    deterministic: bool = False, stream=None):
+    """The gradients (dQ, dK, dV) of ``packed_forward``'s O for an upstream
+    gradient ``do``, from its results and a plan made with ``grad``; o and do
+    [T, H, D] and the others with strides as there.  Rows that belong to no
+    sequence are not written; keys that no query sees get zeros.
+    ``deterministic``, ``dq`` / ``dk`` / ``dv`` and ``stream`` as for
+    ``backward``."""
+    import torch
+    z, D, code = _packed_check(q, plan, lse)
+    if not plan.grad:
+        raise ValueError("the plan was made without grad")
+    dev, t = plan.device, q.dtype
+    rq, ro, rdo = (_rows(x, z.tokens_q, z.heads, D, t, dev, n) for x, n in ((q, "q"), (o, "o"), (do, "do")))
+    rk, rv = (_rows(x, z.tokens_k, z.key_heads, D, t, dev, n) for x, n in ((k, "k"), (v, "v")))
+    flags = FA_BWD_DETERMINISTIC if deterministic else 0
+    n = ctypes.c_size_t()
+    rc = load().fa_packed_bwd_workspace(z, D, flags, n)
+    if rc != 0:
+        raise FAError(rc, "fa_packed_bwd_workspace")
+    with _on(stream, q):
+        dq, dk, dv = (torch.empty(x.shape, dtype=t, device=q.device) if d is None else d
+                      for d, x in ((dq, q), (dk, k), (dv, v)))
+        ws = _workspace(n.value, q)
+    rdq = _rows(dq, z.tokens_q, z.heads, D, t, dev, "dq")
+    rdk, rdv = (_rows(x, z.tokens_k, z.key_heads, D, t, dev, n_) for x, n_ in ((dk, "dk"), (dv, "dv")))
+    rc = load().fa_packed_bwd(rq, rk, rv, ro, rdo, lse.data_ptr(), rdq, rdk, rdv, z, D,
+                              D ** -0.5 if scale is None else scale, code, flags, plan.buffer.data_ptr(),
+                              plan.buffer.numel(), ws.data_ptr(), n.value, _stream_of(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_packed_bwd")
+    return dq, dk, dv
 
 
 # ---- the 4-bit key/value cache

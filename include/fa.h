@@ -345,6 +345,81 @@ FA_API fa_status fa_bwd_sink_workspace(int B, int H, int Hkv, int Nq, int Nkv, i
                                        unsigned int flags, size_t *bytes);
 
 /*
+ * ---- Packed sequences ----
+ *
+ * The tokens of S sequences of different lengths stand behind one another:
+ * sequence s has the query rows cu_q[s] .. cu_q[s + 1] - 1 of q [Tq, H, D] and
+ * the keys cu_k[s] .. cu_k[s + 1] - 1 of k and v [Tk, Hkv, D], and attends to
+ * itself alone.  H is a multiple of Hkv, query head h reading key head
+ * floor(h / (H / Hkv)).  Causal: query i of a sequence of Lq queries and Lk keys
+ * sees its keys j <= i + Lk - Lq (aligned bottom-right).  A query that sees no
+ * key gets O = 0 and LSE = -inf; a key that no query sees gets dK = dV = 0.
+ * Sequences may be empty on either side.  Rows before the first sequence and
+ * behind the last are neither read nor written.
+ *
+ * cu_q, cu_k : int32 [S + 1], device memory, rising within [0, Tq] and [0, Tk]
+ * (a boundary outside, or below an earlier one, is taken as the nearest that is
+ * neither).  They are read on the device, once per batch, by fa_packed_plan,
+ * which lays out the batch's tiles, longest first, in a buffer of the caller's;
+ * the calls of every layer, forward and backward, then take that plan.  It holds
+ * what it needs of cu_q and cu_k and may be captured with the calls into a graph.
+ *
+ * What a sequence holds reaches no other one.  Within a causal sequence V must be
+ * finite in the tiles (128 keys) that a query's tile visits, as for fa_fwd_sink.
+ *
+ * Errors as for fa_fwd, nothing enqueued on any of them.  The calls allocate
+ * nothing and keep nothing between calls; a workspace is the caller's, so calls
+ * that may overlap (other streams, other captured graphs) take different ones.
+ */
+
+/* Rows of one tensor: element (t, h, d) is ptr[t * row + h * head + d] (strides
+ * in elements, multiples of 8, at least D; ptr 16-byte aligned).  So q, k and v
+ * may be slices of one projection's output, and dq, dk and dv of its gradient;
+ * outputs overlap no other argument's elements. */
+typedef struct {
+    void *ptr;
+    long long row, head;
+} fa_rows;
+
+/* Sizes of a batch: S, Tq, Tk, H (at most 65535), Hkv, causal 0 or 1;
+ * (Tq + 128 (S + 1)) * H and (Tk + 128 S) * Hkv at most 2^31 - 65536. */
+typedef struct {
+    int seqs, tokens_q, tokens_k, heads, key_heads, causal;
+} fa_packed_sizes;
+
+/*
+ * fa_packed_plan -- lay out a batch in `plan` (device memory, 16-byte aligned,
+ * of at least fa_packed_plan_bytes), for the forward alone (grad 0) or for both
+ * directions (grad 1).  The calls that take the plan are given the same sizes
+ * (`causal` may differ: the order of the tiles is then not the best).
+ */
+FA_API fa_status fa_packed_plan_bytes(const fa_packed_sizes *sizes, int grad, size_t *bytes);
+FA_API fa_status fa_packed_plan(const int *cu_q, const int *cu_k, const fa_packed_sizes *sizes, int grad, void *plan,
+                                size_t plan_bytes, fa_stream_t stream);
+
+/*
+ * fa_packed_fwd -- O [Tq, H, D] and LSE (float32 [H, Tq]) of a planned batch.
+ * D, scale and dtype as for fa_fwd.
+ */
+FA_API fa_status fa_packed_fwd(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *o, float *LSE,
+                               const fa_packed_sizes *sizes, int D, float scale, fa_dtype dtype, const void *plan,
+                               size_t plan_bytes, fa_stream_t stream);
+
+/*
+ * fa_packed_bwd -- the gradients dQ, dK, dV of fa_packed_fwd's O for an upstream
+ * gradient dO, from its O and LSE and a plan made with grad 1.  flags : 0 or
+ * FA_BWD_DETERMINISTIC, as for fa_bwd_ex.  workspace : device memory, 16-byte
+ * aligned, of at least fa_packed_bwd_workspace bytes; its contents need no
+ * set-up.
+ */
+FA_API fa_status fa_packed_bwd_workspace(const fa_packed_sizes *sizes, int D, unsigned int flags, size_t *bytes);
+FA_API fa_status fa_packed_bwd(const fa_rows *q, const fa_rows *k, const fa_rows *v, const fa_rows *o,
+                               const fa_rows *dO, const float *LSE, const fa_rows *dq, const fa_rows *dk,
+                               const fa_rows *dv, const fa_packed_sizes *sizes, int D, float scale, fa_dtype dtype,
+                               unsigned int flags, const void *plan, size_t plan_bytes, void *workspace,
+                               size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * ---- A key/value cache held in 4 bits ----
  *
  * A cache holds, for K and for V, one packed row per token and key head:
