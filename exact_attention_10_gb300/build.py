@@ -1,12 +1,13 @@
 """Build the CUDA library (libfa_gb300.so) in-tree with nvcc for sm_103a.
 
-Eleven translation units, compiled in parallel and linked into one shared
+Thirteen translation units, compiled in parallel and linked into one shared
 library: csrc/fa_api.cu (the C ABI and the whole-tile kernel variants without
 a mask or with the causal one), csrc/fa_split.cu (the same for the balanced
 schedule), csrc/fa_band.cu (left-bounded band masks, both schedules),
 csrc/fa_sink.cu (windows with sinks, both schedules),
 csrc/fa_bwd.cu and fa_bwd_sink.cu (the backward), csrc/fa_packed.cu and
-fa_bwd_packed.cu (packed sequences), csrc/fa_cache.cu (the 4-bit cache),
+fa_bwd_packed.cu (packed sequences), csrc/fa_paged.cu and
+fa_paged_e4m3.cu (the paged cache), csrc/fa_cache.cu (the 4-bit cache),
 csrc/fa_cache_rows.cu (the weights of its tokens for many query rows) and
 csrc/fa_evict.cu (eviction from it), so the build stays quick on both the
 x86_64 build machine and the aarch64 GPU host.
@@ -24,7 +25,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f) for f in ("fa_api.cu", "fa_split.cu", "fa_band.cu", "fa_sink.cu", "fa_bwd.cu",
                                                "fa_bwd_sink.cu", "fa_cache.cu", "fa_cache_rows.cu",
-                                               "fa_evict.cu", "fa_packed.cu", "fa_bwd_packed.cu")]
+                                               "fa_evict.cu", "fa_packed.cu", "fa_bwd_packed.cu",
+                                               "fa_paged.cu", "fa_paged_e4m3.cu")]
 LIB_PATH = os.path.join(PKG, "libfa_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,427 @@
+// fa_paged.cu -- the paged key/value cache's entry points (include/fa.h): append
+// and read kernels, argument checks, kernel choice and launch.  The attention's
+// kernels are in fa_paged_kernel.cuh.
+#include "fa.h"
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "fa_host.h"
+#include "fa_paged_kernel.cuh"
+#include "fa_paged_launch.h"
+
+namespace {
+
+using fa_host::Arg;
+namespace paged = fa::paged;
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ append, read
+
+struct Rows16 {
+    uint8_t *p;
+    long long row, head;   // bytes
+};
+
+struct MoveParams {
+    Rows16 k, v;                 // the packed tokens
+    uint8_t *kp, *vp;            // pages
+    float *ks, *vs;
+    const int *table, *start, *cu;
+    int tokens, B, Hkv, W, P, page_bits;
+};
+
+// Row of the pool that token i of the packed tokens has, -1: none.  Without cu,
+// token i is sequence i's.
+__device__ __forceinline__ long long pool_row(const MoveParams &p, int i, int h)
+{
+    int b = i, first = i;
+    if (p.cu) {   // the last sequence that begins at i or before
+        int lo = 0, hi = p.B;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (__ldg(p.cu + mid + 1) <= i)
+                lo = mid + 1;
+            else
+                hi = mid;
+        }
+        b = lo;
+        if (b >= p.B)
+            return -1;
+        first = __ldg(p.cu + b);
+        if (i < first)
+            return -1;
+    }
+    const long long t = (long long)__ldg(p.start + b) + (i - first);
+    if (t < 0 || (t >> p.page_bits) >= p.W)
+        return -1;
+    const int id = __ldg(p.table + (long long)b * p.W + (t >> p.page_bits));
+    if ((unsigned)id >= (unsigned)p.P)
+        return -1;
+    return (((long long)id * p.Hkv + h) << p.page_bits) + (t & ((1 << p.page_bits) - 1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float value(uint32_t u, int e)
+{
+    if (BF16)
+        return __uint_as_float(e ? u & 0xffff0000u : u << 16);
+    return __half2float(__ushort_as_half((unsigned short)(e ? u >> 16 : u & 0xffffu)));
+}
+
+__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A group of D / 8 lanes per token and key head, 8 channels a lane, K and V both.
+// Memory bound: it reads 2 x 2 D bytes and writes as much or 2 x (D + 4).  At 8
+// bits scale = max |x| / 448 and code = e4m3(x / scale), each quotient rounded
+// once (a product with a reciprocal would move codes next to a border).
+template <int D, bool BF16, int BITS>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ MoveParams p)
+{
+    constexpr int kLanes = D / 8;
+    const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long r = g / kLanes;
+    const int part = (int)(g % kLanes), lane = threadIdx.x % 32;
+    if (r >= (long long)p.tokens * p.Hkv)   // (whole groups)
+        return;
+    const int i = (int)(r / p.Hkv), h = (int)(r - (long long)i * p.Hkv);
+    const long long at = pool_row(p, i, h);
+    if (at < 0)
+        return;
+    const uint4 x[2] = {*reinterpret_cast<const uint4 *>(p.k.p + i * p.k.row + h * p.k.head + 16 * part),
+                        *reinterpret_cast<const uint4 *>(p.v.p + i * p.v.row + h * p.v.head + 16 * part)};
+    if (BITS == 16) {
+        *reinterpret_cast<uint4 *>(p.kp + at * (2 * D) + 16 * part) = x[0];
+        *reinterpret_cast<uint4 *>(p.vp + at * (2 * D) + 16 * part) = x[1];
+        return;
+    }
+    const uint32_t group = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        float f[8], top = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            f[w] = value<BF16>(paged::word(x[n], w / 2), w & 1);
+            const float a = fabsf(f[w]);
+            top = a > top || a != a ? a : top;   // (a NaN stays)
+        }
+#pragma unroll
+        for (int m = 1; m < kLanes; m *= 2) {
+            const float a = __shfl_xor_sync(group, top, m);
+            top = a > top || a != a ? a : top;
+        }
+        const float scale = __fdiv_rn(top, 448.f);
+        uint32_t c[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float lo = scale == 0.f ? 0.f : __fdiv_rn(f[2 * w], scale), hi = scale == 0.f ? 0.f : __fdiv_rn(f[2 * w + 1], scale);
+            c[w] = to_e4m3(lo, hi);
+        }
+        *reinterpret_cast<uint2 *>((n ? p.vp : p.kp) + at * D + 8 * part) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        if (part == 0)
+            (n ? p.vs : p.ks)[at] = scale;
+    }
+}
+
+// The values of packed tokens, rounded once to the type; zeros for those that have no row.
+template <int D, bool BF16, int BITS>
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ MoveParams p)
+{
+    constexpr int kLanes = D / 8;
+    const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long r = g / kLanes;
+    const int part = (int)(g % kLanes);
+    if (r >= (long long)p.tokens * p.Hkv)
+        return;
+    const int i = (int)(r / p.Hkv), h = (int)(r - (long long)i * p.Hkv);
+    const long long at = pool_row(p, i, h);
+    uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (at >= 0) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const uint8_t *src = (n ? p.vp : p.kp) + at * (D * BITS / 8);
+            if (BITS == 16) {
+                x[n] = *reinterpret_cast<const uint4 *>(src + 16 * part);
+            } else {
+                const uint2 c = *reinterpret_cast<const uint2 *>(src + 8 * part);
+                const float scale = (n ? p.vs : p.ks)[at];
+                uint32_t o[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t u = paged::from_e4m3(w < 2 ? c.x >> (16 * w) : c.y >> (16 * (w - 2)));
+                    o[w] = paged::pack<BF16>(value<false>(u, 0) * scale, value<false>(u, 1) * scale);
+                }
+                x[n] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+    *reinterpret_cast<uint4 *>(p.k.p + i * p.k.row + h * p.k.head + 16 * part) = x[0];
+    *reinterpret_cast<uint4 *>(p.v.p + i * p.v.row + h * p.v.head + 16 * part) = x[1];
+}
+
+// ------------------------------------------------------------------ checks
+
+// What every paged call checks of the cache; `bits` of its rows' page.
+bool pages_ok(const fa_pages *c, int B, int W, int *bits)
+{
+    if (!c || (c->D != 64 && c->D != 128) || (c->bits != 16 && c->bits != 8) || (c->dtype != FA_BF16 && c->dtype != FA_FP16))
+        return false;
+    if (c->pages < 1 || c->key_heads < 1 || c->key_heads > 65535 || B < 1 || W < 1)
+        return false;
+    for (*bits = 4; *bits <= 10 && (1 << *bits) != c->page; ++*bits) {}
+    if (*bits > 10)
+        return false;
+    return (long long)B * W <= fa_host::kMaxRows && ((long long)W << *bits) <= fa_host::kMaxRows &&
+           (long long)B * c->key_heads <= fa_host::kMaxRows &&
+           ((double)c->pages * c->key_heads * c->page < 9e15);
+}
+
+size_t page_bytes(const fa_pages *c)
+{
+    return (size_t)c->pages * c->key_heads * c->page * (size_t)(c->D * c->bits / 8);
+}
+
+// The cache's tensors as arguments; their number.
+int page_args(const fa_pages *c, bool out, Arg *a)
+{
+    a[0] = Arg{c->k, page_bytes(c), out, 16};
+    a[1] = Arg{c->v, page_bytes(c), out, 16};
+    if (c->bits == 16)
+        return 2;
+    const size_t n = (size_t)c->pages * c->key_heads * c->page * 4;
+    a[2] = Arg{c->k_scale, n, out, 16};
+    a[3] = Arg{c->v_scale, n, out, 16};
+    return 4;
+}
+
+fa_status launched()
+{
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Append (k, v inputs) or read (outputs).
+fa_status move(const fa_pages *c, const int *table, int W, int B, const fa_rows *k, const fa_rows *v, int tokens,
+               const int *start, const int *cu, fa_stream_t stream, bool append)
+{
+    int bits;
+    if (!pages_ok(c, B, W, &bits) || tokens < 1 || (long long)tokens * c->key_heads > fa_host::kMaxRows)
+        return FA_ERR_INVALID_VALUE;
+    if (!cu && tokens != B)
+        return FA_ERR_INVALID_VALUE;
+    const int D = c->D, Hkv = c->key_heads;
+    MoveParams p{};
+    Arg args[9];
+    int n = page_args(c, append, args);
+    const fa_rows *rows[2] = {k, v};
+    for (int i = 0; i < 2; ++i) {
+        if (!rows[i])
+            return FA_ERR_INVALID_VALUE;
+        fa_rows r = *rows[i];
+        if (Hkv == 1)
+            r.head = D;
+        if (tokens == 1)
+            r.row = Hkv * (r.head > 0 ? r.head : 0);
+        if (r.row < D || r.head < D || r.row % 8 || r.head % 8 || r.row >= (1ll << 38) || r.head >= (1ll << 38))
+            return FA_ERR_INVALID_VALUE;
+        // (results are written rows apart from one another)
+        if (!append && (Hkv - 1) * r.head + D > r.row && (tokens - 1) * r.row + D > r.head && tokens > 1)
+            return FA_ERR_INVALID_VALUE;
+        args[n++] = Arg{r.ptr, (size_t)((tokens - 1) * r.row + (Hkv - 1) * r.head + D) * 2, !append, 16};
+        (i ? p.v : p.k) = Rows16{static_cast<uint8_t *>(r.ptr), r.row * 2, r.head * 2};
+    }
+    args[n++] = Arg{table, (size_t)B * W * 4, false, 4};
+    args[n++] = Arg{start, (size_t)B * 4, false, 4};
+    if (cu)
+        args[n++] = Arg{cu, ((size_t)B + 1) * 4, false, 4};
+    int dev;
+    const fa_host::DeviceInfo *di;
+    const fa_status st = fa_host::check_args(args, n, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    p.kp = static_cast<uint8_t *>(c->k);
+    p.vp = static_cast<uint8_t *>(c->v);
+    p.ks = c->k_scale;
+    p.vs = c->v_scale;
+    p.table = table;
+    p.start = start;
+    p.cu = cu;
+    p.tokens = tokens;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.W = W;
+    p.P = c->pages;
+    p.page_bits = bits;
+    const unsigned blocks = (unsigned)(((long long)tokens * Hkv * (D / 8) + kThreads - 1) / kThreads);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    auto run = [&](auto kern) {
+        kern<<<blocks, kThreads, 0, s>>>(p);
+        return launched();
+    };
+    auto pick = [&](auto d, auto b) {
+        constexpr int DD = decltype(d)::value;
+        constexpr bool BB = decltype(b)::value;
+        if (append)
+            return c->bits == 16 ? run(append_kernel<DD, BB, 16>) : run(append_kernel<DD, BB, 8>);
+        return c->bits == 16 ? run(read_kernel<DD, BB, 16>) : run(read_kernel<DD, BB, 8>);
+    };
+    using T = std::true_type;
+    using F = std::false_type;
+    const bool bf16 = c->dtype == FA_BF16;
+    if (D == 64)
+        return bf16 ? pick(std::integral_constant<int, 64>{}, T{}) : pick(std::integral_constant<int, 64>{}, F{});
+    return bf16 ? pick(std::integral_constant<int, 128>{}, T{}) : pick(std::integral_constant<int, 128>{}, F{});
+}
+
+// ------------------------------------------------------------------ attention
+
+bool queries_ok(const fa_pages *c, int B, int H, int Nq)
+{
+    return H >= 1 && H % c->key_heads == 0 && Nq >= 1 && (long long)B * H <= fa_host::kMaxRows &&
+           (long long)B * H * Nq <= fa_host::kMaxRows;
+}
+
+// Row blocks of 16 that share a CTA: 1, 2 or 4.
+int blocks_per_cta(int rows)
+{
+    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+
+struct Shape {
+    int nrb, RB, cluster, grid;
+    size_t bytes;   // workspace
+};
+
+Shape shape_of(const fa_pages *c, int B, int H, int Nq, int W, int sms)
+{
+    Shape s{};
+    const int rows = (H / c->key_heads) * Nq;
+    s.nrb = blocks_per_cta(rows);
+    s.RB = (rows + 16 * s.nrb - 1) / (16 * s.nrb);
+    const long long tiles = (long long)B * c->key_heads * s.RB, tokens = (long long)W * c->page;
+    const int room = 2 * sms;
+    int cl = 1;
+    while (cl < 8 && tiles * cl * 2 <= room && (long long)cl * 2 * paged::kUnit <= tokens)
+        cl *= 2;
+    if (tokens <= 1024ll * cl && tiles * cl < (1ll << 31)) {
+        s.cluster = cl;
+        s.grid = (int)(tiles * cl);
+        return s;
+    }
+    s.grid = room;
+    s.bytes = (size_t)2 * room * 16 * s.nrb * (c->D * sizeof(float) + sizeof(float2));
+    return s;
+}
+
+}  // namespace
+
+extern "C" fa_status fa_paged_append(const fa_pages *cache, const int *table, int width, int B, const fa_rows *k,
+                                     const fa_rows *v, int tokens, const int *start, const int *cu, fa_stream_t stream)
+{
+    return move(cache, table, width, B, k, v, tokens, start, cu, stream, true);
+}
+
+extern "C" fa_status fa_paged_read(const fa_pages *cache, const int *table, int width, int B, const fa_rows *k,
+                                   const fa_rows *v, int tokens, const int *start, const int *cu, fa_stream_t stream)
+{
+    return move(cache, table, width, B, k, v, tokens, start, cu, stream, false);
+}
+
+extern "C" fa_status fa_paged_workspace(const fa_pages *cache, int width, int B, int H, int Nq, size_t *bytes)
+{
+    int bits;
+    if (!bytes || !pages_ok(cache, B, width, &bits) || !queries_ok(cache, B, H, Nq))
+        return FA_ERR_INVALID_VALUE;
+    int dev;
+    const fa_host::DeviceInfo *di;
+    const fa_status st = fa_host::current_device(&dev, &di);
+    if (st != FA_OK)
+        return st;
+    *bytes = shape_of(cache, B, H, Nq, width, di->sms).bytes;
+    return FA_OK;
+}
+
+extern "C" fa_status fa_paged_fwd(const void *Q, long long q_batch, long long q_head, long long q_token,
+                                  const fa_pages *cache, const int *table, int width, const int *lens, void *O, float *LSE,
+                                  int B, int H, int Nq, float scale, void *workspace, size_t workspace_bytes,
+                                  fa_stream_t stream)
+{
+    int bits;
+    if (!pages_ok(cache, B, width, &bits) || !queries_ok(cache, B, H, Nq) || !std::isfinite(scale) || !(scale > 0.f))
+        return FA_ERR_INVALID_VALUE;
+    const int D = cache->D;
+    // strides of dimensions of one do not count; others keep 16-byte alignment
+    const long long n[3] = {B, H, Nq}, stride[3] = {q_batch, q_head, q_token};
+    long long st3[3], last = 0;
+    for (int i = 0; i < 3; ++i) {
+        st3[i] = n[i] == 1 ? 0 : stride[i];
+        if (st3[i] < 0 || st3[i] % 8 || st3[i] >= (1ll << 38) || (n[i] > 1 && st3[i] < D))
+            return FA_ERR_INVALID_VALUE;
+        last += (n[i] - 1) * st3[i];
+    }
+    const size_t qrows = (size_t)B * H * Nq;
+    Arg args[10];
+    int m = page_args(cache, false, args);
+    args[m++] = Arg{Q, (size_t)(last + D) * 2, false, 16};
+    args[m++] = Arg{table, (size_t)B * width * 4, false, 4};
+    args[m++] = Arg{lens, (size_t)B * 4, false, 4};
+    args[m++] = Arg{O, qrows * D * 2, true, 16};
+    args[m++] = Arg{LSE, qrows * 4, true, 4};
+    if (workspace)
+        args[m++] = Arg{workspace, workspace_bytes, true, 16};
+    int dev;
+    const fa_host::DeviceInfo *di;
+    fa_status st = fa_host::check_args(args, m, &dev, &di);
+    if (st != FA_OK)
+        return st;
+    const Shape sh = shape_of(cache, B, H, Nq, width, di->sms);
+    if (sh.bytes > 0 && (!workspace || workspace_bytes < sh.bytes))
+        return FA_ERR_INVALID_VALUE;
+    paged::Params p{};
+    p.k = static_cast<const uint8_t *>(cache->k);
+    p.v = static_cast<const uint8_t *>(cache->v);
+    p.ks = cache->k_scale;
+    p.vs = cache->v_scale;
+    p.table = table;
+    p.lens = lens;
+    p.q = static_cast<const uint16_t *>(Q);
+    p.q_b = st3[0];
+    p.q_h = st3[1];
+    p.q_n = st3[2];
+    p.o = O;
+    p.lse = LSE;
+    p.B = B;
+    p.Hkv = cache->key_heads;
+    p.Nq = Nq;
+    p.G = H / cache->key_heads;
+    p.rows = p.G * Nq;
+    p.RB = sh.RB;
+    p.W = width;
+    p.P = cache->pages;
+    p.page_bits = bits;
+    p.qk2 = scale * 1.4426950408889634f;
+    p.cluster = sh.cluster;
+    if (!sh.cluster) {
+        p.part_o = static_cast<float *>(workspace);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * sh.grid * 16 * sh.nrb * D);
+    }
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf16 = cache->dtype == FA_BF16;
+    return cache->bits == 16 ? fa_launch::launch_paged(p, D, bf16, sh.nrb, sh.grid, s, dev)
+                             : fa_launch::launch_paged_e4m3(p, D, bf16, sh.nrb, sh.grid, s, dev);
+}
+
+namespace fa_launch {
+
+fa_status launch_paged(const fa::paged::Params &p, int D, bool bf16, int nrb, int grid, cudaStream_t s, int dev)
+{
+    return launch_paged_bits<16>(p, D, bf16, nrb, grid, s, dev);
+}
+
+}  // namespace fa_launch

@@ -1,0 +1,817 @@
+// fa_paged_kernel.cuh -- attention of each sequence's last tokens against a
+// paged key/value cache, for GB300 (sm_103a).  (Append and read: fa_paged.cu.)
+//
+// Cache.  K and V are pools of pages [P, Hkv, page, D]; token t of sequence b is
+// row t % page of page table[b, t / page].  Rows are held in 16 bits as they are,
+// or in 8 as e4m3 codes with one float scale per token and key head, value = code *
+// scale.
+//
+// Attention.  Query row (g, i) of a key head -- query head h (H / Hkv) + g, the
+// i-th of the Nq last tokens of a sequence of len tokens -- sees the tokens
+// j <= len - Nq + i:
+//   x_j = scale ks_j (q . k_j),  p_j = exp(x_j - m),  O = sum_j (p_j vs_j) v_j / sum_j p_j
+// with ks, vs the scales (1 at 16 bits).
+//
+// What bounds it: every cached row is read once, 2 D (or D + 4) bytes for each of
+// K and V, against 4 G Nq D operations on it -- HBM, at the few query rows per
+// key head of decoding.  So the rows go from global memory straight into the
+// fragments of mma.sync, without shared memory, ldmatrix or transposes through
+// it: the order of the channels in a product is free as long as both operands
+// have the same, so a lane's 16 bytes of a K row are the B fragments of its
+// column (two products, four at 8 bits), and 16 bytes of four V rows, paired by
+// token with byte permutes, those of eight channels (sixteen).  16 query rows are
+// the M of one product; tcgen05's 128 would be eight times a decode step's rows.
+// Up to four blocks of 16 rows share a CTA, whose warps read the same rows of the
+// cache through L1.
+//
+// A warp takes 16 tokens at a time, which lie in one page; the next 16 tokens' K
+// is on its way while V is used, and the other way round, so eight warps per SM
+// hold 64 KB in flight (an SM's share of HBM's bandwidth takes 36 KB at 0.8 us).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "fa.h"
+
+namespace fa {
+namespace paged {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStep = 16;      // tokens a warp takes at a time
+constexpr int kUnit = 64;      // tokens per unit of work handed to the CTAs
+constexpr int kMinUnits = 4;   // units per CTA, at least
+constexpr int kRows = 16;      // query rows of a block
+constexpr float kLn2f = 0.69314718055994530942f;
+// A query row's weights are relative to a reference that is set to its maximum
+// less kLift and moves only when a weight exceeds 2^(kLift + kSlack): most steps
+// then take one vote, and weights as fp16 operands stay in range at the top and
+// whole down to 2^-21 of the maximum.  (The sums are divided by one another.)
+constexpr float kSlack = 8.f, kLift = 7.f;
+
+struct Params {
+    const uint8_t *k, *v;        // pages
+    const float *ks, *vs;        // 8 bits: scales
+    const int *table, *lens;
+    const uint16_t *q;
+    long long q_b, q_h, q_n;     // elements between q's sequences, heads and tokens
+    void *o;                     // [B, H, Nq, D]
+    float *lse;                  // [B, H, Nq]
+    int B, Hkv, Nq, G;           // G: query heads per key head
+    int rows, RB;                // G Nq, and CTA row blocks
+    int W, P, page_bits;         // table width, pages, log2 of the page
+    float qk2;                   // scale * log2(e)
+    int cluster;                 // CTAs per tile (one cluster), or 0: shares and a join
+    float *part_o;               // shares: [2 grid][rows of a CTA block][D] and (m, l)
+    float2 *part_ml;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1)
+{
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi)
+{
+    uint32_t r;
+    if (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two e4m3 codes (the low 16 bits) as two halves, exactly.
+__device__ __forceinline__ uint32_t from_e4m3(uint32_t x)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// A row of the cache is read once per row block: kept out of L1 where nothing
+// else reads it.
+template <bool SHARED>
+__device__ __forceinline__ uint4 ld16(const void *p)
+{
+    uint4 v;
+    if (SHARED)
+        asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    else
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld8(const void *p)
+{
+    uint2 v;
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float2 ldf2(const float *p)
+{
+    float2 v;
+    asm volatile("ld.global.nc.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+
+// ------------------------------------------------------------------ work decomposition
+
+__device__ __forceinline__ int len_of(const Params &p, int b)
+{
+    const int len = p.lens[b];
+    const long long top = (long long)p.W << p.page_bits;
+    return len < 0 ? 0 : (len > top ? (int)top : len);
+}
+
+// Units of a tile of a sequence: at least one, so that rows which see nothing get
+// their O = 0 and LSE = -inf written.
+__device__ __forceinline__ int units_of(int len)
+{
+    return len < 1 ? 1 : (len + kUnit - 1) / kUnit;
+}
+
+// Tiles are ordered by sequence, key head and row block; of the U units in all,
+// CTA k of the G that take part has [U k / G, U (k + 1) / G).
+struct Where {
+    long long total, parts;   // U, G
+    long long first;          // U k / G (0 for k >= G)
+    long long before;         // units of the sequences before b
+    int b;                    // the sequence that holds unit `first`
+};
+
+__device__ __forceinline__ long long share_of(const Where &w, int k)
+{
+    if (w.total < (1ll << 22))   // (k is below 2^10)
+        return (uint32_t)w.total * (uint32_t)k / (uint32_t)w.parts;
+    return w.total * k / w.parts;
+}
+
+// By every warp for itself.
+__device__ inline Where locate(const Params &p, int k, int grid)
+{
+    const int lane = threadIdx.x % 32;
+    const long long HR = (long long)p.Hkv * p.RB;
+    Where w{0, 0, 0, 0, 0};
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        long long n = b0 + lane < p.B ? units_of(len_of(p, b0 + lane)) * HR : 0;
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2)
+            n += __shfl_xor_sync(0xffffffffu, n, m);
+        w.total += n;
+    }
+    const long long g = w.total / kMinUnits;
+    w.parts = g < 1 ? 1 : (g < grid ? g : grid);
+    w.first = k < w.parts ? share_of(w, k) : 0;
+    for (int b0 = 0;; b0 += 32) {   // (total > first: ends)
+        const long long n = b0 + lane < p.B ? units_of(len_of(p, b0 + lane)) * HR : 0;
+        long long inc = n;
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m)
+                inc += v;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, w.first < w.before + inc);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            w.b = b0 + l;
+            w.before += __shfl_sync(0xffffffffu, inc - n, l);
+            return w;
+        }
+        w.before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+// ------------------------------------------------------------------ one warp's attention
+
+// D channels in BITS; channel of accumulator j (of D / 8) and column 2c + e.
+template <int D, int BITS>
+__device__ __forceinline__ int channel(int j, int c, int e)
+{
+    if (BITS == 16)
+        return 64 * (j / 8) + 16 * c + 8 * e + j % 8;
+    return (D / 8) * (2 * c + e) + j;
+}
+
+// 16 tokens of the cache in registers.
+template <int D, int BITS>
+struct Tokens {
+    static constexpr int kKey = BITS == 16 ? D / 32 : D / 64;   // 16-byte chunks a lane holds of each of two K rows
+    uint4 k[2][kKey];            // row lane / 4 (+ 8), chunks lane % 4 + 4 j
+    static constexpr int kVal = BITS == 16 ? D / 64 : 1;        // 16 (D = 64, 8 bits: 8) bytes of each of four V rows
+    uint4 v[4][kVal];            // rows 2c, 2c + 1, 2c + 8, 2c + 9, chunk lane / 4 + 8 j
+    float2 ks[2], vs[2];         // 8 bits: scales of tokens 2c, 2c + 1 (+ 8)
+
+    static constexpr int kRowBytes = D * BITS / 8;
+
+    template <bool SHARED>
+    __device__ __forceinline__ void load_k(const Params &p, long long row, int lane)
+    {
+        const uint8_t *at = p.k + (row + lane / 4) * kRowBytes + (lane % 4) * 16;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < kKey; ++j)
+                k[n][j] = ld16<SHARED>(at + n * 8 * kRowBytes + j * 64);
+        if (BITS == 8) {
+            ks[0] = ldf2(p.ks + row + 2 * (lane % 4));
+            ks[1] = ldf2(p.ks + row + 2 * (lane % 4) + 8);
+        }
+    }
+
+    template <bool SHARED>
+    __device__ __forceinline__ void load_v(const Params &p, long long row, int lane)
+    {
+        const uint8_t *at = p.v + (row + 2 * (lane % 4)) * kRowBytes + (lane / 4) * (BITS == 8 && D == 64 ? 8 : 16);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const uint8_t *r = at + ((n & 1) + (n & 2) * 4) * kRowBytes;
+            if (BITS == 8 && D == 64) {
+                const uint2 x = ld8(r);
+                v[n][0] = make_uint4(x.x, x.y, 0u, 0u);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVal; ++j)
+                    v[n][j] = ld16<SHARED>(r + j * 128);
+            }
+        }
+        if (BITS == 8) {
+            vs[0] = ldf2(p.vs + row + 2 * (lane % 4));
+            vs[1] = ldf2(p.vs + row + 2 * (lane % 4) + 8);
+        }
+    }
+
+    // Rows behind the sequence's last hold anything: V's are zeroed, n tokens left.
+    __device__ __forceinline__ void cut_v(int n, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 2 * (lane % 4) + (i & 1) + (i & 2) * 4;
+            if (t >= n) {
+#pragma unroll
+                for (int j = 0; j < kVal; ++j)
+                    v[i][j] = make_uint4(0u, 0u, 0u, 0u);
+                if (BITS == 8)
+                    (i & 1 ? vs[i / 2].y : vs[i / 2].x) = 0.f;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t word(const uint4 &x, int i)
+{
+    return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+}
+
+// The query rows of a block as A fragments, in the order of K's channels.  At 8
+// bits they are fp16: a row is multiplied by the power of two that brings its
+// largest element to [2^14, 2^15), so an element is exact unless it is 2^-24 of
+// the largest or less, and then off by 2^-40 of it; `mul` takes it out again.
+template <int D, bool BF16, int BITS>
+struct Queries {
+    uint32_t a[D / 16][4];
+    float mul[2];   // rows lane / 4 and lane / 4 + 8: from a product to log2 units
+
+    __device__ __forceinline__ void load(const Params &p, int b, int h, int r0, int lane)
+    {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = r0 + lane / 4 + 8 * e;
+            const bool real = row < p.rows;
+            const int g = real ? row / p.Nq : 0, i = real ? row - g * p.Nq : 0;
+            const uint16_t *src = p.q + b * p.q_b + ((long long)h * p.G + g) * p.q_h + i * p.q_n;
+            uint4 x[D / 32];
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                // 16 bits: chunk lane % 4 + 4 j of 8 channels; 8 bits: the two halves of a chunk of 16
+                const int ch = BITS == 16 ? 8 * (lane % 4 + 4 * j) : 16 * (lane % 4 + 4 * (j / 2)) + 8 * (j & 1);
+                x[j] = real ? *reinterpret_cast<const uint4 *>(src + ch) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            mul[e] = p.qk2;
+            if (BITS == 8) {
+                float f[D / 4], top = 0.f;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t u = word(x[j], w);
+                        if (BF16) {
+                            f[8 * j + 2 * w] = __uint_as_float(u << 16);
+                            f[8 * j + 2 * w + 1] = __uint_as_float(u & 0xffff0000u);
+                        } else {
+                            f[8 * j + 2 * w] = __half2float(__ushort_as_half((unsigned short)(u & 0xffffu)));
+                            f[8 * j + 2 * w + 1] = __half2float(__ushort_as_half((unsigned short)(u >> 16)));
+                        }
+                        top = fmaxf(top, fmaxf(fabsf(f[8 * j + 2 * w]), fabsf(f[8 * j + 2 * w + 1])));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^(14 - exponent of the largest), the exponent kept where both powers are normal numbers
+                int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                ex = ex < -100 ? -100 : (ex > 127 ? 127 : ex);
+                const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+                mul[e] = p.qk2 * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+                    x[j] = make_uint4(pack<false>(f[8 * j] * up, f[8 * j + 1] * up), pack<false>(f[8 * j + 2] * up, f[8 * j + 3] * up),
+                                      pack<false>(f[8 * j + 4] * up, f[8 * j + 5] * up),
+                                      pack<false>(f[8 * j + 6] * up, f[8 * j + 7] * up));
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                a[2 * j][e] = x[j].x;
+                a[2 * j][e + 2] = x[j].y;
+                a[2 * j + 1][e] = x[j].z;
+                a[2 * j + 1][e + 2] = x[j].w;
+            }
+        }
+    }
+};
+
+template <int D, bool BF16, int BITS>
+struct Attend {
+    static constexpr bool MB = BF16 && BITS == 16;   // products in bf16 (8 bits: codes are fp16 numbers)
+    float o[D / 8][4];
+    float m[2], l[2];   // rows lane / 4, + 8; l of this lane's tokens
+
+    __device__ __forceinline__ void reset()
+    {
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[j][i] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    // Scores of the 16 tokens in log2 units: s[n][0, 1] row lane / 4, tokens 8 n + 2c, + 1; s[n][2, 3] row + 8.
+    __device__ __forceinline__ void scores(const Tokens<D, BITS> &t, const Queries<D, BF16, BITS> &q, float (&s)[2][4])
+    {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t b0, b1;
+                if (BITS == 16) {
+                    b0 = word(t.k[n][j / 2], 2 * (j & 1));
+                    b1 = word(t.k[n][j / 2], 2 * (j & 1) + 1);
+                } else {
+                    const uint32_t w = word(t.k[n][j / 4], j % 4);
+                    b0 = from_e4m3(w);
+                    b1 = from_e4m3(w >> 16);
+                }
+                mma<MB>(s[n], q.a[j][0], q.a[j][1], q.a[j][2], q.a[j][3], b0, b1);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[n][i] *= q.mul[i / 2];
+                if (BITS == 8)
+                    s[n][i] *= (i & 1) ? t.ks[n].y : t.ks[n].x;
+            }
+        }
+    }
+
+    // Scores to weights: `hi`: tokens of the 16 that the rows lane / 4 and + 8 see (MASKED).
+    template <bool MASKED>
+    __device__ __forceinline__ void weights(const Tokens<D, BITS> &t, float (&s)[2][4], const int (&hi)[2], int lane)
+    {
+        // 8 bits: the reference is that of p vs, the operand (its logarithm kept where
+        // sums of p do not overflow: scales of 2^-80 and more are weighed in full).
+        float lv[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (MASKED && 8 * n + 2 * (lane % 4) + (i & 1) >= hi[i / 2])
+                    s[n][i] = -INFINITY;
+            }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                lv[n][e] = 0.f;
+                if (BITS == 8)
+                    lv[n][e] = fminf(fmaxf(lg2(e ? t.vs[n].y : t.vs[n].x), -80.f), 120.f);
+                top[0] = fmaxf(top[0], s[n][e] + lv[n][e]);
+                top[1] = fmaxf(top[1], s[n][2 + e] + lv[n][e]);
+            }
+        if (__any_sync(0xffffffffu, top[0] > m[0] + (kLift + kSlack) || top[1] > m[1] + (kLift + kSlack))) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = top[e];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                const float up = fmaxf(m[e], x - kLift);
+                const float f = m[e] == -INFINITY ? 0.f : ex2(m[e] - up);
+                m[e] = up;
+                l[e] *= f;
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][2 * e] *= f;
+                    o[j][2 * e + 1] *= f;
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float ref = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float w = ex2(s[n][2 * e + i] - ref);
+                    l[e] += w;
+                    s[n][2 * e + i] = BITS == 8 ? w * (i ? t.vs[n].y : t.vs[n].x) : w;
+                }
+        }
+    }
+
+    // O += P V, the weights rounded to 16 bits for the product (fp16 at 8 bits).
+    __device__ __forceinline__ void add(const Tokens<D, BITS> &t, const float (&s)[2][4])
+    {
+        const uint32_t a0 = pack<MB>(s[0][0], s[0][1]), a1 = pack<MB>(s[0][2], s[0][3]);
+        const uint32_t a2 = pack<MB>(s[1][0], s[1][1]), a3 = pack<MB>(s[1][2], s[1][3]);
+        if (BITS == 16) {
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 2) {
+                const uint32_t x0 = word(t.v[0][j / 8], (j % 8) / 2), x1 = word(t.v[1][j / 8], (j % 8) / 2);
+                const uint32_t y0 = word(t.v[2][j / 8], (j % 8) / 2), y1 = word(t.v[3][j / 8], (j % 8) / 2);
+                mma<MB>(o[j], a0, a1, a2, a3, __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
+                mma<MB>(o[j + 1], a0, a1, a2, a3, __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 4) {
+                const uint32_t x0 = word(t.v[0][0], j / 4), x1 = word(t.v[1][0], j / 4);
+                const uint32_t y0 = word(t.v[2][0], j / 4), y1 = word(t.v[3][0], j / 4);
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const uint32_t x = __byte_perm(x0, x1, i ? 0x7362 : 0x5140), y = __byte_perm(y0, y1, i ? 0x7362 : 0x5140);
+                    mma<MB>(o[j + i], a0, a1, a2, a3, from_e4m3(x), from_e4m3(y));
+                    mma<MB>(o[j + i + 1], a0, a1, a2, a3, from_e4m3(x >> 16), from_e4m3(y >> 16));
+                }
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------ the kernels
+
+// Shared memory of a CTA: per warp its rows' O and (m, l); then the joined ones.
+template <int D>
+struct Smem {
+    static constexpr int kRow = D + 4;
+    static constexpr int kO = kWarps * kRows * kRow * 4;
+    static constexpr int kBytes = kO + kWarps * kRows * 8;
+};
+
+// Write channels [ch, ch + 4) of row `row` of a key head's rows (query head, token).
+template <int D, bool BF16>
+__device__ __forceinline__ void store_out(const Params &p, int b, int h, int row, int ch, const float (&v)[4], float M,
+                                          float L)
+{
+    const long long at = ((long long)b * p.Hkv + h) * p.rows + row;   // = ((b H + h G + g) Nq + i)
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);       // (NaN stays NaN)
+    const uint2 w = make_uint2(pack<BF16>(v[0] * inv, v[1] * inv), pack<BF16>(v[2] * inv, v[3] * inv));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at * D + ch) = w;
+    if (ch == 0)
+        p.lse[at] = (M + log2f(L)) * kLn2f;
+}
+
+__device__ __forceinline__ float part_weight(const float2 &ml, float M)
+{
+    return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - M);
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+
+// Steps [s0, s1) of 16 tokens of one tile by a warp: s0, s0 + stride, ...
+template <int D, bool BF16, int BITS, bool SHARED>
+__device__ __forceinline__ void run_steps(const Params &p, Attend<D, BF16, BITS> &a, const Queries<D, BF16, BITS> &q, int b,
+                                          int h, int len, const int (&hi)[2], int edge, int s0, int s1, int stride)
+{
+    const int lane = threadIdx.x % 32;
+    const int *pages = p.table + (long long)b * p.W;
+    const int mask = (1 << p.page_bits) - 1;
+    // Pages of the warp's next 32 steps, a lane each; a page outside the pool is -1.
+    auto page_of = [&](int s) -> int {
+        if (s >= s1)
+            return -1;
+        const int id = pages[(s * kStep) >> p.page_bits];
+        return (unsigned)id < (unsigned)p.P ? id : -1;
+    };
+    auto row_of = [&](int id, int s) -> long long {   // first row of step s in the pool
+        return (((long long)id * p.Hkv + h) << p.page_bits) + ((s * kStep) & mask);
+    };
+    int ids = page_of(s0 + lane * stride), next = page_of(s0 + (32 + lane) * stride);
+    Tokens<D, BITS> t;
+    int id = __shfl_sync(0xffffffffu, ids, 0);
+    if (id >= 0) {
+        const long long row = row_of(id, s0);
+        t.template load_k<SHARED>(p, row, lane);
+        t.template load_v<SHARED>(p, row, lane);
+    }
+    int i = 0;
+    for (int s = s0; s < s1; s += stride) {
+        if (++i == 32) {
+            i = 0;
+            ids = next;
+            next = page_of(s + (33 + lane) * stride);
+        }
+        const int id1 = __shfl_sync(0xffffffffu, ids, i);   // (-1 behind the last)
+        const long long row1 = row_of(id1, s + stride);
+        if (id >= 0) {   // tokens of a page outside the pool are hidden
+            float sc[2][4];
+            a.scores(t, q, sc);
+            if (id1 >= 0)
+                t.template load_k<SHARED>(p, row1, lane);
+            if (s * kStep + kStep > edge) {
+                const int at[2] = {hi[0] - s * kStep, hi[1] - s * kStep};
+                t.cut_v(len - s * kStep, lane);
+                a.template weights<true>(t, sc, at, lane);
+            } else {
+                a.template weights<false>(t, sc, hi, lane);
+            }
+            a.add(t, sc);
+        } else if (id1 >= 0) {
+            t.template load_k<SHARED>(p, row1, lane);
+        }
+        if (id1 >= 0)
+            t.template load_v<SHARED>(p, row1, lane);
+        id = id1;
+    }
+}
+
+// Persistent CTAs.  p.cluster > 0: the CTAs of a cluster share one tile's tokens
+// and join through their shared memories: one launch, for few tiles or short
+// caches.  Otherwise CTA c of G runs units [U c / G, U (c + 1) / G) of the ordered
+// tiles, so every CTA reads the same number of tokens whatever the lengths are; a
+// tile's first and last share may be partial (slots 2c, 2c + 1), which
+// merge_kernel joins.  The warps of a CTA take its tokens in turn, NRB of them at
+// a time the same ones for different blocks of 16 query rows.
+template <int D, bool BF16, int BITS, int NRB>
+__global__ void __launch_bounds__(kThreads, 2) attend_kernel(const __grid_constant__ Params p)
+{
+    using S = Smem<D>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int kGroups = kWarps / NRB;   // warps that take turns
+    const int rb = warp % NRB, turn = warp / NRB;
+    float *all_o = reinterpret_cast<float *>(smem);
+    float2 *all_ml = reinterpret_cast<float2 *>(smem + S::kO);
+    const int HR = p.Hkv * p.RB;
+    long long u0 = 0, u1 = 1;
+    int b, hr, ku = 0;
+    uint32_t rank = 0;
+    if (p.cluster) {
+        rank = cluster_rank();
+        const int tile = blockIdx.x / p.cluster;
+        b = tile / HR;
+        hr = tile - b * HR;
+    } else {
+        const Where w = locate(p, blockIdx.x, gridDim.x);
+        if ((long long)blockIdx.x >= w.parts)
+            return;
+        u0 = w.first;
+        u1 = share_of(w, blockIdx.x + 1);
+        b = w.b;
+        const int n = units_of(len_of(p, b));
+        hr = (int)((u0 - w.before) / n);
+        ku = (int)((u0 - w.before) - (long long)hr * n);
+    }
+    for (long long u = u0; u < u1;) {
+        const int len = len_of(p, b), n = units_of(len);
+        int ke;
+        if (p.cluster) {
+            const int per = (n + p.cluster - 1) / p.cluster;
+            ku = min((int)rank * per, n);
+            ke = min(ku + per, n);
+        } else {
+            ke = (long long)n - ku < u1 - u ? n : (int)(ku + (u1 - u));
+        }
+        const bool whole = ku == 0 && ke == n;
+        const int h = hr / p.RB, r0 = (hr - h * p.RB) * (kRows * NRB);
+        const int nrows = min(p.rows - r0, kRows * NRB);
+        const int w0 = r0 + rb * kRows;   // this warp's rows
+
+        Attend<D, BF16, BITS> a;
+        a.reset();
+        if (w0 < p.rows) {
+            Queries<D, BF16, BITS> q;
+            q.load(p, b, h, w0, lane);
+            int hi[2], edge = len;   // tokens the rows see; those before `edge` are seen by all
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = min(w0 + lane / 4 + 8 * e, p.rows - 1);
+                hi[e] = max(len - p.Nq + row % p.Nq + 1, 0);
+                edge = min(edge, hi[e]);
+            }
+            edge = __reduce_min_sync(0xffffffffu, edge);
+            const int s1 = min(ke * (kUnit / kStep), (len + kStep - 1) / kStep);
+            run_steps<D, BF16, BITS, (NRB > 1)>(p, a, q, b, h, len, hi, edge, ku * (kUnit / kStep) + turn, s1, kGroups);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = a.l[e];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int row = warp * kRows + lane / 4 + 8 * e;
+            if (lane % 4 == 0)
+                all_ml[row] = make_float2(a.m[e], l);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < D / 8; j += 4)   // four channels that follow one another
+                    *reinterpret_cast<float4 *>(all_o + row * S::kRow + channel<D, BITS>(j, lane % 4, c)) =
+                        make_float4(a.o[j][2 * e + c], a.o[j + 1][2 * e + c], a.o[j + 2][2 * e + c], a.o[j + 3][2 * e + c]);
+        }
+        __syncthreads();
+        // Join the warps; into warp `rb`'s place (a cluster), the results, or the parts.
+        for (int i = threadIdx.x; i < kRows * NRB * (D / 4); i += kThreads) {
+            const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+            if (row >= nrows)
+                continue;
+            const int at = row;   // of warp row / 16, the first of its block's
+            float M = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k)
+                M = fmaxf(M, all_ml[at + k * NRB * kRows].x);
+            float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                const float2 ml = all_ml[at + k * NRB * kRows];
+                const float f = part_weight(ml, M);
+                const float4 x = *reinterpret_cast<const float4 *>(all_o + (at + k * NRB * kRows) * S::kRow + ch);
+                L += ml.y * f;
+                v[0] += x.x * f;
+                v[1] += x.y * f;
+                v[2] += x.z * f;
+                v[3] += x.w * f;
+            }
+            if (p.cluster > 1) {   // (this thread alone reads these four channels here; (m, l) go behind the barrier)
+                *reinterpret_cast<float4 *>(all_o + at * S::kRow + ch) = make_float4(v[0], v[1], v[2], v[3]);
+                if (ch == 0)
+                    *reinterpret_cast<float2 *>(all_o + at * S::kRow + D) = make_float2(M, L);
+            } else if (p.cluster || whole) {
+                store_out<D, BF16>(p, b, h, r0 + row, ch, v, M, L);
+            } else {
+                const long long slot = (2ll * blockIdx.x + (u == u0 ? 0 : 1)) * (kRows * NRB) + row;
+                *reinterpret_cast<float4 *>(p.part_o + slot * D + ch) = make_float4(v[0], v[1], v[2], v[3]);
+                if (ch == 0)
+                    p.part_ml[slot] = make_float2(M, L);
+            }
+        }
+        if (p.cluster > 1) {
+            cluster_sync();
+            const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+            for (int i = threadIdx.x + (int)rank * kThreads; i < nrows * (D / 4); i += kThreads * p.cluster) {
+                const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+                const uint32_t at = base + (uint32_t)row * (S::kRow * 4);
+                float M = -INFINITY;
+                for (int k = 0; k < p.cluster; ++k)
+                    M = fmaxf(M, ld_cluster2(map_to(at + D * 4, k)).x);
+                float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int k = 0; k < p.cluster; ++k) {
+                    const float2 ml = ld_cluster2(map_to(at + D * 4, k));
+                    const float f = part_weight(ml, M);
+                    const float4 x = ld_cluster4(map_to(at + ch * 4, k));
+                    L += ml.y * f;
+                    v[0] += x.x * f;
+                    v[1] += x.y * f;
+                    v[2] += x.z * f;
+                    v[3] += x.w * f;
+                }
+                store_out<D, BF16>(p, b, h, r0 + row, ch, v, M, L);
+            }
+            cluster_sync();   // nobody leaves while its shared memory is read
+        }
+        if (p.cluster)
+            return;
+        __syncthreads();   // read before the next tile's results overwrite it
+        u += ke - ku;
+        ku = 0;
+        if (++hr == HR) {
+            hr = 0;
+            ++b;
+        }
+    }
+}
+
+// Joins the parts of the tiles that a share boundary cuts: block k looks at the
+// boundary between CTAs k and k + 1 and, if it is the first one inside its tile,
+// adds that tile's parts in order (so the result does not depend on which CTA
+// finished first).
+template <int D, bool BF16, int NRB>
+__global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__ Params p, int grid)
+{
+    const int k = blockIdx.x;
+    const Where w = locate(p, k + 1, grid);   // (lens and table are inputs: the search may run before the attention has ended)
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // by every block, so that this grid ends after the attention has
+    const long long G = w.parts, U = w.total;
+    if (k + 1 >= G)
+        return;
+    const long long edge = w.first;   // first unit of CTA k + 1
+    const int n = units_of(len_of(p, w.b));
+    const int hr = (int)((edge - w.before) / n);
+    const long long t0 = w.before + (long long)hr * n, t1 = t0 + n;   // the tile's units
+    const long long start = share_of(w, k);   // of CTA k's units
+    if (t0 == edge || start > t0)   // not inside a tile, or not its first boundary
+        return;
+    const long long last = (t1 * G - 1) / U;   // CTA holding unit t1 - 1: the largest x with U x / G < t1
+    constexpr int R = kRows * NRB;
+    const int h = hr / p.RB, r0 = (hr - h * p.RB) * R;
+    const int nrows = min(p.rows - r0, R);
+    const long long slot0 = 2 * k + (start == t0 ? 0 : 1);   // CTA k's part: its only one, or its last
+    for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+        float M = -INFINITY;
+        for (long long x = k; x <= last; ++x)
+            M = fmaxf(M, p.part_ml[(x == k ? slot0 : 2 * x) * R + row].x);
+        float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (long long x = k; x <= last; ++x) {
+            const long long at = (x == k ? slot0 : 2 * x) * R + row;
+            const float2 ml = p.part_ml[at];
+            const float f = part_weight(ml, M);
+            const float4 y = *reinterpret_cast<const float4 *>(p.part_o + at * D + ch);
+            L += ml.y * f;
+            v[0] += y.x * f;
+            v[1] += y.y * f;
+            v[2] += y.z * f;
+            v[3] += y.w * f;
+        }
+        store_out<D, BF16>(p, w.b, h, r0 + row, ch, v, M, L);
+    }
+}
+
+}  // namespace paged
+}  // namespace fa

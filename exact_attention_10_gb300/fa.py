@@ -21,7 +21,8 @@ STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_VALUE", 2: "FA_ERR_MISALIGNED", 3: "FA_
 EXPORTS = ("fa_bwd", "fa_bwd_band", "fa_bwd_ex", "fa_bwd_sink", "fa_bwd_sink_workspace", "fa_cache_append", "fa_cache_evict", "fa_cache_fwd", "fa_cache_read",
            "fa_cache_weights", "fa_cache_workspace", "fa_fwd", "fa_fwd_band", "fa_fwd_ex", "fa_fwd_noalloc",
            "fa_fwd_qkv", "fa_fwd_sink", "fa_fwd_sink_workspace", "fa_packed_bwd", "fa_packed_bwd_workspace",
-           "fa_packed_fwd", "fa_packed_plan", "fa_packed_plan_bytes", "fa_sync_status", "fa_status_string")
+           "fa_packed_fwd", "fa_packed_plan", "fa_packed_plan_bytes", "fa_paged_append", "fa_paged_fwd", "fa_paged_read",
+           "fa_paged_workspace", "fa_sync_status", "fa_status_string")
 SCHEDULES = {"auto": 0, "whole_tiles": 1, "balanced": 2}
 
 _lib = None
@@ -35,6 +36,12 @@ class Rows(ctypes.Structure):
 class PackedSizes(ctypes.Structure):
     """fa_packed_sizes."""
     _fields_ = [(n, ctypes.c_int) for n in ("seqs", "tokens_q", "tokens_k", "heads", "key_heads", "causal")]
+
+
+class Pages(ctypes.Structure):
+    """fa_pages."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int) for n in ("pages", "key_heads", "page", "D", "bits", "dtype")]
 
 
 class FAError(RuntimeError):
@@ -99,6 +106,13 @@ def load(path: str = LIB_PATH):
                                                                     vp, size_t, vp, size_t, vp]
     for f in (lib.fa_packed_plan_bytes, lib.fa_packed_plan, lib.fa_packed_fwd, lib.fa_packed_bwd_workspace,
               lib.fa_packed_bwd):
+        f.restype = c_int
+    pages, c_ll = ctypes.POINTER(Pages), ctypes.c_longlong
+    lib.fa_paged_append.argtypes = lib.fa_paged_read.argtypes = [pages, vp, c_int, c_int, rows, rows, c_int, vp, vp, vp]
+    lib.fa_paged_workspace.argtypes = [pages] + [c_int] * 4 + [ctypes.POINTER(size_t)]
+    lib.fa_paged_fwd.argtypes = [vp, c_ll, c_ll, c_ll, pages, vp, c_int, vp, vp, vp, c_int, c_int, c_int, ctypes.c_float,
+                                 vp, size_t, vp]
+    for f in (lib.fa_paged_append, lib.fa_paged_read, lib.fa_paged_workspace, lib.fa_paged_fwd):
         f.restype = c_int
     lib.fa_sync_status.argtypes = [vp]
     lib.fa_sync_status.restype = c_int
@@ -485,6 +499,190 @@ def packed_backward(q, k, v, o, do, lse, plan: PackedPlan, scale: float | None =
     if rc != 0:
         raise FAError(rc, "fa_packed_bwd")
     return dq, dk, dv
+
+
+# ---- the paged key/value cache
+
+class PagedCache(tuple):
+    """K and V of many sequences in pages: the tensors (k, v), [P, Hkv, page, D] in
+    bfloat16 or float16, or (k, v, k_scale, v_scale) with e4m3 rows
+    (torch.float8_e4m3fn) and float32 scales [P, Hkv, page] (the format is in
+    include/fa.h).  ``page`` is a power of two, 16 to 1024.  Checked when it is
+    made; pages are handed to sequences by the tables that the calls take."""
+
+    k, v = (property(itemgetter(i)) for i in range(2))
+
+    def __new__(cls, k, v, k_scale=None, v_scale=None):
+        import torch
+        shape = k.shape
+        if len(shape) != 4 or 0 in shape or v.shape != shape:
+            raise ValueError("a paged cache is [P, Hkv, page, D] for K and for V, none empty")
+        if shape[3] not in (64, 128) or shape[2] not in (16, 32, 64, 128, 256, 512, 1024):
+            raise ValueError("D must be 64 or 128, a page a power of two from 16 to 1024")
+        if v.dtype != k.dtype:
+            raise TypeError("K and V must be of one type")
+        tensors = (k, v)
+        if k.dtype == torch.float8_e4m3fn:
+            if k_scale is None or v_scale is None:
+                raise ValueError("8-bit rows take k_scale and v_scale")
+            if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+                raise ValueError("scales must be [P, Hkv, page]")
+            if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+                raise TypeError("scales are float32")
+            tensors += (k_scale, v_scale)
+        else:
+            _dtype_code(k)
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("16-bit rows have no scales")
+        if not all(t.is_contiguous() for t in tensors):
+            raise ValueError("the cache must be contiguous")
+        if any(t.device != k.device for t in tensors):
+            raise ValueError("the cache must be on one device")
+        self = super().__new__(cls, tensors)
+        self.bits = 16 if len(tensors) == 2 else 8
+        self.device = k.get_device()
+        self.dtype = k.dtype
+        ptrs = [t.data_ptr() for t in tensors] + [None] * (4 - len(tensors))
+        self._args = {}
+        for code, t in ((FA_BF16, torch.bfloat16), (FA_FP16, torch.float16)):
+            if self.bits == 8 or t == k.dtype:
+                self._args[t] = Pages(*ptrs, *shape, self.bits, code)
+        return self
+
+    def __reduce__(self):   # (copying and pickling go through the checks)
+        return PagedCache, tuple(self)
+
+    def args(self, dtype) -> Pages:
+        """What the library takes for values of ``dtype``."""
+        if dtype not in self._args:
+            raise TypeError(f"a cache of {self.dtype} does not hold values of {dtype}")
+        return self._args[dtype]
+
+
+def paged_empty(pages: int, Hkv: int, page: int, D: int, dtype=None, bits: int = 16, device="cuda") -> PagedCache:
+    """A cache of ``pages`` pages of ``page`` tokens for Hkv key heads, all zero:
+    ``bits`` 16 holds rows of ``dtype`` (bfloat16 by default, or float16), 8 e4m3
+    rows and their scales, for values of either type."""
+    import torch
+    if bits not in (8, 16):
+        raise ValueError("bits must be 8 or 16")
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"a cache holds bfloat16 or float16 values, got {dtype}")
+    rows = [torch.zeros((pages, Hkv, page, D), dtype=dtype if bits == 16 else torch.float8_e4m3fn, device=device)
+            for _ in range(2)]
+    scales = [torch.zeros((pages, Hkv, page), dtype=torch.float32, device=device) for _ in range(2)] if bits == 8 else []
+    return PagedCache(*rows, *scales)
+
+
+def _paged_table(cache, table):
+    import torch
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    if table.dtype != torch.int32:
+        raise TypeError("table must be int32")
+    if table.dim() != 2 or 0 in table.shape or not table.is_contiguous():
+        raise ValueError("table must be contiguous [B, width]")
+    if table.get_device() != cache.device:
+        raise ValueError("table must be on the cache's device")
+    return table.shape
+
+
+def _paged_move(name, cache, table, k, v, start, cu, stream):
+    B, W = _paged_table(cache, table)
+    args = cache.args(k.dtype)
+    if k.dim() != 3 or (cu is None and k.shape[0] != B):
+        raise ValueError("k, v must be [T, Hkv, D], T the table's sequences without cu")
+    T, dev = k.shape[0], cache.device
+    rk, rv = (_rows(x, T, args.key_heads, args.D, k.dtype, dev, n) for x, n in ((k, "k"), (v, "v")))
+    rc = getattr(load(), name)(args, table.data_ptr(), W, B, rk, rv, T, _ints(start, B, "start"),
+                               None if cu is None else _ints(cu, B + 1, "cu"), _stream_of(stream, k))
+    if rc != 0:
+        raise FAError(rc, name)
+
+
+def paged_append(cache: PagedCache, table, k, v, start, cu=None, stream=None) -> None:
+    """Write packed tokens k, v [T, Hkv, D] (the last dimension contiguous, other
+    strides multiples of 8) into the cache: rows cu[b] .. cu[b + 1] - 1 are
+    sequence b's and become its tokens start[b] and on (``start`` int32 [B],
+    ``cu`` int32 [B + 1]; without it, T = B, one token each).  Token t of a
+    sequence goes to row t % page of page ``table[b, t // page]`` (int32 [B,
+    width]); tokens whose page lies outside the table or the cache are not
+    written.  Raises FAError on any non-OK status.  Asynchronous on ``stream``
+    (default: the current torch stream)."""
+    _paged_move("fa_paged_append", cache, table, k, v, start, cu, stream)
+
+
+def paged_read(cache: PagedCache, table, start, tokens: int, cu=None, dtype=None, stream=None):
+    """The values (k, v) [tokens, Hkv, D] that those tokens of the cache stand
+    for (``start``, ``cu`` as for ``paged_append``), rounded once to ``dtype``
+    (the cache's type; bfloat16 by default for 8 bits); zeros for rows that
+    belong to no sequence or have no page.  Asynchronous on ``stream``, which the
+    results belong to (see ``forward``)."""
+    import torch
+    _paged_table(cache, table)
+    if not 1 <= tokens <= 0x7FFFFFFF:
+        raise ValueError("tokens must be a 32-bit count of at least 1")
+    if dtype is None:
+        dtype = cache.dtype if cache.bits == 16 else torch.bfloat16
+    args = cache.args(dtype)
+    with _on(stream, cache.k):
+        k = torch.empty((tokens, args.key_heads, args.D), dtype=dtype, device=cache.k.device)
+        v = torch.empty_like(k)
+    _paged_move("fa_paged_read", cache, table, k, v, start, cu, stream)
+    return k, v
+
+
+@lru_cache(maxsize=4096)
+def _paged_workspace(device: int, pages: int, Hkv: int, page: int, D: int, bits: int, W: int, B: int, H: int, Nq: int) -> int:
+    n = ctypes.c_size_t()
+    rc = load().fa_paged_workspace(Pages(None, None, None, None, pages, Hkv, page, D, bits, FA_BF16), W, B, H, Nq,
+                                   ctypes.byref(n))
+    if rc != 0:
+        raise FAError(rc, "fa_paged_workspace")
+    return n.value
+
+
+def paged_forward(q, cache: PagedCache, table, lens, scale: float | None = None, out=None, lse=None, stream=None):
+    """Attention of each sequence's last Nq tokens, q [B, H, Nq, D] (the last
+    dimension contiguous, other strides multiples of 8), against the cache's
+    first lens[b] tokens (theirs among them; ``lens`` int32 [B]), causal; H / Hkv
+    query heads share a key head.  Tokens of a page outside the cache are seen by
+    no query.  Returns (O [B, H, Nq, D], LSE [B, H, Nq]); a query that sees no
+    token gets O = 0 and LSE = -inf.
+
+    Raises FAError on any non-OK status.  Asynchronous on ``stream`` (default: the
+    current torch stream), which the results that are not given belong to (see
+    ``forward``).
+    """
+    import torch
+    B, W = _paged_table(cache, table)
+    args = cache.args(q.dtype)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or shape[3] != args.D or shape[1] % args.key_heads or 0 in shape:
+        raise ValueError(f"q must be [{B}, a multiple of {args.key_heads}, Nq, {args.D}]")
+    H, Nq = shape[1], shape[2]
+    sb, sh, sn, last = q.stride()
+    if last != 1:
+        raise ValueError("q's last dimension must be contiguous")
+    if q.get_device() != cache.device:
+        raise ValueError("q must be on the cache's device")
+    if out is not None and (out.shape != shape or out.dtype != q.dtype or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, of q's shape and type")
+    if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [B, H, Nq]")
+    at = _ints(lens, B, "lens")
+    nbytes = _paged_workspace(cache.device, args.pages, args.key_heads, args.page, args.D, args.bits, W, B, H, Nq)
+    with _on(stream, q):
+        out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = _workspace(nbytes, q)
+    rc = load().fa_paged_fwd(q.data_ptr(), sb, sh, sn, args, table.data_ptr(), W, at, out.data_ptr(),
+                             lse.data_ptr(), B, H, Nq, args.D ** -0.5 if scale is None else scale,
+                             ws.data_ptr() if nbytes else None, nbytes, _stream_of(stream, q))
+    if rc != 0:
+        raise FAError(rc, "fa_paged_fwd")
+    return out, lse
 
 
 # ---- the 4-bit key/value cache

@@ -420,6 +420,72 @@ FA_API fa_status fa_packed_bwd(const fa_rows *q, const fa_rows *k, const fa_rows
                                size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * ---- A paged key/value cache ----
+ *
+ * K and V of many sequences in two pools of pages, [pages, Hkv, page, D] each:
+ * token t of sequence b is row t % page of page table[b, t / page].  `page` is a
+ * power of two, 16 to 1024.  With `bits` 16 the rows are of `dtype`; with 8 a row x
+ * is held as e4m3 codes and one float32 scale per token and key head, k_scale and
+ * v_scale [pages, Hkv, page]:
+ *   scale = max_d |x_d| / 448,  code_d = e4m3(x_d / scale), 0 if scale = 0
+ * (quotients in float32, rounded to nearest even), and stands for code * scale: D +
+ * 4 bytes for 2 D, values off by at most 2^-4 of themselves or 2^-10 of a scale,
+ * but for float32's roundings.  A row that holds an infinity or NaN stands for NaN
+ * or 0 where it is finite.
+ *
+ * table [B, width], lens, start [B] and cu [B + 1] are int32, device memory, read
+ * there, so a captured graph follows their changes.  lens are clamped to [0, width *
+ * page].  Tokens whose page lies outside the pool or the table do not exist: they
+ * are not written, read as zeros, and seen by no query.  Sequences may share
+ * pages; what two of one call's tokens leave in the same row is one of the two.
+ *
+ * Arguments: contiguous tensors unless strides are given, 16-byte aligned (table,
+ * lens, start, cu, LSE: 4); B * width, width * page, B * H * Nq and tokens * Hkv at
+ * most 2^31 - 65536, Hkv at most 65535; D = 64 or 128.  Outputs overlap no other
+ * argument.  Errors as for fa_fwd, nothing enqueued on any of them.  The calls
+ * allocate nothing and keep nothing between calls; calls that may overlap take
+ * different workspaces.
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;   /* 8 bits; else ignored */
+    int pages, key_heads, page, D, bits;
+    fa_dtype dtype;             /* of the values: k, v, Q, O (and the rows at 16 bits) */
+} fa_pages;
+
+/*
+ * fa_paged_append -- write packed tokens k, v [tokens, Hkv, D] into the cache:
+ * those of sequence b are rows cu[b] .. cu[b + 1] - 1 and become its tokens
+ * start[b] and on.  cu NULL: one token for each sequence (tokens = B).  Rows of no
+ * sequence are not read.
+ * fa_paged_read -- the values that those tokens of the cache stand for, rounded
+ * once to the type, into k, v; zeros for rows of no sequence.
+ */
+FA_API fa_status fa_paged_append(const fa_pages *cache, const int *table, int width, int B, const fa_rows *k,
+                                 const fa_rows *v, int tokens, const int *start, const int *cu, fa_stream_t stream);
+FA_API fa_status fa_paged_read(const fa_pages *cache, const int *table, int width, int B, const fa_rows *k,
+                               const fa_rows *v, int tokens, const int *start, const int *cu, fa_stream_t stream);
+
+/*
+ * fa_paged_fwd -- attention of each sequence's last Nq tokens against the cache's
+ * first lens[b] tokens (theirs among them): query i of a sequence sees the tokens
+ * j <= lens[b] - Nq + i; one that sees none gets O = 0 and LSE = -inf.
+ *
+ * Q : [B, H, Nq, D], its strides in elements given (multiples of 8, at least D, but
+ *     for dimensions of one); H a multiple of Hkv.  O : [B, H, Nq, D] and LSE :
+ *     [B, H, Nq] float32, contiguous.
+ * Values of hidden tokens must be finite where a query of the same sequence sees
+ * them; rows behind a sequence's last token may hold anything.
+ * workspace : at least fa_paged_workspace bytes (0 for short caches; NULL is then
+ * fine); its contents need no set-up.
+ */
+FA_API fa_status fa_paged_workspace(const fa_pages *cache, int width, int B, int H, int Nq, size_t *bytes);
+FA_API fa_status fa_paged_fwd(const void *Q, long long q_batch, long long q_head, long long q_token,
+                              const fa_pages *cache, const int *table, int width, const int *lens, void *O, float *LSE,
+                              int B, int H, int Nq, float scale, void *workspace, size_t workspace_bytes,
+                              fa_stream_t stream);
+
+/*
  * ---- A key/value cache held in 4 bits ----
  *
  * A cache holds, for K and for V, one packed row per token and key head:
