@@ -287,14 +287,14 @@ bool queries_ok(const fa_pages *c, int B, int H, int Nq)
            (long long)B * H * Nq <= fa_host::kMaxRows;
 }
 
-// Row blocks of 16 that share a CTA: 1, 2 or 4.
-int blocks_per_cta(int rows)
+// Query rows of a tile, which a CTA's warps share out: 8 or 16 to a warp.
+int tile_rows_for(int rows)
 {
-    return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 struct Shape {
-    int nrb, RB, cluster, grid;
+    int tile_rows, RB, cluster, grid;
     size_t bytes;   // workspace
 };
 
@@ -302,10 +302,10 @@ Shape shape_of(const fa_pages *c, int B, int H, int Nq, int W, int sms)
 {
     Shape s{};
     const int rows = (H / c->key_heads) * Nq;
-    s.nrb = blocks_per_cta(rows);
-    s.RB = (rows + 16 * s.nrb - 1) / (16 * s.nrb);
+    s.tile_rows = tile_rows_for(rows);
+    s.RB = (rows + s.tile_rows - 1) / s.tile_rows;
     const long long tiles = (long long)B * c->key_heads * s.RB, tokens = (long long)W * c->page;
-    const int room = 2 * sms;
+    const int room = fa_launch::paged_ctas(c->D, c->bits, s.tile_rows) * sms;
     int cl = 1;
     while (cl < 8 && tiles * cl * 2 <= room && (long long)cl * 2 * paged::kUnit <= tokens)
         cl *= 2;
@@ -315,7 +315,7 @@ Shape shape_of(const fa_pages *c, int B, int H, int Nq, int W, int sms)
         return s;
     }
     s.grid = room;
-    s.bytes = (size_t)2 * room * 16 * s.nrb * (c->D * sizeof(float) + sizeof(float2));
+    s.bytes = (size_t)2 * room * s.tile_rows * (c->D * sizeof(float) + sizeof(float2));
     return s;
 }
 
@@ -409,19 +409,19 @@ extern "C" fa_status fa_paged_fwd(const void *Q, long long q_batch, long long q_
     p.cluster = sh.cluster;
     if (!sh.cluster) {
         p.part_o = static_cast<float *>(workspace);
-        p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * sh.grid * 16 * sh.nrb * D);
+        p.part_ml = reinterpret_cast<float2 *>(p.part_o + (size_t)2 * sh.grid * sh.tile_rows * D);
     }
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = cache->dtype == FA_BF16;
-    return cache->bits == 16 ? fa_launch::launch_paged(p, D, bf16, sh.nrb, sh.grid, s, dev)
-                             : fa_launch::launch_paged_e4m3(p, D, bf16, sh.nrb, sh.grid, s, dev);
+    return cache->bits == 16 ? fa_launch::launch_paged(p, D, bf16, sh.tile_rows, sh.grid, s, dev)
+                             : fa_launch::launch_paged_e4m3(p, D, bf16, sh.tile_rows, sh.grid, s, dev);
 }
 
 namespace fa_launch {
 
-fa_status launch_paged(const fa::paged::Params &p, int D, bool bf16, int nrb, int grid, cudaStream_t s, int dev)
+fa_status launch_paged(const fa::paged::Params &p, int D, bool bf16, int tile_rows, int grid, cudaStream_t s, int dev)
 {
-    return launch_paged_bits<16>(p, D, bf16, nrb, grid, s, dev);
+    return launch_paged_bits<16>(p, D, bf16, tile_rows, grid, s, dev);
 }
 
 }  // namespace fa_launch

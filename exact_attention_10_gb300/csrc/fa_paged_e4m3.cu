@@ -3,9 +3,9 @@
 
 namespace fa_launch {
 
-fa_status launch_paged_e4m3(const fa::paged::Params &p, int D, bool bf16, int nrb, int grid, cudaStream_t s, int dev)
+fa_status launch_paged_e4m3(const fa::paged::Params &p, int D, bool bf16, int tile_rows, int grid, cudaStream_t s, int dev)
 {
-    return launch_paged_bits<8>(p, D, bf16, nrb, grid, s, dev);
+    return launch_paged_bits<8>(p, D, bf16, tile_rows, grid, s, dev);
 }
 
 }  // namespace fa_launch

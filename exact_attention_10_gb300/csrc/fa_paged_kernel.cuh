@@ -17,16 +17,21 @@
 // key head of decoding.  So the rows go from global memory straight into the
 // fragments of mma.sync, without shared memory, ldmatrix or transposes through
 // it: the order of the channels in a product is free as long as both operands
-// have the same, so a lane's 16 bytes of a K row are the B fragments of its
-// column (two products, four at 8 bits), and 16 bytes of four V rows, paired by
-// token with byte permutes, those of eight channels (sixteen).  16 query rows are
-// the M of one product; tcgen05's 128 would be eight times a decode step's rows.
-// Up to four blocks of 16 rows share a CTA, whose warps read the same rows of the
-// cache through L1.
+// have the same, so a lane's 16 bytes of two K rows are an A fragment of S^T = K
+// Q^T (16 tokens x 16 channels; 8 bits: two), and 16 bytes of four V rows, paired
+// by token with byte permutes, those of O^T += V^T P^T for eight channels (8 bits:
+// sixteen); P^T, the scores' accumulator, becomes its B operand by movmatrix.  The
+// query rows are the N of the products, 8 to a tile: tcgen05's M = 128 rows, or
+// even mma.sync's 16, are more than most decode steps have.  (With the query rows
+// as M, 16 at a time, the same kernel took 150 us for 64 sequences of 1001 to 8192
+// tokens in bf16 and 215 us for 32 of 4001 to 32768 in e4m3: twice the products and
+// accumulators, and half the warps.)  More than 16 rows come in blocks of 16, up to
+// four to a CTA, whose warps read the same rows of the cache through L1.
 //
-// A warp takes 16 tokens at a time, which lie in one page; the next 16 tokens' K
-// is on its way while V is used, and the other way round, so eight warps per SM
-// hold 64 KB in flight (an SM's share of HBM's bandwidth takes 36 KB at 0.8 us).
+// A warp takes 16 tokens at a time, which lie in one page; the next ones' K is on
+// its way while V is used, and the other way round, and all warps of an SM together
+// have more in flight than the 36 KB that its share of HBM's bandwidth takes at 0.8
+// us of latency.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,7 +51,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kStep = 16;      // tokens a warp takes at a time
 constexpr int kUnit = 64;      // tokens per unit of work handed to the CTAs
 constexpr int kMinUnits = 4;   // units per CTA, at least
-constexpr int kRows = 16;      // query rows of a block
 constexpr float kLn2f = 0.69314718055994530942f;
 // A query row's weights are relative to a reference that is set to its maximum
 // less kLift and moves only when a weight exceeds 2^(kLift + kSlack): most steps
@@ -70,6 +74,12 @@ struct Params {
     float *part_o;               // shares: [2 grid][rows of a CTA block][D] and (m, l)
     float2 *part_ml;
 };
+
+// Steps that a warp holds in registers, on their way or in use, and CTAs per SM.
+template <int D, int BITS>
+constexpr int kDepth = D * BITS == 64 * 8 ? 2 : 1;
+template <int D, int BITS, int NT>
+constexpr int kCtas = NT == 1 ? (BITS == 8 || D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -140,11 +150,12 @@ __device__ __forceinline__ uint2 ld8(const void *p)
     return v;
 }
 
-__device__ __forceinline__ float2 ldf2(const float *p)
+// Transpose of an 8 x 8 matrix of 16-bit values held row-wise by the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
-    float2 v;
-    asm volatile("ld.global.nc.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
-    return v;
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // ------------------------------------------------------------------ work decomposition
@@ -217,13 +228,13 @@ __device__ inline Where locate(const Params &p, int k, int grid)
 
 // ------------------------------------------------------------------ one warp's attention
 
-// D channels in BITS; channel of accumulator j (of D / 8) and column 2c + e.
+// Channel of row lane / 4 (e = 0) or lane / 4 + 8 (e = 1) of accumulator tile j (of D / 16).
 template <int D, int BITS>
-__device__ __forceinline__ int channel(int j, int c, int e)
+__device__ __forceinline__ int channel(int j, int r, int e)
 {
     if (BITS == 16)
-        return 64 * (j / 8) + 16 * c + 8 * e + j % 8;
-    return (D / 8) * (2 * c + e) + j;
+        return 64 * (j / 4) + 8 * r + 2 * (j % 4) + e;
+    return (D / 8) * r + 2 * j + e;
 }
 
 // 16 tokens of the cache in registers.
@@ -233,7 +244,7 @@ struct Tokens {
     uint4 k[2][kKey];            // row lane / 4 (+ 8), chunks lane % 4 + 4 j
     static constexpr int kVal = BITS == 16 ? D / 64 : 1;        // 16 (D = 64, 8 bits: 8) bytes of each of four V rows
     uint4 v[4][kVal];            // rows 2c, 2c + 1, 2c + 8, 2c + 9, chunk lane / 4 + 8 j
-    float2 ks[2], vs[2];         // 8 bits: scales of tokens 2c, 2c + 1 (+ 8)
+    float ks[2], vs[2];          // 8 bits: scales of tokens lane / 4 and + 8
 
     static constexpr int kRowBytes = D * BITS / 8;
 
@@ -247,8 +258,8 @@ struct Tokens {
             for (int j = 0; j < kKey; ++j)
                 k[n][j] = ld16<SHARED>(at + n * 8 * kRowBytes + j * 64);
         if (BITS == 8) {
-            ks[0] = ldf2(p.ks + row + 2 * (lane % 4));
-            ks[1] = ldf2(p.ks + row + 2 * (lane % 4) + 8);
+            ks[0] = __ldg(p.ks + row + lane / 4);
+            ks[1] = __ldg(p.ks + row + lane / 4 + 8);
         }
     }
 
@@ -269,8 +280,8 @@ struct Tokens {
             }
         }
         if (BITS == 8) {
-            vs[0] = ldf2(p.vs + row + 2 * (lane % 4));
-            vs[1] = ldf2(p.vs + row + 2 * (lane % 4) + 8);
+            vs[0] = __ldg(p.vs + row + lane / 4);
+            vs[1] = __ldg(p.vs + row + lane / 4 + 8);
         }
     }
 
@@ -284,9 +295,13 @@ struct Tokens {
 #pragma unroll
                 for (int j = 0; j < kVal; ++j)
                     v[i][j] = make_uint4(0u, 0u, 0u, 0u);
-                if (BITS == 8)
-                    (i & 1 ? vs[i / 2].y : vs[i / 2].x) = 0.f;
             }
+        }
+        if (BITS == 8) {
+            if (lane / 4 >= n)
+                vs[0] = 0.f;
+            if (lane / 4 + 8 >= n)
+                vs[1] = 0.f;
         }
     }
 };
@@ -296,23 +311,23 @@ __device__ __forceinline__ uint32_t word(const uint4 &x, int i)
     return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
 }
 
-// The query rows of a block as A fragments, in the order of K's channels.  At 8
+// NT tiles of 8 query rows as B fragments, in the order of K's channels.  At 8
 // bits they are fp16: a row is multiplied by the power of two that brings its
 // largest element to [2^14, 2^15), so an element is exact unless it is 2^-24 of
 // the largest or less, and then off by 2^-40 of it; `mul` takes it out again.
-template <int D, bool BF16, int BITS>
+template <int D, bool BF16, int BITS, int NT>
 struct Queries {
-    uint32_t a[D / 16][4];
-    float mul[2];   // rows lane / 4 and lane / 4 + 8: from a product to log2 units
+    uint32_t b[NT][D / 16][2];
+    float mul[NT][2];   // rows 8 nt + 2c and + 1: from a product to log2 units
 
-    __device__ __forceinline__ void load(const Params &p, int b, int h, int r0, int lane)
+    __device__ __forceinline__ void load(const Params &p, int seq, int h, int r0, int lane)
     {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = r0 + lane / 4 + 8 * e;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = r0 + 8 * nt + lane / 4;
             const bool real = row < p.rows;
             const int g = real ? row / p.Nq : 0, i = real ? row - g * p.Nq : 0;
-            const uint16_t *src = p.q + b * p.q_b + ((long long)h * p.G + g) * p.q_h + i * p.q_n;
+            const uint16_t *src = p.q + seq * p.q_b + ((long long)h * p.G + g) * p.q_h + i * p.q_n;
             uint4 x[D / 32];
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
@@ -320,7 +335,7 @@ struct Queries {
                 const int ch = BITS == 16 ? 8 * (lane % 4 + 4 * j) : 16 * (lane % 4 + 4 * (j / 2)) + 8 * (j & 1);
                 x[j] = real ? *reinterpret_cast<const uint4 *>(src + ch) : make_uint4(0u, 0u, 0u, 0u);
             }
-            mul[e] = p.qk2;
+            float back = p.qk2;   // of this lane's row
             if (BITS == 8) {
                 float f[D / 4], top = 0.f;
 #pragma unroll
@@ -343,7 +358,7 @@ struct Queries {
                 int ex = (int)(__float_as_uint(top) >> 23) - 127;
                 ex = ex < -100 ? -100 : (ex > 127 ? 127 : ex);
                 const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-                mul[e] = p.qk2 * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+                back = p.qk2 * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
                     x[j] = make_uint4(pack<false>(f[8 * j] * up, f[8 * j + 1] * up), pack<false>(f[8 * j + 2] * up, f[8 * j + 3] * up),
@@ -352,153 +367,171 @@ struct Queries {
             }
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
-                a[2 * j][e] = x[j].x;
-                a[2 * j][e + 2] = x[j].y;
-                a[2 * j + 1][e] = x[j].z;
-                a[2 * j + 1][e + 2] = x[j].w;
+                b[nt][2 * j][0] = x[j].x;
+                b[nt][2 * j][1] = x[j].y;
+                b[nt][2 * j + 1][0] = x[j].z;
+                b[nt][2 * j + 1][1] = x[j].w;
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                mul[nt][e] = BITS == 8 ? __shfl_sync(0xffffffffu, back, 4 * (2 * (lane % 4) + e)) : back;
         }
     }
 };
 
-template <int D, bool BF16, int BITS>
+template <int D, bool BF16, int BITS, int NT>
 struct Attend {
     static constexpr bool MB = BF16 && BITS == 16;   // products in bf16 (8 bits: codes are fp16 numbers)
-    float o[D / 8][4];
-    float m[2], l[2];   // rows lane / 4, + 8; l of this lane's tokens
+    float o[NT][D / 16][4];     // O^T: channels of row lane / 4, query rows 2c, 2c + 1; of row lane / 4 + 8
+    float m[NT][2], l[NT][2];   // rows 8 nt + 2c, + 1; l of this lane's tokens
 
     __device__ __forceinline__ void reset()
     {
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[j][i] = 0.f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
-    }
-
-    // Scores of the 16 tokens in log2 units: s[n][0, 1] row lane / 4, tokens 8 n + 2c, + 1; s[n][2, 3] row + 8.
-    __device__ __forceinline__ void scores(const Tokens<D, BITS> &t, const Queries<D, BF16, BITS> &q, float (&s)[2][4])
-    {
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                uint32_t b0, b1;
-                if (BITS == 16) {
-                    b0 = word(t.k[n][j / 2], 2 * (j & 1));
-                    b1 = word(t.k[n][j / 2], 2 * (j & 1) + 1);
-                } else {
-                    const uint32_t w = word(t.k[n][j / 4], j % 4);
-                    b0 = from_e4m3(w);
-                    b1 = from_e4m3(w >> 16);
-                }
-                mma<MB>(s[n], q.a[j][0], q.a[j][1], q.a[j][2], q.a[j][3], b0, b1);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[n][i] *= q.mul[i / 2];
-                if (BITS == 8)
-                    s[n][i] *= (i & 1) ? t.ks[n].y : t.ks[n].x;
-            }
+                for (int i = 0; i < 4; ++i)
+                    o[nt][j][i] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
         }
     }
 
-    // Scores to weights: `hi`: tokens of the 16 that the rows lane / 4 and + 8 see (MASKED).
+    // Scores of the 16 tokens in log2 units: s[nt][0, 1] token lane / 4, rows 2c, 2c + 1; s[nt][2, 3] token lane / 4 + 8.
+    __device__ __forceinline__ void scores(const Tokens<D, BITS> &t, const Queries<D, BF16, BITS, NT> &q, float (&s)[NT][4])
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            uint32_t a[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (BITS == 16) {
+                    a[n] = word(t.k[n][j / 2], 2 * (j & 1));
+                    a[n + 2] = word(t.k[n][j / 2], 2 * (j & 1) + 1);
+                } else {
+                    const uint32_t w = word(t.k[n][j / 4], j % 4);
+                    a[n] = from_e4m3(w);
+                    a[n + 2] = from_e4m3(w >> 16);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma<MB>(s[nt], a[0], a[1], a[2], a[3], q.b[nt][j][0], q.b[nt][j][1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[nt][i] *= q.mul[nt][i & 1];
+                if (BITS == 8)
+                    s[nt][i] *= t.ks[i / 2];
+            }
+    }
+
+    // Scores to weights, the operand's (times V's scale).  `hi`: tokens of the 16 that rows 8 nt + 2c and + 1 see (MASKED).
     template <bool MASKED>
-    __device__ __forceinline__ void weights(const Tokens<D, BITS> &t, float (&s)[2][4], const int (&hi)[2], int lane)
+    __device__ __forceinline__ void weights(const Tokens<D, BITS> &t, float (&s)[NT][4], const int (&hi)[NT][2], int lane)
     {
         // 8 bits: the reference is that of p vs, the operand (its logarithm kept where
         // sums of p do not overflow: scales of 2^-80 and more are weighed in full).
-        float lv[2][2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (MASKED && 8 * n + 2 * (lane % 4) + (i & 1) >= hi[i / 2])
-                    s[n][i] = -INFINITY;
-            }
-        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                lv[n][e] = 0.f;
-                if (BITS == 8)
-                    lv[n][e] = fminf(fmaxf(lg2(e ? t.vs[n].y : t.vs[n].x), -80.f), 120.f);
-                top[0] = fmaxf(top[0], s[n][e] + lv[n][e]);
-                top[1] = fmaxf(top[1], s[n][2 + e] + lv[n][e]);
-            }
-        if (__any_sync(0xffffffffu, top[0] > m[0] + (kLift + kSlack) || top[1] > m[1] + (kLift + kSlack))) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = top[e];
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                const float up = fmaxf(m[e], x - kLift);
-                const float f = m[e] == -INFINITY ? 0.f : ex2(m[e] - up);
-                m[e] = up;
-                l[e] *= f;
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][2 * e] *= f;
-                    o[j][2 * e + 1] *= f;
-                }
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float ref = m[e] == -INFINITY ? 0.f : m[e];
+        float lv[2] = {0.f, 0.f};
+        if (BITS == 8) {
 #pragma unroll
             for (int n = 0; n < 2; ++n)
+                lv[n] = fminf(fmaxf(lg2(t.vs[n]), -80.f), 120.f);
+        }
+        bool up = false;
+        float top[NT][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float w = ex2(s[n][2 * e + i] - ref);
-                    l[e] += w;
-                    s[n][2 * e + i] = BITS == 8 ? w * (i ? t.vs[n].y : t.vs[n].x) : w;
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (MASKED && lane / 4 + 8 * (i / 2) >= hi[nt][i & 1])
+                    s[nt][i] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[nt][e] = fmaxf(s[nt][e] + lv[0], s[nt][2 + e] + lv[1]);
+                up |= top[nt][e] > m[nt][e] + (kLift + kSlack);
+            }
+        }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = top[nt][e];
+#pragma unroll
+                    for (int k = 4; k < 32; k *= 2)
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+                    const float now = fmaxf(m[nt][e], x - kLift);
+                    const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - now);
+                    m[nt][e] = now;
+                    l[nt][e] *= f;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[nt][j][e] *= f;
+                        o[nt][j][2 + e] *= f;
+                    }
                 }
         }
-    }
-
-    // O += P V, the weights rounded to 16 bits for the product (fp16 at 8 bits).
-    __device__ __forceinline__ void add(const Tokens<D, BITS> &t, const float (&s)[2][4])
-    {
-        const uint32_t a0 = pack<MB>(s[0][0], s[0][1]), a1 = pack<MB>(s[0][2], s[0][3]);
-        const uint32_t a2 = pack<MB>(s[1][0], s[1][1]), a3 = pack<MB>(s[1][2], s[1][3]);
-        if (BITS == 16) {
 #pragma unroll
-            for (int j = 0; j < D / 8; j += 2) {
-                const uint32_t x0 = word(t.v[0][j / 8], (j % 8) / 2), x1 = word(t.v[1][j / 8], (j % 8) / 2);
-                const uint32_t y0 = word(t.v[2][j / 8], (j % 8) / 2), y1 = word(t.v[3][j / 8], (j % 8) / 2);
-                mma<MB>(o[j], a0, a1, a2, a3, __byte_perm(x0, x1, 0x5410), __byte_perm(y0, y1, 0x5410));
-                mma<MB>(o[j + 1], a0, a1, a2, a3, __byte_perm(x0, x1, 0x7632), __byte_perm(y0, y1, 0x7632));
-            }
-        } else {
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < D / 8; j += 4) {
-                const uint32_t x0 = word(t.v[0][0], j / 4), x1 = word(t.v[1][0], j / 4);
-                const uint32_t y0 = word(t.v[2][0], j / 4), y1 = word(t.v[3][0], j / 4);
+            for (int e = 0; e < 2; ++e) {
+                const float ref = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const uint32_t x = __byte_perm(x0, x1, i ? 0x7362 : 0x5140), y = __byte_perm(y0, y1, i ? 0x7362 : 0x5140);
-                    mma<MB>(o[j + i], a0, a1, a2, a3, from_e4m3(x), from_e4m3(y));
-                    mma<MB>(o[j + i + 1], a0, a1, a2, a3, from_e4m3(x >> 16), from_e4m3(y >> 16));
+                for (int n = 0; n < 2; ++n) {
+                    const float w = ex2(s[nt][2 * n + e] - ref);
+                    l[nt][e] += w;
+                    s[nt][2 * n + e] = BITS == 8 ? w * t.vs[n] : w;
                 }
             }
+    }
+
+    // O^T += V^T P^T, the weights rounded to 16 bits for the product (fp16 at 8 bits).
+    __device__ __forceinline__ void add(const Tokens<D, BITS> &t, const float (&s)[NT][4])
+    {
+        uint32_t b[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            b[nt][0] = transpose8(pack<MB>(s[nt][0], s[nt][1]));
+            b[nt][1] = transpose8(pack<MB>(s[nt][2], s[nt][3]));
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            uint32_t a[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {   // tokens 2c, 2c + 1; then 2c + 8, 2c + 9
+                if (BITS == 16) {
+                    const uint32_t x = word(t.v[2 * n][j / 4], j % 4), y = word(t.v[2 * n + 1][j / 4], j % 4);
+                    a[2 * n] = __byte_perm(x, y, 0x5410);
+                    a[2 * n + 1] = __byte_perm(x, y, 0x7632);
+                } else {
+                    const uint32_t x = __byte_perm(word(t.v[2 * n][0], j / 2), word(t.v[2 * n + 1][0], j / 2), j & 1 ? 0x7362 : 0x5140);
+                    a[2 * n] = from_e4m3(x);
+                    a[2 * n + 1] = from_e4m3(x >> 16);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma<MB>(o[nt][j], a[0], a[1], a[2], a[3], b[nt][0], b[nt][1]);
         }
     }
 };
 
 // ------------------------------------------------------------------ the kernels
 
-// Shared memory of a CTA: per warp its rows' O and (m, l); then the joined ones.
-template <int D>
+// Shared memory of a CTA: per warp its rows' O and (m, l).
+template <int D, int NT>
 struct Smem {
     static constexpr int kRow = D + 4;
-    static constexpr int kO = kWarps * kRows * kRow * 4;
-    static constexpr int kBytes = kO + kWarps * kRows * 8;
+    static constexpr int kO = kWarps * 8 * NT * kRow * 4;
+    static constexpr int kBytes = kO + kWarps * 8 * NT * 8;
 };
 
 // Write channels [ch, ch + 4) of row `row` of a key head's rows (query head, token).
@@ -554,9 +587,10 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t a)
 }
 
 // Steps [s0, s1) of 16 tokens of one tile by a warp: s0, s0 + stride, ...
-template <int D, bool BF16, int BITS, bool SHARED>
-__device__ __forceinline__ void run_steps(const Params &p, Attend<D, BF16, BITS> &a, const Queries<D, BF16, BITS> &q, int b,
-                                          int h, int len, const int (&hi)[2], int edge, int s0, int s1, int stride)
+template <int D, bool BF16, int BITS, int NT, bool SHARED>
+__device__ __forceinline__ void run_steps(const Params &p, Attend<D, BF16, BITS, NT> &a,
+                                          const Queries<D, BF16, BITS, NT> &q, int b, int h, int len,
+                                          const int (&hi)[NT][2], int edge, int s0, int s1, int stride)
 {
     const int lane = threadIdx.x % 32;
     const int *pages = p.table + (long long)b * p.W;
@@ -572,41 +606,57 @@ __device__ __forceinline__ void run_steps(const Params &p, Attend<D, BF16, BITS>
         return (((long long)id * p.Hkv + h) << p.page_bits) + ((s * kStep) & mask);
     };
     int ids = page_of(s0 + lane * stride), next = page_of(s0 + (32 + lane) * stride);
-    Tokens<D, BITS> t;
-    int id = __shfl_sync(0xffffffffu, ids, 0);
-    if (id >= 0) {
-        const long long row = row_of(id, s0);
-        t.template load_k<SHARED>(p, row, lane);
-        t.template load_v<SHARED>(p, row, lane);
-    }
-    int i = 0;
-    for (int s = s0; s < s1; s += stride) {
-        if (++i == 32) {
-            i = 0;
+    int at = 0;   // lane of `ids` that has the page of the step to load
+    auto next_id = [&](int s) -> int {   // of step s, steps in turn (-1 behind the last)
+        if (at == 32) {
+            at = 0;
             ids = next;
-            next = page_of(s + (33 + lane) * stride);
+            next = page_of(s + (32 + lane) * stride);
         }
-        const int id1 = __shfl_sync(0xffffffffu, ids, i);   // (-1 behind the last)
-        const long long row1 = row_of(id1, s + stride);
-        if (id >= 0) {   // tokens of a page outside the pool are hidden
-            float sc[2][4];
-            a.scores(t, q, sc);
-            if (id1 >= 0)
-                t.template load_k<SHARED>(p, row1, lane);
-            if (s * kStep + kStep > edge) {
-                const int at[2] = {hi[0] - s * kStep, hi[1] - s * kStep};
-                t.cut_v(len - s * kStep, lane);
-                a.template weights<true>(t, sc, at, lane);
-            } else {
-                a.template weights<false>(t, sc, hi, lane);
+        return __shfl_sync(0xffffffffu, ids, at++);
+    };
+    constexpr int N = kDepth<D, BITS>;
+    Tokens<D, BITS> t[N];
+    int id[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        id[i] = next_id(s0 + i * stride);
+        if (id[i] >= 0) {
+            const long long row = row_of(id[i], s0 + i * stride);
+            t[i].template load_k<SHARED>(p, row, lane);
+            t[i].template load_v<SHARED>(p, row, lane);
+        }
+    }
+    for (int s = s0; s < s1;) {
+#pragma unroll
+        for (int i = 0; i < N; ++i, s += stride) {
+            const int id1 = next_id(s + N * stride);
+            const long long row1 = row_of(id1, s + N * stride);
+            if (id[i] >= 0) {   // (tokens of a page outside the pool are hidden; behind the last step there is none)
+                float sc[NT][4];
+                a.scores(t[i], q, sc);
+                if (id1 >= 0)
+                    t[i].template load_k<SHARED>(p, row1, lane);
+                if (s * kStep + kStep > edge) {
+                    int see[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        see[nt][0] = hi[nt][0] - s * kStep;
+                        see[nt][1] = hi[nt][1] - s * kStep;
+                    }
+                    t[i].cut_v(len - s * kStep, lane);
+                    a.template weights<true>(t[i], sc, see, lane);
+                } else {
+                    a.template weights<false>(t[i], sc, hi, lane);
+                }
+                a.add(t[i], sc);
+            } else if (id1 >= 0) {
+                t[i].template load_k<SHARED>(p, row1, lane);
             }
-            a.add(t, sc);
-        } else if (id1 >= 0) {
-            t.template load_k<SHARED>(p, row1, lane);
+            if (id1 >= 0)
+                t[i].template load_v<SHARED>(p, row1, lane);
+            id[i] = id1;
         }
-        if (id1 >= 0)
-            t.template load_v<SHARED>(p, row1, lane);
-        id = id1;
     }
 }
 
@@ -616,11 +666,12 @@ __device__ __forceinline__ void run_steps(const Params &p, Attend<D, BF16, BITS>
 // tiles, so every CTA reads the same number of tokens whatever the lengths are; a
 // tile's first and last share may be partial (slots 2c, 2c + 1), which
 // merge_kernel joins.  The warps of a CTA take its tokens in turn, NRB of them at
-// a time the same ones for different blocks of 16 query rows.
-template <int D, bool BF16, int BITS, int NRB>
-__global__ void __launch_bounds__(kThreads, 2) attend_kernel(const __grid_constant__ Params p)
+// a time the same ones for different blocks of 8 NT query rows.
+template <int D, bool BF16, int BITS, int NT, int NRB>
+__global__ void __launch_bounds__(kThreads, kCtas<D, BITS, NT>) attend_kernel(const __grid_constant__ Params p)
 {
-    using S = Smem<D>;
+    constexpr int kRows = 8 * NT;   // query rows of a warp
+    using S = Smem<D, NT>;
     extern __shared__ __align__(16) uint8_t smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -663,36 +714,36 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const __grid_consta
         const int nrows = min(p.rows - r0, kRows * NRB);
         const int w0 = r0 + rb * kRows;   // this warp's rows
 
-        Attend<D, BF16, BITS> a;
+        Attend<D, BF16, BITS, NT> a;
         a.reset();
         if (w0 < p.rows) {
-            Queries<D, BF16, BITS> q;
+            Queries<D, BF16, BITS, NT> q;
             q.load(p, b, h, w0, lane);
-            int hi[2], edge = len;   // tokens the rows see; those before `edge` are seen by all
+            int hi[NT][2], edge = len;   // tokens the rows see; those before `edge` are seen by all
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = min(w0 + lane / 4 + 8 * e, p.rows - 1);
-                hi[e] = max(len - p.Nq + row % p.Nq + 1, 0);
-                edge = min(edge, hi[e]);
+            for (int i = 0; i < 2 * NT; ++i) {
+                const int row = min(w0 + 8 * (i / 2) + 2 * (lane % 4) + i % 2, p.rows - 1);
+                hi[i / 2][i % 2] = max(len - p.Nq + row % p.Nq + 1, 0);
+                edge = min(edge, hi[i / 2][i % 2]);
             }
             edge = __reduce_min_sync(0xffffffffu, edge);
             const int s1 = min(ke * (kUnit / kStep), (len + kStep - 1) / kStep);
-            run_steps<D, BF16, BITS, (NRB > 1)>(p, a, q, b, h, len, hi, edge, ku * (kUnit / kStep) + turn, s1, kGroups);
+            run_steps<D, BF16, BITS, NT, (NRB > 1)>(p, a, q, b, h, len, hi, edge, ku * (kUnit / kStep) + turn, s1, kGroups);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float l = a.l[e];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            const int row = warp * kRows + lane / 4 + 8 * e;
-            if (lane % 4 == 0)
-                all_ml[row] = make_float2(a.m[e], l);
+        for (int i = 0; i < 2 * NT; ++i) {
+            const int nt = i / 2, e = i % 2;
+            float l = a.l[nt][e];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int k = 4; k < 32; k *= 2)
+                l += __shfl_xor_sync(0xffffffffu, l, k);
+            const int row = warp * kRows + 8 * nt + 2 * (lane % 4) + e;
+            if (lane < 4)
+                all_ml[row] = make_float2(a.m[nt][e], l);
 #pragma unroll
-                for (int j = 0; j < D / 8; j += 4)   // four channels that follow one another
-                    *reinterpret_cast<float4 *>(all_o + row * S::kRow + channel<D, BITS>(j, lane % 4, c)) =
-                        make_float4(a.o[j][2 * e + c], a.o[j + 1][2 * e + c], a.o[j + 2][2 * e + c], a.o[j + 3][2 * e + c]);
+            for (int j = 0; j < D / 16; j += 2)   // four channels that follow one another
+                *reinterpret_cast<float4 *>(all_o + row * S::kRow + channel<D, BITS>(j, lane / 4, 0)) =
+                    make_float4(a.o[nt][j][e], a.o[nt][j][2 + e], a.o[nt][j + 1][e], a.o[nt][j + 1][2 + e]);
         }
         __syncthreads();
         // Join the warps; into warp `rb`'s place (a cluster), the results, or the parts.
@@ -700,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const __grid_consta
             const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
             if (row >= nrows)
                 continue;
-            const int at = row;   // of warp row / 16, the first of its block's
+            const int at = row;   // of warp row / kRows, the first of its block's
             float M = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kGroups; ++k)
@@ -769,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const __grid_consta
 // Joins the parts of the tiles that a share boundary cuts: block k looks at the
 // boundary between CTAs k and k + 1 and, if it is the first one inside its tile,
 // adds that tile's parts in order (so the result does not depend on which CTA
-// finished first).
-template <int D, bool BF16, int NRB>
+// finished first).  R: rows of a tile.
+template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__ Params p, int grid)
 {
     const int k = blockIdx.x;
@@ -787,7 +838,6 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
     if (t0 == edge || start > t0)   // not inside a tile, or not its first boundary
         return;
     const long long last = (t1 * G - 1) / U;   // CTA holding unit t1 - 1: the largest x with U x / G < t1
-    constexpr int R = kRows * NRB;
     const int h = hr / p.RB, r0 = (hr - h * p.RB) * R;
     const int nrows = min(p.rows - r0, R);
     const long long slot0 = 2 * k + (start == t0 ? 0 : 1);   // CTA k's part: its only one, or its last
