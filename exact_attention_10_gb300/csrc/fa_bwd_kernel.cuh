@@ -135,6 +135,7 @@ struct SinkParams : Params {
 // of the pass, N is the tokens, Npad the rows of the statistics per head.
 struct PackedParams : Params {
     const int4 *header, *list;
+    const int *order;
     int H, group;           // query heads, and those per key head
     int heads;              // of a tile: H (dQ pass) or H / group (KV)
     int causal;
@@ -145,19 +146,6 @@ template <class P>
 constexpr bool kPackedPass = false;
 template <>
 constexpr bool kPackedPass<PackedParams> = true;
-
-// Work tiles of the pass.
-template <bool KV>
-__device__ __forceinline__ int work_tiles(const Params &p)
-{
-    return p.T;
-}
-template <bool KV>
-__device__ __forceinline__ int work_tiles(const PackedParams &p)
-{
-    const int4 h = ld_plan(p.header);
-    return (KV ? h.z : h.y) * p.heads;
-}
 
 template <class P>
 constexpr bool kSinkPass = false;
@@ -565,6 +553,23 @@ __device__ __forceinline__ int bwd_tile(int r, int c, int G)
     return r * G + ((r & 1) ? G - 1 - c : c);
 }
 
+// This CTA's tile of round r into t; false: there is none.
+template <bool KV>
+__device__ __forceinline__ bool work_tile(const Params &p, int r, int &t)
+{
+    t = bwd_tile(r, blockIdx.x, gridDim.x);
+    return t < p.T;
+}
+
+template <bool KV>
+__device__ __forceinline__ bool work_tile(const PackedParams &p, int r, int &t)
+{
+    const int4 h = ld_plan(p.header);
+    const int T = (KV ? h.z : h.y) * p.heads;
+    t = packed_tile(p.order, r, blockIdx.x, gridDim.x, T);
+    return t < T;
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
@@ -695,14 +700,46 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
     using C = BCfg<D, KV, FQ>;
     int step = 0, tiles = 0;
     bool ok = true;
+    // Step j of the work into the next stage (rings of pairs).
+    auto load_step = [&](const auto &wk, int j) -> bool {
+        const int row = wk.tile(j) * kTile, bh = wk.head(j);
+        const int st = step % C::kStages;
+        const uint32_t use = (uint32_t)(step / C::kStages);
+        if (!warp_wait(b.empty(st), (use & 1u) ^ 1u, c, kSiteBwdSlotEmpty))
+            return false;
+        if (ptx::elect_one()) {
+            const uint32_t dst = sStage + st * C::kStageBytes;
+            ptx::mbar_arrive_expect_tx(b.full(st), C::kStageBytes);
+            for (int x = 0; x < C::kBoxes; ++x) {
+                bwd_box<!KV>(dst + x * C::kBoxBytes, tmS0, b.full(st), x * 64, row, bh, p, wk);
+                bwd_box<!KV>(dst + C::kTileBytes + x * C::kBoxBytes, tmS1, b.full(st), x * 64, row, bh, p, wk);
+            }
+            if (KV) {   // the query tile's lg and delta: 512 bytes each, 16-byte aligned (Npad % 128 == 0)
+                size_t off = (size_t)bh * p.Npad + row;
+                if constexpr (kPackedPass<P>)
+                    off = (size_t)bh * p.Npad + (size_t)wk.qtile(wk.tile(j)) * kTile;
+                ptx::bulk_load(dst + 2 * C::kTileBytes, p.lg + off, kTile * 4, b.full(st));
+                ptx::bulk_load(dst + 2 * C::kTileBytes + kTile * 4, p.dl + off, kTile * 4, b.full(st));
+            }
+        }
+        __syncwarp();
+        ++step;
+        return true;
+    };
     for (int r = 0; ok; ++r) {
-        const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= work_tiles<KV>(p))
+        int t;
+        if (!work_tile<KV>(p, r, t))
             break;
         const auto wk = bwd_work<KV>(p, causal, t);
         const int n = wk.n;
         if (kSinkPass<P> && n == 0)
             continue;
+        // Packed sequences, whose tiles may be a few steps long: the first step's
+        // tiles load while the resident ones are still in use.
+        constexpr bool EARLY = kPackedPass<P> && !C::kSplitRing;
+        if (EARLY) {
+            if (!load_step(wk, 0)) { ok = false; break; }
+        }
         if (tiles > 0 && !warp_wait(b.res_empty(), (uint32_t)(tiles - 1) & 1u, c, kSiteBwdResEmpty))
             break;
         if (ptx::elect_one()) {
@@ -714,9 +751,9 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
         }
         __syncwarp();
         ++tiles;
-        for (int j = 0; j < n; ++j, ++step) {
-            const int row = wk.tile(j) * kTile, bh = wk.head(j);
+        for (int j = 0; j < n; ++j) {
             if (C::kSplitRing) {   // K into ring 0, V into ring 1, each on its own barriers
+                const int row = wk.tile(j) * kTile, bh = wk.head(j);
                 const int k0 = step % C::kRing0, k1 = step % C::kRing1;
                 if (!warp_wait(b.empty(k0), ((uint32_t)(step / C::kRing0) & 1u) ^ 1u, c, kSiteBwdSlotEmpty) ||
                     !warp_wait(b.empty1(k1), ((uint32_t)(step / C::kRing1) & 1u) ^ 1u, c, kSiteBwdSlotEmpty)) {
@@ -733,30 +770,13 @@ __device__ void bwd_load(const CUtensorMap *tmR0, const CUtensorMap *tmR1, const
                     }
                 }
                 __syncwarp();
+                ++step;
                 continue;
             }
-            const int st = step % C::kStages;
-            const uint32_t use = (uint32_t)(step / C::kStages);
-            if (!warp_wait(b.empty(st), (use & 1u) ^ 1u, c, kSiteBwdSlotEmpty)) {
+            if ((!EARLY || j > 0) && !load_step(wk, j)) {
                 ok = false;
                 break;
             }
-            if (ptx::elect_one()) {
-                const uint32_t dst = sStage + st * C::kStageBytes;
-                ptx::mbar_arrive_expect_tx(b.full(st), C::kStageBytes);
-                for (int x = 0; x < C::kBoxes; ++x) {
-                    bwd_box<!KV>(dst + x * C::kBoxBytes, tmS0, b.full(st), x * 64, row, bh, p, wk);
-                    bwd_box<!KV>(dst + C::kTileBytes + x * C::kBoxBytes, tmS1, b.full(st), x * 64, row, bh, p, wk);
-                }
-                if (KV) {   // the query tile's lg and delta: 512 bytes each, 16-byte aligned (Npad % 128 == 0)
-                    size_t off = (size_t)bh * p.Npad + row;
-                    if constexpr (kPackedPass<P>)
-                        off = (size_t)bh * p.Npad + (size_t)wk.qtile(wk.tile(j)) * kTile;
-                    ptx::bulk_load(dst + 2 * C::kTileBytes, p.lg + off, kTile * 4, b.full(st));
-                    ptx::bulk_load(dst + 2 * C::kTileBytes + kTile * 4, p.dl + off, kTile * 4, b.full(st));
-                }
-            }
-            __syncwarp();
         }
     }
     // Tail: every copy issued has landed (time-bounded), so no asynchronous
@@ -821,8 +841,8 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
     };
 
     for (int r = 0; ok; ++r) {
-        const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= work_tiles<KV>(p))
+        int t;
+        if (!work_tile<KV>(p, r, t))
             break;
         const auto wk = bwd_work<KV>(p, causal, t);
         const int n = wk.n;
@@ -954,8 +974,8 @@ __device__ void bwd_compute(const P &p, uint32_t tmem, uint32_t sStage, BBars<D,
     const uint64_t qk2 = ptx::f2_pack(p.qk2, p.qk2);
     int step = 0, tiles = 0;
     for (int r = 0;; ++r) {
-        const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= work_tiles<KV>(p))
+        int t;
+        if (!work_tile<KV>(p, r, t))
             break;
         const auto wk = bwd_work<KV>(p, CAUSAL, t);
         const int bh = wk.rh, rt = wk.rt, n = wk.n;
@@ -1163,8 +1183,8 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
     };
 
     for (int r = 0; ok; ++r) {
-        const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= work_tiles<KV>(p))
+        int t;
+        if (!work_tile<KV>(p, r, t))
             break;
         const auto wk = bwd_work<KV>(p, causal, t);
         const int n = wk.n;
@@ -1261,8 +1281,8 @@ __device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uin
     const uint64_t qk2 = ptx::f2_pack(p.qk2, p.qk2);
     int g = 0, tiles = 0;
     for (int r = 0;; ++r) {
-        const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= work_tiles<KV>(p))
+        int t;
+        if (!work_tile<KV>(p, r, t))
             break;
         const auto wk = bwd_work<KV>(p, CAUSAL, t);
         const int bh = wk.rh, rt = wk.rt, n = wk.n;
@@ -1451,8 +1471,8 @@ __device__ void bwd_mma_dq(const P &p, uint32_t sRes, uint32_t sDs, uint32_t tme
     int g = 0, tiles = 0;
     bool ok = true;
     for (int r = 0; ok; ++r) {
-        const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= work_tiles<true>(p))
+        int t;
+        if (!work_tile<true>(p, r, t))
             break;
         const auto wk = bwd_work<true>(p, CAUSAL, t);
         const int n = wk.n;
@@ -1529,8 +1549,8 @@ __device__ void bwd_dq_out(const CUtensorMap *tmDQ, const P &p, uint32_t tmem, u
     int g = 0;
     bool ok = true;
     for (int r = 0; ok; ++r) {
-        const int t = bwd_tile(r, blockIdx.x, gridDim.x);
-        if (t >= work_tiles<true>(p))
+        int t;
+        if (!work_tile<true>(p, r, t))
             break;
         const auto wk = bwd_work<true>(p, CAUSAL, t);
         const int n = wk.n;

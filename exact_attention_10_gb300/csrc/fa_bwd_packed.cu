@@ -37,22 +37,20 @@ fa_status launch_all(const PackedBwdLaunch &a, cudaStream_t s, int dev)
     p.H = a.z.H;
     p.group = a.z.H / a.z.Hkv;
     p.causal = a.causal;
-    auto blocks = [&](int list, int heads) {
-        const long long t = pk::capacity(a.z, list) * heads;
-        return (int)(t < a.sms ? t : a.sms);
-    };
     fa_status st;
     if (!fused) {   // dQ in a pass of its own
         p.list = plan + pk::list_word(a.z, 1);
+        p.order = reinterpret_cast<const int *>(plan + pk::order_word(a.z, 1));
         p.heads = a.z.H;
         p.dA = a.dq.ptr;
         p.a_row = a.dq.row * 2;
         p.a_head = a.dq.head * 2;
-        st = launch_pass<D, BF16, true, false, false, P>(a.tq, a.tdo, a.tk, a.tv, a.tq, p, blocks(1, a.z.H), s, dev);
+        st = launch_pass<D, BF16, true, false, false, P>(a.tq, a.tdo, a.tk, a.tv, a.tq, p, pk::grid(a.z, 1, a.sms), s, dev);
         if (st != FA_OK)
             return st;
     }
     p.list = plan + pk::list_word(a.z, 2);
+    p.order = reinterpret_cast<const int *>(plan + pk::order_word(a.z, 2));
     p.heads = a.z.Hkv;
     p.dA = a.dk.ptr;
     p.dB = a.dv.ptr;
@@ -60,7 +58,7 @@ fa_status launch_all(const PackedBwdLaunch &a, cudaStream_t s, int dev)
     p.a_head = a.dk.head * 2;
     p.b_row = a.dv.row * 2;
     p.b_head = a.dv.head * 2;
-    const int g = blocks(2, a.z.Hkv);
+    const int g = pk::grid(a.z, 2, a.sms);
     if constexpr (D == 64)
         st = fused ? launch_pass<D, BF16, true, true, true, P>(a.tk, a.tv, a.tq, a.tdo, a.tdqa, p, g, s, dev)
                    : launch_pass<D, BF16, true, true, false, P>(a.tk, a.tv, a.tq, a.tdo, a.tq, p, g, s, dev);

@@ -211,7 +211,7 @@ struct Cfg {
     // after everything else (the merge area, which whole-tile launches do not
     // have): moving the other barriers by their 32 bytes measured 4.6 %
     // slower on long causal calls at D = 128.
-    static constexpr int kVBarBytes = kSplitKV ? 16 * kStages : 0;
+    static constexpr int kVBarBytes = kSplitKV ? 16 * kStages + 16 : 0;   // (and the split Q buffer's two)
     __host__ __device__ static constexpr int vbar_off(bool split)
     {
         return split ? ((kJobOff + kJobSlots * (int)sizeof(MergeJob) + 7) & ~7) : kMiscOff + 16;
@@ -264,10 +264,12 @@ __device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, in
 {
     if constexpr (MASK == kMaskPacked) {
         static_assert(!SPLIT, "packed sequences run whole tiles");
-        if (it.t >= __ldg(s.count) * s.H)
+        const int T = __ldg(s.count) * s.H, t = packed_tile(s.order, it.u, it.c, s.G, T);
+        if (t >= T)
             return false;
-        const int e = (int)((uint32_t)it.t / (uint32_t)s.H);
-        bh = it.t - e * s.H;   // the query head
+        ++it.u;
+        const int e = (int)((uint32_t)t / (uint32_t)s.H);
+        bh = t - e * s.H;   // the query head
         const int4 seq = ld_plan(s.list + 2 * (size_t)e), at = ld_plan(s.list + 2 * (size_t)e + 1);
         tile.q0 = seq.x;
         tile.Lq = seq.y;
@@ -278,8 +280,6 @@ __device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, in
         tile.nw[1] = packed::key_steps(ct * kCtaRows + kBM, seq.y, seq.w, s.causal);
         pt.kb = 0;
         pt.ke = tile.nw[0] > tile.nw[1] ? tile.nw[0] : tile.nw[1];
-        ++it.u;
-        it.t = it.u * s.G + ((it.u & 1) ? s.G - 1 - it.c : it.c);
         return true;
     } else if constexpr (MASK == kMaskSink && !SPLIT) {
         return sched_next_whole(s, it, pt, bh, ct, tile);
@@ -325,6 +325,13 @@ __device__ __forceinline__ int key_head(const S &s, int bh)
     else
         return bh;
 }
+
+// At D = 128 there is one Q buffer.  Packed sequences, whose tiles may be a few
+// steps long, fill and release its two halves apart (Q tile 1's on barriers of its
+// own), so that the next tile's Q tile 0 loads during this one's last step, which
+// is Q tile 1's alone when causal.
+template <int D, int MASK>
+constexpr bool kSplitQ = MASK == kMaskPacked && Cfg<D>::kQBufs == 1;
 
 // Separate-P order (S_{j+1} issued while the softmax of step j runs): always
 // at D = 64; at D = 128 when no CTA tile has a second Q tile.
@@ -426,6 +433,9 @@ struct Bars {
     __device__ uint32_t empty(int s) const { return base + 8u * (Cfg<D>::kStages + s); }
     __device__ uint32_t v_full(int s) const { return vbase + 8u * s; }                          // split: V_j landed
     __device__ uint32_t v_empty(int s) const { return vbase + 8u * (Cfg<D>::kStages + s); }     // split: V_j read
+    // split Q (packed, D = 128): Q tile 1's half
+    __device__ uint32_t q1_full() const { return vbase + 8u * (2 * Cfg<D>::kStages); }
+    __device__ uint32_t q1_empty() const { return vbase + 8u * (2 * Cfg<D>::kStages + 1); }
     __device__ uint32_t q_full(int qb) const { return base + 8u * (2 * Cfg<D>::kStages + qb); }
     __device__ uint32_t q_empty(int qb) const { return base + 8u * (2 * Cfg<D>::kStages + Cfg<D>::kQBufs + qb); }
     __device__ uint32_t per_tile(int w, int k) const
@@ -494,6 +504,7 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
     using C = Cfg<D>;
     int step = 0;   // K/V stages filled so far (K halves when split)
     int it = 0;     // parts started by this CTA (one Q load each)
+    [[maybe_unused]] int it1 = 0;   // split Q: those with a Q tile 1
     int nv = 0;     // split: V halves filled so far; V of step nv is pending while nv < step
     int pv_bh = 0, pv_row = 0;   // ... its head and first key
     [[maybe_unused]] int pv_k0 = 0;   // ... packed: its sequence's first key row
@@ -519,6 +530,18 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
         ++nv;
         return true;
     };
+    [[maybe_unused]] auto load_q1 = [&](int bh, int ct, int q0) -> bool {
+        if (!warp_wait(b.q1_empty(), ((uint32_t)it1 & 1u) ^ 1u, c, kSiteLoadQEmpty))
+            return false;
+        if (ptx::elect_one()) {
+            ptx::mbar_arrive_expect_tx(b.q1_full(), C::kTileBytes);
+            for (int x = 0; x < C::kBoxes; ++x)
+                load_box<PACKED>(sQ + C::kTileBytes + x * C::kBoxBytes, tmQ, b.q1_full(), x * 64, ct * kCtaRows + kBM, bh, q0);
+        }
+        __syncwarp();
+        ++it1;
+        return true;
+    };
     PartIter parts;
     parts.init_t<SPLIT>(p.sch, blockIdx.x);
     Part pt;
@@ -533,8 +556,9 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
         if (!warp_wait(b.q_empty(qb), (quse & 1u) ^ 1u, c, kSiteLoadQEmpty)) { ok = false; break; }
         if (ptx::elect_one()) {
             const uint32_t dst = sQ + qb * C::kQBufBytes;
-            ptx::mbar_arrive_expect_tx(b.q_full(qb), kQTiles * C::kTileBytes);
-            for (int w = 0; w < kQTiles; ++w)
+            constexpr int kLoads = kSplitQ<D, MASK> ? 1 : kQTiles;
+            ptx::mbar_arrive_expect_tx(b.q_full(qb), kLoads * C::kTileBytes);
+            for (int w = 0; w < kLoads; ++w)
                 for (int x = 0; x < C::kBoxes; ++x) {
                     if constexpr (PACKED)
                         load_box<true>(dst + w * C::kTileBytes + x * C::kBoxBytes, tmQ, b.q_full(qb), x * 64,
@@ -574,6 +598,9 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
                     }
             }
             __syncwarp();
+            if constexpr (kSplitQ<D, MASK>) {   // Q tile 1 behind the first step's K and V, as mma_parts wants them
+                if (j == 0 && tile.nw[1] > 0 && !load_q1(bh, ct, tile.q0)) { ++step; ok = false; break; }
+            }
             if (SKV) {   // V of the previous step, then this step's V becomes the pending one
                 if (nv < step && !load_v()) { ++step; ok = false; break; }
                 pv_bh = kvh;
@@ -585,6 +612,13 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
     }
     if (SKV && ok && nv < step)   // the last step's V
         load_v();
+    if constexpr (kSplitQ<D, MASK>) {
+        if (it1 > 0) {
+            warp_wait(b.q1_full(), (uint32_t)(it1 - 1) & 1u, c, kSiteTail);
+            if (!*c.abort_flag)
+                warp_wait(b.q1_empty(), (uint32_t)(it1 - 1) & 1u, c, kSiteTail);
+        }
+    }
     // Tail: every copy issued has landed and (unless aborting) every stage and
     // the Q buffer have been released by the MMA warp, so no asynchronous
     // write or arrive targets this CTA's shared memory after exit.
@@ -826,6 +860,8 @@ __device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, B
     using C = Cfg<D>;
     const Bars<D> b = m.b;
     int step = 0, it = 0;   // K/V steps and parts so far
+    [[maybe_unused]] int it1 = 0;   // split Q: parts with a Q tile 1
+    constexpr bool SPLITQ = kSplitQ<D, MASK>;
     int prev = -1;          // stage of the step whose P.V (interleaved: Q tile 1's) is still to come, -1: none
     bool pv = false, acc = false, pfew = false;   // whether this warp's tile has that P.V, adds to O, and is of few sinks
     constexpr bool PACKED = MASK == kMaskPacked;
@@ -887,12 +923,25 @@ __device__ void mma_parts(const P &p, MmaIssuer<D, BF16, SEP> &m, MmaIssuer<D, B
             } else {
                 if (j < n0 && !m.issue_s(st, few))
                     return;
+                if (SPLITQ && j == n0 - 1) {
+                    if (ptx::elect_one())
+                        ptx::mma_commit(b.q_empty(qb));
+                    __syncwarp();
+                }
                 if (prev >= 0 && !finish())
                     return;
+                if (SPLITQ && j == 0 && n1 > 0) {
+                    if (!warp_wait(b.q1_full(), (uint32_t)it1 & 1u, m.c, kSiteMmaQFull))
+                        return;
+                    ptx::tc_fence_after_sync();
+                    ++it1;
+                }
                 if (j < n1 && !m1.issue_s(st, few))
                     return;
-                if (j == n - 1 && ptx::elect_one())
-                    ptx::mma_commit(b.q_empty(qb));
+                if (SPLITQ ? j == n1 - 1 : j == n - 1) {
+                    if (ptx::elect_one())
+                        ptx::mma_commit(SPLITQ ? b.q1_empty() : b.q_empty(qb));
+                }
                 __syncwarp();
                 if (PACKED)
                     zero_tail<D>(sV + (uint32_t)(st * C::kStageBytes), rows);
@@ -1762,6 +1811,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_init(b.v_full(s), 1);
                 ptx::mbar_init(b.v_empty(s), C::kMmaWarps);
             }
+        }
+        if (kSplitQ<D, MASK>) {
+            ptx::mbar_init(b.q1_full(), 1);
+            ptx::mbar_init(b.q1_empty(), 1);
         }
         for (int qb = 0; qb < C::kQBufs; ++qb) {
             ptx::mbar_init(b.q_full(qb), 1);

@@ -22,6 +22,7 @@ struct PlanParams {
     pk::Sizes z;
     int causal, lists;
     int4 *plan;
+    int grid[3];   // CTAs of the calls that walk each list
 };
 
 // Exclusive scan of one value per thread over the block (a sum, or a maximum
@@ -170,6 +171,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (l == 1)
             p.plan[pk::table_word(p.z) + e] = make_int4(q.x + i * pk::kTile, min(pk::kTile, q.y - i * pk::kTile), 0, 0);
     }
+    __syncthreads();
+    // The order: per round, rank the CTAs by what they have so far.  (Each tile
+    // costs about two steps more than its own: its first loads and last stores.)
+    __shared__ int load[pk::kOrderGrid];
+    int *order = reinterpret_cast<int *>(p.plan + pk::order_word(p.z, l));
+    const int G = p.grid[l], heads = l == 2 ? p.z.Hkv : p.z.H, mul = l == 2 ? p.z.H / p.z.Hkv : 1;
+    if (G > pk::kOrderGrid)
+        return;
+    int mine = 0;
+    for (int r = 0; r < pk::kOrderRounds && r * (long long)G < (long long)n * heads; ++r) {
+        if (t < G)
+            load[t] = mine;
+        __syncthreads();
+        if (t < G) {
+            int rank = 0;
+            for (int i = 0; i < G; ++i)
+                rank += load[i] < mine || (load[i] == mine && i < t);
+            const int x = r * G + rank;
+            const bool real = x < n * heads;
+            order[r * G + t] = real ? x : n * heads;
+            if (real) {
+                const int e = x / heads;
+                mine += cost(entries[2 * (size_t)e], entries[2 * (size_t)e + 1].x) * mul + 2;
+            }
+        }
+        __syncthreads();
+    }
 }
 
 // Sizes that every packed call checks: rows and padded rows within 32-bit indices.
@@ -304,7 +332,8 @@ extern "C" fa_status fa_packed_plan(const int *cu_q, const int *cu_k, const fa_p
     const fa_status st = fa_host::check_args(args, 3, &dev, &di);
     if (st != FA_OK)
         return st;
-    const PlanParams p{cu_q, cu_k, z, sizes->causal, grad ? 3 : 1, static_cast<int4 *>(plan)};
+    const PlanParams p{cu_q, cu_k, z, sizes->causal, grad ? 3 : 1, static_cast<int4 *>(plan),
+                       {pk::grid(z, 0, di->sms), pk::grid(z, 1, di->sms), pk::grid(z, 2, di->sms)}};
     plan_kernel<<<p.lists, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -346,8 +375,8 @@ extern "C" fa_status fa_packed_fwd(const fa_rows *q, const fa_rows *k, const fa_
     p.sch.group = z.H / z.Hkv;
     p.sch.count = static_cast<const int *>(plan);
     p.sch.list = static_cast<const int4 *>(plan) + pk::list_word(z, 0);
-    const long long tiles = pk::capacity(z, 0) * z.H;
-    p.sch.G = (int)(tiles < di->sms ? tiles : di->sms);
+    p.sch.order = reinterpret_cast<const int *>(static_cast<const int4 *>(plan) + pk::order_word(z, 0));
+    p.sch.G = pk::grid(z, 0, di->sms);
     return fa_launch::launch_mask<fa::kMaskPacked, false>(D, bf16, tq, tk, tv, p, p.sch.G,
                                                           reinterpret_cast<cudaStream_t>(stream), dev);
 }
