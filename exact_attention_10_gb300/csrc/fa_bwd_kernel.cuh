@@ -134,10 +134,9 @@ struct SinkParams : Params {
 // Packed sequences (fa_packed.h): tiles and lengths come from the plan's list
 // of the pass, N is the tokens, Npad the rows of the statistics per head.
 struct PackedParams : Params {
-    const int4 *header, *list;
-    const int *order;
-    int H, group;           // query heads, and those per key head
-    int heads;              // of a tile: H (dQ pass) or H / group (KV)
+    const int4 *slots;      // of the pass
+    int rounds;             // slots of a CTA
+    int group;              // query heads per key head
     int causal;
     long long a_row, a_head, b_row, b_head;   // bytes between rows and heads of dA and dB
 };
@@ -401,22 +400,42 @@ struct PackedWork {
     int rh, rt, n;
     int q0, Lq, k0, Lk;    // the sequence
     int qt0;               // its first query tile among all sequences'
-    int per, s0, group;    // KV: as in SinkWork; per = 0: the empty tile
+    int per, s0, group;    // KV: as in SinkWork
+    bool none;             // KV: no query sees the tile: one step with the empty query tile
     int empty;             // the empty query tile
-    __device__ int head(int j) const { return KV ? rh * group + (per ? j / per : 0) : rh / group; }
-    __device__ int tile(int j) const { return KV ? (per ? s0 + j % per : 0) : j; }
+    // Steps are asked for in turn, so head and tile follow without a division (in
+    // the MMA warp and the compute warps it cost 10 % of the fused pass): `first` is
+    // the first step of the head `hd`, counted from the group's first.
+    mutable int first, hd;
+    __device__ void seek(int j) const
+    {
+        if (KV && j - first >= per) {
+            first += per;
+            ++hd;
+        }
+    }
+    __device__ int head(int j) const
+    {
+        seek(j);
+        return KV ? rh * group + hd : rh / group;
+    }
+    __device__ int tile(int j) const
+    {
+        seek(j);
+        return KV ? s0 + j - first : j;
+    }
     __device__ int slot() const { return -1; }
     __device__ int rows(int j) const { return (KV ? Lq : Lk) - tile(j) * kTile; }   // of step j's tile (128 or more: all)
-    __device__ int qtile(int t) const { return KV && per == 0 ? empty : qt0 + t; }   // among all sequences', of tile t
+    __device__ int qtile(int t) const { return KV && none ? empty : qt0 + t; }   // among all sequences', of tile t
 };
 
 template <bool KV>
 __device__ __forceinline__ PackedWork<KV> bwd_work(const PackedParams &p, bool, int t)
 {
     PackedWork<KV> w;
-    const int e = (int)((uint32_t)t / (uint32_t)p.heads);
-    w.rh = t - e * p.heads;
-    const int4 seq = ld_plan(p.list + 2 * (size_t)e), at = ld_plan(p.list + 2 * (size_t)e + 1);
+    int4 seq, at;
+    packed_slot(p.slots, p.rounds, blockIdx.x, t, seq, at);
+    w.rh = at.z;
     w.q0 = seq.x;
     w.Lq = seq.y;
     w.k0 = seq.z;
@@ -424,15 +443,18 @@ __device__ __forceinline__ PackedWork<KV> bwd_work(const PackedParams &p, bool, 
     w.rt = at.x;
     w.qt0 = at.y;
     w.group = p.group;
-    w.empty = ld_plan(p.header).y;
-    w.per = w.s0 = 0;
+    w.empty = at.w - 1;
+    w.per = 1;
+    w.s0 = w.first = w.hd = 0;
+    w.none = false;
     if (KV) {
         const int s0 = packed::first_query_tile(w.rt, w.Lq, w.Lk, p.causal);
-        if (s0 >= 0) {
+        w.none = s0 < 0;
+        if (!w.none) {
             w.s0 = s0;
             w.per = (w.Lq + kTile - 1) / kTile - s0;
         }
-        w.n = w.per ? w.per * p.group : 1;
+        w.n = w.none ? 1 : w.per * p.group;
     } else {
         w.n = packed::key_steps(w.rt * kTile, w.Lq, w.Lk, p.causal);
     }
@@ -508,8 +530,8 @@ __device__ __forceinline__ StepMask work_mask(const P &p, const W &wk, bool caus
     if constexpr (kPackedPass<P>) {
         StepMask m{-1024, 1024, true};
         if (p.causal) {
-            const long long e = (long long)wk.Lk - wk.Lq - (long long)kTile * (kt - qt);
-            m.e_hi = (int)(e < -1024 ? -1024 : (e > 1024 ? 1024 : e));
+            const int e = (int)((uint32_t)(wk.Lk - wk.Lq) - (uint32_t)kTile * (uint32_t)(kt - qt));   // (within 32 bits)
+            m.e_hi = max(-1024, min(1024, e));
             m.whole = m.e_hi >= kTile - 1;
         }
         if (KV && wk.Lk - kt * kTile < kTile)
@@ -561,13 +583,13 @@ __device__ __forceinline__ bool work_tile(const Params &p, int r, int &t)
     return t < p.T;
 }
 
+// (packed: t is the round, whose slot holds the tile)
 template <bool KV>
 __device__ __forceinline__ bool work_tile(const PackedParams &p, int r, int &t)
 {
-    const int4 h = ld_plan(p.header);
-    const int T = (KV ? h.z : h.y) * p.heads;
-    t = packed_tile(p.order, r, blockIdx.x, gridDim.x, T);
-    return t < T;
+    int4 seq, at;
+    t = r;
+    return packed_slot(p.slots, p.rounds, blockIdx.x, r, seq, at);
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
@@ -670,26 +692,25 @@ __device__ __forceinline__ void bwd_box(uint32_t dst, const CUtensorMap *tm, uin
         load_box<false>(dst, tm, bar, x, row, head, 0);
 }
 
-// The rows behind its sequence in step j's pair of streamed tiles, global step g,
-// zeroed as far as the products over them go (packed::tail_ksteps), by the MMA
-// warp; and those products' k-steps.
-template <int D, bool KV, bool FQ = false, class P, class W>
-__device__ __forceinline__ void zero_streamed(const P &, const W &wk, int j, uint32_t sStage, int g)
+// What a pair of streamed tiles, global step g, holds behind its `rows` rows of
+// the sequence, zeroed as far as the products over them go (packed::tail_ksteps),
+// by the MMA warp; and step j's rows.
+template <int D, bool KV, bool FQ = false, class P>
+__device__ __forceinline__ void zero_streamed(const P &, int rows, uint32_t sStage, int g)
 {
     if constexpr (kPackedPass<P>) {
-        const int n = wk.rows(j);
-        zero_tail<D>(BCfg<D, KV, FQ>::slot0(sStage, g), n);
-        zero_tail<D>(BCfg<D, KV, FQ>::slot1(sStage, g), n);
+        zero_tail<D>(BCfg<D, KV, FQ>::slot0(sStage, g), rows);
+        zero_tail<D>(BCfg<D, KV, FQ>::slot1(sStage, g), rows);
     }
 }
 
 template <class P, class W>
-__device__ __forceinline__ int streamed_ksteps(const P &, const W &wk, int j)
+__device__ __forceinline__ int streamed_rows(const P &, const W &wk, int j)
 {
     if constexpr (kPackedPass<P>)
-        return packed::tail_ksteps(wk.rows(j));
+        return wk.rows(j);
     else
-        return kTile / 16;
+        return kTile;
 }
 
 template <int D, bool KV, bool FQ, class P>
@@ -853,7 +874,8 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
         ptx::tc_fence_after_sync();
         if (!stage_ready(g))
             break;
-        zero_streamed<D, KV>(p, wk, 0, sStage, g);
+        int rows = streamed_rows(p, wk, 0);
+        zero_streamed<D, KV>(p, rows, sStage, g);
         issue_sd(g, r0_lo, 0u, tS, b.sd_full());
         issue_sd(g, r1_lo, (uint32_t)C::kTileBytes, tDP, b.dp_full());
         for (int j = 0; j < n; ++j, ++g) {
@@ -875,7 +897,7 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
             const uint32_t sa = sStage + (uint32_t)(st * C::kStageBytes);
             const uint32_t m0_lo = desc_lo(sa + C::kTileBytes, C::kBoxBytes);   // dO
             const uint32_t m1_lo = desc_lo(sa, C::kBoxBytes);                   // Q
-            const int ks = streamed_ksteps(p, wk, j);
+            const int ks = packed::tail_ksteps(rows);
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
@@ -889,7 +911,8 @@ __device__ void bwd_mma(const P &p, bool causal, uint32_t sRes, uint32_t sStage,
                     ok = false;
                     break;
                 }
-                zero_streamed<D, KV>(p, wk, j + 1, sStage, g + 1);
+                rows = streamed_rows(p, wk, j + 1);
+                zero_streamed<D, KV>(p, rows, sStage, g + 1);
                 issue_sd(g + 1, r0_lo, 0u, tS, b.sd_full());
             }
             if (ptx::elect_one()) {
@@ -1193,17 +1216,20 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
         if (!warp_wait(b.res_full(), (uint32_t)tiles & 1u, c, kSiteBwdResFull))
             break;
         ptx::tc_fence_after_sync();
-        auto tails = [&](int js, int gs) {
-            return [&, js, gs]() { zero_streamed<D, KV, FQ>(p, wk, js, sStage, gs); };
+        int rows = streamed_rows(p, wk, 0), rows1 = kTile;
+        auto tails = [&](int n, int gs) {
+            return [&, n, gs]() { zero_streamed<D, KV, FQ>(p, n, sStage, gs); };
         };
         if constexpr (kPackedPass<P> && FQ) {   // the resident tiles' rows, which dQ sums over
             zero_tail<D>(sRes, wk.Lk - wk.rt * kTile);
             zero_tail<D>(sRes + C::kTileBytes, wk.Lk - wk.rt * kTile);
         }
-        if (!issue_sd(g, tails(0, g)))
+        if (!issue_sd(g, tails(rows, g)))
             break;
-        for (int j = 0; j < n; ++j, ++g) {
-            if (j + 1 < n && !issue_sd(g + 1, tails(j + 1, g + 1))) {
+        for (int j = 0; j < n; ++j, ++g, rows = rows1) {
+            if (j + 1 < n)
+                rows1 = streamed_rows(p, wk, j + 1);
+            if (j + 1 < n && !issue_sd(g + 1, tails(rows1, g + 1))) {
                 ok = false;
                 break;
             }
@@ -1228,7 +1254,7 @@ __device__ void bwd_mma_pipe(const P &p, bool causal, uint32_t sRes, uint32_t sS
             const uint32_t m1_lo = desc_lo(C::slot0(sStage, g), C::kBoxBytes);                               // KV: Q
             const uint32_t tA0 = tmem + (KV ? C::kColP : C::kColDS + 64u * (uint32_t)(g & 1));
             const uint32_t tA1 = tmem + C::kColDS;
-            const int ks = streamed_ksteps(p, wk, j);
+            const int ks = packed::tail_ksteps(rows);
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)

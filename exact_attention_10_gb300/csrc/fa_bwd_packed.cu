@@ -33,15 +33,12 @@ fa_status launch_all(const PackedBwdLaunch &a, cudaStream_t s, int dev)
     p.BH = a.z.H;
     p.qk2 = a.scale * 1.4426950408889634f;
     p.scale = a.scale;
-    p.header = plan;
-    p.H = a.z.H;
     p.group = a.z.H / a.z.Hkv;
     p.causal = a.causal;
     fa_status st;
     if (!fused) {   // dQ in a pass of its own
-        p.list = plan + pk::list_word(a.z, 1);
-        p.order = reinterpret_cast<const int *>(plan + pk::order_word(a.z, 1));
-        p.heads = a.z.H;
+        p.slots = plan + pk::list_word(a.z, 1);
+        p.rounds = pk::rounds(a.z, 1, pk::grid(a.z, 1, a.sms));
         p.dA = a.dq.ptr;
         p.a_row = a.dq.row * 2;
         p.a_head = a.dq.head * 2;
@@ -49,9 +46,8 @@ fa_status launch_all(const PackedBwdLaunch &a, cudaStream_t s, int dev)
         if (st != FA_OK)
             return st;
     }
-    p.list = plan + pk::list_word(a.z, 2);
-    p.order = reinterpret_cast<const int *>(plan + pk::order_word(a.z, 2));
-    p.heads = a.z.Hkv;
+    p.slots = plan + pk::list_word(a.z, 2);
+    p.rounds = pk::rounds(a.z, 2, pk::grid(a.z, 2, a.sms));
     p.dA = a.dk.ptr;
     p.dB = a.dv.ptr;
     p.a_row = a.dk.row * 2;

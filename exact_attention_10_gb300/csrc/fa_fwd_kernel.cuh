@@ -264,13 +264,11 @@ __device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, in
 {
     if constexpr (MASK == kMaskPacked) {
         static_assert(!SPLIT, "packed sequences run whole tiles");
-        const int T = __ldg(s.count) * s.H, t = packed_tile(s.order, it.u, it.c, s.G, T);
-        if (t >= T)
+        int4 seq, at;
+        if (!packed_slot(s.slots, s.rounds, it.c, it.u, seq, at))
             return false;
         ++it.u;
-        const int e = (int)((uint32_t)t / (uint32_t)s.H);
-        bh = t - e * s.H;   // the query head
-        const int4 seq = ld_plan(s.list + 2 * (size_t)e), at = ld_plan(s.list + 2 * (size_t)e + 1);
+        bh = at.z;   // the query head
         tile.q0 = seq.x;
         tile.Lq = seq.y;
         tile.k0 = seq.z;

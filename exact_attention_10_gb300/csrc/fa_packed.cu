@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __shared__ int scratch[kPlanWarps];
     __shared__ int hist[kBuckets];
     const int l = blockIdx.x, t = threadIdx.x, S = p.z.S;
-    int4 *entries = p.plan + pk::list_word(p.z, l);
+    int4 *entries = p.plan + pk::entry_word(p.z, l);
     int4 *seqs = p.plan + pk::scratch_word(p.z, l);   // two words a sequence: {q0, Lq, k0, Lk}, {first entry, first query tile}
     const int tile = l == 0 ? 2 * pk::kTile : pk::kTile;
 
@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             b = b1;
         }
     }
-    int n;
-    int at = block_scan<false>(nt, scratch, n), qt = block_scan<false>(nq, scratch, total);
+    int n, total_q;   // entries of the list, query tiles in all
+    int at = block_scan<false>(nt, scratch, n), qt = block_scan<false>(nq, scratch, total_q);
     for (int s = s0; s < s1; ++s) {
         const int4 q = seqs[2 * (size_t)s];
         seqs[2 * (size_t)s + 1] = make_int4(at, qt, 0, 0);
@@ -172,15 +172,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             p.plan[pk::table_word(p.z) + e] = make_int4(q.x + i * pk::kTile, min(pk::kTile, q.y - i * pk::kTile), 0, 0);
     }
     __syncthreads();
-    // The order: per round, rank the CTAs by what they have so far.  (Each tile
+    // The slots: per round, rank the CTAs by what they have so far.  (Each tile
     // costs about two steps more than its own: its first loads and last stores.)
     __shared__ int load[pk::kOrderGrid];
-    int *order = reinterpret_cast<int *>(p.plan + pk::order_word(p.z, l));
-    const int G = p.grid[l], heads = l == 2 ? p.z.Hkv : p.z.H, mul = l == 2 ? p.z.H / p.z.Hkv : 1;
-    if (G > pk::kOrderGrid)
-        return;
+    int4 *slots = p.plan + pk::list_word(p.z, l);
+    const int G = p.grid[l], R = pk::rounds(p.z, l, G), heads = pk::heads_of(p.z, l), mul = l == 2 ? p.z.H / p.z.Hkv : 1;
+    const int T = n * heads;
+    auto fill = [&](int c, int r, int x) -> int {   // CTA c's tile of round r is tile x; its cost
+        int4 *at = slots + 2 * ((long long)c * R + r);
+        if (x >= T) {
+            at[1] = make_int4(0, 0, 0, 0);
+            return 0;
+        }
+        const int e = x / heads;
+        const int4 q = entries[2 * (size_t)e], w = entries[2 * (size_t)e + 1];
+        at[0] = q;
+        at[1] = make_int4(w.x, w.y, x - e * heads, total_q + 1);
+        return cost(q, w.x) * mul + 2;
+    };
     int mine = 0;
-    for (int r = 0; r < pk::kOrderRounds && r * (long long)G < (long long)n * heads; ++r) {
+    for (int r = 0; r < pk::kOrderRounds && r < R; ++r) {
         if (t < G)
             load[t] = mine;
         __syncthreads();
@@ -188,15 +199,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             int rank = 0;
             for (int i = 0; i < G; ++i)
                 rank += load[i] < mine || (load[i] == mine && i < t);
-            const int x = r * G + rank;
-            const bool real = x < n * heads;
-            order[r * G + t] = real ? x : n * heads;
-            if (real) {
-                const int e = x / heads;
-                mine += cost(entries[2 * (size_t)e], entries[2 * (size_t)e + 1].x) * mul + 2;
-            }
+            mine += fill(t, r, r * G + rank);
         }
         __syncthreads();
+    }
+    for (long long x = (long long)pk::kOrderRounds * G + t; x < (long long)R * G; x += kPlanThreads) {
+        const int r = (int)(x / G), i = (int)(x - (long long)r * G);
+        fill((r & 1) ? G - 1 - i : i, r, x < T ? (int)x : T);
     }
 }
 
@@ -371,12 +380,10 @@ extern "C" fa_status fa_packed_fwd(const fa_rows *q, const fa_rows *k, const fa_
     p.o_head = r[3].head * 2;
     p.wide = ((reinterpret_cast<uintptr_t>(o->ptr) | (uintptr_t)p.o_row | (uintptr_t)p.o_head) & 31u) == 0;
     p.sch.causal = sizes->causal;
-    p.sch.H = z.H;
     p.sch.group = z.H / z.Hkv;
-    p.sch.count = static_cast<const int *>(plan);
-    p.sch.list = static_cast<const int4 *>(plan) + pk::list_word(z, 0);
-    p.sch.order = reinterpret_cast<const int *>(static_cast<const int4 *>(plan) + pk::order_word(z, 0));
+    p.sch.slots = static_cast<const int4 *>(plan) + pk::list_word(z, 0);
     p.sch.G = pk::grid(z, 0, di->sms);
+    p.sch.rounds = pk::rounds(z, 0, p.sch.G);
     return fa_launch::launch_mask<fa::kMaskPacked, false>(D, bf16, tq, tk, tv, p, p.sch.G,
                                                           reinterpret_cast<cudaStream_t>(stream), dev);
 }

@@ -9,21 +9,24 @@
 //   list 0  forward: CTA tiles of 256 query rows
 //   list 1  dQ pass and the rows' statistics: query tiles of 128 rows
 //   list 2  dK/dV pass: key tiles of 128 rows
-// -- of which entry e's heads are tiles e * heads .. e * heads + heads - 1.  The
-// persistent CTAs take a tile each in rounds: of a round's tiles the longest goes
-// to the CTA whose tiles so far are the fewest steps, for kOrderRounds rounds that
-// the plan lays out (`order`), and then in serpentine order.  (Serpentine rounds
-// alone leave the busiest of 152 CTAs 16 % above the mean in the dK/dV pass of 6
-// documents of 500 to 8001 tokens, 572 tiles; so laid out, 5 %.)  The list is as
-// long as the sequences make it; its length is in the plan's header, and its room
-// is bounded by the token counts.
+// -- an entry of which is a tile of one sequence, and a tile of work one of its
+// heads.  The persistent CTAs take a tile each in rounds: of a round's tiles the
+// longest goes to the CTA whose tiles so far are the fewest steps, for kOrderRounds
+// rounds, and then in serpentine order.  (Serpentine rounds alone leave the busiest
+// of 152 CTAs 16 % above the mean in the dK/dV pass of 6 documents of 500 to 8001
+// tokens, 572 tiles; so laid out, 5 %.)
 //
-// Plan layout, in 16-byte words: a header {n0, n1, n2, 0}, then per list its
-// entries (two words: {q0, Lq, k0, Lk}, {tile, first query tile of the
-// sequence, 0, 0}), two scratch words per sequence and two more, and its order;
-// then list 1's table by query tile, {first row, rows, 0, 0}, in the sequences' order with one
-// empty tile behind the last (the dK/dV pass's step of a key tile that no query
-// sees).
+// What a role of the kernels needs of a tile is one slot of two words, {q0, Lq, k0,
+// Lk} and {tile, first query tile of the sequence, head, query tiles in all + 1},
+// the last 0 where there is none; a CTA's slots follow one another, so after the
+// first of four they are in L1.  (Looked up by way of order, entry and head, a tile
+// began 0.7 us later.)
+//
+// Plan layout, in 16-byte words: a header {n0, n1, n2, 0} of entries per list; per
+// list its slots, then scratch (its entries, longest first, and two words per
+// sequence and two more); then list 1's table by query tile, {first row, rows, 0,
+// 0}, in the sequences' order with one empty tile behind the last (the dK/dV pass's
+// step of a key tile that no query sees).
 #pragma once
 
 #include <cstddef>
@@ -40,8 +43,7 @@ namespace packed {
 
 constexpr int kTile = 128;
 constexpr int kOrderRounds = 16;
-constexpr int kOrderGrid = kSchedMaxGrid;                       // CTAs that an order is laid out for, at most
-constexpr int kOrderWords = kOrderRounds * kOrderGrid / 4;
+constexpr int kOrderGrid = kSchedMaxGrid;   // CTAs, at most
 
 struct Sizes {
     int S, Tq, Tk, H, Hkv;
@@ -52,24 +54,29 @@ FA_HD long long capacity(const Sizes &z, int l)
 {
     return (l == 0 ? z.Tq / 256 : l == 1 ? z.Tq / kTile : z.Tk / kTile) + (long long)z.S;
 }
-FA_HD long long list_word(const Sizes &z, int l)   // first word of list l
+FA_HD int heads_of(const Sizes &z, int l) { return l == 2 ? z.Hkv : z.H; }
+// Slots that list l has room for (CTAs' rounds are as many for all of them).
+FA_HD long long slots(const Sizes &z, int l) { return capacity(z, l) * heads_of(z, l) + kOrderGrid; }
+FA_HD long long list_word(const Sizes &z, int l)   // first word of list l: its slots
 {
     long long w = 1;
     for (int i = 0; i < l; ++i)
-        w += 2 * (capacity(z, i) + z.S + 1) + kOrderWords;
+        w += 2 * (slots(z, i) + capacity(z, i) + z.S + 1);
     return w;
 }
-FA_HD long long scratch_word(const Sizes &z, int l) { return list_word(z, l) + 2 * capacity(z, l); }
-FA_HD long long order_word(const Sizes &z, int l) { return scratch_word(z, l) + 2 * (z.S + 1ll); }
+FA_HD long long entry_word(const Sizes &z, int l) { return list_word(z, l) + 2 * slots(z, l); }
+FA_HD long long scratch_word(const Sizes &z, int l) { return entry_word(z, l) + 2 * capacity(z, l); }
 FA_HD long long table_word(const Sizes &z) { return list_word(z, 3); }
 // Words of a plan for the forward alone, or for both directions.
 FA_HD long long plan_words(const Sizes &z, bool grad) { return grad ? table_word(z) + capacity(z, 1) + 1 : list_word(z, 1); }
-// CTAs that walk list l.
+// CTAs that walk list l, and the rounds that their slots have room for.
 FA_HD int grid(const Sizes &z, int l, int sms)
 {
-    const long long t = capacity(z, l) * (l == 2 ? z.Hkv : z.H);
-    return (int)(t < sms ? t : sms);
+    const long long t = capacity(z, l) * heads_of(z, l);
+    const int top = sms < kOrderGrid ? sms : kOrderGrid;
+    return (int)(t < top ? t : top);
 }
+FA_HD int rounds(const Sizes &z, int l, int G) { return (int)((capacity(z, l) * heads_of(z, l) + G - 1) / G); }
 // Rows of the backward's row statistics per head: a whole number of query tiles.
 FA_HD long long padded_rows(const Sizes &z) { return (capacity(z, 1) + 1) * kTile; }
 
@@ -119,10 +126,9 @@ FA_HD int tail_ksteps(int n)
 
 // The forward's schedule: list 0 of a plan.
 struct PackedSchedule : Schedule {
-    const int4 *list;
-    const int *count;   // entries
-    const int *order;
-    int H, group;       // query heads, and those per key head
+    const int4 *slots;
+    int rounds;         // slots of a CTA
+    int group;          // query heads per key head
 };
 
 struct PackedTile {
@@ -136,13 +142,15 @@ __device__ __forceinline__ int4 ld_plan(const int4 *p)
     return __ldg(p);
 }
 
-// Tile that CTA c of G takes in round r of a list's T tiles; T or more: none, now and later.
-__device__ __forceinline__ int packed_tile(const int *order, int r, int c, int G, int T)
+// CTA c's slot of round r; false: there is none.
+__device__ __forceinline__ bool packed_slot(const int4 *slots, int rounds, int c, int r, int4 &seq, int4 &at)
 {
-    if (r < packed::kOrderRounds && G <= packed::kOrderGrid)
-        return r * (long long)G < T ? __ldg(order + r * G + c) : T;
-    const long long t = (long long)r * G + ((r & 1) ? G - 1 - c : c);
-    return t < T ? (int)t : T;
+    if (r >= rounds)
+        return false;
+    const int4 *p = slots + 2 * ((long long)c * rounds + r);
+    seq = ld_plan(p);
+    at = ld_plan(p + 1);
+    return at.w != 0;
 }
 
 #endif

@@ -10,6 +10,7 @@
 #include "fa_host.h"
 #include "fa_paged_kernel.cuh"
 #include "fa_paged_launch.h"
+#include "sm103_ptx.cuh"
 
 namespace {
 
@@ -78,14 +79,65 @@ __device__ __forceinline__ uint32_t to_e4m3(float lo, float hi)
     return r;
 }
 
-// A group of D / 8 lanes per token and key head, 8 channels a lane, K and V both.
-// Memory bound: it reads 2 x 2 D bytes and writes as much or 2 x (D + 4).  At 8
-// bits scale = max |x| / 448 and code = e4m3(x / scale), each quotient rounded
-// once (a product with a reciprocal would move codes next to a border).
+// A group of D / 32 lanes per token and key head, four chunks of 8 channels a lane,
+// a group's chunks next to one another; K and V both, so eight loads are under way
+// a lane.  Memory bound: a row is read once and written once, 2 D bytes each, or D
+// + 4 at 8 bits.
+constexpr int kChunks = 4;
+
+// Codes of a lane's chunks at 8 bits: scale = max |x| / 448, code = e4m3(x / scale),
+// each quotient rounded once (a product with a reciprocal would move codes next to a
+// border).  A quotient is a product with the reciprocal of the scale corrected twice by
+// its residual, Markstein's division: the reciprocal is rounded correctly, so after the
+// first correction the quotient is off by less than a unit and after the second it is
+// rounded correctly, as long as the residual is exact -- which scales of 2^-60 to
+// 2^100 see to (a residual that counts is then above 2^-149); others divide.  (By
+// division alone, and with a quarter of the channels a lane, 8 prompts of 1000 to 8192
+// tokens took 63 us, by this XXX.)
+template <int D, bool BF16>
+__device__ __forceinline__ void quantise(const uint4 (&x)[kChunks], uint32_t group, uint2 (&codes)[kChunks], float &scale)
+{
+    uint32_t top = 0;   // largest magnitudes as 16-bit integers, in which their order is the same, NaN above all
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            top = __vmaxu2(top, paged::word(x[i], w) & 0x7fff7fffu);
+#pragma unroll
+    for (int m = 1; m < D / 32; m *= 2)
+        top = __vmaxu2(top, __shfl_xor_sync(group, top, m));
+    top = max(top & 0xffffu, top >> 16);
+    scale = __fdiv_rn(value<BF16>(top, 0), 448.f);
+    const bool normal = scale >= 8.673617e-19f && scale <= 1.2676506e30f;   // 2^-60, 2^100
+    const float inv = __frcp_rn(scale);
+    const uint64_t inv2 = fa::ptx::f2_pack(inv, inv), neg2 = fa::ptx::f2_pack(-scale, -scale);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        uint32_t c[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t u = paged::word(x[i], w);
+            float lo = value<BF16>(u, 0), hi = value<BF16>(u, 1);
+            if (normal) {
+                const uint64_t v = fa::ptx::f2_pack(lo, hi);
+                uint64_t q = fa::ptx::f2_mul(v, inv2);
+                q = fa::ptx::f2_fma(fa::ptx::f2_fma(q, neg2, v), inv2, q);
+                q = fa::ptx::f2_fma(fa::ptx::f2_fma(q, neg2, v), inv2, q);
+                fa::ptx::f2_unpack(q, lo, hi);
+            } else {
+                lo = scale == 0.f ? 0.f : __fdiv_rn(lo, scale);
+                hi = scale == 0.f ? 0.f : __fdiv_rn(hi, scale);
+            }
+            c[w] = to_e4m3(lo, hi);
+        }
+        codes[i] = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    }
+}
+
 template <int D, bool BF16, int BITS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ MoveParams p)
 {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / (8 * kChunks);
     const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long r = g / kLanes;
     const int part = (int)(g % kLanes), lane = threadIdx.x % 32;
@@ -95,38 +147,32 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const long long at = pool_row(p, i, h);
     if (at < 0)
         return;
-    const uint4 x[2] = {*reinterpret_cast<const uint4 *>(p.k.p + i * p.k.row + h * p.k.head + 16 * part),
-                        *reinterpret_cast<const uint4 *>(p.v.p + i * p.v.row + h * p.v.head + 16 * part)};
-    if (BITS == 16) {
-        *reinterpret_cast<uint4 *>(p.kp + at * (2 * D) + 16 * part) = x[0];
-        *reinterpret_cast<uint4 *>(p.vp + at * (2 * D) + 16 * part) = x[1];
-        return;
+    uint4 x[2][kChunks];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const Rows16 &t = n ? p.v : p.k;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+            x[n][c] = *reinterpret_cast<const uint4 *>(t.p + i * t.row + h * t.head + 16 * (part + kLanes * c));
     }
     const uint32_t group = ((1u << kLanes) - 1u) << (lane & ~(kLanes - 1));
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        float f[8], top = 0.f;
+        uint8_t *dst = (n ? p.vp : p.kp) + at * (D * BITS / 8);
+        if (BITS == 16) {
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            f[w] = value<BF16>(paged::word(x[n], w / 2), w & 1);
-            const float a = fabsf(f[w]);
-            top = a > top || a != a ? a : top;   // (a NaN stays)
-        }
+            for (int c = 0; c < kChunks; ++c)
+                *reinterpret_cast<uint4 *>(dst + 16 * (part + kLanes * c)) = x[n][c];
+        } else {
+            uint2 codes[kChunks];
+            float scale;
+            quantise<D, BF16>(x[n], group, codes, scale);
 #pragma unroll
-        for (int m = 1; m < kLanes; m *= 2) {
-            const float a = __shfl_xor_sync(group, top, m);
-            top = a > top || a != a ? a : top;
+            for (int c = 0; c < kChunks; ++c)
+                *reinterpret_cast<uint2 *>(dst + 8 * (part + kLanes * c)) = codes[c];
+            if (part == 0)
+                (n ? p.vs : p.ks)[at] = scale;
         }
-        const float scale = __fdiv_rn(top, 448.f);
-        uint32_t c[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float lo = scale == 0.f ? 0.f : __fdiv_rn(f[2 * w], scale), hi = scale == 0.f ? 0.f : __fdiv_rn(f[2 * w + 1], scale);
-            c[w] = to_e4m3(lo, hi);
-        }
-        *reinterpret_cast<uint2 *>((n ? p.vp : p.kp) + at * D + 8 * part) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-        if (part == 0)
-            (n ? p.vs : p.ks)[at] = scale;
     }
 }
 
@@ -134,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 template <int D, bool BF16, int BITS>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ MoveParams p)
 {
-    constexpr int kLanes = D / 8;
+    constexpr int kLanes = D / (8 * kChunks);
     const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long r = g / kLanes;
     const int part = (int)(g % kLanes);
@@ -142,28 +188,45 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
         return;
     const int i = (int)(r / p.Hkv), h = (int)(r - (long long)i * p.Hkv);
     const long long at = pool_row(p, i, h);
-    uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    uint4 x[2][kChunks] = {};
     if (at >= 0) {
+        uint2 codes[2][kChunks];
+        float scale[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const uint8_t *src = (n ? p.vp : p.kp) + at * (D * BITS / 8);
-            if (BITS == 16) {
-                x[n] = *reinterpret_cast<const uint4 *>(src + 16 * part);
-            } else {
-                const uint2 c = *reinterpret_cast<const uint2 *>(src + 8 * part);
-                const float scale = (n ? p.vs : p.ks)[at];
-                uint32_t o[4];
+            if (BITS == 8)
+                scale[n] = (n ? p.vs : p.ks)[at];
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t u = paged::from_e4m3(w < 2 ? c.x >> (16 * w) : c.y >> (16 * (w - 2)));
-                    o[w] = paged::pack<BF16>(value<false>(u, 0) * scale, value<false>(u, 1) * scale);
-                }
-                x[n] = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int c = 0; c < kChunks; ++c) {
+                if (BITS == 16)
+                    x[n][c] = *reinterpret_cast<const uint4 *>(src + 16 * (part + kLanes * c));
+                else
+                    codes[n][c] = *reinterpret_cast<const uint2 *>(src + 8 * (part + kLanes * c));
             }
         }
+        if (BITS == 8) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t u = paged::from_e4m3(w < 2 ? codes[n][c].x >> (16 * w) : codes[n][c].y >> (16 * (w - 2)));
+                        o[w] = paged::pack<BF16>(value<false>(u, 0) * scale[n], value<false>(u, 1) * scale[n]);
+                    }
+                    x[n][c] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+        }
     }
-    *reinterpret_cast<uint4 *>(p.k.p + i * p.k.row + h * p.k.head + 16 * part) = x[0];
-    *reinterpret_cast<uint4 *>(p.v.p + i * p.v.row + h * p.v.head + 16 * part) = x[1];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const Rows16 &t = n ? p.v : p.k;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+            *reinterpret_cast<uint4 *>(t.p + i * t.row + h * t.head + 16 * (part + kLanes * c)) = x[n][c];
+    }
 }
 
 // ------------------------------------------------------------------ checks
@@ -258,7 +321,7 @@ fa_status move(const fa_pages *c, const int *table, int W, int B, const fa_rows 
     p.W = W;
     p.P = c->pages;
     p.page_bits = bits;
-    const unsigned blocks = (unsigned)(((long long)tokens * Hkv * (D / 8) + kThreads - 1) / kThreads);
+    const unsigned blocks = (unsigned)(((long long)tokens * Hkv * (D / (8 * kChunks)) + kThreads - 1) / kThreads);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto run = [&](auto kern) {
         kern<<<blocks, kThreads, 0, s>>>(p);

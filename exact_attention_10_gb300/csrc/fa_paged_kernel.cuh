@@ -78,8 +78,13 @@ struct Params {
 // Steps that a warp holds in registers, on their way or in use, and CTAs per SM.
 template <int D, int BITS>
 constexpr int kDepth = D * BITS == 64 * 8 ? 2 : 1;
+// Where two tiles of query rows would leave room for two CTAs only, their fragments
+// are read from shared memory at every step (16 rows, D = 128, 16 bits: 250 registers
+// with them, and XXX us for 16 sequences of 2000 to 16384 tokens).
 template <int D, int BITS, int NT>
-constexpr int kCtas = NT == 1 ? (BITS == 8 || D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
+constexpr bool kSharedQ = NT == 2 && D == 128;
+template <int D, int BITS, int NT>
+constexpr int kCtas = NT == 1 ? (BITS == 8 || D == 64 ? 4 : 3) : 3;
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -318,6 +323,7 @@ __device__ __forceinline__ uint32_t word(const uint4 &x, int i)
 template <int D, bool BF16, int BITS, int NT>
 struct Queries {
     uint32_t b[NT][D / 16][2];
+    uint32_t shared;    // kSharedQ: this lane's fragments, 512 bytes a channel tile apart
     float mul[NT][2];   // rows 8 nt + 2c and + 1: from a product to log2 units
 
     __device__ __forceinline__ void load(const Params &p, int seq, int h, int r0, int lane)
@@ -377,6 +383,20 @@ struct Queries {
                 mul[nt][e] = BITS == 8 ? __shfl_sync(0xffffffffu, back, 4 * (2 * (lane % 4) + e)) : back;
         }
     }
+
+    // kSharedQ: from registers to shared memory (each warp its own).
+    __device__ __forceinline__ void share(uint32_t at, int lane)
+    {
+        shared = at + lane * 16;
+        if constexpr (NT == 2) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(shared + j * 512), "r"(b[0][j][0]),
+                             "r"(b[0][j][1]), "r"(b[1][j][0]), "r"(b[1][j][1])
+                             : "memory");
+        }
+        __syncwarp();
+    }
 };
 
 template <int D, bool BF16, int BITS, int NT>
@@ -419,9 +439,18 @@ struct Attend {
                     a[n + 2] = from_e4m3(w >> 16);
                 }
             }
+            if constexpr (kSharedQ<D, BITS, NT>) {
+                uint32_t b[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                             : "r"(q.shared + j * 512));
+                mma<MB>(s[0], a[0], a[1], a[2], a[3], b[0], b[1]);
+                mma<MB>(s[NT - 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+            } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                mma<MB>(s[nt], a[0], a[1], a[2], a[3], q.b[nt][j][0], q.b[nt][j][1]);
+                for (int nt = 0; nt < NT; ++nt)
+                    mma<MB>(s[nt], a[0], a[1], a[2], a[3], q.b[nt][j][0], q.b[nt][j][1]);
+            }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -531,7 +560,8 @@ template <int D, int NT>
 struct Smem {
     static constexpr int kRow = D + 4;
     static constexpr int kO = kWarps * 8 * NT * kRow * 4;
-    static constexpr int kBytes = kO + kWarps * 8 * NT * 8;
+    static constexpr int kQ = kO + kWarps * 8 * NT * 8;   // query fragments, per warp (kSharedQ)
+    static constexpr int kBytes = kQ + (NT == 2 && D == 128 ? kWarps * (D / 16) * 512 : 0);
 };
 
 // Write channels [ch, ch + 4) of row `row` of a key head's rows (query head, token).
@@ -719,6 +749,8 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, BITS, NT>) attend_kernel(co
         if (w0 < p.rows) {
             Queries<D, BF16, BITS, NT> q;
             q.load(p, b, h, w0, lane);
+            if constexpr (kSharedQ<D, BITS, NT>)
+                q.share((uint32_t)__cvta_generic_to_shared(smem) + S::kQ + warp * (D / 16) * 512, lane);
             int hi[NT][2], edge = len;   // tokens the rows see; those before `edge` are seen by all
 #pragma unroll
             for (int i = 0; i < 2 * NT; ++i) {
@@ -819,11 +851,20 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, BITS, NT>) attend_kernel(co
 
 // Joins the parts of the tiles that a share boundary cuts: block k looks at the
 // boundary between CTAs k and k + 1 and, if it is the first one inside its tile,
-// adds that tile's parts in order (so the result does not depend on which CTA
-// finished first).  R: rows of a tile.
+// adds that tile's parts in a fixed order (so the result does not depend on which
+// CTA finished first).  R: rows of a tile.  A tile of a long sequence has some tens
+// of parts: threads take four channels of one row, with few rows several threads
+// every so many of the parts, and eight loads are under way at a time (one after
+// another, two sequences of 131072 tokens took 15 us here).
+constexpr int kMergeThreads = 512;
+
 template <int D, bool BF16, int R>
-__global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__ Params p, int grid)
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ Params p, int grid)
 {
+    constexpr int kItems = R * (D / 4), kSplit = kItems < kMergeThreads ? kMergeThreads / kItems : 1;
+    __shared__ float top[R];
+    __shared__ float4 sum[kSplit][kItems < kMergeThreads ? kItems : 1];
+    __shared__ float low[kSplit][R];
     const int k = blockIdx.x;
     const Where w = locate(p, k + 1, grid);   // (lens and table are inputs: the search may run before the attention has ended)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // by every block, so that this grid ends after the attention has
@@ -837,29 +878,69 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
     const long long start = share_of(w, k);   // of CTA k's units
     if (t0 == edge || start > t0)   // not inside a tile, or not its first boundary
         return;
-    const long long last = (t1 * G - 1) / U;   // CTA holding unit t1 - 1: the largest x with U x / G < t1
+    const int parts = (int)((t1 * G - 1) / U) - k + 1;   // up to the CTA holding unit t1 - 1: the largest x with U x / G < t1
     const int h = hr / p.RB, r0 = (hr - h * p.RB) * R;
     const int nrows = min(p.rows - r0, R);
-    const long long slot0 = 2 * k + (start == t0 ? 0 : 1);   // CTA k's part: its only one, or its last
-    for (int i = threadIdx.x; i < nrows * (D / 4); i += kThreads) {
-        const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
-        float M = -INFINITY;
-        for (long long x = k; x <= last; ++x)
-            M = fmaxf(M, p.part_ml[(x == k ? slot0 : 2 * x) * R + row].x);
-        float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    const int slot0 = 2 * k + (start == t0 ? 0 : 1);   // CTA k's part: its only one, or its last
+    auto row_of = [&](int x, int row) -> long long { return (long long)(x ? 2 * (k + x) : slot0) * R + row; };
+    {   // the rows' maxima, a group of lanes to a row
+        constexpr int kLanes = kMergeThreads / R < 32 ? kMergeThreads / R : 32;
+        const int row = threadIdx.x / kLanes;
+        if (row < nrows) {
+            float M = -INFINITY;
 #pragma unroll 4
-        for (long long x = k; x <= last; ++x) {
-            const long long at = (x == k ? slot0 : 2 * x) * R + row;
+            for (int x = threadIdx.x % kLanes; x < parts; x += kLanes)
+                M = fmaxf(M, p.part_ml[row_of(x, row)].x);
+            const uint32_t group = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes % 32)) - 1u) << (threadIdx.x % 32 & ~(kLanes - 1));
+#pragma unroll
+            for (int m = kLanes / 2; m > 0; m /= 2)
+                M = fmaxf(M, __shfl_xor_sync(group, M, m));
+            if (threadIdx.x % kLanes == 0)
+                top[row] = M;
+        }
+    }
+    __syncthreads();
+    const int g = threadIdx.x / kItems;   // (0 where a thread has an item of its own or more)
+    for (int i = threadIdx.x - g * kItems; i < nrows * (D / 4); i += kMergeThreads) {
+        const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+        const float M = top[row];
+        float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int x = g; x < parts; x += kSplit) {
+            const long long at = row_of(x, row);
             const float2 ml = p.part_ml[at];
-            const float f = part_weight(ml, M);
             const float4 y = *reinterpret_cast<const float4 *>(p.part_o + at * D + ch);
+            const float f = part_weight(ml, M);
             L += ml.y * f;
             v[0] += y.x * f;
             v[1] += y.y * f;
             v[2] += y.z * f;
             v[3] += y.w * f;
         }
-        store_out<D, BF16>(p, w.b, h, r0 + row, ch, v, M, L);
+        if (kSplit == 1) {
+            store_out<D, BF16>(p, w.b, h, r0 + row, ch, v, M, L);
+        } else {
+            sum[g][i] = make_float4(v[0], v[1], v[2], v[3]);
+            if (ch == 0)
+                low[g][row] = L;
+        }
+    }
+    if (kSplit == 1)
+        return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < nrows * (D / 4); i += kMergeThreads) {
+        const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+        float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < kSplit; ++x) {
+            const float4 y = sum[x][i];
+            L += low[x][row];
+            v[0] += y.x;
+            v[1] += y.y;
+            v[2] += y.z;
+            v[3] += y.w;
+        }
+        store_out<D, BF16>(p, w.b, h, r0 + row, ch, v, top[row], L);
     }
 }
 

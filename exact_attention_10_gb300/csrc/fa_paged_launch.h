@@ -55,6 +55,7 @@ fa_status launch_paged_t(const fa::paged::Params &p, int grid, cudaStream_t s, i
         return FA_OK;
     // right behind it (programmatic dependent launch): the join of split tiles
     cfg.gridDim = dim3((unsigned)(grid - 1));
+    cfg.blockDim = dim3(paged::kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
