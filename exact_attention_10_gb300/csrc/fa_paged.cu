@@ -93,7 +93,7 @@ constexpr int kChunks = 4;
 // rounded correctly, as long as the residual is exact -- which scales of 2^-60 to
 // 2^100 see to (a residual that counts is then above 2^-149); others divide.  (By
 // division alone, and with a quarter of the channels a lane, 8 prompts of 1000 to 8192
-// tokens took 63 us, by this XXX.)
+// tokens took 63 us, so 36.)
 template <int D, bool BF16>
 __device__ __forceinline__ void quantise(const uint4 (&x)[kChunks], uint32_t group, uint2 (&codes)[kChunks], float &scale)
 {
@@ -138,7 +138,7 @@ template <int D, bool BF16, int BITS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ MoveParams p)
 {
     constexpr int kLanes = D / (8 * kChunks);
-    const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long g = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long r = g / kLanes;
     const int part = (int)(g % kLanes), lane = threadIdx.x % 32;
     if (r >= (long long)p.tokens * p.Hkv)   // (whole groups)
@@ -181,7 +181,7 @@ template <int D, bool BF16, int BITS>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ MoveParams p)
 {
     constexpr int kLanes = D / (8 * kChunks);
-    const long long g = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const long long g = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long r = g / kLanes;
     const int part = (int)(g % kLanes);
     if (r >= (long long)p.tokens * p.Hkv)
@@ -321,10 +321,14 @@ fa_status move(const fa_pages *c, const int *table, int W, int B, const fa_rows 
     p.W = W;
     p.P = c->pages;
     p.page_bits = bits;
-    const unsigned blocks = (unsigned)(((long long)tokens * Hkv * (D / (8 * kChunks)) + kThreads - 1) / kThreads);
+    // (few tokens over as many SMs as there are: 64 of them, 8 key heads, in 8 blocks took
+    // 7.4 us for append and read, in 32 5.9)
+    const long long lanes = (long long)tokens * Hkv * (D / (8 * kChunks));
+    const int threads = lanes < (long long)kThreads * di->sms ? 64 : kThreads;
+    const unsigned blocks = (unsigned)((lanes + threads - 1) / threads);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     auto run = [&](auto kern) {
-        kern<<<blocks, kThreads, 0, s>>>(p);
+        kern<<<blocks, threads, 0, s>>>(p);
         return launched();
     };
     auto pick = [&](auto d, auto b) {

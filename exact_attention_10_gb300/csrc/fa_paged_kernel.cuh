@@ -78,13 +78,14 @@ struct Params {
 // Steps that a warp holds in registers, on their way or in use, and CTAs per SM.
 template <int D, int BITS>
 constexpr int kDepth = D * BITS == 64 * 8 ? 2 : 1;
-// Where two tiles of query rows would leave room for two CTAs only, their fragments
-// are read from shared memory at every step (16 rows, D = 128, 16 bits: 250 registers
-// with them, and XXX us for 16 sequences of 2000 to 16384 tokens).
+// At 8 bits and D = 128 the fragments of two tiles of query rows are read from shared
+// memory at every step, which makes room for a third CTA: 16 sequences of 2000 to 16384
+// tokens, 16 rows, 66.8 -> 58.7 us.  (At 16 bits the tokens fill the registers: three
+// CTAs spill and take 89.4 us, two 81.1.)
 template <int D, int BITS, int NT>
-constexpr bool kSharedQ = NT == 2 && D == 128;
+constexpr bool kSharedQ = NT == 2 && D == 128 && BITS == 8;
 template <int D, int BITS, int NT>
-constexpr int kCtas = NT == 1 ? (BITS == 8 || D == 64 ? 4 : 3) : 3;
+constexpr int kCtas = NT == 1 ? (BITS == 8 || D == 64 ? 4 : 3) : (BITS == 8 || D == 64 ? 3 : 2);
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -556,12 +557,12 @@ struct Attend {
 // ------------------------------------------------------------------ the kernels
 
 // Shared memory of a CTA: per warp its rows' O and (m, l).
-template <int D, int NT>
+template <int D, int BITS, int NT>
 struct Smem {
     static constexpr int kRow = D + 4;
     static constexpr int kO = kWarps * 8 * NT * kRow * 4;
     static constexpr int kQ = kO + kWarps * 8 * NT * 8;   // query fragments, per warp (kSharedQ)
-    static constexpr int kBytes = kQ + (NT == 2 && D == 128 ? kWarps * (D / 16) * 512 : 0);
+    static constexpr int kBytes = kQ + (kSharedQ<D, BITS, NT> ? kWarps * (D / 16) * 512 : 0);
 };
 
 // Write channels [ch, ch + 4) of row `row` of a key head's rows (query head, token).
@@ -701,7 +702,7 @@ template <int D, bool BF16, int BITS, int NT, int NRB>
 __global__ void __launch_bounds__(kThreads, kCtas<D, BITS, NT>) attend_kernel(const __grid_constant__ Params p)
 {
     constexpr int kRows = 8 * NT;   // query rows of a warp
-    using S = Smem<D, NT>;
+    using S = Smem<D, BITS, NT>;
     extern __shared__ __align__(16) uint8_t smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -855,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<D, BITS, NT>) attend_kernel(co
 // CTA finished first).  R: rows of a tile.  A tile of a long sequence has some tens
 // of parts: threads take four channels of one row, with few rows several threads
 // every so many of the parts, and eight loads are under way at a time (one after
-// another, two sequences of 131072 tokens took 15 us here).
+// another, two sequences of up to 131072 tokens took 9 us longer).
 constexpr int kMergeThreads = 512;
 
 template <int D, bool BF16, int R>

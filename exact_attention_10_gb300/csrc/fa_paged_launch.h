@@ -28,7 +28,7 @@ template <int D, bool BF16, int BITS, int NT, int NRB>
 fa_status launch_paged_t(const fa::paged::Params &p, int grid, cudaStream_t s, int dev)
 {
     namespace paged = fa::paged;
-    constexpr int smem = paged::Smem<D, NT>::kBytes;
+    constexpr int smem = paged::Smem<D, BITS, NT>::kBytes;
     static bool set[fa_host::kMaxDevices] = {};
     auto kern = paged::attend_kernel<D, BF16, BITS, NT, NRB>;
     const fa_status st = fa_host::allow_smem(reinterpret_cast<const void *>(kern), smem, dev, set);

@@ -165,6 +165,9 @@ def _on(stream, t):
     return torch.cuda.stream(stream)
 
 
+_HERE = nullcontext()   # ... where there is nothing to switch
+
+
 def _workspace(nbytes: int, t):
     """Device memory from torch's allocator (None: none needed)."""
     import torch
@@ -456,8 +459,8 @@ def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=No
     rq = _rows(q, z.tokens_q, z.heads, D, t, dev, "q")
     rk, rv = (_rows(x, z.tokens_k, z.key_heads, D, t, dev, n) for x, n in ((k, "k"), (v, "v")))
     if out is None or lse is None:
-        with _on(stream, q):
-            out = torch.empty((z.tokens_q, z.heads, D), dtype=t, device=q.device) if out is None else out
+        with _on(stream, q) if stream is not None else _HERE:
+            out = torch.empty(q.shape, dtype=t, device=q.device) if out is None else out
             lse = torch.empty((z.heads, z.tokens_q), dtype=torch.float32, device=q.device) if lse is None else lse
     ro = _rows(out, z.tokens_q, z.heads, D, t, dev, "out")
     rc = load().fa_packed_fwd(rq, rk, rv, ro, lse.data_ptr(), z, D, D ** -0.5 if scale is None else scale, code,
@@ -542,6 +545,7 @@ class PagedCache(tuple):
         self.bits = 16 if len(tensors) == 2 else 8
         self.device = k.get_device()
         self.dtype = k.dtype
+        self.sizes = tuple(shape)   # P, Hkv, page, D
         ptrs = [t.data_ptr() for t in tensors] + [None] * (4 - len(tensors))
         self._args = {}
         for code, t in ((FA_BF16, torch.bfloat16), (FA_FP16, torch.float16)):
@@ -591,10 +595,11 @@ def _paged_table(cache, table):
 def _paged_move(name, cache, table, k, v, start, cu, stream):
     B, W = _paged_table(cache, table)
     args = cache.args(k.dtype)
-    if k.dim() != 3 or (cu is None and k.shape[0] != B):
+    if len(k.shape) != 3 or (cu is None and k.shape[0] != B):
         raise ValueError("k, v must be [T, Hkv, D], T the table's sequences without cu")
     T, dev = k.shape[0], cache.device
-    rk, rv = (_rows(x, T, args.key_heads, args.D, k.dtype, dev, n) for x, n in ((k, "k"), (v, "v")))
+    _, Hkv, _, D = cache.sizes
+    rk, rv = _rows(k, T, Hkv, D, k.dtype, dev, "k"), _rows(v, T, Hkv, D, k.dtype, dev, "v")
     rc = getattr(load(), name)(args, table.data_ptr(), W, B, rk, rv, T, _ints(start, B, "start"),
                                None if cu is None else _ints(cu, B + 1, "cu"), _stream_of(stream, k))
     if rc != 0:
@@ -625,9 +630,10 @@ def paged_read(cache: PagedCache, table, start, tokens: int, cu=None, dtype=None
         raise ValueError("tokens must be a 32-bit count of at least 1")
     if dtype is None:
         dtype = cache.dtype if cache.bits == 16 else torch.bfloat16
-    args = cache.args(dtype)
-    with _on(stream, cache.k):
-        k = torch.empty((tokens, args.key_heads, args.D), dtype=dtype, device=cache.k.device)
+    cache.args(dtype)
+    _, Hkv, _, D = cache.sizes
+    with _on(stream, cache.k) if stream is not None else _HERE:
+        k = torch.empty((tokens, Hkv, D), dtype=dtype, device=table.device)
         v = torch.empty_like(k)
     _paged_move("fa_paged_read", cache, table, k, v, start, cu, stream)
     return k, v
@@ -658,10 +664,11 @@ def paged_forward(q, cache: PagedCache, table, lens, scale: float | None = None,
     import torch
     B, W = _paged_table(cache, table)
     args = cache.args(q.dtype)
+    pages, Hkv, page, D = cache.sizes
     shape = q.shape
-    if len(shape) != 4 or shape[0] != B or shape[3] != args.D or shape[1] % args.key_heads or 0 in shape:
-        raise ValueError(f"q must be [{B}, a multiple of {args.key_heads}, Nq, {args.D}]")
-    H, Nq = shape[1], shape[2]
+    if len(shape) != 4 or shape[0] != B or shape[3] != D or shape[1] % Hkv or 0 in shape:
+        raise ValueError(f"q must be [{B}, a multiple of {Hkv}, Nq, {D}]")
+    _, H, Nq, _ = shape
     sb, sh, sn, last = q.stride()
     if last != 1:
         raise ValueError("q's last dimension must be contiguous")
@@ -672,13 +679,14 @@ def paged_forward(q, cache: PagedCache, table, lens, scale: float | None = None,
     if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [B, H, Nq]")
     at = _ints(lens, B, "lens")
-    nbytes = _paged_workspace(cache.device, args.pages, args.key_heads, args.page, args.D, args.bits, W, B, H, Nq)
-    with _on(stream, q):
-        out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
-        ws = _workspace(nbytes, q)
+    nbytes = _paged_workspace(cache.device, pages, Hkv, page, D, cache.bits, W, B, H, Nq)
+    if out is None or lse is None or nbytes:
+        with _on(stream, q) if stream is not None else _HERE:
+            out = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
+            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
+            ws = _workspace(nbytes, q)
     rc = load().fa_paged_fwd(q.data_ptr(), sb, sh, sn, args, table.data_ptr(), W, at, out.data_ptr(),
-                             lse.data_ptr(), B, H, Nq, args.D ** -0.5 if scale is None else scale,
+                             lse.data_ptr(), B, H, Nq, D ** -0.5 if scale is None else scale,
                              ws.data_ptr() if nbytes else None, nbytes, _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_paged_fwd")
