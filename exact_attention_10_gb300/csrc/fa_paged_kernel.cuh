@@ -75,17 +75,17 @@ struct Params {
     float2 *part_ml;
 };
 
-// Steps that a warp holds in registers, on their way or in use, and CTAs per SM.
-template <int D, int BITS>
-constexpr int kDepth = D * BITS == 64 * 8 ? 2 : 1;
 // At 8 bits and D = 128 the fragments of two tiles of query rows are read from shared
 // memory at every step, which makes room for a third CTA: 16 sequences of 2000 to 16384
 // tokens, 16 rows, 66.8 -> 58.7 us.  (At 16 bits the tokens fill the registers: three
 // CTAs spill and take 89.4 us, two 81.1.)
 template <int D, int BITS, int NT>
 constexpr bool kSharedQ = NT == 2 && D == 128 && BITS == 8;
+// CTAs per SM: as many as the registers allow, but for spills (D = 64, 8 bits: 4, 5
+// and 6 took 105, 96 and 97 us for 32 sequences of 4001 to 32768 tokens; D = 64, 16
+// bits, 64 of 1001 to 8192: 4, 5 and 6 74.8, 76.5 and 82.1).
 template <int D, int BITS, int NT>
-constexpr int kCtas = NT == 1 ? (BITS == 8 || D == 64 ? 4 : 3) : (BITS == 8 || D == 64 ? 3 : 2);
+constexpr int kCtas = NT == 1 ? (D == 64 ? (BITS == 8 ? 5 : 4) : (BITS == 8 ? 4 : 3)) : (BITS == 8 || D == 64 ? 3 : 2);
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -646,48 +646,40 @@ __device__ __forceinline__ void run_steps(const Params &p, Attend<D, BF16, BITS,
         }
         return __shfl_sync(0xffffffffu, ids, at++);
     };
-    constexpr int N = kDepth<D, BITS>;
-    Tokens<D, BITS> t[N];
-    int id[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        id[i] = next_id(s0 + i * stride);
-        if (id[i] >= 0) {
-            const long long row = row_of(id[i], s0 + i * stride);
-            t[i].template load_k<SHARED>(p, row, lane);
-            t[i].template load_v<SHARED>(p, row, lane);
-        }
+    Tokens<D, BITS> t;
+    int id = next_id(s0);
+    if (id >= 0) {
+        const long long row = row_of(id, s0);
+        t.template load_k<SHARED>(p, row, lane);
+        t.template load_v<SHARED>(p, row, lane);
     }
-    for (int s = s0; s < s1;) {
-#pragma unroll
-        for (int i = 0; i < N; ++i, s += stride) {
-            const int id1 = next_id(s + N * stride);
-            const long long row1 = row_of(id1, s + N * stride);
-            if (id[i] >= 0) {   // (tokens of a page outside the pool are hidden; behind the last step there is none)
-                float sc[NT][4];
-                a.scores(t[i], q, sc);
-                if (id1 >= 0)
-                    t[i].template load_k<SHARED>(p, row1, lane);
-                if (s * kStep + kStep > edge) {
-                    int see[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        see[nt][0] = hi[nt][0] - s * kStep;
-                        see[nt][1] = hi[nt][1] - s * kStep;
-                    }
-                    t[i].cut_v(len - s * kStep, lane);
-                    a.template weights<true>(t[i], sc, see, lane);
-                } else {
-                    a.template weights<false>(t[i], sc, hi, lane);
-                }
-                a.add(t[i], sc);
-            } else if (id1 >= 0) {
-                t[i].template load_k<SHARED>(p, row1, lane);
-            }
+    for (int s = s0; s < s1; s += stride) {
+        const int id1 = next_id(s + stride);
+        const long long row1 = row_of(id1, s + stride);
+        if (id >= 0) {   // (tokens of a page outside the pool are hidden)
+            float sc[NT][4];
+            a.scores(t, q, sc);
             if (id1 >= 0)
-                t[i].template load_v<SHARED>(p, row1, lane);
-            id[i] = id1;
+                t.template load_k<SHARED>(p, row1, lane);
+            if (s * kStep + kStep > edge) {
+                int see[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    see[nt][0] = hi[nt][0] - s * kStep;
+                    see[nt][1] = hi[nt][1] - s * kStep;
+                }
+                t.cut_v(len - s * kStep, lane);
+                a.template weights<true>(t, sc, see, lane);
+            } else {
+                a.template weights<false>(t, sc, hi, lane);
+            }
+            a.add(t, sc);
+        } else if (id1 >= 0) {
+            t.template load_k<SHARED>(p, row1, lane);
         }
+        if (id1 >= 0)
+            t.template load_v<SHARED>(p, row1, lane);
+        id = id1;
     }
 }
 

@@ -546,11 +546,8 @@ class PagedCache(tuple):
         self.device = k.get_device()
         self.dtype = k.dtype
         self.sizes = tuple(shape)   # P, Hkv, page, D
-        ptrs = [t.data_ptr() for t in tensors] + [None] * (4 - len(tensors))
-        self._args = {}
-        for code, t in ((FA_BF16, torch.bfloat16), (FA_FP16, torch.float16)):
-            if self.bits == 8 or t == k.dtype:
-                self._args[t] = Pages(*ptrs, *shape, self.bits, code)
+        self._codes = {t: code for code, t in ((FA_BF16, torch.bfloat16), (FA_FP16, torch.float16))
+                       if self.bits == 8 or t == k.dtype}
         return self
 
     def __reduce__(self):   # (copying and pickling go through the checks)
@@ -558,9 +555,12 @@ class PagedCache(tuple):
 
     def args(self, dtype) -> Pages:
         """What the library takes for values of ``dtype``."""
-        if dtype not in self._args:
+        code = self._codes.get(dtype)
+        if code is None:
             raise TypeError(f"a cache of {self.dtype} does not hold values of {dtype}")
-        return self._args[dtype]
+        if self.bits == 16:
+            return Pages(self[0].data_ptr(), self[1].data_ptr(), None, None, *self.sizes, 16, code)
+        return Pages(*[t.data_ptr() for t in self], *self.sizes, 8, code)
 
 
 def paged_empty(pages: int, Hkv: int, page: int, D: int, dtype=None, bits: int = 16, device="cuda") -> PagedCache:
