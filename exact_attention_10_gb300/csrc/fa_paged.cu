@@ -372,6 +372,12 @@ Shape shape_of(const fa_pages *c, int B, int H, int Nq, int W, int sms)
     s.tile_rows = tile_rows_for(rows);
     s.RB = (rows + s.tile_rows - 1) / s.tile_rows;
     const long long tiles = (long long)B * c->key_heads * s.RB, tokens = (long long)W * c->page;
+    // A tile's tokens go to a cluster of up to 8 CTAs, as far as there is room for them,
+    // if that leaves a CTA at most 1024; otherwise even shares of all tokens are joined
+    // by a second launch.  Clusters against shares, us (D = 128, 16 bits, 4 query heads
+    // to a key head, lengths from half the capacity to all of it): 8 tiles of capacity
+    // 1024 5.8 / 9.8, 8192 10.7 / 12.3; 128 tiles 1024 12.2 / 14.9, 2048 21.8 / 20.4, 4096
+    // 42.7 / 36.6; 512 tiles 512 21.7 / 23.4, 1024 38.7 / 37.5, 2048 72.3 / 65.6.
     const int room = fa_launch::paged_ctas(c->D, c->bits, s.tile_rows) * sms;
     int cl = 1;
     while (cl < 8 && tiles * cl * 2 <= room && (long long)cl * 2 * paged::kUnit <= tokens)
