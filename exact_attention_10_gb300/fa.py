@@ -369,10 +369,23 @@ class PackedPlan:
     makes it); the calls of every layer take it.  ``buffer`` holds the layout,
     ``sizes`` the batch's sizes."""
 
-    __slots__ = ("buffer", "sizes", "grad", "device")
+    __slots__ = ("buffer", "nbytes", "sizes", "shape", "grad", "_bytes")
 
     def __init__(self, buffer, sizes, grad):
-        self.buffer, self.sizes, self.grad, self.device = buffer, sizes, grad, buffer.get_device()
+        self.buffer, self.nbytes, self.sizes, self.grad = buffer, buffer.numel(), sizes, grad
+        self.shape = sizes.tokens_q, sizes.heads, sizes.tokens_k, sizes.key_heads
+        self._bytes = {}
+
+    def workspace(self, D: int, flags: int) -> int:
+        """Bytes of workspace that the backward takes (fa_packed_bwd_workspace)."""
+        n = self._bytes.get((D, flags))
+        if n is None:
+            size = ctypes.c_size_t()
+            rc = load().fa_packed_bwd_workspace(self.sizes, D, flags, size)
+            if rc != 0:
+                raise FAError(rc, "fa_packed_bwd_workspace")
+            n = self._bytes[D, flags] = size.value
+        return n
 
 
 def packed_plan(cu, tokens: int, H: int, Hkv: int | None = None, cu_k=None, tokens_k: int | None = None,
@@ -410,13 +423,13 @@ def packed_plan(cu, tokens: int, H: int, Hkv: int | None = None, cu_k=None, toke
     return PackedPlan(buffer, sizes, bool(grad))
 
 
-def _rows(t, rows: int, heads: int, D: int, dtype, device: int, name: str) -> Rows:
-    if t.shape != (rows, heads, D):
-        raise ValueError(f"{name} must be [{rows}, {heads}, {D}]")
-    if t.dtype != dtype:
+def _rows(t, shape, dtype, name: str) -> Rows:
+    """fa_rows of a tensor of ``shape`` [rows, heads, D] (the library checks its
+    device and alignment)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be of q's type")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the plan's device")
     row, head, last = t.stride()
     if last != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
@@ -424,20 +437,21 @@ def _rows(t, rows: int, heads: int, D: int, dtype, device: int, name: str) -> Ro
 
 
 def _packed_check(q, plan, lse):
+    """(sizes, shapes of queries and of keys, dtype code)."""
     import torch
     if not isinstance(plan, PackedPlan):
         raise TypeError("plan must be a PackedPlan (packed_plan)")
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [T, H, D]")
-    z = plan.sizes
+    T, H, Tk, Hkv = plan.shape
     if lse is not None:
-        if lse.shape != (z.heads, z.tokens_q) or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous [{z.heads}, {z.tokens_q}]")
-        if lse.dtype != torch.float32:
+        if lse.shape != (H, T) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous [{H}, {T}]")
+        if lse.dtype is not torch.float32:
             raise TypeError("lse must be float32")
-        if lse.get_device() != plan.device:
-            raise ValueError("lse must be on the plan's device")
-    return z, q.shape[2], _dtype_code(q)
+    D = shape[2]
+    return plan.sizes, (T, H, D), (Tk, Hkv, D), _dtype_code(q)
 
 
 def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=None, lse=None, stream=None):
@@ -454,17 +468,16 @@ def packed_forward(q, k, v, plan: PackedPlan, scale: float | None = None, out=No
     belong to (see ``forward``).
     """
     import torch
-    z, D, code = _packed_check(q, plan, lse)
-    dev, t = plan.device, q.dtype
-    rq = _rows(q, z.tokens_q, z.heads, D, t, dev, "q")
-    rk, rv = (_rows(x, z.tokens_k, z.key_heads, D, t, dev, n) for x, n in ((k, "k"), (v, "v")))
+    z, qs, ks, code = _packed_check(q, plan, lse)
+    t, D = q.dtype, qs[2]
+    rq, rk, rv = _rows(q, qs, t, "q"), _rows(k, ks, t, "k"), _rows(v, ks, t, "v")
     if out is None or lse is None:
         with _on(stream, q) if stream is not None else _HERE:
-            out = torch.empty(q.shape, dtype=t, device=q.device) if out is None else out
-            lse = torch.empty((z.heads, z.tokens_q), dtype=torch.float32, device=q.device) if lse is None else lse
-    ro = _rows(out, z.tokens_q, z.heads, D, t, dev, "out")
-    rc = load().fa_packed_fwd(rq, rk, rv, ro, lse.data_ptr(), z, D, D ** -0.5 if scale is None else scale, code,
-                              plan.buffer.data_ptr(), plan.buffer.numel(), _stream_of(stream, q))
+            out = torch.empty(qs, dtype=t, device=q.device) if out is None else out
+            lse = torch.empty((qs[1], qs[0]), dtype=torch.float32, device=q.device) if lse is None else lse
+    rc = load().fa_packed_fwd(rq, rk, rv, _rows(out, qs, t, "out"), lse.data_ptr(), z, D,
+                              D ** -0.5 if scale is None else scale, code, plan.buffer.data_ptr(), plan.nbytes,
+                              _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_packed_fwd")
     return out, lse
@@ -479,26 +492,21 @@ def packed_backward(q, k, v, o, do, lse, plan: PackedPlan, scale: float | None =
     ``deterministic``, ``dq`` / ``dk`` / ``dv`` and ``stream`` as for
     ``backward``."""
     import torch
-    z, D, code = _packed_check(q, plan, lse)
+    z, qs, ks, code = _packed_check(q, plan, lse)
     if not plan.grad:
         raise ValueError("the plan was made without grad")
-    dev, t = plan.device, q.dtype
-    rq, ro, rdo = (_rows(x, z.tokens_q, z.heads, D, t, dev, n) for x, n in ((q, "q"), (o, "o"), (do, "do")))
-    rk, rv = (_rows(x, z.tokens_k, z.key_heads, D, t, dev, n) for x, n in ((k, "k"), (v, "v")))
+    t, D = q.dtype, qs[2]
+    rq, ro, rdo = _rows(q, qs, t, "q"), _rows(o, qs, t, "o"), _rows(do, qs, t, "do")
+    rk, rv = _rows(k, ks, t, "k"), _rows(v, ks, t, "v")
     flags = FA_BWD_DETERMINISTIC if deterministic else 0
-    n = ctypes.c_size_t()
-    rc = load().fa_packed_bwd_workspace(z, D, flags, n)
-    if rc != 0:
-        raise FAError(rc, "fa_packed_bwd_workspace")
-    with _on(stream, q):
+    nbytes = plan.workspace(D, flags)
+    with _on(stream, q) if stream is not None else _HERE:
         dq, dk, dv = (torch.empty(x.shape, dtype=t, device=q.device) if d is None else d
                       for d, x in ((dq, q), (dk, k), (dv, v)))
-        ws = _workspace(n.value, q)
-    rdq = _rows(dq, z.tokens_q, z.heads, D, t, dev, "dq")
-    rdk, rdv = (_rows(x, z.tokens_k, z.key_heads, D, t, dev, n_) for x, n_ in ((dk, "dk"), (dv, "dv")))
-    rc = load().fa_packed_bwd(rq, rk, rv, ro, rdo, lse.data_ptr(), rdq, rdk, rdv, z, D,
-                              D ** -0.5 if scale is None else scale, code, flags, plan.buffer.data_ptr(),
-                              plan.buffer.numel(), ws.data_ptr(), n.value, _stream_of(stream, q))
+        ws = _workspace(nbytes, q)
+    rc = load().fa_packed_bwd(rq, rk, rv, ro, rdo, lse.data_ptr(), _rows(dq, qs, t, "dq"), _rows(dk, ks, t, "dk"),
+                              _rows(dv, ks, t, "dv"), z, D, D ** -0.5 if scale is None else scale, code, flags,
+                              plan.buffer.data_ptr(), plan.nbytes, ws.data_ptr(), nbytes, _stream_of(stream, q))
     if rc != 0:
         raise FAError(rc, "fa_packed_bwd")
     return dq, dk, dv
@@ -543,11 +551,10 @@ class PagedCache(tuple):
             raise ValueError("the cache must be on one device")
         self = super().__new__(cls, tensors)
         self.bits = 16 if len(tensors) == 2 else 8
-        self.device = k.get_device()
-        self.dtype = k.dtype
+        self.device, self.dtype = k.get_device(), k.dtype
         self.sizes = tuple(shape)   # P, Hkv, page, D
-        self._codes = {t: code for code, t in ((FA_BF16, torch.bfloat16), (FA_FP16, torch.float16))
-                       if self.bits == 8 or t == k.dtype}
+        self._args = {t: Pages(None, None, None, None, *shape, self.bits, code)
+                      for code, t in ((FA_BF16, torch.bfloat16), (FA_FP16, torch.float16)) if self.bits == 8 or t == k.dtype}
         return self
 
     def __reduce__(self):   # (copying and pickling go through the checks)
@@ -555,12 +562,13 @@ class PagedCache(tuple):
 
     def args(self, dtype) -> Pages:
         """What the library takes for values of ``dtype``."""
-        code = self._codes.get(dtype)
-        if code is None:
+        args = self._args.get(dtype)
+        if args is None:
             raise TypeError(f"a cache of {self.dtype} does not hold values of {dtype}")
-        if self.bits == 16:
-            return Pages(self[0].data_ptr(), self[1].data_ptr(), None, None, *self.sizes, 16, code)
-        return Pages(*[t.data_ptr() for t in self], *self.sizes, 8, code)
+        args.k, args.v = self[0].data_ptr(), self[1].data_ptr()
+        if self.bits == 8:
+            args.k_scale, args.v_scale = self[2].data_ptr(), self[3].data_ptr()
+        return args
 
 
 def paged_empty(pages: int, Hkv: int, page: int, D: int, dtype=None, bits: int = 16, device="cuda") -> PagedCache:
@@ -583,13 +591,12 @@ def _paged_table(cache, table):
     import torch
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
-    if table.dtype != torch.int32:
+    if table.dtype is not torch.int32:
         raise TypeError("table must be int32")
-    if table.dim() != 2 or 0 in table.shape or not table.is_contiguous():
+    shape = table.shape
+    if len(shape) != 2 or 0 in shape or not table.is_contiguous():
         raise ValueError("table must be contiguous [B, width]")
-    if table.get_device() != cache.device:
-        raise ValueError("table must be on the cache's device")
-    return table.shape
+    return shape
 
 
 def _paged_move(name, cache, table, k, v, start, cu, stream):
@@ -597,9 +604,10 @@ def _paged_move(name, cache, table, k, v, start, cu, stream):
     args = cache.args(k.dtype)
     if len(k.shape) != 3 or (cu is None and k.shape[0] != B):
         raise ValueError("k, v must be [T, Hkv, D], T the table's sequences without cu")
-    T, dev = k.shape[0], cache.device
     _, Hkv, _, D = cache.sizes
-    rk, rv = _rows(k, T, Hkv, D, k.dtype, dev, "k"), _rows(v, T, Hkv, D, k.dtype, dev, "v")
+    T = k.shape[0]
+    shape = T, Hkv, D
+    rk, rv = _rows(k, shape, k.dtype, "k"), _rows(v, shape, k.dtype, "v")
     rc = getattr(load(), name)(args, table.data_ptr(), W, B, rk, rv, T, _ints(start, B, "start"),
                                None if cu is None else _ints(cu, B + 1, "cu"), _stream_of(stream, k))
     if rc != 0:
@@ -672,8 +680,6 @@ def paged_forward(q, cache: PagedCache, table, lens, scale: float | None = None,
     sb, sh, sn, last = q.stride()
     if last != 1:
         raise ValueError("q's last dimension must be contiguous")
-    if q.get_device() != cache.device:
-        raise ValueError("q must be on the cache's device")
     if out is not None and (out.shape != shape or out.dtype != q.dtype or not out.is_contiguous()):
         raise ValueError("out must be contiguous, of q's shape and type")
     if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
