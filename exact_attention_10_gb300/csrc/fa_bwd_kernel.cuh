@@ -139,6 +139,8 @@ struct PackedParams : Params {
     int group;              // query heads per key head
     int causal;
     long long a_row, a_head, b_row, b_head;   // bytes between rows and heads of dA and dB
+    int parts, Hkv;         // KV: parts of a key tile, at most
+    float *part;            // KV, parts > 1: their dK and dV, [key tiles][Hkv][parts][2][128][D] fp32, not yet scaled
 };
 
 template <class P>
@@ -401,6 +403,7 @@ struct PackedWork {
     int q0, Lq, k0, Lk;    // the sequence
     int qt0;               // its first query tile among all sequences'
     int per, s0, group;    // KV: as in SinkWork
+    int part;              // KV: where a part's sums go, -1: the whole tile
     bool none;             // KV: no query sees the tile: one step with the empty query tile
     int empty;             // the empty query tile
     // Steps are asked for in turn, so head and tile follow without a division (in
@@ -424,7 +427,7 @@ struct PackedWork {
         seek(j);
         return KV ? s0 + j - first : j;
     }
-    __device__ int slot() const { return -1; }
+    __device__ int slot() const { return KV ? part : -1; }
     __device__ int rows(int j) const { return (KV ? Lq : Lk) - tile(j) * kTile; }   // of step j's tile (128 or more: all)
     __device__ int qtile(int t) const { return KV && none ? empty : qt0 + t; }   // among all sequences', of tile t
 };
@@ -435,13 +438,14 @@ __device__ __forceinline__ PackedWork<KV> bwd_work(const PackedParams &p, bool, 
     PackedWork<KV> w;
     int4 seq, at;
     packed_slot(p.slots, p.rounds, blockIdx.x, t, seq, at);
-    w.rh = at.z;
+    w.rh = KV ? at.z & 0xffff : at.z;
     w.q0 = seq.x;
     w.Lq = seq.y;
     w.k0 = seq.z;
     w.Lk = seq.w;
-    w.rt = at.x;
+    w.rt = KV ? packed::part_tile(at.x) : at.x;
     w.qt0 = at.y;
+    w.part = -1;
     w.group = p.group;
     w.empty = at.w - 1;
     w.per = 1;
@@ -455,6 +459,14 @@ __device__ __forceinline__ PackedWork<KV> bwd_work(const PackedParams &p, bool, 
             w.per = (w.Lq + kTile - 1) / kTile - s0;
         }
         w.n = w.none ? 1 : w.per * p.group;
+        const int of = packed::parts_of(at.x), i = packed::part_of(at.x);
+        if (of > 1) {
+            const int base = packed::part_step(w.n, i, of);
+            w.n = packed::part_step(w.n, i + 1, of) - base;
+            w.hd = base / w.per;
+            w.first = w.hd * w.per - base;
+            w.part = ((at.z >> 16) * p.Hkv + w.rh) * p.parts + i;
+        }
     } else {
         w.n = packed::key_steps(w.rt * kTile, w.Lq, w.Lk, p.causal);
     }
@@ -972,6 +984,12 @@ __device__ __forceinline__ float *part_row(const SinkParams &p, int slot, int h,
     return p.part + (((size_t)slot * 2 + h) * kTile + row) * D;
 }
 
+template <int D>
+__device__ __forceinline__ float *part_row(const PackedParams &p, int slot, int h, int row)
+{
+    return p.part + (((size_t)slot * 2 + h) * kTile + row) * D;
+}
+
 __device__ __forceinline__ void store_part32(float *dst, const uint32_t (&v)[32])
 {
 #pragma unroll
@@ -1106,7 +1124,7 @@ __device__ void bwd_compute(const P &p, uint32_t tmem, uint32_t sStage, BBars<D,
                 uint32_t v[32];
                 ptx::tmem_ld32(tA + 32 * cc, v);
                 ptx::tmem_wait_ld();
-                if (kSinkPass<P> && wk.slot() >= 0)
+                if ((kSinkPass<P> || kPackedPass<P>) && wk.slot() >= 0)
                     store_part32(part_row<D>(p, wk.slot(), h, lane_row) + 32 * cc, v);
                 else if (grow < end)
                     store_row32<BF16>(dst + cc * 64, v, mul);
@@ -1448,7 +1466,7 @@ __device__ void bwd_compute_pipe(const P &p, uint32_t tmem, uint32_t sStage, uin
                 uint32_t v[32];
                 ptx::tmem_ld32(tA + 32 * cc, v);
                 ptx::tmem_wait_ld();
-                if (kSinkPass<P> && wk.slot() >= 0)
+                if ((kSinkPass<P> || kPackedPass<P>) && wk.slot() >= 0)
                     store_part32(part_row<D>(p, wk.slot(), h, row) + 32 * cc, v);
                 else if (grow < end)
                     store_row32<BF16>(dst + cc * 64, v, mul);
@@ -1897,6 +1915,45 @@ __global__ void __launch_bounds__(256)
         o.z = BF16 ? ptx::pack_bf16x2(b.x * scale, b.y * scale) : ptx::pack_f16x2(b.x * scale, b.y * scale);
         o.w = BF16 ? ptx::pack_bf16x2(b.z * scale, b.w * scale) : ptx::pack_f16x2(b.z * scale, b.w * scale);
         *reinterpret_cast<uint4 *>(dQ + (long long)(at.x + i) * p.o_row + h * p.o_head + 16 * part) = o;
+    }
+}
+
+// Key tiles cut into parts: dK = scale * sum of the parts' dK, dV the sum of their dV,
+// in the input type, the parts added in order (8 values a thread).  blockIdx.x: key
+// tile, .y: key head, .z: 0 dV, 1 dK.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) reduce_parts_kernel(const __grid_constant__ PackedParams p, const int4 *table)
+{
+    fq::grid_wait();   // launched right behind the pass: its parts are complete
+    const int4 at = ld_plan(table + blockIdx.x);
+    const int kvh = blockIdx.y, h = blockIdx.z;
+    if (at.z <= 1)   // written by the pass itself, or no tile
+        return;
+    const int slot = ((int)blockIdx.x * p.Hkv + kvh) * p.parts;
+    const float mul = h ? p.scale : 1.f;
+    char *dst = static_cast<char *>(h ? p.dA : p.dB) + (long long)at.x * (h ? p.a_row : p.b_row) +
+                (long long)kvh * (h ? p.a_head : p.b_head);
+    for (int i = threadIdx.x; i < at.y * (D / 8); i += 256) {
+        const int row = i / (D / 8), col = (i % (D / 8)) * 8;
+        float a[8] = {};
+#pragma unroll 4
+        for (int c = 0; c < at.z; ++c) {
+            const float4 *src = reinterpret_cast<const float4 *>(part_row<D>(p, slot + c, h, row) + col);
+            const float4 x = src[0], y = src[1];
+            a[0] += x.x;
+            a[1] += x.y;
+            a[2] += x.z;
+            a[3] += x.w;
+            a[4] += y.x;
+            a[5] += y.y;
+            a[6] += y.z;
+            a[7] += y.w;
+        }
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = BF16 ? ptx::pack_bf16x2(a[2 * k] * mul, a[2 * k + 1] * mul) : ptx::pack_f16x2(a[2 * k] * mul, a[2 * k + 1] * mul);
+        *reinterpret_cast<uint4 *>(dst + (long long)row * (h ? p.a_row : p.b_row) + col * 2) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 

@@ -54,14 +54,25 @@ fa_status launch_all(const PackedBwdLaunch &a, cudaStream_t s, int dev)
     p.a_head = a.dk.head * 2;
     p.b_row = a.dv.row * 2;
     p.b_head = a.dv.head * 2;
+    p.parts = pk::max_parts(a.z);
+    p.Hkv = a.z.Hkv;
+    p.part = a.part;
     const int g = pk::grid(a.z, 2, a.sms);
     if constexpr (D == 64)
         st = fused ? launch_pass<D, BF16, true, true, true, P>(a.tk, a.tv, a.tq, a.tdo, a.tdqa, p, g, s, dev)
                    : launch_pass<D, BF16, true, true, false, P>(a.tk, a.tv, a.tq, a.tdo, a.tq, p, g, s, dev);
     else
         st = launch_pass<D, BF16, true, true, false, P>(a.tk, a.tv, a.tq, a.tdo, a.tq, p, g, s, dev);
-    if (st != FA_OK || !fused)
+    if (st != FA_OK)
         return st;
+    if (p.parts > 1 &&
+        launch_dependent(fa::bwd::reduce_parts_kernel<D, BF16>, dim3((unsigned)pk::key_tiles(a.z), (unsigned)a.z.Hkv, 2),
+                         dim3(256), 0, s, p, plan + pk::key_table_word(a.z)) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    if (!fused)
+        return FA_OK;
     rows.o_row = a.dq.row * 2;
     rows.o_head = a.dq.head * 2;
     if (launch_dependent(fa::bwd::fa_bwd_dq_convert_packed<BF16>, grid, dim3(256), 0, s, (const float *)a.dqa,

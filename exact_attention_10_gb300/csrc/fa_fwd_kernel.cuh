@@ -246,8 +246,9 @@ struct FwdParamsT {
 };
 using FwdParams = FwdParamsT<Schedule>;
 using SinkParams = FwdParamsT<SinkSchedule>;
-struct PackedParams : FwdParamsT<PackedSchedule> {   // N: tokens, causal in sch
+struct PackedParams : FwdParamsT<PackedSchedule> {   // N: 128 if no tile has a second Q tile, else more; causal in sch
     long long o_row, o_head;   // bytes between O's rows and heads
+    long long lse_head;        // tokens
     int wide;                  // O's rows start on 32 bytes
 };
 template <int MASK>
@@ -270,12 +271,13 @@ __device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, in
         ++it.u;
         bh = at.z;   // the query head
         tile.q0 = seq.x;
-        tile.Lq = seq.y;
+        tile.rows = seq.y;
+        tile.off = at.x;
         tile.k0 = seq.z;
         tile.Lk = seq.w;
-        ct = at.x;
-        tile.nw[0] = packed::key_steps(ct * kCtaRows, seq.y, seq.w, s.causal);
-        tile.nw[1] = packed::key_steps(ct * kCtaRows + kBM, seq.y, seq.w, s.causal);
+        ct = 0;   // (rows are counted from the tile's first)
+        tile.nw[0] = packed::tile_steps(0, seq.y, at.x, seq.w, s.causal);
+        tile.nw[1] = packed::tile_steps(kBM, seq.y, at.x, seq.w, s.causal);
         pt.kb = 0;
         pt.ke = tile.nw[0] > tile.nw[1] ? tile.nw[0] : tile.nw[1];
         return true;
@@ -1123,9 +1125,8 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
         const auto keys = step_keys<MASK>(p.sch, tile, ct);   // the tile's key steps
         int row_lo = 0, row_hi = p.Nkv, edge_lo = 0, edge_hi = p.Nkv;
         if constexpr (MASK == kMaskPacked) {
-            const int first = ct * kCtaRows + w * kBM;
-            row_hi = packed::row_end(min(row, tile.Lq - 1), tile.Lq, tile.Lk, p.sch.causal);
-            edge_hi = packed::row_end(first, tile.Lq, tile.Lk, p.sch.causal);   // (at most Lk)
+            row_hi = packed::row_end(min(row, tile.rows - 1) + tile.off, tile.Lk, p.sch.causal);
+            edge_hi = packed::row_end(w * kBM + tile.off, tile.Lk, p.sch.causal);   // (at most Lk)
         } else if (CAUSAL) {
             const int first = ct * kCtaRows + w * kBM, r = min(row, p.N - 1);
             row_hi = sched_row_hi(p.sch, r);
@@ -1668,7 +1669,7 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
             const int row = ct * kCtaRows + w * kBM + t;
             bool valid = row < p.N;
             if constexpr (MASK == kMaskPacked)
-                valid = row < tile.Lq;
+                valid = row < tile.rows;
             const uint32_t tO = tmem + C::col_o(w) + lane_off;
             if (whole) {
                 uint8_t *orow =
@@ -1699,7 +1700,7 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
                 }
                 if (valid) {
                     if constexpr (MASK == kMaskPacked)
-                        p.LSE[(size_t)bh * p.N + tile.q0 + row] = (st.x + log2f(st.y)) * kLn2;
+                        p.LSE[bh * p.lse_head + tile.q0 + row] = (st.x + log2f(st.y)) * kLn2;
                     else
                         p.LSE[(size_t)bh * p.N + row] = (st.x + log2f(st.y)) * kLn2;
                 }

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int l = blockIdx.x, t = threadIdx.x, S = p.z.S;
     int4 *entries = p.plan + pk::entry_word(p.z, l);
     int4 *seqs = p.plan + pk::scratch_word(p.z, l);   // two words a sequence: {q0, Lq, k0, Lk}, {first entry, first query tile}
-    const int tile = l == 0 ? 2 * pk::kTile : pk::kTile;
+    const int tile = l == 0 ? pk::cta_rows(p.z) : pk::kTile;
 
     // sequences, `per` after one another to a thread
     const int per = (S + kPlanThreads - 1) / kPlanThreads;
@@ -123,26 +123,59 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
         return lo;
     };
-    auto cost = [&](const int4 &q, int i) -> int {   // steps
+    const int heads = pk::heads_of(p.z, l), mul = l == 2 ? p.z.H / p.z.Hkv : 1, most = l == 2 ? pk::max_parts(p.z) : 1;
+    auto steps = [&](const int4 &q, int i) -> int {
         if (l == 0)
-            return pk::key_steps(i * tile, q.y, q.w, p.causal) + pk::key_steps(i * tile + pk::kTile, q.y, q.w, p.causal);
+            return pk::key_steps(i * tile, q.y, q.w, p.causal) +
+                   (tile > pk::kTile ? pk::key_steps(i * tile + pk::kTile, q.y, q.w, p.causal) : 0);
         if (l == 1)
             return pk::key_steps(i * tile, q.y, q.w, p.causal);
         const int f = pk::first_query_tile(i, q.y, q.w, p.causal);
-        return f < 0 ? 1 : (q.y + pk::kTile - 1) / pk::kTile - f;
+        return f < 0 ? 1 : ((q.y + pk::kTile - 1) / pk::kTile - f) * mul;
     };
-    int top = 0;
+    // Parts, where some tile is longer than a CTA's share of all steps by more than a
+    // quarter: of half a share, and kPartSteps at least.  (Causal, D = 128: one sequence
+    // of 8192 tokens, 4 query heads on one key head, the longest tile 4.7 shares: 492 us
+    // uncut, 272 cut; 4 on 4, 1.2 shares: 194 and 228.  Cutting the long ones alone left
+    // 8 on one at 512 us instead of 463.)
+    __shared__ unsigned long long all_steps;
+    int limit = 0x7fffffff;
+    if (most > 1) {   // (few tiles)
+        if (t == 0)
+            all_steps = 0;
+        __syncthreads();
+        int longest = 0;
+        for (int e = t; e < n; e += kPlanThreads) {
+            const int s = seq_of(e), c = steps(seqs[2 * (size_t)s], e - seqs[2 * (size_t)s + 1].x);
+            atomicAdd(&all_steps, (unsigned long long)c * heads);
+            longest = max(longest, c);
+        }
+        block_scan<true>(longest, scratch, total);   // (its barriers are behind every sum)
+        const unsigned long long share = all_steps / p.grid[l];
+        if (total > share + share / 4)
+            limit = (int)max((unsigned long long)pk::kPartSteps, share / 2);
+    }
+    auto parts = [&](int c) { return c <= limit ? 1 : min(most, (c + limit - 1) / limit); };
+    auto cost = [&](int c, int part, int of) { return of == 1 ? c : pk::part_step(c, part + 1, of) - pk::part_step(c, part, of); };
+
+    int top = 0, total_parts = 0;
     for (int e = t; e < n; e += kPlanThreads) {
         const int s = seq_of(e);
-        top = max(top, cost(seqs[2 * (size_t)s], e - seqs[2 * (size_t)s + 1].x));
+        const int c = steps(seqs[2 * (size_t)s], e - seqs[2 * (size_t)s + 1].x), of = most > 1 ? parts(c) : 1;
+        top = max(top, (c + of - 1) / of);
+        total_parts += of;
     }
     block_scan<true>(top, scratch, total);
     top = total;
+    int entries_n;
+    block_scan<false>(total_parts, scratch, entries_n);
     // buckets from the longest tiles to the shortest
     auto bucket = [&](int c) { return kBuckets - 1 - (top < kBuckets ? c : (int)((long long)c * kBuckets / (top + 1ll))); };
     for (int e = t; e < n; e += kPlanThreads) {
         const int s = seq_of(e);
-        atomicAdd(&hist[bucket(cost(seqs[2 * (size_t)s], e - seqs[2 * (size_t)s + 1].x))], 1);
+        const int c = steps(seqs[2 * (size_t)s], e - seqs[2 * (size_t)s + 1].x), of = most > 1 ? parts(c) : 1;
+        for (int i = 0; i < of; ++i)
+            atomicAdd(&hist[bucket(cost(c, i, of))], 1);
     }
     __syncthreads();
     {
@@ -164,20 +197,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     for (int e = t; e < n; e += kPlanThreads) {
         const int s = seq_of(e);
         const int4 q = seqs[2 * (size_t)s], w = seqs[2 * (size_t)s + 1];
-        const int i = e - w.x;
-        const int pos = atomicAdd(&hist[bucket(cost(q, i))], 1);   // (tiles of a bucket in any order: they are independent)
-        entries[2 * (size_t)pos] = q;
-        entries[2 * (size_t)pos + 1] = make_int4(i, w.y, 0, 0);
+        const int i = e - w.x, c = steps(q, i), of = most > 1 ? parts(c) : 1;
+        for (int k = 0; k < of; ++k) {
+            const int pos = atomicAdd(&hist[bucket(cost(c, k, of))], 1);   // (tiles of a bucket in any order: they are independent)
+            entries[2 * (size_t)pos] = q;
+            entries[2 * (size_t)pos + 1] = make_int4(pk::pack_part(i, k, of), w.y, e, 0);
+        }
         if (l == 1)
             p.plan[pk::table_word(p.z) + e] = make_int4(q.x + i * pk::kTile, min(pk::kTile, q.y - i * pk::kTile), 0, 0);
+        if (l == 2)
+            p.plan[pk::key_table_word(p.z) + e] = make_int4(q.z + i * pk::kTile, min(pk::kTile, q.w - i * pk::kTile), of, 0);
     }
+    if (l == 2)   // key tiles that there are not
+        for (long long e = n + t; e < pk::key_tiles(p.z); e += kPlanThreads)
+            p.plan[pk::key_table_word(p.z) + e] = make_int4(0, 0, 0, 0);
     __syncthreads();
     // The slots: per round, rank the CTAs by what they have so far.  (Each tile
     // costs about two steps more than its own: its first loads and last stores.)
     __shared__ int load[pk::kOrderGrid];
     int4 *slots = p.plan + pk::list_word(p.z, l);
-    const int G = p.grid[l], R = pk::rounds(p.z, l, G), heads = pk::heads_of(p.z, l), mul = l == 2 ? p.z.H / p.z.Hkv : 1;
-    const int T = n * heads;
+    const int G = p.grid[l], R = pk::rounds(p.z, l, G);
+    const int T = entries_n * heads;
     auto fill = [&](int c, int r, int x) -> int {   // CTA c's tile of round r is tile x; its cost
         int4 *at = slots + 2 * ((long long)c * R + r);
         if (x >= T) {
@@ -186,9 +226,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         }
         const int e = x / heads;
         const int4 q = entries[2 * (size_t)e], w = entries[2 * (size_t)e + 1];
-        at[0] = q;
-        at[1] = make_int4(w.x, w.y, x - e * heads, total_q + 1);
-        return cost(q, w.x) * mul + 2;
+        const int i = pk::part_tile(w.x), h = x - e * heads;
+        if (l == 0) {
+            const int first = i * tile;
+            at[0] = make_int4(q.x + first, min(tile, q.y - first), q.z, q.w);
+            at[1] = make_int4(first + q.w - q.y, 0, h, 1);
+        } else {
+            at[0] = q;
+            at[1] = make_int4(w.x, w.y, most > 1 ? h | w.z << 16 : h, total_q + 1);
+        }
+        return cost(steps(q, i), pk::part_of(w.x), pk::parts_of(w.x)) + 2;
     };
     int mine = 0;
     for (int r = 0; r < pk::kOrderRounds && r < R; ++r) {
@@ -373,8 +420,9 @@ extern "C" fa_status fa_packed_fwd(const fa_rows *q, const fa_rows *k, const fa_
     fa::PackedParams p{};
     p.O = o->ptr;
     p.LSE = LSE;
-    p.N = z.Tq;
+    p.N = pk::cta_rows(z);
     p.Nkv = z.Tk;
+    p.lse_head = z.Tq;
     p.qk_scale = scale * 1.4426950408889634f;   // scale * log2(e)
     p.o_row = r[3].row * 2;
     p.o_head = r[3].head * 2;
@@ -393,7 +441,7 @@ extern "C" fa_status fa_packed_bwd_workspace(const fa_packed_sizes *sizes, int D
     pk::Sizes z;
     if (!bytes || (D != 64 && D != 128) || (flags & ~FA_BWD_DETERMINISTIC) || !sizes_ok(sizes, &z))
         return FA_ERR_INVALID_VALUE;
-    *bytes = (size_t)pk::padded_rows(z) * z.H * (2 + (fused_dq(D, flags) ? D : 0)) * sizeof(float);
+    *bytes = ((size_t)pk::padded_rows(z) * z.H * (2 + (fused_dq(D, flags) ? D : 0)) + (size_t)pk::part_floats(z, D)) * sizeof(float);
     return FA_OK;
 }
 
@@ -434,6 +482,7 @@ extern "C" fa_status fa_packed_bwd(const fa_rows *q, const fa_rows *k, const fa_
     a.lg = static_cast<float *>(workspace);
     a.dl = a.lg + rows;
     a.dqa = a.dl + rows;
+    a.part = a.dqa + (a.fused ? rows * D : 0);
     if (a.fused && !fa_host::encode_rows_f32(&a.tdqa, a.dqa, (long long)rows, D))
         return FA_ERR_CUDA;
     auto rows_of = [](const Rows &x) { return fa_rows{const_cast<void *>(x.p), x.row, x.head}; };

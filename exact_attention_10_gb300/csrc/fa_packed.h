@@ -6,7 +6,7 @@
 // Lengths are device data, so a kernel on the device (fa_packed_plan.cu) lays
 // out the work once per batch and every layer's calls read it: up to three
 // lists of tiles, each longest first --
-//   list 0  forward: CTA tiles of 256 query rows
+//   list 0  forward: CTA tiles of 256 query rows (128 where there are few)
 //   list 1  dQ pass and the rows' statistics: query tiles of 128 rows
 //   list 2  dK/dV pass: key tiles of 128 rows
 // -- an entry of which is a tile of one sequence, and a tile of work one of its
@@ -17,8 +17,9 @@
 // tokens, 572 tiles; so laid out, 5 %.)
 //
 // What a role of the kernels needs of a tile is one slot of two words, {q0, Lq, k0,
-// Lk} and {tile, first query tile of the sequence, head, query tiles in all + 1},
-// the last 0 where there is none; a CTA's slots follow one another, so after the
+// Lk} and {tile, first query tile of the sequence, head, query tiles in all + 1} --
+// in list 0 {its first row, its rows, k0, Lk} and {the first row's key position, 0,
+// head, 1} -- the last 0 where there is none; a CTA's slots follow one another, so after the
 // first of four they are in L1.  (Looked up by way of order, entry and head, a tile
 // began 0.7 us later.)
 //
@@ -26,7 +27,8 @@
 // list its slots, then scratch (its entries, longest first, and two words per
 // sequence and two more); then list 1's table by query tile, {first row, rows, 0,
 // 0}, in the sequences' order with one empty tile behind the last (the dK/dV pass's
-// step of a key tile that no query sees).
+// step of a key tile that no query sees); then list 2's by key tile, {first row, rows,
+// parts, 0}.
 #pragma once
 
 #include <cstddef>
@@ -49,10 +51,33 @@ struct Sizes {
     int S, Tq, Tk, H, Hkv;
 };
 
+// Whether the forward's CTA tiles are of 128 rows: where tiles of 256 would be about
+// one to a CTA, the longest alone sets the time.  (Causal, D = 128, tiles of 256 / 128,
+// us: 8192 tokens, 4 heads, 132 tiles of 256 106 / 71; 4096 and 2000 tokens, 8 heads, 200
+// tiles 57 / 46; 8192 tokens, 8 heads, 264 tiles 107 / 129.)
+FA_HD bool few(const Sizes &z) { return (z.Tq / 256 + (long long)z.S) * z.H <= kOrderGrid * 4 / 3; }
+FA_HD int cta_rows(const Sizes &z) { return few(z) ? kTile : 2 * kTile; }
+// Key tiles there may be, and the parts that one's query tiles may be cut into in the
+// dK/dV pass: with few key tiles and heads the longest alone would set the time.  A
+// part's sums go to a workspace, and reduce_parts_kernel adds them.
+FA_HD long long key_tiles(const Sizes &z) { return z.Tk / kTile + (long long)z.S; }
+FA_HD int max_parts(const Sizes &z)
+{
+    const long long n = (4 * kOrderGrid + key_tiles(z) * z.Hkv - 1) / (key_tiles(z) * z.Hkv);
+    return n > 16 ? 16 : (int)n;
+}
+constexpr int kPartSteps = 8;   // of a part, at least
+// A slot's or an entry's tile with its part (of parts), and its head with the key tile's number in all.
+FA_HD int pack_part(int tile, int part, int parts) { return (int)((unsigned)tile | (unsigned)part << 24 | (unsigned)(parts - 1) << 28); }
+FA_HD int part_tile(int x) { return x & 0xffffff; }
+FA_HD int part_of(int x) { return (x >> 24) & 15; }
+FA_HD int parts_of(int x) { return (int)((unsigned)x >> 28) + 1; }
+// First of n steps of part i of `parts`.
+FA_HD int part_step(int n, int i, int parts) { return (int)((long long)n * i / parts); }
 // Entries that list l has room for, and all of it in 16-byte words.
 FA_HD long long capacity(const Sizes &z, int l)
 {
-    return (l == 0 ? z.Tq / 256 : l == 1 ? z.Tq / kTile : z.Tk / kTile) + (long long)z.S;
+    return l == 2 ? key_tiles(z) * max_parts(z) : (l == 0 ? z.Tq / cta_rows(z) : z.Tq / kTile) + (long long)z.S;
 }
 FA_HD int heads_of(const Sizes &z, int l) { return l == 2 ? z.Hkv : z.H; }
 // Slots that list l has room for (CTAs' rounds are as many for all of them).
@@ -68,7 +93,13 @@ FA_HD long long entry_word(const Sizes &z, int l) { return list_word(z, l) + 2 *
 FA_HD long long scratch_word(const Sizes &z, int l) { return entry_word(z, l) + 2 * capacity(z, l); }
 FA_HD long long table_word(const Sizes &z) { return list_word(z, 3); }
 // Words of a plan for the forward alone, or for both directions.
-FA_HD long long plan_words(const Sizes &z, bool grad) { return grad ? table_word(z) + capacity(z, 1) + 1 : list_word(z, 1); }
+FA_HD long long key_table_word(const Sizes &z) { return table_word(z) + capacity(z, 1) + 1; }
+FA_HD long long plan_words(const Sizes &z, bool grad) { return grad ? key_table_word(z) + key_tiles(z) : list_word(z, 1); }
+// fp32 values of the parts' dK and dV.
+FA_HD long long part_floats(const Sizes &z, int D)
+{
+    return max_parts(z) > 1 ? key_tiles(z) * z.Hkv * max_parts(z) * 2 * kTile * D : 0;
+}
 // CTAs that walk list l, and the rounds that their slots have room for.
 FA_HD int grid(const Sizes &z, int l, int sms)
 {
@@ -80,24 +111,25 @@ FA_HD int rounds(const Sizes &z, int l, int G) { return (int)((capacity(z, l) * 
 // Rows of the backward's row statistics per head: a whole number of query tiles.
 FA_HD long long padded_rows(const Sizes &z) { return (capacity(z, 1) + 1) * kTile; }
 
-// Keys that query row r of a sequence sees: [0, row_end).
-FA_HD int row_end(int r, int Lq, int Lk, bool causal)
+// Keys that a query row at key position `at` sees: [0, row_end).
+FA_HD int row_end(int at, int Lk, bool causal)
 {
     if (!causal)
         return Lk;
-    const int e = r + (Lk - Lq) + 1;
-    return e < 0 ? 0 : (e > Lk ? Lk : e);
+    return at < 0 ? 0 : (at >= Lk ? Lk : at + 1);
 }
-// Key tiles that query rows first .. first + 127 visit: at least one (rows that
-// see nothing get their zeros from a masked step), none where there is no row.
-FA_HD int key_steps(int first, int Lq, int Lk, bool causal)
+// Key tiles that query rows first .. first + 127 of `rows` visit, row 0 at key
+// position `off`: at least one (rows that see nothing get their zeros from a masked
+// step), none where there is no row.
+FA_HD int tile_steps(int first, int rows, int off, int Lk, bool causal)
 {
-    if (first >= Lq)
+    if (first >= rows)
         return 0;
-    const int last = first + kTile - 1 < Lq - 1 ? first + kTile - 1 : Lq - 1;
-    const int n = (int)(((unsigned)row_end(last, Lq, Lk, causal) + kTile - 1) / kTile);
+    const int last = first + kTile - 1 < rows - 1 ? first + kTile - 1 : rows - 1;
+    const int n = (int)(((unsigned)row_end(last + off, Lk, causal) + kTile - 1) / kTile);
     return n < 1 ? 1 : n;
 }
+FA_HD int key_steps(int first, int Lq, int Lk, bool causal) { return tile_steps(first, Lq, Lk - Lq, Lk, causal); }
 // First query tile that sees a key of key tile kt; -1 if none does.
 FA_HD int first_query_tile(int kt, int Lq, int Lk, bool causal)
 {
@@ -132,7 +164,8 @@ struct PackedSchedule : Schedule {
 };
 
 struct PackedTile {
-    int q0, Lq, k0, Lk;   // the sequence
+    int q0, rows, off;    // its first row, its rows, the first's key position
+    int k0, Lk;           // the sequence's keys
     int nw[2];            // key steps of its two Q tiles
     static constexpr bool few = false;
 };

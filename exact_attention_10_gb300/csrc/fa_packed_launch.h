@@ -16,6 +16,7 @@ struct PackedBwdLaunch {
     fa_rows o, dO, dq, dk, dv;
     const float *LSE;              // [H, Tq]
     float *lg, *dl, *dqa;          // workspace: [H][padded rows], and with D fused
+    float *part;                   // workspace: parts of key tiles (fa::packed::part_floats)
     const void *plan;
     fa::packed::Sizes z;
     int D, sms;

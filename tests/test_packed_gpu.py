@@ -13,6 +13,10 @@ query sees one key its gradients dQ and dK are exactly 0, the difference of two
 fp32 sums of D products that are the same but for their order and the roundings
 of their partial sums: |dP - delta| <= e = 2 D 2^-24 sum_d (|dO v| + |dO O|), to
 which the bounds add its way into them, scale sum_j p e |k| and scale sum_i p e |q|.
+Where a query sees a few keys and one has nearly all the weight, its gradients are
+small against what delta = rowsum(dO O) makes of O's own rounding to the type, off by
+up to d = eps/2 sum_d |dO O|: dS is off by p d, and a row of dQ by scale sum_j p d |k|, of
+dK by scale sum_i p d |q|, which the bounds of single rows add.
 """
 from __future__ import annotations
 
@@ -61,7 +65,8 @@ def reference(q, k, v, cq, ck, causal, scale, do=None):
     lse = torch.zeros((H, Tq), dtype=torch.float64, device="cuda")
     delta = torch.zeros_like(lse)
     dk, dv, fk = (torch.zeros(k.shape, dtype=torch.float64, device="cuda") for _ in range(3))
-    fq = torch.zeros_like(o)
+    fq, gq, gk = torch.zeros_like(o), torch.zeros_like(o), torch.zeros_like(fk)
+    half = torch.finfo(q.dtype).eps / 2 if q.dtype != torch.float64 else 0.0
     for a, b, c, d in zip(cq, cq[1:], ck, ck[1:]):
         if a == b:
             continue
@@ -85,7 +90,11 @@ def reference(q, k, v, cq, ck, causal, scale, do=None):
                 e = p * (2 * D * 2.0 ** -24) * (w.abs() @ z.abs().T + (w * o[a:b, h]).abs().sum(1, keepdim=True))
                 fq[a:b, h] = scale * e @ y.abs()
                 fk[c:d, h // G] += scale * e.T @ x.abs()
-    return o, lse, pv, delta, dq, dk, dv, fq, fk, torch.zeros_like(fk)
+                e = p * (half * (w * o[a:b, h]).abs().sum(1, keepdim=True))
+                gq[a:b, h] = scale * e @ y.abs()
+                gk[c:d, h // G] += scale * e.T @ x.abs()
+    none = torch.zeros_like(fk)
+    return o, lse, pv, delta, dq, dk, dv, fq, fk, none, gq, gk, none
 
 
 def check_forward(o, lse, ref, dtype):
@@ -101,12 +110,12 @@ def check_forward(o, lse, ref, dtype):
 
 def check_grads(got, ref, dtype):
     u = U[dtype]
-    for name, g, r, f in zip(("dQ", "dK", "dV"), got, ref, ref[3:]):
+    for name, g, r, f, gr in zip(("dQ", "dK", "dV"), got, ref, ref[3:], ref[6:]):
         g = g.double()
         assert bool(g.isfinite().all()), name
         rms = r.square().mean().sqrt()
         assert float((g - r).norm()) <= 1.5 * u * float(r.norm()) + float(f.norm()), name
-        row = 12 * u * (r.abs().amax(-1) + rms) + f.amax(-1)
+        row = 12 * u * (r.abs().amax(-1) + rms) + (f + gr).amax(-1)
         assert bool(((g - r).abs().amax(-1) <= row).all()), name
 
 
@@ -130,6 +139,9 @@ SHAPES = [
     ([1] * 40 + [260] + [0] * 3 + [33] * 9, None, 2, 1),
     ([60, 68], [500, 1000], 4, 1),                # at most 128 query tokens in all
     ([1030], [2100], 2, 1),
+    # enough tiles for those of 256 rows (the others are of 128)
+    ([300] * 20 + [513, 1, 0], None, 12, 4),
+    ([200, 290, 129] * 7, [0, 350, 100] * 7, 12, 12),
 ]
 
 
@@ -212,6 +224,28 @@ def test_rows_outside_and_neighbours_that_are_not_finite(D):
         ref = reference(*(torch.where(bad[:, None, None], torch.zeros_like(x), x) for x in (q, k, v)), cq, cq, False,
                         D ** -0.5, torch.where(bad[:, None, None], torch.zeros_like(do), do))
         check_grads([x[good] for x in fused], [x[good] for x in ref[4:]], "bf16")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_key_tiles_in_parts(causal, D):
+    """Few key tiles, many query rows to each: their query tiles are cut into parts, whose sums are the same bits every
+    time; sequences without queries or keys among them, and gradients into slices."""
+    lens, klens, H, Hkv = [2000, 130, 0, 700, 5], [2000, 300, 90, 650, 0], 8, 1
+    q, k, v, do = batch(lens, klens, H, Hkv, D, "bf16", seed=31)
+    cq, cu = _cu(lens)
+    ck, cu_k = _cu(klens)
+    plan = fa.packed_plan(cu, q.shape[0], H, Hkv, cu_k=cu_k, tokens_k=k.shape[0], causal=causal, grad=True)
+    o, lse = fa.packed_forward(q, k, v, plan)
+    kv = torch.full((k.shape[0], 3, D), 5.0, dtype=q.dtype, device="cuda")
+    dq, dk, dv = fa.packed_backward(q, k, v, o, do, lse, plan, dk=kv[:, 0:1], dv=kv[:, 2:3])
+    _ok()
+    check_grads((dq, dk, dv), reference(q, k, v, cq, ck, causal, D ** -0.5, do)[4:], "bf16")
+    assert bool((kv[:, 1] == 5.0).all())
+    for _ in range(3):
+        again = fa.packed_backward(q, k, v, o, do, lse, plan, deterministic=D == 64)
+        assert torch.equal(again[1], dk) and torch.equal(again[2], dv)
+    _ok()
 
 
 def test_low_scores_in_a_ragged_tile():
