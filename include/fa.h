@@ -431,7 +431,7 @@ FA_API fa_status fa_packed_bwd(const fa_rows *q, const fa_rows *k, const fa_rows
  * (quotients in float32, rounded to nearest even), and stands for code * scale: D +
  * 4 bytes for 2 D, values off by at most 2^-4 of themselves or 2^-10 of a scale,
  * but for float32's roundings.  A row that holds an infinity or NaN stands for NaN
- * or 0 where it is finite.
+ * throughout.
  *
  * table [B, width], lens, start [B] and cu [B + 1] are int32, device memory, read
  * there, so a captured graph follows their changes.  lens are clamped to [0, width *

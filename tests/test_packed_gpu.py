@@ -342,6 +342,25 @@ def test_another_stream_and_a_captured_graph():
         check_grads(grads, ref[4:], "bf16")
 
 
+def test_a_stream_of_its_own():
+    """Plan, forward and backward on a stream given by the call, while the current one does something else."""
+    lens, H, Hkv, D = [300, 41], 4, 2, 64
+    q, k, v, do = batch(lens, lens, H, Hkv, D, "fp16", seed=15)
+    cq, cu = _cu(lens)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    plan = fa.packed_plan(cu, sum(lens), H, Hkv, causal=True, grad=True, stream=st)
+    o, lse = fa.packed_forward(q, k, v, plan, stream=st)
+    junk = [torch.full((1 << 20,), 9.0, device="cuda") for _ in range(4)]   # (must not get the results' memory)
+    grads = fa.packed_backward(q, k, v, o, do, lse, plan, stream=st)
+    torch.cuda.current_stream().wait_stream(st)
+    _ok()
+    ref = reference(q, k, v, cq, cq, True, D ** -0.5, do)
+    check_forward(o, lse, ref, "fp16")
+    check_grads(grads, ref[4:], "fp16")
+    assert all(bool((x == 9.0).all()) for x in junk)
+
+
 def test_gradient_against_differences():
     """The directional derivative of sum(O dO) in float64 arithmetic, against the kernel's gradients."""
     H, Hkv, D, lens = 2, 1, 64, [40, 150]

@@ -404,6 +404,25 @@ def test_prompts_then_decoding():
                 assert bool(((res - p @ z).abs() <= bound).all())
 
 
+def test_streams_of_their_own():
+    """Append, read and attention on a stream given by the call."""
+    lens = [70, 33]
+    g = torch.Generator(device="cuda").manual_seed(37)
+    k, v = (torch.randn((103, 2, 64), generator=g, device="cuda").half() for _ in range(2))
+    q = torch.randn((2, 4, 1, 64), generator=g, device="cuda").half()
+    cache, table = fa.paged_empty(8, 2, 32, 64, torch.float16, 8), ints([[5, 0, 7], [2, 1, -1]])
+    zero, cu, n = ints([0, 0]), ints([0, 70, 103]), ints(lens)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    fa.paged_append(cache, table, k, v, zero, cu=cu, stream=st)
+    rk, _ = fa.paged_read(cache, table, zero, 103, cu=cu, dtype=torch.float16, stream=st)
+    o, lse = fa.paged_forward(q, cache, table, n, stream=st)
+    torch.cuda.current_stream().wait_stream(st)
+    _ok()
+    assert torch.equal(rk, held(k, 8).float().half())
+    check(q, o, lse, k, v, [0, 70], lens, 0.125, 8, "fp16")
+
+
 def test_copies_of_a_cache():
     cache = fa.paged_empty(4, 2, 16, 64, bits=8)
     twin = copy.deepcopy(cache)
