@@ -1,10 +1,10 @@
-// fa_launch.cuh -- kernel selection and launch, shared by the four
+// fa_launch.cuh -- kernel selection and launch, shared by the five
 // translation units that instantiate the kernels: fa_api.cu (whole-tile
 // variants without a mask or with the causal one, and the C ABI), fa_split.cu
 // (the same for the balanced schedule), fa_band.cu (left-bounded band masks,
-// both schedules) and fa_sink.cu (windows with sinks, both schedules).  Four
-// units keep each nvcc run to eight kernels and let the build compile them in
-// parallel.
+// both schedules), fa_sink.cu (windows with sinks, both schedules) and
+// fa_packed.cu (packed sequences).  Five units keep each nvcc run to eight
+// kernels and let the build compile them in parallel.
 #pragma once
 
 #include <cuda.h>
@@ -53,7 +53,7 @@ fa_status launch_variant(const CUtensorMap &q, const CUtensorMap &k, const CUten
     return FA_OK;
 }
 
-// The variants of one mask (kMaskNone, kMaskCausal, kMaskBand or kMaskSink) and schedule.
+// The variants of one mask (kMaskNone, kMaskCausal, kMaskBand, kMaskSink or kMaskPacked) and schedule.
 template <int MASK, bool SPLIT>
 fa_status launch_mask(int D, bool bf16, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                       const fa::ParamsOf<MASK> &p, int grid, cudaStream_t s, int dev)

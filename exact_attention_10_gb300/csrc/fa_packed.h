@@ -59,14 +59,17 @@ FA_HD bool few(const Sizes &z) { return (z.Tq / 256 + (long long)z.S) * z.H <= k
 FA_HD int cta_rows(const Sizes &z) { return few(z) ? kTile : 2 * kTile; }
 // Key tiles there may be, and the parts that one's query tiles may be cut into in the
 // dK/dV pass: with few key tiles and heads the longest alone would set the time.  A
-// part's sums go to a workspace, and reduce_parts_kernel adds them.
+// part's sums go to a workspace, and reduce_parts_kernel adds them.  At most 16, no
+// more than make four parts to a CTA, nor than the steps that a tile may have give.
+constexpr int kPartSteps = 8;   // of a part, at least
 FA_HD long long key_tiles(const Sizes &z) { return z.Tk / kTile + (long long)z.S; }
 FA_HD int max_parts(const Sizes &z)
 {
     const long long n = (4 * kOrderGrid + key_tiles(z) * z.Hkv - 1) / (key_tiles(z) * z.Hkv);
-    return n > 16 ? 16 : (int)n;
+    const long long m = ((z.Tq / kTile + 1ll) * (z.H / z.Hkv) + kPartSteps - 1) / kPartSteps;
+    const long long p = n < m ? n : m;
+    return p > 16 ? 16 : (int)p;
 }
-constexpr int kPartSteps = 8;   // of a part, at least
 // A slot's or an entry's tile with its part (of parts), and its head with the key tile's number in all.
 FA_HD int pack_part(int tile, int part, int parts) { return (int)((unsigned)tile | (unsigned)part << 24 | (unsigned)(parts - 1) << 28); }
 FA_HD int part_tile(int x) { return x & 0xffffff; }

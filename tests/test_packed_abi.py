@@ -102,7 +102,7 @@ def test_plan_room(lib):
     n = ctypes.c_size_t()
     for S, tq, tk in ((1, 1, 1), (3, 100, 700), (64, 36000, 36001)):
         keys = tk // 128 + S
-        parts = min(16, -(-640 // (2 * keys)))
+        parts = min(16, -(-640 // (2 * keys)), -(-(tq // 128 + 1) * 2 // 8))
         caps = [tq // (128 if (tq // 256 + S) * 4 <= 213 else 256) + S, tq // 128 + S, keys * parts]
         words = [1 + 2 * (caps[0] * 4 + 160 + caps[0] + S + 1)]
         words.append(1 + sum(2 * (c * h + 160 + c + S + 1) for c, h in zip(caps, (4, 4, 2))) + caps[1] + 1 + keys)
