@@ -277,7 +277,7 @@ __device__ __forceinline__ bool next_tile(PartIter &it, const S &s, Part &pt, in
         tile.Lk = seq.w;
         ct = 0;   // (rows are counted from the tile's first)
         tile.nw[0] = packed::tile_steps(0, seq.y, at.x, seq.w, s.causal);
-        tile.nw[1] = packed::tile_steps(kBM, seq.y, at.x, seq.w, s.causal);
+        tile.nw[1] = s.pairs ? tile.nw[0] : packed::tile_steps(kBM, seq.y, at.x, seq.w, s.causal);
         pt.kb = 0;
         pt.ke = tile.nw[0] > tile.nw[1] ? tile.nw[0] : tile.nw[1];
         return true;
@@ -530,13 +530,15 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
         ++nv;
         return true;
     };
-    [[maybe_unused]] auto load_q1 = [&](int bh, int ct, int q0) -> bool {
+    [[maybe_unused]] auto load_q1 = [&](int bh, int q0) -> bool {
         if (!warp_wait(b.q1_empty(), ((uint32_t)it1 & 1u) ^ 1u, c, kSiteLoadQEmpty))
             return false;
         if (ptx::elect_one()) {
             ptx::mbar_arrive_expect_tx(b.q1_full(), C::kTileBytes);
             for (int x = 0; x < C::kBoxes; ++x)
-                load_box<PACKED>(sQ + C::kTileBytes + x * C::kBoxBytes, tmQ, b.q1_full(), x * 64, ct * kCtaRows + kBM, bh, q0);
+                if constexpr (PACKED)
+                    load_box<true>(sQ + C::kTileBytes + x * C::kBoxBytes, tmQ, b.q1_full(), x * 64, p.sch.row(1),
+                                   p.sch.head(bh, 1), q0);
         }
         __syncwarp();
         ++it1;
@@ -561,8 +563,8 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
             for (int w = 0; w < kLoads; ++w)
                 for (int x = 0; x < C::kBoxes; ++x) {
                     if constexpr (PACKED)
-                        load_box<true>(dst + w * C::kTileBytes + x * C::kBoxBytes, tmQ, b.q_full(qb), x * 64,
-                                       ct * kCtaRows + w * kBM, bh, tile.q0);
+                        load_box<true>(dst + w * C::kTileBytes + x * C::kBoxBytes, tmQ, b.q_full(qb), x * 64, p.sch.row(w),
+                                       p.sch.head(bh, w), tile.q0);
                     else
                         ptx::tma_load_3d(dst + w * C::kTileBytes + x * C::kBoxBytes, tmQ, b.q_full(qb), x * 64,
                                          ct * kCtaRows + w * kBM, bh);
@@ -599,7 +601,7 @@ __device__ void load_role(const CUtensorMap *tmQ, const CUtensorMap *tmK, const 
             }
             __syncwarp();
             if constexpr (kSplitQ<D, MASK>) {   // Q tile 1 behind the first step's K and V, as mma_parts wants them
-                if (j == 0 && tile.nw[1] > 0 && !load_q1(bh, ct, tile.q0)) { ++step; ok = false; break; }
+                if (j == 0 && tile.nw[1] > 0 && !load_q1(bh, tile.q0)) { ++step; ok = false; break; }
             }
             if (SKV) {   // V of the previous step, then this step's V becomes the pending one
                 if (nv < step && !load_v()) { ++step; ok = false; break; }
@@ -1125,8 +1127,9 @@ __device__ void softmax_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, float2
         const auto keys = step_keys<MASK>(p.sch, tile, ct);   // the tile's key steps
         int row_lo = 0, row_hi = p.Nkv, edge_lo = 0, edge_hi = p.Nkv;
         if constexpr (MASK == kMaskPacked) {
-            row_hi = packed::row_end(min(row, tile.rows - 1) + tile.off, tile.Lk, p.sch.causal);
-            edge_hi = packed::row_end(w * kBM + tile.off, tile.Lk, p.sch.causal);   // (at most Lk)
+            const int first = p.sch.row(w);
+            row_hi = packed::row_end(min(first + t, tile.rows - 1) + tile.off, tile.Lk, p.sch.causal);
+            edge_hi = packed::row_end(first + tile.off, tile.Lk, p.sch.causal);   // (at most Lk)
         } else if (CAUSAL) {
             const int first = ct * kCtaRows + w * kBM, r = min(row, p.N - 1);
             row_hi = sched_row_hi(p.sch, r);
@@ -1666,16 +1669,18 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
             const bool whole = !SPLIT || (pt.kb == 0 && pt.ke >= nw);   // no other part holds steps of this Q tile
             const float inv_l = (st.y > 0.f) ? 1.f / st.y : 0.f;   // a row that saw no key: O = 0
             const uint64_t il2 = ptx::f2_pack(inv_l, inv_l);
-            const int row = ct * kCtaRows + w * kBM + t;
+            int row = ct * kCtaRows + w * kBM + t;
             bool valid = row < p.N;
-            if constexpr (MASK == kMaskPacked)
+            if constexpr (MASK == kMaskPacked) {
+                row = p.sch.row(w) + t;
                 valid = row < tile.rows;
+            }
             const uint32_t tO = tmem + C::col_o(w) + lane_off;
             if (whole) {
                 uint8_t *orow =
                     reinterpret_cast<uint8_t *>(p.O) + ((size_t)bh * p.N + (size_t)(valid ? row : 0)) * D * 2;
                 if constexpr (MASK == kMaskPacked)
-                    orow = reinterpret_cast<uint8_t *>(p.O) + (tile.q0 + (valid ? row : 0)) * p.o_row + bh * p.o_head;
+                    orow = reinterpret_cast<uint8_t *>(p.O) + (tile.q0 + (valid ? row : 0)) * p.o_row + p.sch.head(bh, w) * p.o_head;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t o[32];
@@ -1700,7 +1705,7 @@ __device__ void epilogue_role(const P &p, uint32_t tmem, Bars<D> b, Ctl c, uint3
                 }
                 if (valid) {
                     if constexpr (MASK == kMaskPacked)
-                        p.LSE[bh * p.lse_head + tile.q0 + row] = (st.x + log2f(st.y)) * kLn2;
+                        p.LSE[p.sch.head(bh, w) * p.lse_head + tile.q0 + row] = (st.x + log2f(st.y)) * kLn2;
                     else
                         p.LSE[(size_t)bh * p.N + row] = (st.x + log2f(st.y)) * kLn2;
                 }

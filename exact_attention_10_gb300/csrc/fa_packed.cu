@@ -125,9 +125,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     };
     const int heads = pk::heads_of(p.z, l), mul = l == 2 ? p.z.H / p.z.Hkv : 1, most = l == 2 ? pk::max_parts(p.z) : 1;
     auto steps = [&](const int4 &q, int i) -> int {
-        if (l == 0)
-            return pk::key_steps(i * tile, q.y, q.w, p.causal) +
-                   (tile > pk::kTile ? pk::key_steps(i * tile + pk::kTile, q.y, q.w, p.causal) : 0);
+        if (l == 0) {
+            const int c = pk::key_steps(i * tile, q.y, q.w, p.causal);
+            if (pk::pairs(p.z))
+                return 2 * c;
+            return c + (tile > pk::kTile ? pk::key_steps(i * tile + pk::kTile, q.y, q.w, p.causal) : 0);
+        }
         if (l == 1)
             return pk::key_steps(i * tile, q.y, q.w, p.causal);
         const int f = pk::first_query_tile(i, q.y, q.w, p.causal);
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         if (l == 0) {
             const int first = i * tile;
             at[0] = make_int4(q.x + first, min(tile, q.y - first), q.z, q.w);
-            at[1] = make_int4(first + q.w - q.y, 0, h, 1);
+            at[1] = make_int4(first + q.w - q.y, 0, pk::pairs(p.z) ? 2 * h : h, 1);
         } else {
             at[0] = q;
             at[1] = make_int4(w.x, w.y, most > 1 ? h | w.z << 16 : h, total_q + 1);
@@ -420,7 +423,8 @@ extern "C" fa_status fa_packed_fwd(const fa_rows *q, const fa_rows *k, const fa_
     fa::PackedParams p{};
     p.O = o->ptr;
     p.LSE = LSE;
-    p.N = pk::cta_rows(z);
+    p.N = pk::few(z) ? pk::kTile : 2 * pk::kTile;
+    p.sch.pairs = pk::pairs(z);
     p.Nkv = z.Tk;
     p.lse_head = z.Tq;
     p.qk_scale = scale * 1.4426950408889634f;   // scale * log2(e)

@@ -6,7 +6,7 @@
 // Lengths are device data, so a kernel on the device (fa_packed_plan.cu) lays
 // out the work once per batch and every layer's calls read it: up to three
 // lists of tiles, each longest first --
-//   list 0  forward: CTA tiles of 256 query rows (128 where there are few)
+//   list 0  forward: CTA tiles of 256 query rows, or 128 (few, pairs)
 //   list 1  dQ pass and the rows' statistics: query tiles of 128 rows
 //   list 2  dK/dV pass: key tiles of 128 rows
 // -- an entry of which is a tile of one sequence, and a tile of work one of its
@@ -56,7 +56,13 @@ struct Sizes {
 // us: 8192 tokens, 4 heads, 132 tiles of 256 106 / 71; 4096 and 2000 tokens, 8 heads, 200
 // tiles 57 / 46; 8192 tokens, 8 heads, 264 tiles 107 / 129.)
 FA_HD bool few(const Sizes &z) { return (z.Tq / 256 + (long long)z.S) * z.H <= kOrderGrid * 4 / 3; }
-FA_HD int cta_rows(const Sizes &z) { return few(z) ? kTile : 2 * kTile; }
+// Otherwise a CTA tile's two Q tiles are the same 128 rows of two heads that share a key
+// head, where an even number of them does: both visit the same steps (of 256 rows of a
+// causal sequence the second Q tile's last is its alone), and no sequence's last 128 rows
+// are left single.  (Causal, D = 128, 32 heads on 8: 152 prompts of 256 tokens 165 -> 153
+// us, of 128 tokens 97 -> 74; 64 of 64 to 2048 382 -> 348.)
+FA_HD bool pairs(const Sizes &z) { return !few(z) && z.H / z.Hkv % 2 == 0; }
+FA_HD int cta_rows(const Sizes &z) { return few(z) || pairs(z) ? kTile : 2 * kTile; }
 // Key tiles there may be, and the parts that one's query tiles may be cut into in the
 // dK/dV pass: with few key tiles and heads the longest alone would set the time.  A
 // part's sums go to a workspace, and reduce_parts_kernel adds them.  At most 16, no
@@ -82,7 +88,7 @@ FA_HD long long capacity(const Sizes &z, int l)
 {
     return l == 2 ? key_tiles(z) * max_parts(z) : (l == 0 ? z.Tq / cta_rows(z) : z.Tq / kTile) + (long long)z.S;
 }
-FA_HD int heads_of(const Sizes &z, int l) { return l == 2 ? z.Hkv : z.H; }
+FA_HD int heads_of(const Sizes &z, int l) { return l == 2 ? z.Hkv : l == 0 && pairs(z) ? z.H / 2 : z.H; }
 // Slots that list l has room for (CTAs' rounds are as many for all of them).
 FA_HD long long slots(const Sizes &z, int l) { return capacity(z, l) * heads_of(z, l) + kOrderGrid; }
 FA_HD long long list_word(const Sizes &z, int l)   // first word of list l: its slots
@@ -164,6 +170,9 @@ struct PackedSchedule : Schedule {
     const int4 *slots;
     int rounds;         // slots of a CTA
     int group;          // query heads per key head
+    int pairs;          // Q tile w is head bh + w's (packed::pairs)
+    __device__ int row(int w) const { return pairs ? 0 : w * packed::kTile; }   // first row of Q tile w
+    __device__ int head(int bh, int w) const { return pairs ? bh + w : bh; }
 };
 
 struct PackedTile {

@@ -103,9 +103,11 @@ def test_plan_room(lib):
     for S, tq, tk in ((1, 1, 1), (3, 100, 700), (64, 36000, 36001)):
         keys = tk // 128 + S
         parts = min(16, -(-640 // (2 * keys)), -(-(tq // 128 + 1) * 2 // 8))
-        caps = [tq // (128 if (tq // 256 + S) * 4 <= 213 else 256) + S, tq // 128 + S, keys * parts]
-        words = [1 + 2 * (caps[0] * 4 + 160 + caps[0] + S + 1)]
-        words.append(1 + sum(2 * (c * h + 160 + c + S + 1) for c, h in zip(caps, (4, 4, 2))) + caps[1] + 1 + keys)
+        few = (tq // 256 + S) * 4 <= 213
+        caps = [tq // 128 + S, tq // 128 + S, keys * parts]   # (pairs of heads, or few: tiles of 128 rows)
+        h0 = 4 if few else 2
+        words = [1 + 2 * (caps[0] * h0 + 160 + caps[0] + S + 1)]
+        words.append(1 + sum(2 * (c * h + 160 + c + S + 1) for c, h in zip(caps, (h0, 4, 2))) + caps[1] + 1 + keys)
         for grad in (0, 1):
             assert lib.fa_packed_plan_bytes(_sizes(seqs=S, tokens_q=tq, tokens_k=tk), grad, n) == 0
             assert n.value == 16 * words[grad]

@@ -142,6 +142,9 @@ SHAPES = [
     # enough tiles for those of 256 rows (the others are of 128)
     ([300] * 20 + [513, 1, 0], None, 12, 4),
     ([200, 290, 129] * 7, [0, 350, 100] * 7, 12, 12),
+    # ... and pairs of heads
+    ([300] * 20 + [513, 1, 0], None, 16, 4),
+    ([200, 290, 129] * 7, [0, 350, 100] * 7, 12, 6),
 ]
 
 
