@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import copy
 import math
+import os
 
 import pytest
 import torch
@@ -421,6 +422,27 @@ def test_streams_of_their_own():
     _ok()
     assert torch.equal(rk, held(k, 8).float().half())
     check(q, o, lse, k, v, [0, 70], lens, 0.125, 8, "fp16")
+
+
+def test_the_readme_block():
+    """The README's python block on packed sequences and the paged cache, run as it stands with small sizes."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        blocks = [b.split("```")[0] for b in f.read().split("```python\n")[1:]]
+    text, = (b for b in blocks if b.startswith("# packed sequences"))
+    g = torch.Generator(device="cuda").manual_seed(41)
+    H, Hkv, D, lens, T = 4, 2, 64, ints([50, 3]), 53
+    q, do = (torch.randn((T, H, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn((T, Hkv, D), generator=g, device="cuda").bfloat16() for _ in range(2))
+    tokens = [(torch.randn((2, H, 1, D), generator=g, device="cuda").bfloat16(),
+               *(torch.randn((2, Hkv, D), generator=g, device="cuda").bfloat16() for _ in range(2))) for _ in range(20)]
+    names = dict(fa=fa, torch=torch, q=q, k=k, v=v, do=do, H=H, Hkv=Hkv, D=D, T=T, cu=ints([0, 50, 53]), start=ints([0, 0]),
+                 lens=lens, pages=12, table=torch.arange(12, dtype=torch.int32, device="cuda").view(2, 6), tokens=tokens)
+    exec(compile(text, "README.md", "exec"), names)
+    _ok()
+    assert lens.tolist() == [70, 23]
+    hk = [torch.cat([x[a:b], *(t[1 + i][s:s + 1] for t in tokens)]) for i, x in ((0, k), (1, v)) for s, a, b in ((0, 0, 50), (1, 50, 53))]
+    check(tokens[-1][0], names["o"], names["lse"], torch.cat(hk[:2]), torch.cat(hk[2:]), [0, 70], [70, 23], D ** -0.5, 16, "bf16")
 
 
 def test_copies_of_a_cache():
